@@ -240,10 +240,12 @@ ks_status_t ks_fused_add_rms_norm_planned(void *x, void *residual, const void *w
 /*
  * Device-side faults of the current device: the OR of the fault words the kernels set (bit 0,
  * KS_FAULT_WAIT_TIMEOUT: a staged kernel gave up waiting for a bulk copy after about 2 s, left
- * its row loop and returned; its outputs are then incomplete). Reading synchronises with the
- * device. clear != 0 zeroes the words after reading. KS_ERR_CUDA if the read fails.
+ * its row loop and returned; its outputs are then incomplete; bit 1, KS_FAULT_BAD_INDEX: a slot,
+ * page or length that ks_rotary_to_pages or ks_paged_attention read on the device was out of range
+ * and its access was left out). Reading synchronises with the device. clear != 0 zeroes the words after reading. KS_ERR_CUDA if the read fails.
  */
 #define KS_FAULT_WAIT_TIMEOUT 1
+#define KS_FAULT_BAD_INDEX 2
 ks_status_t ks_device_faults(int32_t *flags, int32_t clear);
 
 /*
@@ -378,6 +380,122 @@ ks_status_t ks_softmax_planned(void *out, const void *x, int64_t rows, int64_t h
 ks_status_t ks_layer_norm_planned(void *out, const void *x, const void *weight, const void *bias,
                                   int64_t rows, int64_t hidden, float eps, ks_dtype_t dtype,
                                   const ks_plan_t *plan, ks_stream_t stream);
+
+/*
+ * Rotary positions. Pair j of each head is rotated by the angle position * f_j, in FP32, rounded
+ * once:
+ *     (x, y) -> (x c - y s, y c + x s),   c = scale * cos(position * f_j), s = scale * sin(...)
+ * The pairs are (j, j + rotary_dim / 2), or neighbours (2j, 2j + 1) with KS_ROTARY_INTERLEAVED;
+ * the values from rotary_dim on are copied. KS_ROTARY_INVERSE turns the other way (the inverse
+ * for scale 1, and the gradient of the forward turn for any scale).
+ *
+ * Frequencies come as fractions of a turn in 64-bit fixed point, steps[j] = round(f_j / (2 pi) *
+ * 2^64): position * steps[j] mod 2^64 is the angle exactly reduced, so far positions lose
+ * nothing. Scaling for long contexts is a change of the steps (and of scale).
+ *
+ * Tensors are [tokens, heads, head_dim] with contiguous head rows; strides are in elements. An
+ * output may be exactly its input (in place); otherwise it must not share memory with any input.
+ * The parts of one fused projection (one token stride) count as apart.
+ *
+ * ks_rotary writes q_out and k_out (v, the cache and slots are not looked at); either side may
+ * be absent (its head count 0). ks_rotary_to_pages rotates q into q_out and k into the cache, and
+ * copies v into it: token t's rows go to slot slots[t], that is page slots[t] / page_size, place
+ * slots[t] % page_size. A negative slot writes neither row (a padding token); a slot past the pool
+ * is left out too and sets KS_FAULT_BAD_INDEX. Slots of a call must differ: of two tokens with one
+ * slot, either's values are left. rotary_dim 0 only writes the cache (steps and positions unread).
+ *
+ * Errors as for ks_rms_norm: KS_ERR_INVALID_ARGUMENT for sizes, strides, alignment to the element
+ * (indices: 8 bytes) or NULL pointers; KS_ERR_OVERLAP as above, and when the cache shares memory
+ * with q, k, v or q_out. tokens == 0 launches nothing. Rows and strides of 16 bytes take vector
+ * kernels, anything else a scalar kernel of the same arithmetic.
+ */
+#define KS_ROTARY_INTERLEAVED 1
+#define KS_ROTARY_INVERSE 2
+typedef struct ks_rotary_args {
+    void *q_out;                 /* [tokens, q_heads, head_dim] */
+    const void *q;
+    void *k_out;                 /* [tokens, kv_heads, head_dim]; ks_rotary only */
+    const void *k;
+    const void *v;               /* [tokens, kv_heads, head_dim]; ks_rotary_to_pages only */
+    const int64_t *positions;    /* [tokens]; any int64, negative too */
+    const int64_t *steps;        /* [rotary_dim / 2] */
+    void *k_pages;               /* [pages, page_size, kv_heads, head_dim], any stride order */
+    void *v_pages;
+    const int64_t *slots;        /* [tokens] */
+    int64_t tokens, q_heads, kv_heads, head_dim, rotary_dim; /* head_dim 1 .. 1024 */
+    int64_t pages, page_size;
+    int64_t q_out_token_stride, q_out_head_stride;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_out_token_stride, k_out_head_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t k_page_stride, k_slot_stride, k_pages_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_pages_head_stride;
+    float scale;                 /* finite; multiplies the rotated values */
+    int32_t flags;               /* KS_ROTARY_* bits */
+    int32_t dtype;               /* ks_dtype_t */
+    int32_t reserved;
+} ks_rotary_args_t;
+ks_status_t ks_rotary(const ks_rotary_args_t *args, ks_stream_t stream);
+ks_status_t ks_rotary_to_pages(const ks_rotary_args_t *args, ks_stream_t stream);
+
+/*
+ * Attention of each sequence's new tokens over its paged cache (which already holds the new
+ * tokens' keys and values, as ks_rotary_to_pages leaves them):
+ *     out[t, h] = sum_j softmax_j(scale * q[t, h] . k_j) v_j
+ * Sequence b has the packed tokens q_starts[b] .. q_starts[b + 1] - 1 and the first kv_lens[b]
+ * keys of the pages that row b of the page table lists: key j is place j % page_size of page
+ * page_table[b * table_stride + j / page_size]. With KS_ATTENTION_CAUSAL the i-th of n new tokens
+ * sees the keys j < kv_lens[b] - n + i + 1, without it all of them; a row that sees none is 0.
+ * Query head h reads key/value head h / (q_heads / kv_heads). The same entry serves single
+ * tokens, chunks of a prompt and batches of both; sequences may have no new token or no key.
+ *
+ * FP32 scores, maxima, sums and outputs, one rounding at the end; the probabilities are rounded
+ * to the 16-bit type for the product with the values. Results are the same from run to run; a
+ * call of other sizes (or another max_q_len) may add up in another order.
+ *
+ * What is not part of a sequence is not read: table entries past its last page, and cache places
+ * at and past kv_lens[b] (whatever they hold). Keys that only some rows of a call's tile see must
+ * hold finite values (a NaN at a new token's place may reach the tokens before it). Rows of out
+ * outside every sequence are left as they were. A length or start out of range is brought into
+ * range, and a page outside the pool reads as zeros; each sets KS_FAULT_BAD_INDEX.
+ *
+ * The workspace is device memory, 16-byte aligned, of at least the bytes that
+ * ks_paged_attention_workspace gives for the same sizes on the current device (it reads the
+ * struct's sizes, flags and dtype alone); its contents do not matter. Calls that may run at once need workspaces of their own. A captured call may be
+ * replayed with other contents of kv_lens, q_starts and page_table.
+ *
+ * Errors: KS_ERR_UNSUPPORTED_DTYPE for KS_DTYPE_F32; KS_ERR_INVALID_ARGUMENT for sizes, NULL
+ * pointers, data or strides that are not multiples of 16 bytes, a workspace that is too small;
+ * KS_ERR_OVERLAP when out shares memory with q or the cache. tokens == 0 or seqs == 0 launches
+ * nothing.
+ */
+#define KS_ATTENTION_CAUSAL 1
+typedef struct ks_attention_args {
+    void *out;                   /* [tokens, q_heads, head_dim] */
+    const void *q;               /* [tokens, q_heads, head_dim] */
+    const void *k_pages;         /* [pages, page_size, kv_heads, head_dim], any stride order */
+    const void *v_pages;
+    const int32_t *page_table;   /* [seqs, table_pages], row stride table_stride */
+    const int32_t *kv_lens;      /* [seqs] */
+    const int32_t *q_starts;     /* [seqs + 1], non-decreasing */
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t tokens, seqs, q_heads, kv_heads, head_dim; /* head_dim: a multiple of 8, at most 256 */
+    int64_t pages, page_size, table_pages, table_stride;
+    int64_t max_q_len;           /* most new tokens of a sequence, 0 if unknown: picks the kernel
+                                    only; any value gives right results */
+    int64_t out_token_stride, out_head_stride;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_page_stride, k_slot_stride, k_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_head_stride;
+    float scale;                 /* finite */
+    int32_t flags;               /* KS_ATTENTION_* bits */
+    int32_t dtype;               /* KS_DTYPE_F16 or KS_DTYPE_BF16 */
+    int32_t reserved;
+} ks_attention_args_t;
+ks_status_t ks_paged_attention_workspace(const ks_attention_args_t *args, int64_t *bytes);
+ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stream);
 
 /* Library version, major*10000 + minor*100 + patch. */
 int32_t ks_version(void);

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -22,11 +23,21 @@ KERNEL_NAMES = {0: "none", 1: "warp_row", 2: "cta_row", 3: "scalar", 4: "bulk_ro
 # ks_plan_launch's op codes
 OP_RMS_NORM, OP_FUSED_ADD_RMS_NORM, OP_SILU_AND_MUL, OP_SOFTMAX, OP_LAYER_NORM = range(5)
 KS_FAULT_WAIT_TIMEOUT = 1
+KS_FAULT_BAD_INDEX = 2
 KS_PLAN_NO_PREFETCH = 1
 KS_PLAN_PDL = 2
 KS_PLAN_AFFINE_SMEM = 4
 KS_PLAN_SMEM_ROWS = 8
 KS_LAUNCH_PDL = 1
+KS_ROTARY_INTERLEAVED = 1
+KS_ROTARY_INVERSE = 2
+KS_ATTENTION_CAUSAL = 1
+
+# The argument structs of the decode operators, fields in the header's order: pointers, 64-bit
+# sizes and strides, then the float and three 32-bit fields. Packed into bytes, whose address is
+# the C argument.
+ROTARY_ARGS = struct.Struct("=10Q23qfiii")     # ks_rotary_args_t
+ATTENTION_ARGS = struct.Struct("=8Q21qfiii")   # ks_attention_args_t
 
 # Every symbol include/ks.h declares (checked by the CPU test of the boundary).
 EXPORTED = ("ks_rms_norm", "ks_fused_add_rms_norm", "ks_status_string", "ks_last_error",
@@ -35,7 +46,8 @@ EXPORTED = ("ks_rms_norm", "ks_fused_add_rms_norm", "ks_status_string", "ks_last
             "ks_host_chunk_rows", "ks_fused_add_rms_norm_host_noalloc", "ks_set_launch_options",
             "ks_get_launch_options", "ks_silu_and_mul", "ks_softmax", "ks_layer_norm",
             "ks_silu_and_mul_planned", "ks_softmax_planned", "ks_layer_norm_planned",
-            "ks_version")
+            "ks_rotary", "ks_rotary_to_pages", "ks_paged_attention",
+            "ks_paged_attention_workspace", "ks_version")
 
 
 class KsLibraryMissing(RuntimeError):
@@ -125,6 +137,11 @@ def load(path: str | None = None):
         lib.ks_softmax_planned.restype = ctypes.c_int
         lib.ks_layer_norm_planned.argtypes = [vp, vp, vp, vp, i64, i64, f32, ctypes.c_int, PP, vp]
         lib.ks_layer_norm_planned.restype = ctypes.c_int
+        for f in (lib.ks_rotary, lib.ks_rotary_to_pages, lib.ks_paged_attention):
+            f.argtypes = [ctypes.c_char_p, vp]
+            f.restype = ctypes.c_int
+        lib.ks_paged_attention_workspace.argtypes = [ctypes.c_char_p, ctypes.POINTER(i64)]
+        lib.ks_paged_attention_workspace.restype = ctypes.c_int
         lib.ks_version.argtypes = []
         lib.ks_version.restype = i32
         _lib = lib
@@ -248,6 +265,25 @@ def ks_layer_norm_planned(out: int, x: int, weight: int | None, bias: int | None
                           stream: int | None) -> int:
     return load().ks_layer_norm_planned(out, x, weight, bias, rows, hidden, eps, dtype,
                                         ctypes.byref(plan), stream)
+
+
+def ks_rotary(args: bytes | None, stream: int | None) -> int:
+    return load().ks_rotary(args, stream)
+
+
+def ks_rotary_to_pages(args: bytes | None, stream: int | None) -> int:
+    return load().ks_rotary_to_pages(args, stream)
+
+
+def ks_paged_attention(args: bytes | None, stream: int | None) -> int:
+    return load().ks_paged_attention(args, stream)
+
+
+def ks_paged_attention_workspace(args: bytes | None) -> tuple[int, int]:
+    """(status, bytes) for a call of these sizes on the current device."""
+    need = ctypes.c_int64(0)
+    st = load().ks_paged_attention_workspace(args, ctypes.byref(need))
+    return st, need.value
 
 
 def ks_version() -> int:

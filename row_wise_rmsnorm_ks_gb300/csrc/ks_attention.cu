@@ -1,0 +1,572 @@
+// Attention of new tokens over a paged key/value cache: the kernel for few rows per key/value head
+// (single tokens, short drafts), the join of split rows, and the C entry points.
+//
+// Mathematics, per query row with scores s_j = scale * q.k_j over the keys it sees:
+//   m = max s_j, l = sum exp(s_j - m), o = sum exp(s_j - m) v_j / l
+// in one pass with a running maximum: when m grows, l and o are scaled by exp(m_old - m_new).
+// Scores, maxima, sums and outputs are FP32. The probabilities are rounded to the inputs' 16-bit
+// type for the second matrix product (relative error 2^-9 for bf16, 2^-12 for fp16, averaged over
+// the keys); the sum l adds them before that rounding.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "ks_attention.cuh"
+
+namespace ks {
+namespace {
+
+constexpr int kRows = 16;                 // rows of a tile: one mma.m16n8k16 tile
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kSub = 16;                  // keys of a warp's step
+constexpr int kUnit = kWarps * kSub;      // keys of a unit: a step of each warp
+
+// Few rows make this a stream of the cache: per key of 128 values 512 bytes, 16 query rows cost
+// two 16x8x16 matrix instructions, a tenth of the time its bytes take. Each warp therefore runs
+// alone on every fourth 16-key step, with its own ring of asynchronous 16-byte copies in shared
+// memory (no barrier in the loop), its own maximum, sum and output registers; the four are joined
+// when the row tile ends.
+template <int kDim>
+struct Rows16 {
+    static constexpr int kStages = kDim == 64 ? 4 : 3;
+    static constexpr int kStepBytes = 2 * kSub * kDim * 2;  // keys and values of a step
+    static constexpr int kRingBytes = kWarps * kStages * kStepBytes;
+    static constexpr int kQBytes = kRows * kDim * 2;
+    static constexpr int kSmem = kRingBytes + kQBytes;
+    static constexpr int kCtasPerSm = kDim == 64 ? 3 : kDim == 128 ? 2 : 1;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros, src is not read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    uint32_t w;
+    memcpy(&w, &h, 4);
+    return w;
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    uint32_t w;
+    memcpy(&w, &h, 4);
+    return w;
+}
+
+// Shared-memory address of 16-byte chunk c of row r in a tile of kDim 16-bit values a row: chunks
+// are exchanged within a row by the row's low bits, so that ldmatrix reads eight rows without
+// bank conflicts.
+template <int kDim>
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int c) {
+    return base + (uint32_t)(r * (kDim * 2) + ((c ^ (r & 7)) << 4));
+}
+
+template <typename T, int kDim>
+__global__ void __launch_bounds__(kThreads, Rows16<kDim>::kCtasPerSm)
+attn_rows16_kernel(const __grid_constant__ AttnArgs s) {
+    using C = Rows16<kDim>;
+    constexpr bool kQRegs = kDim <= 128;  // above, the output registers leave no room for them
+    constexpr int kSteps = kDim / 16;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const ks_attention_args_t &a = s.a;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int ctas = gridDim.x, cta = blockIdx.x;
+    grid_dependency_wait();
+    allow_dependents_launch();
+    if (threadIdx.x == 0) attn_joins(s, ctas)[cta].pieces = 0;
+    AttnCursor cur = attn_begin<kThreads>(s, cta, ctas);
+    if (cur.left <= 0) return;
+    AttnSeq q = attn_seq(a, cur.seq);
+
+    const int dim = (int)a.head_dim, chunks = dim / 8;
+    const uint32_t ring = smem_addr(smem) + warp * C::kStages * C::kStepBytes;
+    uint8_t *q_smem = smem + C::kRingBytes;
+    const uint32_t q_addr = smem_addr(q_smem);
+    const int page_size = (int)a.page_size;
+
+    while (true) {
+        const int units = attn_tile_units(s, q, cur.row_tile);
+        const int first = cur.unit, last = (int)min((int64_t)units, first + cur.left);
+        const int sees = attn_tile_keys(s, q, cur.row_tile);
+        const int kv_head = cur.head / s.head_splits;
+        const T *k_base = (const T *)a.k_pages + kv_head * a.k_head_stride;
+        const T *v_base = (const T *)a.v_pages + kv_head * a.v_head_stride;
+        const int32_t *table = a.page_table + (int64_t)cur.seq * a.table_stride;
+
+        // Page of the lane's key (lanes 0..15: the step's 16 keys), read one step ahead.
+        auto look_up = [&](int unit) -> int {
+            const int key = unit * kUnit + warp * kSub + (lane & 15);
+            return unit < last && key < sees ? __ldg(table + key / page_size) : -1;
+        };
+        auto load_step = [&](int unit, int stage, int page) {
+            const int key = unit * kUnit + warp * kSub + (lane & 15);
+            const bool wanted = unit < last && key < sees;
+            const bool good = wanted && (uint32_t)page < (uint64_t)a.pages;
+            if (wanted && !good) atomicOr(&g_fault_flags, kFaultBadIndex);
+            const int slot = key % page_size;
+            const int64_t ko = good ? page * a.k_page_stride + slot * a.k_slot_stride : -1;
+            const int64_t vo = good ? page * a.v_page_stride + slot * a.v_slot_stride : -1;
+            const uint32_t kt = ring + stage * C::kStepBytes, vt = kt + kSub * kDim * 2;
+            constexpr int kLanes = kDim / 8 < 8 ? kDim / 8 : 8;  // lanes per row: 128 bytes
+            constexpr int kRowsAtOnce = 32 / kLanes;
+#pragma unroll
+            for (int r0 = 0; r0 < kSub; r0 += kRowsAtOnce) {
+                const int r = r0 + lane / kLanes;
+                const int64_t kr = __shfl_sync(0xFFFFFFFFu, ko, r), vr = __shfl_sync(0xFFFFFFFFu, vo, r);
+#pragma unroll
+                for (int c0 = 0; c0 < kDim / 8; c0 += kLanes) {
+                    const int c = c0 + lane % kLanes;
+                    const bool in = kr >= 0 && c < chunks;
+                    cp_async16(tile_addr<kDim>(kt, r, c), in ? (const void *)(k_base + kr + c * 8) : a.q, in);
+                    cp_async16(tile_addr<kDim>(vt, r, c), in ? (const void *)(v_base + vr + c * 8) : a.q, in);
+                }
+            }
+        };
+
+        int page = look_up(first);
+#pragma unroll
+        for (int i = 0; i < C::kStages - 1; ++i) {
+            const int next = look_up(first + i + 1);
+            load_step(first + i, i, page);
+            cp_async_commit();
+            page = next;
+        }
+        // the query rows, zeros where the tile has none
+        for (int i = threadIdx.x; i < kRows * (kDim / 8); i += kThreads) {
+            const int r = i / (kDim / 8), c = i % (kDim / 8);
+            int token, head;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (attn_row(s, q.q0, q.n, cur.head, cur.row_tile, r, &token, &head) && c < chunks)
+                x = *reinterpret_cast<const uint4 *>((const T *)a.q + token * a.q_token_stride +
+                                                     head * a.q_head_stride + c * 8);
+            *reinterpret_cast<uint4 *>(q_smem + (tile_addr<kDim>(0, r, c))) = x;
+        }
+        __syncthreads();
+        uint32_t qf[kQRegs ? kSteps : 1][4];
+        auto load_q = [&](uint32_t (&f)[4], int k) {
+            ldmatrix4(f, tile_addr<kDim>(q_addr, lane & 15, k * 2 + (lane >> 4)));
+        };
+        if (kQRegs) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) load_q(qf[kQRegs ? k : 0], k);
+        }
+
+        // keys that this thread's two rows see
+        int limit[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int in_seq = cur.row_tile * s.tile_tokens + (lane / 4 + 8 * i) / s.tile_heads;
+            limit[i] = (a.flags & KS_ATTENTION_CAUSAL) ? min(sees, q.keys - q.n + in_seq + 1) : sees;
+        }
+        const int all_see = (a.flags & KS_ATTENTION_CAUSAL)
+                                ? min(sees, q.keys - q.n + cur.row_tile * s.tile_tokens + 1) : sees;
+
+        float o[kDim / 8][4];
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+
+        int stage = 0;
+        for (int unit = first; unit < last; ++unit) {
+            {
+                const int ahead = unit + C::kStages - 1;
+                const int to = stage == 0 ? C::kStages - 1 : stage - 1;
+                const int next = look_up(ahead + 1);
+                load_step(ahead, to, page);
+                cp_async_commit();
+                page = next;
+            }
+            cp_async_wait<C::kStages - 1>();
+            __syncwarp();
+            const uint32_t kt = ring + stage * C::kStepBytes, vt = kt + kSub * kDim * 2;
+            const int key0 = unit * kUnit + warp * kSub;
+            if (key0 < sees) {
+                float sc[2][4] = {};
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    uint32_t b[4];
+                    ldmatrix4(b, tile_addr<kDim>(kt, (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)));
+                    if (!kQRegs) load_q(qf[0], k);
+                    mma16816<T>(sc[0], qf[kQRegs ? k : 0], b[0], b[1]);
+                    mma16816<T>(sc[1], qf[kQRegs ? k : 0], b[2], b[3]);
+                }
+                const bool masked = key0 + kSub > all_see;
+                float top[2] = {m[0], m[1]};
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x = sc[t][i] * s.scale_log2;
+                        if (masked && key0 + t * 8 + (lane % 4) * 2 + (i & 1) >= limit[i / 2]) x = -INFINITY;
+                        sc[t][i] = x;
+                        top[i / 2] = fmaxf(top[i / 2], x);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
+                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
+                }
+                if (__any_sync(0xFFFFFFFFu, top[0] != m[0] || top[1] != m[1])) {
+                    const float f0 = exp2_approx(m[0] - attn_base(top[0])), f1 = exp2_approx(m[1] - attn_base(top[1]));
+                    l[0] *= f0;
+                    l[1] *= f1;
+#pragma unroll
+                    for (int i = 0; i < kDim / 8; ++i) {
+                        o[i][0] *= f0;
+                        o[i][1] *= f0;
+                        o[i][2] *= f1;
+                        o[i][3] *= f1;
+                    }
+                    m[0] = top[0];
+                    m[1] = top[1];
+                }
+                const float b0 = attn_base(m[0]), b1 = attn_base(m[1]);
+                uint32_t p[4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float x0 = exp2_approx(sc[t][0] - b0), x1 = exp2_approx(sc[t][1] - b0);
+                    const float x2 = exp2_approx(sc[t][2] - b1), x3 = exp2_approx(sc[t][3] - b1);
+                    l[0] += x0 + x1;
+                    l[1] += x2 + x3;
+                    p[2 * t] = pack16<T>(x0, x1);
+                    p[2 * t + 1] = pack16<T>(x2, x3);
+                }
+#pragma unroll
+                for (int d = 0; d < kDim / 16; ++d) {
+                    uint32_t b[4];
+                    ldmatrix4_trans(b, tile_addr<kDim>(vt, (lane & 7) + (((lane >> 3) & 1) << 3), d * 2 + (lane >> 4)));
+                    mma16816<T>(o[2 * d], p, b[0], b[1]);
+                    mma16816<T>(o[2 * d + 1], p, b[2], b[3]);
+                }
+            }
+            __syncwarp();  // all lanes have read this stage before it is refilled
+            stage = stage + 1 == C::kStages ? 0 : stage + 1;
+        }
+        cp_async_wait<0>();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+        }
+
+        // Join the four warps in shared memory, over the ring.
+        constexpr int kPitch = kDim + 4;
+        float *ow = reinterpret_cast<float *>(smem);  // [kWarps][kRows][kPitch]
+        float *mw = ow + kWarps * kRows * kPitch;      // [kWarps][kRows], then the sums
+        static_assert((kWarps * kRows * (kPitch + 2)) * 4 <= C::kRingBytes, "the join fits the ring");
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i) {
+            float *at = ow + (warp * kRows + lane / 4) * kPitch + i * 8 + (lane % 4) * 2;
+            at[0] = o[i][0];
+            at[1] = o[i][1];
+            at[8 * kPitch] = o[i][2];
+            at[8 * kPitch + 1] = o[i][3];
+        }
+        if (lane % 4 == 0) {
+            mw[warp * kRows + lane / 4] = m[0];
+            mw[warp * kRows + lane / 4 + 8] = m[1];
+            mw[(kWarps + warp) * kRows + lane / 4] = l[0];
+            mw[(kWarps + warp) * kRows + lane / 4 + 8] = l[1];
+        }
+        __syncthreads();
+        const bool whole = first == 0 && last == units;
+        float *part = attn_slot(s, cta, first == 0 ? 1 : 0);
+        for (int i = threadIdx.x; i < kRows * (kDim / 4); i += kThreads) {
+            const int r = i / (kDim / 4), c = (i % (kDim / 4)) * 4;
+            if (c >= dim) continue;
+            float mm = -INFINITY, ll = 0.0f, acc[4] = {};
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mw[w * kRows + r]);
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = exp2_approx(mw[w * kRows + r] - attn_base(mm));
+                ll += f * mw[(kWarps + w) * kRows + r];
+                const float4 x = *reinterpret_cast<const float4 *>(ow + (w * kRows + r) * kPitch + c);
+                acc[0] += f * x.x;
+                acc[1] += f * x.y;
+                acc[2] += f * x.z;
+                acc[3] += f * x.w;
+            }
+            if (whole) {
+                int token, head;
+                if (attn_row(s, q.q0, q.n, cur.head, cur.row_tile, r, &token, &head)) {
+                    const float inv = attn_inverse(ll);
+                    uint2 y = make_uint2(pack16<T>(acc[0] * inv, acc[1] * inv), pack16<T>(acc[2] * inv, acc[3] * inv));
+                    *reinterpret_cast<uint2 *>((T *)a.out + token * a.out_token_stride + head * a.out_head_stride + c) = y;
+                }
+            } else {
+                // 8-byte stores: the slots are only known to begin on 8 bytes
+                *reinterpret_cast<float2 *>(part + r * dim + c) = make_float2(acc[0], acc[1]);
+                *reinterpret_cast<float2 *>(part + r * dim + c + 2) = make_float2(acc[2], acc[3]);
+                if (c == 0) {
+                    part[kRows * dim + r] = mm;
+                    part[kRows * dim + kRows + r] = ll;
+                }
+            }
+        }
+        if (!whole && first == 0 && threadIdx.x == 0) {
+            AttnJoin j = {};
+            j.pieces = (int32_t)(attn_owner(cur, cur.at + units - 1) - cta + 1);
+            j.seq = cur.seq;
+            j.head = cur.head;
+            j.row_tile = cur.row_tile;
+            j.q0 = q.q0;
+            j.q_len = q.n;
+            attn_joins(s, ctas)[cta] = j;
+        }
+        cur.at += last - first;
+        cur.left -= last - first;
+        if (cur.left <= 0) break;
+        attn_next(s, cur, q);
+        __syncthreads();  // the join's reads are done before the ring is filled again
+    }
+}
+
+// Joins the row tiles that several CTAs shared: block (c, y) takes rows y, y + gridDim.y, ... of
+// the tile that CTA c began. The pieces are added in the order of their keys.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads)
+attn_join_kernel(const __grid_constant__ AttnArgs s, int ctas) {
+    grid_dependency_wait();
+    allow_dependents_launch();
+    const ks_attention_args_t &a = s.a;
+    const int c = blockIdx.x, dim = (int)a.head_dim;
+    const AttnJoin j = attn_joins(s, ctas)[c];
+    if (j.pieces <= 0) return;
+    const int quads = dim / 4, per = kJoinThreads / quads;  // rows a block handles at once
+    const int col = (threadIdx.x % quads) * 4, sub = threadIdx.x / quads;
+    if (sub >= per) return;
+    for (int r = blockIdx.y * per + sub; r < s.rows; r += gridDim.y * per) {
+        int token, head;
+        if (!attn_row(s, j.q0, j.q_len, j.head, j.row_tile, r, &token, &head)) continue;
+        float mm = -INFINITY, ll = 0.0f, acc[4] = {};
+        for (int i = 0; i < j.pieces; ++i) {
+            const float *part = attn_slot(s, c + i, i == 0 ? 1 : 0);
+            const float pm = part[s.rows * dim + r], pl = part[s.rows * dim + s.rows + r];
+            const float2 x = *reinterpret_cast<const float2 *>(part + r * dim + col);
+            const float2 y = *reinterpret_cast<const float2 *>(part + r * dim + col + 2);
+            const float top = fmaxf(mm, pm), base = attn_base(top);
+            const float f = exp2_approx(mm - base), g = exp2_approx(pm - base);
+            mm = top;
+            ll = ll * f + pl * g;
+            acc[0] = acc[0] * f + x.x * g;
+            acc[1] = acc[1] * f + x.y * g;
+            acc[2] = acc[2] * f + y.x * g;
+            acc[3] = acc[3] * f + y.y * g;
+        }
+        const float inv = attn_inverse(ll);
+        const uint2 y = make_uint2(pack16<T>(acc[0] * inv, acc[1] * inv), pack16<T>(acc[2] * inv, acc[3] * inv));
+        *reinterpret_cast<uint2 *>((T *)a.out + token * a.out_token_stride + head * a.out_head_stride + col) = y;
+    }
+}
+
+// ------------------------------------------------------------------------------- host side
+
+// How a call is launched: the row-tile height, the keys of a unit and the CTAs. Depends on
+// host-known sizes only.
+struct AttnPlan {
+    AttnArgs s;
+    int ctas;
+    const void *kernel;
+    int threads, smem;
+};
+
+template <typename T>
+const void *rows16_kernel(int dim, int *smem, int *per_sm) {
+    if (dim <= 64) {
+        *smem = Rows16<64>::kSmem;
+        *per_sm = Rows16<64>::kCtasPerSm;
+        return (const void *)attn_rows16_kernel<T, 64>;
+    }
+    if (dim <= 128) {
+        *smem = Rows16<128>::kSmem;
+        *per_sm = Rows16<128>::kCtasPerSm;
+        return (const void *)attn_rows16_kernel<T, 128>;
+    }
+    *smem = Rows16<256>::kSmem;
+    *per_sm = Rows16<256>::kCtasPerSm;
+    return (const void *)attn_rows16_kernel<T, 256>;
+}
+
+int64_t ceil_to(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+void attn_plan(const ks_attention_args_t &a, int sms, AttnPlan *p) {
+    p->s.a = a;
+    p->s.group = (int32_t)(a.q_heads / a.kv_heads);
+    p->s.scale_log2 = a.scale * 1.4426950408889634f;
+    p->s.rows = kRows;
+    p->s.unit = kUnit;
+    int per_sm = 1;
+    p->kernel = a.dtype == KS_DTYPE_BF16 ? rows16_kernel<__nv_bfloat16>((int)a.head_dim, &p->smem, &per_sm)
+                                         : rows16_kernel<__half>((int)a.head_dim, &p->smem, &per_sm);
+    p->threads = kThreads;
+    p->s.head_splits = (int32_t)ceil_to(p->s.group, p->s.rows);
+    p->s.tile_heads = (int32_t)ceil_to(p->s.group, p->s.head_splits);
+    p->s.tile_tokens = p->s.head_splits > 1 ? 1 : p->s.rows / p->s.tile_heads;
+    // No more CTAs than the call can have units.
+    const int64_t tiles = ceil_to(a.tokens, p->s.tile_tokens) + a.seqs;
+    const int64_t tile_units = ceil_to(a.table_pages * a.page_size, p->s.unit) + 1;
+    const int64_t heads = a.kv_heads * p->s.head_splits;
+    int64_t ctas = (int64_t)sms * per_sm;
+    if (tile_units < ctas && tiles < ctas && heads < ctas && tile_units * tiles * heads < ctas)
+        ctas = tile_units * tiles * heads;
+    p->ctas = (int)ctas;
+}
+
+int64_t attn_workspace_bytes(const AttnPlan &p) {
+    return p.ctas * (2 * attn_slot_floats(p.s.rows, p.s.a.head_dim) * (int64_t)sizeof(float) + (int64_t)sizeof(AttnJoin));
+}
+
+// The checks of the sizes, and those of the tensors; neither needs a device.
+ks_status_t attn_check_sizes(const ks_attention_args_t &a) {
+    if (a.dtype == KS_DTYPE_F32)
+        return fail(KS_ERR_UNSUPPORTED_DTYPE, "paged attention takes float16 and bfloat16 (its products run on the tensor cores)");
+    const int e = elem_bytes((ks_dtype_t)a.dtype);
+    if (e == 0) return fail(KS_ERR_UNSUPPORTED_DTYPE, "dtype code %d is not a ks_dtype_t", (int)a.dtype);
+    if (a.tokens < 0 || a.tokens > 0x7fffffff || a.seqs < 0 || a.seqs > 0x7ffffffe)
+        return fail(KS_ERR_INVALID_ARGUMENT, "tokens and seqs must be in 0 .. 2^31-1");
+    if (a.head_dim < 8 || a.head_dim > 256 || a.head_dim % 8)
+        return fail(KS_ERR_INVALID_ARGUMENT, "head_dim must be a multiple of 8 in 8 .. 256 (got %lld)", (long long)a.head_dim);
+    if (a.kv_heads < 1 || a.q_heads < 1 || a.q_heads > 65536 || a.q_heads % a.kv_heads)
+        return fail(KS_ERR_INVALID_ARGUMENT, "q_heads must be a multiple of kv_heads, both in 1 .. 65536");
+    if (a.page_size < 1 || a.page_size > (1 << 20) || a.pages < 0 || a.pages > 0x7fffffff)
+        return fail(KS_ERR_INVALID_ARGUMENT, "page_size must be in 1 .. 2^20 and pages in 0 .. 2^31-1");
+    if (a.table_pages < 0 || a.table_pages > 0x7fffffff || a.table_stride < 0)
+        return fail(KS_ERR_INVALID_ARGUMENT, "the page table's sizes are out of range");
+    if (a.max_q_len < 0) return fail(KS_ERR_INVALID_ARGUMENT, "max_q_len must be >= 0");
+    if (a.flags & ~KS_ATTENTION_CAUSAL) return fail(KS_ERR_INVALID_ARGUMENT, "unknown attention flags 0x%x", (unsigned)a.flags);
+    return KS_SUCCESS;
+}
+
+ks_status_t attn_check_tensors(const ks_attention_args_t &a) {
+    const int e = 2;
+    if (!std::isfinite(a.scale)) return fail(KS_ERR_INVALID_ARGUMENT, "scale must be finite");
+    if (a.tokens == 0 || a.seqs == 0) return KS_SUCCESS;
+    if (!a.out || !a.q || !a.kv_lens || !a.q_starts || (a.table_pages > 0 && !a.page_table) ||
+        (a.pages > 0 && (!a.k_pages || !a.v_pages)))
+        return fail(KS_ERR_INVALID_ARGUMENT, "NULL pointer with tokens > 0");
+    if (misaligned(4, a.kv_lens, a.q_starts, a.page_table))
+        return fail(KS_ERR_INVALID_ARGUMENT, "kv_lens, q_starts and page_table must be aligned to 4 bytes");
+    const int64_t strides[] = {a.q_token_stride, a.q_head_stride, a.out_token_stride, a.out_head_stride,
+                               a.k_page_stride, a.k_slot_stride, a.k_head_stride,
+                               a.v_page_stride, a.v_slot_stride, a.v_head_stride};
+    const int64_t counts[] = {a.tokens, a.q_heads, a.tokens, a.q_heads, a.pages, a.page_size, a.kv_heads,
+                              a.pages, a.page_size, a.kv_heads};
+    for (int i = 0; i < 10; ++i) {
+        if (strides[i] < 0 || (__int128)strides[i] * counts[i] > ((__int128)1 << 60))
+            return fail(KS_ERR_INVALID_ARGUMENT, "a stride is negative or a tensor too large");
+        if (counts[i] > 1 && strides[i] % 8)
+            return fail(KS_ERR_INVALID_ARGUMENT, "strides must be multiples of 8 elements (16 bytes)");
+    }
+    if (((uintptr_t)a.q | (uintptr_t)a.out | (uintptr_t)a.k_pages | (uintptr_t)a.v_pages) & 15u)
+        return fail(KS_ERR_INVALID_ARGUMENT, "q, out and the cache must be aligned to 16 bytes");
+    const int64_t D = a.head_dim, T = a.tokens;
+    const bool heads_inner = (a.q_heads == 1 || a.out_head_stride >= D) &&
+                             (T == 1 || a.out_token_stride >= (a.q_heads - 1) * a.out_head_stride + D);
+    const bool tokens_inner = (T == 1 || a.out_token_stride >= D) &&
+                              (a.q_heads == 1 || a.out_head_stride >= (T - 1) * a.out_token_stride + D);
+    if (!heads_inner && !tokens_inner) return fail(KS_ERR_OVERLAP, "rows of out share storage");
+    const int64_t out_n = ((T - 1) * a.out_token_stride + (a.q_heads - 1) * a.out_head_stride + D) * e;
+    const int64_t q_n = ((T - 1) * a.q_token_stride + (a.q_heads - 1) * a.q_head_stride + D) * e;
+    if (overlaps(a.out, out_n, a.q, q_n)) return fail(KS_ERR_OVERLAP, "out and q storage overlap");
+    if (a.pages > 0) {
+        const int64_t k_n = ((a.pages - 1) * a.k_page_stride + (a.page_size - 1) * a.k_slot_stride + (a.kv_heads - 1) * a.k_head_stride + D) * e;
+        const int64_t v_n = ((a.pages - 1) * a.v_page_stride + (a.page_size - 1) * a.v_slot_stride + (a.kv_heads - 1) * a.v_head_stride + D) * e;
+        if (overlaps(a.out, out_n, a.k_pages, k_n) || overlaps(a.out, out_n, a.v_pages, v_n))
+            return fail(KS_ERR_OVERLAP, "out and the cache overlap");
+    }
+    return KS_SUCCESS;
+}
+
+}  // namespace
+
+int fault_flags_attention(bool clear) { return fault_flags_t(clear); }
+
+}  // namespace ks
+
+using namespace ks;
+
+extern "C" {
+
+ks_status_t ks_paged_attention_workspace(const ks_attention_args_t *args, int64_t *bytes) {
+    if (!args || !bytes) return fail(KS_ERR_INVALID_ARGUMENT, "args or bytes is NULL");
+    *bytes = 0;
+    ks_status_t st = attn_check_sizes(*args);
+    if (st != KS_SUCCESS || args->tokens == 0 || args->seqs == 0) return st;
+    int sms = 0;
+    if ((st = device_sms(&sms)) != KS_SUCCESS) return st;
+    AttnPlan p;
+    attn_plan(*args, sms, &p);
+    *bytes = attn_workspace_bytes(p);
+    return KS_SUCCESS;
+}
+
+ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stream) {
+    if (!args) return fail(KS_ERR_INVALID_ARGUMENT, "args is NULL");
+    ks_status_t st = attn_check_sizes(*args);
+    if (st == KS_SUCCESS) st = attn_check_tensors(*args);
+    if (st != KS_SUCCESS || args->tokens == 0 || args->seqs == 0) return st;
+    if (!args->workspace || ((uintptr_t)args->workspace & 15u))
+        return fail(KS_ERR_INVALID_ARGUMENT, "the workspace must be device memory aligned to 16 bytes");
+    int sms = 0;
+    if ((st = device_sms(&sms)) != KS_SUCCESS) return st;
+    AttnPlan p;
+    attn_plan(*args, sms, &p);
+    const int64_t need = attn_workspace_bytes(p);
+    if (args->workspace_bytes < need)
+        return fail(KS_ERR_INVALID_ARGUMENT, "the workspace has %lld bytes, %lld are needed",
+                    (long long)args->workspace_bytes, (long long)need);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!allow_smem(p.kernel, (size_t)p.smem)) return fail(KS_ERR_CUDA, "shared memory of %d bytes refused", p.smem);
+    void *kp[] = {&p.s};
+    cudaError_t ce = launch_kernel(p.kernel, dim3((unsigned)p.ctas), dim3((unsigned)p.threads), (size_t)p.smem, kp, s,
+                                   launch_pdl_enabled());
+    if (ce == cudaSuccess && p.ctas > 1) {
+        // The join is scheduled while the last CTAs finish and waits for them on the device.
+        const int per = kJoinThreads / (int)(args->head_dim / 4);
+        void *jp[] = {&p.s, &p.ctas};
+        const void *f = args->dtype == KS_DTYPE_BF16 ? (const void *)attn_join_kernel<__nv_bfloat16>
+                                                     : (const void *)attn_join_kernel<__half>;
+        ce = launch_kernel(f, dim3((unsigned)p.ctas, (unsigned)((p.s.rows + per - 1) / per)), dim3(kJoinThreads), 0, jp,
+                           s, true);
+    }
+    if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));
+    return KS_SUCCESS;
+}
+
+}  // extern "C"

@@ -1,0 +1,252 @@
+// What the paged-attention kernels share: the call's shape, the division of its work over CTAs,
+// which query row a tile's row is, and the join of split rows.
+//
+// Division of the work. The queries of one sequence and one key/value head (all heads of its
+// group, token after token) are cut into row tiles of at most M rows, and the keys a row tile sees
+// into units of TN keys. All units of a call, in the order sequence, head, row tile, unit, are
+// shared out evenly: CTA c of G takes units [U c / G, U (c + 1) / G)
+// (G no more than U). A row tile whose units fall
+// to several CTAs is split over its long axis; each of them leaves its running maximum, sum and
+// unnormalised output in the workspace and a second kernel joins them in a fixed order, so results
+// do not depend on timing. The lengths are read on the device: the launch depends on host-known
+// sizes only, and a captured graph may be replayed with other lengths.
+#pragma once
+
+#include "ks_kernels.cuh"
+
+namespace ks {
+
+struct AttnArgs {
+    ks_attention_args_t a;
+    int32_t group;       // query heads per key/value head
+    int32_t tile_heads;  // heads of a group in a row tile
+    int32_t head_splits; // row tiles a token's group is cut into (1 unless group > M)
+    int32_t tile_tokens; // tokens in a row tile
+    int32_t unit;        // keys per unit (TN)
+    int32_t rows;        // rows of a tile (M)
+    float scale_log2;    // scale * log2(e)
+};
+
+// What a CTA left in its second partial slot: the beginning of a row tile that later CTAs finish.
+struct AttnJoin {
+    int32_t pieces;      // 0: nothing to join
+    int32_t seq, head, row_tile;
+    int32_t q0, q_len;
+    int32_t pad[2];
+};
+
+constexpr int kJoinThreads = 128;
+
+// A sequence's new tokens [q0, q0 + n) and key count, brought into range (and reported) where the
+// given indices are not: nothing outside the tensors is ever addressed.
+struct AttnSeq {
+    int32_t q0, n, keys;
+};
+
+__device__ __forceinline__ AttnSeq attn_seq(const ks_attention_args_t &a, int b) {
+    const int64_t tokens = a.tokens, room = min(a.table_pages * a.page_size, (int64_t)0x7fffffff);
+    const int32_t q0 = a.q_starts[b], q1 = a.q_starts[b + 1], keys = a.kv_lens[b];
+    AttnSeq s;
+    s.q0 = (int32_t)min(max((int64_t)q0, (int64_t)0), tokens);
+    const int32_t end = (int32_t)min(max((int64_t)q1, (int64_t)s.q0), tokens);
+    s.n = end - s.q0;
+    s.keys = (int32_t)min(max((int64_t)keys, (int64_t)0), room);
+    if (s.q0 != q0 || end != q1 || s.keys != keys) atomicOr(&g_fault_flags, kFaultBadIndex);
+    return s;
+}
+
+// sum over i in [0, n) of floor((a i + b) / m), for n, a, b >= 0 and m > 0: the whole multiples of
+// m in a and b sum in closed form; for what is left (a, b < m), the points under the line are
+// counted along the other axis, which is the same sum with a and m changed over.
+__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t total = 0;
+    while (n > 0) {
+        total += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+        a %= m;
+        b %= m;
+        const int64_t top = a * n + b;  // m times the line's height at n
+        if (top < m) break;
+        n = top / m;
+        b = top % m;
+        const int64_t t = a;
+        a = m;
+        m = t;
+    }
+    return total;
+}
+
+// Row tiles of a sequence for one head (head splits aside).
+__device__ __forceinline__ int attn_row_tiles(const AttnArgs &s, const AttnSeq &q) {
+    return (q.n + s.tile_tokens - 1) / s.tile_tokens;
+}
+
+// Keys that the last token of row tile `rt` sees (the most any row of it sees), 0 if none.
+__device__ __forceinline__ int attn_tile_keys(const AttnArgs &s, const AttnSeq &q, int rt) {
+    if (!(s.a.flags & KS_ATTENTION_CAUSAL)) return q.keys;
+    const int64_t last = min((int64_t)(rt + 1) * s.tile_tokens, (int64_t)q.n);
+    return (int)max((int64_t)0, min((int64_t)q.keys, (int64_t)q.keys - q.n + last));
+}
+
+// Units of row tile `rt`: at least one, so that a tile that sees nothing still writes its zeros.
+__device__ __forceinline__ int attn_tile_units(const AttnArgs &s, const AttnSeq &q, int rt) {
+    return max(1, (attn_tile_keys(s, q, rt) + s.unit - 1) / s.unit);
+}
+
+// Units of the row tiles [0, k) of one head.
+__device__ inline int64_t attn_units_before(const AttnArgs &s, const AttnSeq &q, int k) {
+    const int tiles = attn_row_tiles(s, q);
+    if (k <= 0) return 0;
+    if (!(s.a.flags & KS_ATTENTION_CAUSAL)) return (int64_t)k * attn_tile_units(s, q, 0);
+    int64_t total = 0;
+    if (k == tiles) {  // the last tile is cut off at the last token: by itself
+        total = attn_tile_units(s, q, tiles - 1);
+        --k;
+    }
+    // tile i < tiles - 1 sees past + (i + 1) tile_tokens keys; up to one unit of them counts as one
+    const int64_t past = (int64_t)q.keys - q.n, tt = s.tile_tokens, un = s.unit;
+    int64_t one = past >= un ? 0 : (un - past) / tt;  // tiles i with past + (i + 1) tt <= un
+    one = min(one, (int64_t)k);
+    return total + one + floor_sum(k - one, un, tt, past + (one + 1) * tt + un - 1);
+}
+
+// A CTA's place in the call's units.
+struct AttnCursor {
+    int32_t seq, head, row_tile, unit;  // head: key/value head * head_splits + split
+    int64_t left;                       // units this CTA still has to do
+    int64_t at;                         // index of the current unit among all
+    int64_t units;                      // all units of the call
+    int32_t ctas;                       // CTAs that have units
+};
+
+// The CTA that has unit u: the last c with U c / G < u + 1.
+__device__ __forceinline__ int64_t attn_owner(const AttnCursor &c, int64_t u) {
+    return ((u + 1) * c.ctas - 1) / c.units;
+}
+
+// Finds the CTA's first unit: the sequences' units are summed by the block (a contiguous run of
+// sequences per thread, a scan over the threads), then the thread whose run holds the CTA's first
+// unit walks it. All threads of the block call it; kThreads a multiple of 32, at most 1024.
+template <int kThreads>
+__device__ inline AttnCursor attn_begin(const AttnArgs &s, int cta, int ctas) {
+    __shared__ int64_t warp_units[kThreads / 32];
+    __shared__ int32_t found_seq;
+    __shared__ int64_t found_before;
+    const int t = threadIdx.x, seqs = (int)s.a.seqs;
+    const int per = (seqs + kThreads - 1) / kThreads;
+    const int64_t heads = s.a.kv_heads * s.head_splits;
+    const int lo = min(seqs, t * per), hi = min(seqs, lo + per);
+    int64_t mine = 0;
+    for (int b = lo; b < hi; ++b) {
+        const AttnSeq q = attn_seq(s.a, b);
+        mine += heads * attn_units_before(s, q, attn_row_tiles(s, q));
+    }
+    int64_t upto = mine;
+    const int lane = t & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) warp_units[t / 32] = upto;
+    if (t == 0) found_seq = -1;
+    __syncthreads();
+    int64_t units = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == t / 32) upto += units;
+        units += warp_units[w];
+    }
+    AttnCursor c = {};
+    c.units = units;
+    // with fewer units than CTAs, the first CTAs take one each: a row tile's pieces are then always
+    // those of consecutive CTAs
+    c.ctas = (int32_t)min((int64_t)ctas, units);
+    if (cta >= c.ctas) return c;
+    c.at = units * cta / c.ctas;
+    c.left = units * (cta + 1) / c.ctas - c.at;
+    int64_t before = upto - mine;
+    if (c.left > 0 && before <= c.at && c.at < upto) {
+        for (int b = lo; b < hi; ++b) {
+            const AttnSeq q = attn_seq(s.a, b);
+            const int64_t n = heads * attn_units_before(s, q, attn_row_tiles(s, q));
+            if (c.at < before + n) {
+                found_seq = b;
+                found_before = before;
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    if (c.left <= 0 || found_seq < 0) {
+        c.left = 0;
+        return c;
+    }
+    c.seq = found_seq;
+    const AttnSeq q = attn_seq(s.a, c.seq);
+    const int tiles = attn_row_tiles(s, q);
+    const int64_t per_head = attn_units_before(s, q, tiles);
+    int64_t u = c.at - found_before;
+    c.head = (int32_t)(u / per_head);
+    u %= per_head;
+    int low = 0, high = tiles - 1;  // the last row tile that begins at or before u
+    while (low < high) {
+        const int mid = (low + high + 1) / 2;
+        if (attn_units_before(s, q, mid) <= u) low = mid;
+        else high = mid - 1;
+    }
+    c.row_tile = low;
+    c.unit = (int32_t)(u - attn_units_before(s, q, low));
+    return c;
+}
+
+// Moves to the next row tile with units (called only while units are left).
+__device__ __forceinline__ void attn_next(const AttnArgs &s, AttnCursor &c, AttnSeq &q) {
+    c.unit = 0;
+    if (++c.row_tile < attn_row_tiles(s, q)) return;
+    c.row_tile = 0;
+    if (++c.head < s.a.kv_heads * s.head_splits) return;
+    c.head = 0;
+    do {
+        ++c.seq;
+        if (c.seq >= s.a.seqs) return;  // not reached while units are left
+        q = attn_seq(s.a, c.seq);
+    } while (q.n == 0);
+}
+
+// Row r of a row tile: its token among all and its query head; false if the tile has no such row.
+__device__ __forceinline__ bool attn_row(const AttnArgs &s, int q0, int n, int head, int row_tile,
+                                         int r, int *token, int *q_head) {
+    const int i = r / s.tile_heads, g = (head % s.head_splits) * s.tile_heads + r % s.tile_heads;
+    const int in_seq = row_tile * s.tile_tokens + i;
+    *token = q0 + in_seq;
+    *q_head = (head / s.head_splits) * s.group + g;
+    return i < s.tile_tokens && in_seq < n && g < s.group;
+}
+
+// Workspace: per CTA two slots of rows * (dim + 2) floats (outputs, maxima, sums), then an
+// AttnJoin per CTA.
+__host__ __device__ inline int64_t attn_slot_floats(int64_t rows, int64_t dim) {
+    return rows * (dim + 2);
+}
+
+__device__ __forceinline__ float *attn_slot(const AttnArgs &s, int64_t cta, int slot) {
+    return (float *)s.a.workspace + (cta * 2 + slot) * attn_slot_floats(s.rows, s.a.head_dim);
+}
+
+__device__ __forceinline__ AttnJoin *attn_joins(const AttnArgs &s, int64_t ctas) {
+    return (AttnJoin *)((float *)s.a.workspace + ctas * 2 * attn_slot_floats(s.rows, s.a.head_dim));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / l, and 0 for a row that saw no key.
+__device__ __forceinline__ float attn_inverse(float l) { return l == 0.0f ? 0.0f : __frcp_rn(l); }
+
+// A maximum that can be subtracted: of a row that saw nothing yet, 0.
+__device__ __forceinline__ float attn_base(float m) { return m == -INFINITY ? 0.0f : m; }
+
+}  // namespace ks

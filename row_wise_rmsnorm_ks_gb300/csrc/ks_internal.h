@@ -72,6 +72,15 @@ int fault_flags_bf16(bool clear);
 int fault_flags_f16(bool clear);
 int fault_flags_f32(bool clear);
 int fault_flags_ops(bool clear);
+int fault_flags_rotary(bool clear);
+int fault_flags_attention(bool clear);
+// Launch helpers shared by the operators' translation units: the current device's SM count, the
+// launch itself (pdl: with programmatic stream serialization), and leave for `smem` bytes of
+// dynamic shared memory (once per device and kernel; false if they do not fit).
+ks_status_t device_sms(int *out);
+cudaError_t launch_kernel(const void *f, dim3 grid, dim3 block, size_t smem, void **args,
+                          cudaStream_t s, bool pdl);
+bool allow_smem(const void *f, size_t smem);
 cudaError_t launch_bf16(const ks_plan_t &p, bool fused, const RowArgs &a, cudaStream_t s);
 cudaError_t launch_f16(const ks_plan_t &p, bool fused, const RowArgs &a, cudaStream_t s);
 cudaError_t launch_f32(const ks_plan_t &p, bool fused, const RowArgs &a, cudaStream_t s);

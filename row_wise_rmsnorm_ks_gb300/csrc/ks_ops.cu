@@ -1622,6 +1622,15 @@ ks_status_t op_plan(int op, int64_t rows, int64_t hidden, ks_dtype_t dtype, bool
 
 int fault_flags_ops(bool clear) { return fault_flags_t(clear); }
 
+ks_status_t device_sms(int *out) { return sm_count(out); }
+
+cudaError_t launch_kernel(const void *f, dim3 grid, dim3 block, size_t smem, void **args,
+                          cudaStream_t s, bool pdl) {
+    return launch_ex(f, grid, block, smem, args, s, pdl);
+}
+
+bool allow_smem(const void *f, size_t smem) { return allow_dynamic_smem(f, smem); }
+
 }  // namespace ks
 
 using namespace ks;
