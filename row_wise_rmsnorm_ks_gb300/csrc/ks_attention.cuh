@@ -12,7 +12,7 @@
 // sizes only, and a captured graph may be replayed with other lengths.
 #pragma once
 
-#include "ks_kernels.cuh"
+#include "ks_decode.cuh"
 
 namespace ks {
 

@@ -1620,7 +1620,17 @@ ks_status_t op_plan(int op, int64_t rows, int64_t hidden, ks_dtype_t dtype, bool
     return KS_SUCCESS;
 }
 
-int fault_flags_ops(bool clear) { return fault_flags_t(clear); }
+// All operators besides the norms answer together: this unit's word and those of the rotary and
+// attention units.
+int fault_flags_ops(bool clear) {
+    const int parts[3] = {fault_flags_t(clear), fault_flags_rotary(clear), fault_flags_attention(clear)};
+    int all = 0;
+    for (int v : parts) {
+        if (v < 0) return -1;
+        all |= v;
+    }
+    return all;
+}
 
 ks_status_t device_sms(int *out) { return sm_count(out); }
 

@@ -6,14 +6,12 @@
 
 namespace ks {
 
-// Device-side fault word: bit 0 is set by a wait that gave up, bit 1 by an index out of range. Each translation unit that
+// Device-side fault word: bit 0 is set by a wait that gave up. Each translation unit that
 // includes this header has its own copy (no relocatable device code); the host reads and clears
 // all of them through ks_device_faults().
 static __device__ unsigned int g_fault_flags = 0;
 
 constexpr unsigned int kFaultWaitTimeout = 1u;
-// A slot, page or length read on the device was out of range; the access was left out.
-constexpr unsigned int kFaultBadIndex = 2u;
 // A wait gives up after this long (nanoseconds of %globaltimer); a healthy wait lasts about a
 // microsecond.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;

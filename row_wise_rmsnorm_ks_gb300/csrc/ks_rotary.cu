@@ -18,7 +18,7 @@
 
 #include <cmath>
 
-#include "ks_kernels.cuh"
+#include "ks_decode.cuh"
 
 namespace ks {
 namespace {
