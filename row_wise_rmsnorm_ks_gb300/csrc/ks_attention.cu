@@ -402,8 +402,8 @@ attn_join_kernel(const __grid_constant__ AttnArgs s, int ctas) {
 struct AttnPlan {
     AttnArgs s;
     int ctas;
-    const void *kernel;
-    int threads, smem;
+    const void *kernel;  // the 16-row kernel, NULL for the tensor-core one
+    int smem;
 };
 
 template <typename T>
@@ -425,16 +425,24 @@ const void *rows16_kernel(int dim, int *smem, int *per_sm) {
 
 int64_t ceil_to(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-void attn_plan(const ks_attention_args_t &a, int sms, AttnPlan *p) {
+// Up to 16 rows per key/value head fill one tile of the 16-row kernel; more go to the tensor-core
+// kernel where it takes the call's pages.
+bool attn_many_rows(const ks_attention_args_t &a) {
+    const int64_t q_len = a.max_q_len > 0 && a.max_q_len < a.tokens ? a.max_q_len : a.tokens;
+    return q_len * (a.q_heads / a.kv_heads) > kRows;
+}
+
+void attn_plan(const ks_attention_args_t &a, bool tc, int sms, AttnPlan *p) {
     p->s.a = a;
     p->s.group = (int32_t)(a.q_heads / a.kv_heads);
     p->s.scale_log2 = a.scale * 1.4426950408889634f;
-    p->s.rows = kRows;
-    p->s.unit = kUnit;
+    p->s.rows = tc ? attn_tc_rows() : kRows;
+    p->s.unit = tc ? attn_tc_unit() : kUnit;
     int per_sm = 1;
-    p->kernel = a.dtype == KS_DTYPE_BF16 ? rows16_kernel<__nv_bfloat16>((int)a.head_dim, &p->smem, &per_sm)
+    p->smem = 0;
+    p->kernel = nullptr;
+    if (!tc) p->kernel = a.dtype == KS_DTYPE_BF16 ? rows16_kernel<__nv_bfloat16>((int)a.head_dim, &p->smem, &per_sm)
                                          : rows16_kernel<__half>((int)a.head_dim, &p->smem, &per_sm);
-    p->threads = kThreads;
     p->s.head_splits = (int32_t)ceil_to(p->s.group, p->s.rows);
     p->s.tile_heads = (int32_t)ceil_to(p->s.group, p->s.head_splits);
     p->s.tile_tokens = p->s.head_splits > 1 ? 1 : p->s.rows / p->s.tile_heads;
@@ -531,8 +539,13 @@ ks_status_t ks_paged_attention_workspace(const ks_attention_args_t *args, int64_
     int sms = 0;
     if ((st = device_sms(&sms)) != KS_SUCCESS) return st;
     AttnPlan p;
-    attn_plan(*args, sms, &p);
+    attn_plan(*args, false, sms, &p);
     *bytes = attn_workspace_bytes(p);
+    if (attn_many_rows(*args) && attn_tc_sizes(*args)) {
+        attn_plan(*args, true, sms, &p);
+        const int64_t more = attn_workspace_bytes(p);
+        *bytes = *bytes > more ? *bytes : more;
+    }
     return KS_SUCCESS;
 }
 
@@ -546,24 +559,29 @@ ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stre
     int sms = 0;
     if ((st = device_sms(&sms)) != KS_SUCCESS) return st;
     AttnPlan p;
-    attn_plan(*args, sms, &p);
+    attn_plan(*args, attn_many_rows(*args) && attn_tc_fits(*args), sms, &p);
     const int64_t need = attn_workspace_bytes(p);
     if (args->workspace_bytes < need)
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace has %lld bytes, %lld are needed",
                     (long long)args->workspace_bytes, (long long)need);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!allow_smem(p.kernel, (size_t)p.smem)) return fail(KS_ERR_CUDA, "shared memory of %d bytes refused", p.smem);
-    void *kp[] = {&p.s};
-    cudaError_t ce = launch_kernel(p.kernel, dim3((unsigned)p.ctas), dim3((unsigned)p.threads), (size_t)p.smem, kp, s,
-                                   launch_pdl_enabled());
+    cudaError_t ce;
+    if (p.kernel) {
+        if (!allow_smem(p.kernel, (size_t)p.smem)) return fail(KS_ERR_CUDA, "shared memory of %d bytes refused", p.smem);
+        void *kp[] = {&p.s};
+        ce = launch_kernel(p.kernel, dim3((unsigned)p.ctas), dim3(kThreads), (size_t)p.smem, kp, s, launch_pdl_enabled());
+    } else {
+        ce = attn_tc_launch(p.s, p.ctas, s, launch_pdl_enabled());
+    }
     if (ce == cudaSuccess && p.ctas > 1) {
         // The join is scheduled while the last CTAs finish and waits for them on the device.
         const int per = kJoinThreads / (int)(args->head_dim / 4);
         void *jp[] = {&p.s, &p.ctas};
         const void *f = args->dtype == KS_DTYPE_BF16 ? (const void *)attn_join_kernel<__nv_bfloat16>
                                                      : (const void *)attn_join_kernel<__half>;
-        ce = launch_kernel(f, dim3((unsigned)p.ctas, (unsigned)((p.s.rows + per - 1) / per)), dim3(kJoinThreads), 0, jp,
-                           s, true);
+        const int row_blocks = (p.s.rows + per - 1) / per;
+        ce = launch_kernel(f, dim3((unsigned)p.ctas, (unsigned)(row_blocks < 16 ? row_blocks : 16)), dim3(kJoinThreads), 0,
+                           jp, s, true);
     }
     if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));
     return KS_SUCCESS;

@@ -249,4 +249,12 @@ __device__ __forceinline__ float attn_inverse(float l) { return l == 0.0f ? 0.0f
 // A maximum that can be subtracted: of a row that saw nothing yet, 0.
 __device__ __forceinline__ float attn_base(float m) { return m == -INFINITY ? 0.0f : m; }
 
+// The tensor-core kernel (ks_attention_tc.cu): whether it takes a call's sizes, and its strides too,
+// the rows and keys of its tiles, and its launch.
+bool attn_tc_sizes(const ks_attention_args_t &a);
+bool attn_tc_fits(const ks_attention_args_t &a);
+int attn_tc_rows();
+int attn_tc_unit();
+cudaError_t attn_tc_launch(const AttnArgs &s, int ctas, cudaStream_t stream, bool pdl);
+
 }  // namespace ks

@@ -1,0 +1,593 @@
+// Paged attention on the fifth-generation tensor cores, for many query rows per key/value head
+// (chunks of a prompt, batches of chunks and single tokens).
+//
+// A CTA works on a row tile of 256 query rows, two tiles of 128 that share every 128-key step of
+// the cache: S = Q K^T and O += P V are tcgen05.mma with S, P and O in tensor memory, which they
+// fill exactly (two 128-column S, over which P is written, two 128-column O). Twelve warps:
+//   warps 0-3, 4-7  softmax of tile 0 and 1, one row per thread (no shuffles): S to registers,
+//                   running maximum, exponentials, P back to tensor memory; at the end of a row
+//                   tile O to the output or the workspace;
+//   warp 8          issues the matrix instructions;
+//   warp 9          copies pages to shared memory by TMA, one lane per page and 64 columns
+//                   (warps 10 and 11 only complete the third warpgroup, for the register split).
+// While one tile is in its softmax, the matrix instructions of the other run: the order is
+// P0 V, Q0 K(next), P1 V, Q1 K(next). O is rescaled by the softmax warps, and only when a row's
+// maximum has grown by more than 2^8: until then the old maximum stays the row's base, which changes
+// nothing in the quotient and keeps P below 256.
+//
+// Bound by the tensor cores for long chunks (2 * 128 * 128 * 2 * dim operations a step and tile).
+// For few rows of a tile it is a stream of the cache like the 16-row kernel's.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "ks_attention.cuh"
+
+namespace ks {
+namespace {
+
+constexpr int kTile = 128;         // rows of a matrix tile
+constexpr int kRows = 2 * kTile;   // rows of a row tile
+constexpr int kKeys = 128;         // keys of a step
+constexpr int kSoftmaxThreads = 256, kThreads = kSoftmaxThreads + 128;
+// Registers: 384 threads launch with 168 each; the softmax warpgroups take 232 (128 scores a thread and
+// their probabilities), the third keeps 40: 128 * (232 + 232 + 40) = 384 * 168.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kHalfBytes = kKeys * 128;  // 128 rows of 64 values
+constexpr float kGrowth = 8.0f;    // log2 of how far a row's maximum may pass its base
+
+template <int kDim>
+struct Tc {
+    static constexpr int kHalves = kDim / 64;
+    static constexpr int kTileBytes = kHalves * kHalfBytes;  // a tile of Q, K or V
+    static constexpr int kStages = kDim == 128 ? 5 : 10;
+    static constexpr int kBars = 2 * kStages + 9;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kBars * 8 + 16;
+    static constexpr uint32_t kO = 256;  // tensor-memory columns: S0 0, S1 128, then the O tiles
+};
+
+// ---- tensor-core primitives
+
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead) {
+    // 128-byte swizzle; 8-row groups 1024 bytes apart; `lead` between 64-value blocks of a
+    // non-transposed operand
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+
+// FP32 accumulators, both operands of T, M = 128, N = n; bit 16: B's rows are its K dimension.
+template <typename T>
+__host__ __device__ constexpr uint32_t mma_shape(int n, bool b_by_rows) {
+    const uint32_t t = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    return 1u << 4 | t << 7 | t << 10 | (b_by_rows ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 |
+           (uint32_t)(kTile / 16) << 24;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(shape),
+        "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(shape),
+        "r"((uint32_t)add)
+        : "memory");
+}
+// Arrives on `bar` when all matrix instructions this thread issued so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+#define KS_R4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+#define KS_W4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+
+// 32 columns of this warp's 32 lanes, a lane's row in one thread's registers.
+__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : KS_W4(r, 0), KS_W4(r, 4), KS_W4(r, 8), KS_W4(r, 12), KS_W4(r, 16), KS_W4(r, 20), KS_W4(r, 24), KS_W4(r, 28)
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        KS_R4(r, 0), KS_R4(r, 4), KS_R4(r, 8), KS_R4(r, 12), KS_R4(r, 16), KS_R4(r, 20), KS_R4(r, 24), KS_R4(r, 28)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int col, int slot, int head, int page,
+                                         uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst), "l"(map), "r"(col), "r"(slot), "r"(head), "r"(page), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Waits for phase `parity`; false when the wait's limit passed or another role gave up. The role
+// then leaves its loop: everybody meets at the kernel's end, with the fault word set.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*gave_up) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(&g_fault_flags, kFaultWaitTimeout);
+            *gave_up = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack_pair(float x, float y) {
+    uint32_t w;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        memcpy(&w, &h, 4);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        memcpy(&w, &h, 4);
+    }
+    return w;
+}
+
+// The part of a CTA's work that one row tile is: the same for all roles.
+struct Segment {
+    int first, last;   // units (128-key steps)
+    int units;         // of the row tile
+    int rows;          // rows in use
+    bool two;          // the second tile has rows
+};
+
+__device__ __forceinline__ Segment segment(const AttnArgs &s, const AttnCursor &c, const AttnSeq &q) {
+    Segment g;
+    g.units = attn_tile_units(s, q, c.row_tile);
+    g.first = c.unit;
+    g.last = (int)min((int64_t)g.units, g.first + c.left);
+    g.rows = min(s.tile_tokens, q.n - c.row_tile * s.tile_tokens) * s.tile_heads;
+    g.two = g.rows > kTile;
+    return g;
+}
+
+// Goes on to the CTA's next row tile; false when its share is done.
+__device__ __forceinline__ bool next_segment(const AttnArgs &s, AttnCursor &c, AttnSeq &q, const Segment &g) {
+    c.at += g.last - g.first;
+    c.left -= g.last - g.first;
+    if (c.left <= 0) return false;
+    attn_next(s, c, q);
+    return true;
+}
+
+template <typename T, int kDim>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUtensorMap k_map,
+               const __grid_constant__ CUtensorMap v_map) {
+    using C = Tc<kDim>;
+    static_assert(128 * (2 * kSoftmaxRegs + kOtherRegs) <= kThreads * 168, "the split draws on the launch's registers");
+    extern __shared__ uint8_t raw[];
+    const ks_attention_args_t &a = s.a;
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+    uint8_t *smem = raw + (base - smem_addr(raw));
+    const uint32_t q_addr = base, ring = base + 2 * C::kTileBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (2 + C::kStages) * C::kTileBytes);
+    uint64_t *full = bars, *empty = bars + C::kStages;
+    uint64_t *q_full = empty + C::kStages, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 2, *done = o_full + 2;
+    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(bars + C::kBars);
+    volatile uint32_t *gave_up = tmem_at + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int cta = blockIdx.x, ctas = gridDim.x;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(q_full + w, kTile);
+            mbar_init(s_full + w, 1);
+            mbar_init(p_full + w, kTile);
+            mbar_init(o_full + w, 1);
+        }
+        mbar_init(done, 1);
+        *gave_up = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_at))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_at;
+    grid_dependency_wait();
+    allow_dependents_launch();
+    if (threadIdx.x == 0) attn_joins(s, ctas)[cta].pieces = 0;
+    AttnCursor cur = attn_begin<kThreads>(s, cta, ctas);
+    bool more = cur.left > 0;
+    AttnSeq q = {};
+    if (more) q = attn_seq(a, cur.seq);
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 9) {
+        // ---- copies
+        const int page_size = (int)a.page_size, in_tile = min(page_size, kKeys);  // keys of a copy
+        const int part = lane / C::kHalves, half = lane % C::kHalves;
+        uint32_t at = 0;  // tiles copied so far: K and V of each step in turn
+        while (more) {
+            const Segment g = segment(s, cur, q);
+            const int head = cur.head / s.head_splits;
+            const int32_t *table = a.page_table + (int64_t)cur.seq * a.table_stride;
+            bool ok = true;
+            for (int j = g.first; j < g.last && ok; ++j) {
+                const int key = j * kKeys + part * in_tile;
+                const bool wanted = part * in_tile < kKeys && key < q.keys;
+                int page = 0, slot = 0;
+                if (wanted) {
+                    page = __ldg(table + key / page_size);
+                    slot = key % page_size;
+                    if ((uint32_t)page >= (uint64_t)a.pages) {  // past the pool: the copy fills zeros
+                        atomicOr(&g_fault_flags, kFaultBadIndex);
+                        page = (int)a.pages;
+                    }
+                }
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, wanted)) * in_tile * 128;
+                for (int v = 0; v < 2 && ok; ++v, ++at) {
+                    const uint32_t stage = at % C::kStages;
+                    ok = bar_wait(empty + stage, (at / C::kStages & 1) ^ 1, gave_up);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(full + stage, bytes);
+                    __syncwarp();
+                    if (wanted)
+                        tma_load(ring + stage * C::kTileBytes + half * kHalfBytes + part * in_tile * 128,
+                                 v ? &v_map : &k_map, half * 64, slot, head, page, smem_addr(full + stage));
+                }
+            }
+            more = ok && next_segment(s, cur, q, g);
+        }
+        // nothing of this CTA's is in flight when it ends, also after a wait that gave up
+        const uint32_t from = at > (uint32_t)C::kStages ? at - C::kStages : 0;
+        for (uint32_t i = from; i < at; ++i) (void)mbar_wait_bounded(full + i % C::kStages, i / C::kStages & 1);
+    } else if (warp == 8) {
+        // ---- matrix instructions
+        constexpr uint32_t qk = mma_shape<T>(kKeys, false), pv = mma_shape<T>(kDim, true);
+        uint32_t at = 0, q_uses = 0, q_uses1 = 0, p_uses[2] = {0, 0};
+        auto stage_addr = [&](uint32_t i) { return ring + i % C::kStages * C::kTileBytes; };
+        auto wait_tile = [&](uint32_t i) { return bar_wait(full + i % C::kStages, i / C::kStages & 1, gave_up); };
+        auto issue_qk = [&](int w, uint32_t k_tile) {
+#pragma unroll
+            for (int i = 0; i < kDim / 16; ++i) {
+                const uint32_t off = i / 4 * kHalfBytes + i % 4 * 32;
+                mma_ss(tmem + w * 128, tile_desc(q_addr + w * C::kTileBytes + off, 16), tile_desc(k_tile + off, 16), qk,
+                       i > 0);
+            }
+            mma_commit(smem_addr(s_full + w));
+        };
+        while (more) {
+            const Segment g = segment(s, cur, q);
+            const int tiles = g.two ? 2 : 1;
+            bool ok = bar_wait(q_full, q_uses++ & 1, gave_up);
+            if (g.two) ok = ok && bar_wait(q_full + 1, q_uses1++ & 1, gave_up);
+            ok = ok && wait_tile(at);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            fence_after();
+            if (lane == 0) {
+                for (int w = 0; w < tiles; ++w) issue_qk(w, stage_addr(at));
+                mma_commit(smem_addr(empty + at % C::kStages));
+            }
+            __syncwarp();
+            for (int j = g.first; j < g.last; ++j, at += 2) {
+                const bool last = j + 1 == g.last;
+                ok = wait_tile(at + 1) && (last || wait_tile(at + 2));
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint32_t v_tile = stage_addr(at + 1), k_next = stage_addr(at + 2);
+                const int valid = q.keys - j * kKeys;
+                if (valid < kKeys) {
+                    // rows behind the sequence's last key hold anything: P is 0 there, and so must V be
+                    const uint32_t zero_from = (uint32_t)max(valid, 0) * 128;
+                    for (int h = 0; h < C::kHalves; ++h)
+                        for (uint32_t b = zero_from + lane * 16; b < (uint32_t)kHalfBytes; b += 512)
+                            *reinterpret_cast<uint4 *>(smem + (v_tile - base) + h * kHalfBytes + b) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                for (int w = 0; w < tiles && ok; ++w) {
+                    ok = bar_wait(p_full + w, p_uses[w]++ & 1, gave_up);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int i = 0; i < kKeys / 16; ++i)
+                            mma_ts(tmem + C::kO + w * 128, tmem + w * 128 + i * 8, tile_desc(v_tile + i * 2048, kHalfBytes),
+                                   pv, j > g.first || i > 0);
+                        if (last) mma_commit(smem_addr(o_full + w));
+                        else issue_qk(w, k_next);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    mma_commit(smem_addr(empty + (at + 1) % C::kStages));
+                    if (!last) mma_commit(smem_addr(empty + (at + 2) % C::kStages));
+                }
+                __syncwarp();
+            }
+            more = ok && next_segment(s, cur, q, g);
+        }
+        // every instruction and arrival of this CTA is done when it ends, also after a wait that gave up
+        if (lane == 0) mma_commit(smem_addr(done));
+        __syncwarp();
+        (void)mbar_wait_bounded(done, 0);
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        // ---- softmax
+        const int w = warp / 4, row = threadIdx.x % kTile;
+        const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
+        const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + C::kO + w * 128;
+        const int dim = (int)a.head_dim;
+        const bool causal = (a.flags & KS_ATTENTION_CAUSAL) != 0;
+        // The products run with |scale|: a negative one turns the query's signs. 0 becomes the least
+        // normal number, whose products with finite scores vanish and which leaves -inf as it is.
+        const float scale = fmaxf(fabsf(s.scale_log2), 1.17549435e-38f);
+        const uint32_t sign = s.scale_log2 < 0.0f ? 0x80008000u : 0u;
+        uint32_t s_uses = 0, o_uses = 0;
+        while (more) {
+            const Segment g = segment(s, cur, q);
+            if (w == 1 && !g.two) {
+                more = next_segment(s, cur, q, g);
+                continue;
+            }
+            const int r = w * kTile + row;
+            int token, head;
+            const bool real = attn_row(s, q.q0, q.n, cur.head, cur.row_tile, r, &token, &head);
+            {
+                const T *src = (const T *)a.q + token * a.q_token_stride + head * a.q_head_stride;
+                uint8_t *dst = smem + w * C::kTileBytes + row * 128;
+#pragma unroll
+                for (int c = 0; c < kDim / 8; ++c) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (real && c * 8 < dim) x = *reinterpret_cast<const uint4 *>(src + c * 8);
+                    x.x ^= sign;
+                    x.y ^= sign;
+                    x.z ^= sign;
+                    x.w ^= sign;
+                    *reinterpret_cast<uint4 *>(dst + c / 8 * kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = x;
+                }
+                fence_async_smem();
+                fence_before();
+                bar_arrive(q_full + w);
+            }
+            const int sees = attn_tile_keys(s, q, cur.row_tile);
+            const int tile_first = cur.row_tile * s.tile_tokens;
+            const int limit = causal ? min(sees, q.keys - q.n + tile_first + r / s.tile_heads + 1) : sees;
+            const int all_see = causal ? min(sees, q.keys - q.n + tile_first + w * kTile / s.tile_heads + 1) : sees;
+
+            float m = -INFINITY, l = 0.0f;
+            bool ok = true;
+            for (int j = g.first; j < g.last; ++j) {
+                ok = bar_wait(s_full + w, s_uses++ & 1, gave_up);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_load32(x[c], s_at + c * 32);
+                tmem_wait_load();
+                const int key0 = j * kKeys;
+                if (key0 + kKeys > all_see) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (key0 + c * 32 + i >= limit) x[c][i] = 0xFF800000u;  // -inf
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(x[c][i]));
+                const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+                if (j == g.first) {
+                    m = best;
+                } else if (__any_sync(0xFFFFFFFFu, best > m + kGrowth)) {
+                    const float to = best > m + kGrowth ? best : m;
+                    const float f = exp2_approx(m - attn_base(to));
+                    l *= f;
+                    m = to;
+#pragma unroll
+                    for (int c = 0; c < kDim / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_load32(o, o_at + c * 32);
+                        tmem_wait_load();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_store32(o_at + c * 32, o);
+                    }
+                }
+                const float off = -attn_base(m);
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int c = h * 2 + i / 16, e = i % 16 * 2;
+                        const float y = exp2_approx(fmaf(__uint_as_float(x[c][e]), scale, off));
+                        const float z = exp2_approx(fmaf(__uint_as_float(x[c][e + 1]), scale, off));
+                        sum[i & 1] += y;
+                        sum[2 + (i & 1)] += z;
+                        p[i] = pack_pair<T>(y, z);
+                    }
+                    tmem_store32(s_at + h * 32, p);
+                }
+                tmem_wait_store();
+                fence_before();
+                bar_arrive(p_full + w);
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            }
+            if (!ok) break;
+            ok = bar_wait(o_full + w, o_uses++ & 1, gave_up);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            fence_after();
+            const bool whole = g.first == 0 && g.last == g.units;
+            const float inv = attn_inverse(l);
+            float *part = attn_slot(s, cta, g.first == 0 ? 1 : 0);
+            T *dst = (T *)a.out + token * a.out_token_stride + head * a.out_head_stride;
+#pragma unroll
+            for (int c = 0; c < kDim / 32; ++c) {
+                uint32_t o[32];
+                tmem_load32(o, o_at + c * 32);
+                tmem_wait_load();
+                if (real && whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = pack_pair<T>(__uint_as_float(o[i + 2 * k]) * inv, __uint_as_float(o[i + 2 * k + 1]) * inv);
+                        if (c * 32 + i < dim)
+                            *reinterpret_cast<uint4 *>(dst + c * 32 + i) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                } else if (real) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        if (c * 32 + i < dim)
+                            *reinterpret_cast<uint4 *>(part + r * dim + c * 32 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+                __syncwarp();
+            }
+            fence_before();  // O is read before the next row tile's first product overwrites it
+            if (!whole && real) {
+                part[kRows * dim + r] = m;
+                part[kRows * dim + kRows + r] = l;
+            }
+            if (!whole && g.first == 0 && threadIdx.x == 0) {
+                AttnJoin j = {};
+                j.pieces = (int32_t)(attn_owner(cur, cur.at + g.units - 1) - cta + 1);
+                j.seq = cur.seq;
+                j.head = cur.head;
+                j.row_tile = cur.row_tile;
+                j.q0 = q.q0;
+                j.q_len = q.n;
+                attn_joins(s, ctas)[cta] = j;
+            }
+            more = next_segment(s, cur, q, g);
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ------------------------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static std::once_flag once;
+    static EncodeTiled f = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+            found == cudaDriverEntryPointSuccess)
+            f = (EncodeTiled)p;
+        else
+            (void)cudaGetLastError();
+    });
+    return f;
+}
+
+// The pool as a 4-dimensional tensor, columns, slots, heads, pages; boxes of 64 columns and as many
+// slots as a step takes of a page. Columns past head_dim and pages past the pool read as zeros.
+bool pool_map(CUtensorMap *map, const ks_attention_args_t &a, const void *p, int64_t page, int64_t slot, int64_t head) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.page_size, (cuuint64_t)a.kv_heads, (cuuint64_t)a.pages};
+    // a dimension of one entry has no stride of its own: any valid one
+    const cuuint64_t strides[3] = {(cuuint64_t)(a.page_size > 1 ? slot * 2 : 16 * ((a.head_dim + 7) / 8)),
+                                   (cuuint64_t)(a.kv_heads > 1 ? head * 2 : 16 * ((a.head_dim + 7) / 8)),
+                                   (cuuint64_t)(a.pages > 1 ? page * 2 : 16 * ((a.head_dim + 7) / 8))};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(a.page_size < kKeys ? a.page_size : kKeys), 1, 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    return encode(map, a.dtype == KS_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<void *>(p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+const void *tc_kernel(int dim, int *smem) {
+    *smem = dim <= 64 ? Tc<64>::kSmem : Tc<128>::kSmem;
+    return dim <= 64 ? (const void *)attn_tc_kernel<T, 64> : (const void *)attn_tc_kernel<T, 128>;
+}
+
+}  // namespace
+
+bool attn_tc_sizes(const ks_attention_args_t &a) {
+    // a copy's box begins on an 8-row group of the swizzled tile, and a step is whole pages or part of one
+    return a.head_dim <= 128 && a.page_size % 8 == 0 && (kKeys % a.page_size == 0 || a.page_size % kKeys == 0);
+}
+
+bool attn_tc_fits(const ks_attention_args_t &a) {
+    if (!attn_tc_sizes(a)) return false;
+    // the tensor map's strides are below 2^40 bytes and not zero
+    const int64_t strides[6] = {a.k_page_stride, a.k_slot_stride, a.k_head_stride, a.v_page_stride, a.v_slot_stride, a.v_head_stride};
+    const int64_t counts[6] = {a.pages, a.page_size, a.kv_heads, a.pages, a.page_size, a.kv_heads};
+    for (int i = 0; i < 6; ++i)
+        if (counts[i] > 1 && (strides[i] == 0 || strides[i] >= (1ll << 39))) return false;
+    return a.pages > 0;
+}
+
+int attn_tc_rows() { return kRows; }
+int attn_tc_unit() { return kKeys; }
+
+cudaError_t attn_tc_launch(const AttnArgs &s, int ctas, cudaStream_t stream, bool pdl) {
+    const ks_attention_args_t &a = s.a;
+    AttnArgs args = s;
+    CUtensorMap k_map, v_map;
+    if (!pool_map(&k_map, a, a.k_pages, a.k_page_stride, a.k_slot_stride, a.k_head_stride) ||
+        !pool_map(&v_map, a, a.v_pages, a.v_page_stride, a.v_slot_stride, a.v_head_stride))
+        return cudaErrorInvalidValue;
+    int smem = 0;
+    const void *f = a.dtype == KS_DTYPE_BF16 ? tc_kernel<__nv_bfloat16>((int)a.head_dim, &smem)
+                                             : tc_kernel<__half>((int)a.head_dim, &smem);
+    if (!allow_smem(f, (size_t)smem)) return cudaErrorInvalidConfiguration;
+    void *kp[] = {&args, &k_map, &v_map};
+    return launch_kernel(f, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, kp, stream, pdl);
+}
+
+int fault_flags_attention_tc(bool clear) { return fault_flags_t(clear); }
+
+}  // namespace ks

@@ -74,6 +74,7 @@ int fault_flags_f32(bool clear);
 int fault_flags_ops(bool clear);
 int fault_flags_rotary(bool clear);
 int fault_flags_attention(bool clear);
+int fault_flags_attention_tc(bool clear);
 // Launch helpers shared by the operators' translation units: the current device's SM count, the
 // launch itself (pdl: with programmatic stream serialization), and leave for `smem` bytes of
 // dynamic shared memory (once per device and kernel; false if they do not fit).

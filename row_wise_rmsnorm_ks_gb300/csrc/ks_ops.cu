@@ -1623,7 +1623,8 @@ ks_status_t op_plan(int op, int64_t rows, int64_t hidden, ks_dtype_t dtype, bool
 // All operators besides the norms answer together: this unit's word and those of the rotary and
 // attention units.
 int fault_flags_ops(bool clear) {
-    const int parts[3] = {fault_flags_t(clear), fault_flags_rotary(clear), fault_flags_attention(clear)};
+    const int parts[4] = {fault_flags_t(clear), fault_flags_rotary(clear), fault_flags_attention(clear),
+                          fault_flags_attention_tc(clear)};
     int all = 0;
     for (int v : parts) {
         if (v < 0) return -1;
