@@ -7,11 +7,11 @@
 //   warps 0-3, 4-7  softmax of tile 0 and 1, one row per thread (no shuffles): S to registers,
 //                   running maximum, exponentials, P back to tensor memory; at the end of a row
 //                   tile O to the output or the workspace;
-//   warp 8          issues the matrix instructions;
-//   warp 9          copies pages to shared memory by TMA, one lane per page and 64 columns
-//                   (warps 10 and 11 only complete the third warpgroup, for the register split).
-// While one tile is in its softmax, the matrix instructions of the other run: the order is
-// P0 V, Q0 K(next), P1 V, Q1 K(next). O is rescaled by the softmax warps, and only when a row's
+//   warps 8 and 10  issue the matrix instructions of tile 0 and 1: P V in two halves as P comes,
+//                   then Q K(next), which overwrites S and P behind it in order;
+//   warp 9          copies pages to shared memory by TMA, one lane per page and 64 columns;
+//   warp 11         clears value rows behind a sequence's last key.
+// While one tile is in its softmax, the matrix instructions of the other run. O is rescaled by the softmax warps, and only when a row's
 // maximum has grown by more than 2^8: until then the old maximum stays the row's base, which changes
 // nothing in the quotient and keeps P below 256.
 //
@@ -42,19 +42,18 @@ struct Tc {
     static constexpr int kHalves = kDim / 64;
     static constexpr int kTileBytes = kHalves * kHalfBytes;  // a tile of Q, K or V
     static constexpr int kStages = kDim == 128 ? 5 : 10;
-    static constexpr int kBars = 2 * kStages + 9;
+    static constexpr int kBars = 3 * kStages + 12;
     static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kBars * 8 + 16;
     static constexpr uint32_t kO = 256;  // tensor-memory columns: S0 0, S1 128, then the O tiles
 };
 
 // ---- tensor-core primitives
 
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead) {
-    // 128-byte swizzle; 8-row groups 1024 bytes apart; `lead` between 64-value blocks of a
-    // non-transposed operand
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
-}
+// Shared-memory operands are described by two words. Low: the address and, for an operand whose rows
+// are the product's K dimension, the distance of its 64-value blocks (both over 16); an offset within
+// the tile is added to it. High: 128-byte swizzle, groups of 8 rows 1024 bytes apart.
+constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return addr >> 4 | (lead >> 4) << 16; }
 
 // FP32 accumulators, both operands of T, M = 128, N = n; bit 16: B's rows are its K dimension.
 template <typename T>
@@ -64,18 +63,21 @@ __host__ __device__ constexpr uint32_t mma_shape(int n, bool b_by_rows) {
            (uint32_t)(kTile / 16) << 24;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+// One step of 16 along K: D (+)= A B, A in shared or tensor memory.
+template <bool kAdd>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(shape),
-        "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "n"(kDescHigh),
+        "r"(shape), "n"((int)kAdd)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(shape),
-        "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "n"(kDescHigh),
+        "r"(shape), "r"(add)
         : "memory");
 }
 // Arrives on `bar` when all matrix instructions this thread issued so far are done.
@@ -97,15 +99,29 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr) {
         : KS_W4(r, 0), KS_W4(r, 4), KS_W4(r, 8), KS_W4(r, 12), KS_W4(r, 16), KS_W4(r, 20), KS_W4(r, 24), KS_W4(r, 28)
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-        KS_R4(r, 0), KS_R4(r, 4), KS_R4(r, 8), KS_R4(r, 12), KS_R4(r, 16), KS_R4(r, 20), KS_R4(r, 24), KS_R4(r, 28)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr),
+        KS_R4(r, 0), KS_R4(r, 4), KS_R4(r, 8), KS_R4(r, 12)
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 columns of the lane's row times f, in place.
+__device__ __forceinline__ void tmem_scale16(uint32_t addr, float f) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : KS_W4(r, 0), KS_W4(r, 4), KS_W4(r, 8), KS_W4(r, 12)
+        : "r"(addr));
+    tmem_wait_load();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+    tmem_store16(addr, r);
+}
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int col, int slot, int head, int page,
                                          uint32_t bar) {
@@ -149,12 +165,24 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
     return w;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // The part of a CTA's work that one row tile is: the same for all roles.
 struct Segment {
     int first, last;   // units (128-key steps)
     int units;         // of the row tile
-    int rows;          // rows in use
     bool two;          // the second tile has rows
+};
+
+// Each warp keeps its place in the CTA's work in shared memory: between row tiles it is needed
+// once, and the softmax has no registers to spare for it.
+struct Place {
+    AttnCursor cur;
+    AttnSeq q;
 };
 
 __device__ __forceinline__ Segment segment(const AttnArgs &s, const AttnCursor &c, const AttnSeq &q) {
@@ -162,18 +190,22 @@ __device__ __forceinline__ Segment segment(const AttnArgs &s, const AttnCursor &
     g.units = attn_tile_units(s, q, c.row_tile);
     g.first = c.unit;
     g.last = (int)min((int64_t)g.units, g.first + c.left);
-    g.rows = min(s.tile_tokens, q.n - c.row_tile * s.tile_tokens) * s.tile_heads;
-    g.two = g.rows > kTile;
+    g.two = min(s.tile_tokens, q.n - c.row_tile * s.tile_tokens) * s.tile_heads > kTile;
     return g;
 }
 
-// Goes on to the CTA's next row tile; false when its share is done.
-__device__ __forceinline__ bool next_segment(const AttnArgs &s, AttnCursor &c, AttnSeq &q, const Segment &g) {
-    c.at += g.last - g.first;
-    c.left -= g.last - g.first;
-    if (c.left <= 0) return false;
-    attn_next(s, c, q);
-    return true;
+// Goes on to the CTA's next row tile; false when its share is done. All lanes of the
+// warp call it, or (kWarp false) the one that works.
+template <bool kWarp = true>
+__device__ __forceinline__ bool next_segment(const AttnArgs &s, Place &p, int steps) {
+    if (kWarp) __syncwarp();
+    if (!kWarp || threadIdx.x % 32 == 0) {
+        p.cur.at += steps;
+        p.cur.left -= steps;
+        if (p.cur.left > 0) attn_next(s, p.cur, p.q);
+    }
+    if (kWarp) __syncwarp();
+    return p.cur.left > 0;
 }
 
 template <typename T, int kDim>
@@ -189,7 +221,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     const uint32_t q_addr = base, ring = base + 2 * C::kTileBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (2 + C::kStages) * C::kTileBytes);
     uint64_t *full = bars, *empty = bars + C::kStages;
-    uint64_t *q_full = empty + C::kStages, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 2, *done = o_full + 2;
+    uint64_t *q_full = empty + C::kStages, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *p_half = o_full + 2, *done = p_half + 2, *tail = done + 2;
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile uint32_t *gave_up = tmem_at + 1;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -198,15 +231,17 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, 1);
+            mbar_init(empty + i, 3);  // warps 8, 10 and 11
+            mbar_init(tail + i, 1);
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(q_full + w, kTile);
             mbar_init(s_full + w, 1);
             mbar_init(p_full + w, kTile);
             mbar_init(o_full + w, 1);
+            mbar_init(p_half + w, kTile);
+            mbar_init(done + w, 1);
         }
-        mbar_init(done, 1);
         *gave_up = 0;
         fence_mbar_init();
     }
@@ -222,10 +257,18 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     grid_dependency_wait();
     allow_dependents_launch();
     if (threadIdx.x == 0) attn_joins(s, ctas)[cta].pieces = 0;
-    AttnCursor cur = attn_begin<kThreads>(s, cta, ctas);
-    bool more = cur.left > 0;
-    AttnSeq q = {};
-    if (more) q = attn_seq(a, cur.seq);
+    __shared__ Place places[kThreads / 32];
+    Place &place = places[warp];
+    bool more;
+    {
+        const AttnCursor c = attn_begin<kThreads>(s, cta, ctas);
+        more = c.left > 0;
+        if (lane == 0 && more) {
+            place.cur = c;
+            place.q = attn_seq(a, c.seq);
+        }
+        __syncwarp();
+    }
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -235,13 +278,13 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         const int part = lane / C::kHalves, half = lane % C::kHalves;
         uint32_t at = 0;  // tiles copied so far: K and V of each step in turn
         while (more) {
-            const Segment g = segment(s, cur, q);
-            const int head = cur.head / s.head_splits;
-            const int32_t *table = a.page_table + (int64_t)cur.seq * a.table_stride;
+            const Segment g = segment(s, place.cur, place.q);
+            const int head = place.cur.head / s.head_splits, keys = place.q.keys;
+            const int32_t *table = a.page_table + (int64_t)place.cur.seq * a.table_stride;
             bool ok = true;
             for (int j = g.first; j < g.last && ok; ++j) {
                 const int key = j * kKeys + part * in_tile;
-                const bool wanted = part * in_tile < kKeys && key < q.keys;
+                const bool wanted = part * in_tile < kKeys && key < keys;
                 int page = 0, slot = 0;
                 if (wanted) {
                     page = __ldg(table + key / page_size);
@@ -264,84 +307,114 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                                  v ? &v_map : &k_map, half * 64, slot, head, page, smem_addr(full + stage));
                 }
             }
-            more = ok && next_segment(s, cur, q, g);
+            more = ok && next_segment(s, place, g.last - g.first);
         }
         // nothing of this CTA's is in flight when it ends, also after a wait that gave up
         const uint32_t from = at > (uint32_t)C::kStages ? at - C::kStages : 0;
         for (uint32_t i = from; i < at; ++i) (void)mbar_wait_bounded(full + i % C::kStages, i / C::kStages & 1);
-    } else if (warp == 8) {
-        // ---- matrix instructions
+    } else if (warp != 11) {
+        // ---- matrix instructions of tile w: one thread issues them
+        const int w = warp == 8 ? 0 : 1;
         constexpr uint32_t qk = mma_shape<T>(kKeys, false), pv = mma_shape<T>(kDim, true);
-        uint32_t at = 0, q_uses = 0, q_uses1 = 0, p_uses[2] = {0, 0};
+        const uint32_t s_at = tmem + w * 128, o_at = tmem + C::kO + w * 128;
+        const uint32_t q_low = desc_low(q_addr + w * C::kTileBytes, 16);
+        uint32_t at = 0, q_uses = 0, p_uses = 0;
+        uint32_t tails = 0;  // phase of each stage's tail barrier, a bit each
         auto stage_addr = [&](uint32_t i) { return ring + i % C::kStages * C::kTileBytes; };
         auto wait_tile = [&](uint32_t i) { return bar_wait(full + i % C::kStages, i / C::kStages & 1, gave_up); };
-        auto issue_qk = [&](int w, uint32_t k_tile) {
+        auto free_tile = [&](uint32_t i) { mma_commit(smem_addr(empty + i % C::kStages)); };
+        auto issue_qk = [&](uint32_t k_tile) {
+            const uint32_t k_low = desc_low(k_tile, 16);
+            mma_ss<false>(s_at, q_low, k_low, qk);
 #pragma unroll
-            for (int i = 0; i < kDim / 16; ++i) {
-                const uint32_t off = i / 4 * kHalfBytes + i % 4 * 32;
-                mma_ss(tmem + w * 128, tile_desc(q_addr + w * C::kTileBytes + off, 16), tile_desc(k_tile + off, 16), qk,
-                       i > 0);
+            for (int i = 1; i < kDim / 16; ++i) {
+                const uint32_t off = (i / 4 * kHalfBytes + i % 4 * 32) >> 4;
+                mma_ss<true>(s_at, q_low + off, k_low + off, qk);
             }
             mma_commit(smem_addr(s_full + w));
         };
-        while (more) {
-            const Segment g = segment(s, cur, q);
-            const int tiles = g.two ? 2 : 1;
-            bool ok = bar_wait(q_full, q_uses++ & 1, gave_up);
-            if (g.two) ok = ok && bar_wait(q_full + 1, q_uses1++ & 1, gave_up);
-            ok = ok && wait_tile(at);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+        while (lane == 0 && more) {
+            const Segment g = segment(s, place.cur, place.q);
+            const int keys = place.q.keys;
+            bool ok;
+            if (w == 1 && !g.two) {  // this tile has no rows: its share of the stages is given back
+                ok = true;
+                for (int i = 2 * (g.last - g.first); i > 0 && ok; --i, ++at) {
+                    ok = wait_tile(at);
+                    if (ok) bar_arrive(empty + at % C::kStages);
+                }
+                if (keys < g.last * kKeys) tails ^= 1u << (at - 1) % C::kStages;
+                more = ok && next_segment<false>(s, place, g.last - g.first);
+                continue;
+            }
+            ok = bar_wait(q_full + w, q_uses++ & 1, gave_up) && wait_tile(at);
             if (!ok) break;
             fence_after();
-            if (lane == 0) {
-                for (int w = 0; w < tiles; ++w) issue_qk(w, stage_addr(at));
-                mma_commit(smem_addr(empty + at % C::kStages));
-            }
-            __syncwarp();
+            issue_qk(stage_addr(at));
+            free_tile(at);
             for (int j = g.first; j < g.last; ++j, at += 2) {
-                const bool last = j + 1 == g.last;
-                ok = wait_tile(at + 1) && (last || wait_tile(at + 2));
+                ok = wait_tile(at + 1);
+                if (ok && keys < (j + 1) * kKeys) {
+                    const uint32_t v_stage = (at + 1) % C::kStages;
+                    ok = bar_wait(tail + v_stage, tails >> v_stage & 1, gave_up);
+                    tails ^= 1u << v_stage;
+                }
+                ok = ok && bar_wait(p_half + w, p_uses & 1, gave_up);
+                if (!ok) break;
+                fence_after();
+                const uint32_t v_low = desc_low(stage_addr(at + 1), kHalfBytes);
+                mma_ts(o_at, s_at, v_low, pv, j > g.first);
+#pragma unroll
+                for (int i = 1; i < kKeys / 32; ++i) mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
+                ok = bar_wait(p_full + w, p_uses++ & 1, gave_up);
+                if (!ok) break;
+                fence_after();
+#pragma unroll
+                for (int i = kKeys / 32; i < kKeys / 16; ++i) mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
+                free_tile(at + 1);
+                if (j + 1 == g.last) {
+                    mma_commit(smem_addr(o_full + w));
+                } else {
+                    ok = wait_tile(at + 2);
+                    if (!ok) break;
+                    issue_qk(stage_addr(at + 2));
+                    free_tile(at + 2);
+                }
+            }
+            more = ok && next_segment<false>(s, place, g.last - g.first);
+        }
+        // every instruction and arrival of this warp is done when it ends, also after a wait that gave up
+        if (lane == 0) {
+            mma_commit(smem_addr(done + w));
+            (void)mbar_wait_bounded(done + w, 0);
+        }
+    } else {
+        // ---- the step a sequence ends in: value rows behind its last key hold anything, and a product
+        // with their probability 0 would let a NaN through, so they are set to 0. This warp follows every
+        // tile through the ring (a barrier's phases can be told apart one apart, no further).
+        uint32_t at = 0;
+        while (more) {
+            const Segment g = segment(s, place.cur, place.q);
+            const int valid = place.q.keys - (g.last - 1) * kKeys;
+            bool ok = true;
+            for (uint32_t end = at + 2 * (g.last - g.first); at < end && ok; ++at) {
+                const uint32_t stage = at % C::kStages;
+                ok = bar_wait(full + stage, at / C::kStages & 1, gave_up);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                const uint32_t v_tile = stage_addr(at + 1), k_next = stage_addr(at + 2);
-                const int valid = q.keys - j * kKeys;
-                if (valid < kKeys) {
-                    // rows behind the sequence's last key hold anything: P is 0 there, and so must V be
-                    const uint32_t zero_from = (uint32_t)max(valid, 0) * 128;
+                if (at + 1 == end && valid < kKeys) {  // the row tile's last values
+                    uint8_t *v_tile = smem + (2 + stage) * C::kTileBytes;
                     for (int h = 0; h < C::kHalves; ++h)
-                        for (uint32_t b = zero_from + lane * 16; b < (uint32_t)kHalfBytes; b += 512)
-                            *reinterpret_cast<uint4 *>(smem + (v_tile - base) + h * kHalfBytes + b) = make_uint4(0, 0, 0, 0);
+                        for (uint32_t b = (uint32_t)max(valid, 0) * 128 + lane * 16; b < (uint32_t)kHalfBytes; b += 512)
+                            *reinterpret_cast<uint4 *>(v_tile + h * kHalfBytes + b) = make_uint4(0, 0, 0, 0);
                     fence_async_smem();
                     __syncwarp();
+                    if (lane == 0) bar_arrive(tail + stage);
                 }
-                for (int w = 0; w < tiles && ok; ++w) {
-                    ok = bar_wait(p_full + w, p_uses[w]++ & 1, gave_up);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    fence_after();
-                    if (lane == 0) {
-#pragma unroll
-                        for (int i = 0; i < kKeys / 16; ++i)
-                            mma_ts(tmem + C::kO + w * 128, tmem + w * 128 + i * 8, tile_desc(v_tile + i * 2048, kHalfBytes),
-                                   pv, j > g.first || i > 0);
-                        if (last) mma_commit(smem_addr(o_full + w));
-                        else issue_qk(w, k_next);
-                    }
-                    __syncwarp();
-                }
-                if (!ok) break;
-                if (lane == 0) {
-                    mma_commit(smem_addr(empty + (at + 1) % C::kStages));
-                    if (!last) mma_commit(smem_addr(empty + (at + 2) % C::kStages));
-                }
-                __syncwarp();
+                if (lane == 0) bar_arrive(empty + stage);
             }
-            more = ok && next_segment(s, cur, q, g);
+            more = ok && next_segment(s, place, g.last - g.first);
         }
-        // every instruction and arrival of this CTA is done when it ends, also after a wait that gave up
-        if (lane == 0) mma_commit(smem_addr(done));
-        __syncwarp();
-        (void)mbar_wait_bounded(done, 0);
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -356,16 +429,19 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         const float scale = fmaxf(fabsf(s.scale_log2), 1.17549435e-38f);
         const uint32_t sign = s.scale_log2 < 0.0f ? 0x80008000u : 0u;
         uint32_t s_uses = 0, o_uses = 0;
+        const int r = w * kTile + row;
         while (more) {
-            const Segment g = segment(s, cur, q);
+            const Segment g = segment(s, place.cur, place.q);
             if (w == 1 && !g.two) {
-                more = next_segment(s, cur, q, g);
+                more = next_segment(s, place, g.last - g.first);
                 continue;
             }
-            const int r = w * kTile + row;
-            int token, head;
-            const bool real = attn_row(s, q.q0, q.n, cur.head, cur.row_tile, r, &token, &head);
+            int limit, all_see;  // keys this thread's row sees, and all rows of the tile
             {
+                const AttnSeq q = place.q;
+                const int row_tile = place.cur.row_tile;
+                int token, head;
+                const bool real = attn_row(s, q.q0, q.n, place.cur.head, row_tile, r, &token, &head);
                 const T *src = (const T *)a.q + token * a.q_token_stride + head * a.q_head_stride;
                 uint8_t *dst = smem + w * C::kTileBytes + row * 128;
 #pragma unroll
@@ -381,11 +457,11 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 fence_async_smem();
                 fence_before();
                 bar_arrive(q_full + w);
+                const int sees = attn_tile_keys(s, q, row_tile);
+                const int first = q.keys - q.n + row_tile * s.tile_tokens + 1;
+                limit = causal ? min(sees, first + r / s.tile_heads) : sees;
+                all_see = causal ? min(sees, first + w * kTile / s.tile_heads) : sees;
             }
-            const int sees = attn_tile_keys(s, q, cur.row_tile);
-            const int tile_first = cur.row_tile * s.tile_tokens;
-            const int limit = causal ? min(sees, q.keys - q.n + tile_first + r / s.tile_heads + 1) : sees;
-            const int all_see = causal ? min(sees, q.keys - q.n + tile_first + w * kTile / s.tile_heads + 1) : sees;
 
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
@@ -408,9 +484,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
+                for (int i = 0; i < 32; i += 2)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(x[c][i]));
+                    for (int c = 0; c < 4; ++c)
+                        top[c] = max3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
                 const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
                 if (j == g.first) {
                     m = best;
@@ -419,47 +496,47 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                     const float f = exp2_approx(m - attn_base(to));
                     l *= f;
                     m = to;
-#pragma unroll
-                    for (int c = 0; c < kDim / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_load32(o, o_at + c * 32);
-                        tmem_wait_load();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_store32(o_at + c * 32, o);
-                    }
+#pragma unroll 1
+                    for (int c = 0; c < kDim / 16; ++c) tmem_scale16(o_at + c * 16, f);
                 }
-                const float off = -attn_base(m);
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const float2 mul = make_float2(scale, scale), off = make_float2(-attn_base(m), -attn_base(m));
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int c = h * 2 + i / 16, e = i % 16 * 2;
-                        const float y = exp2_approx(fmaf(__uint_as_float(x[c][e]), scale, off));
-                        const float z = exp2_approx(fmaf(__uint_as_float(x[c][e + 1]), scale, off));
-                        sum[i & 1] += y;
-                        sum[2 + (i & 1)] += z;
-                        p[i] = pack_pair<T>(y, z);
+                    for (int i = 0; i < 16; ++i) {
+                        float2 y = make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
+                        y = pair_fma<true>(y, mul, off);
+                        y.x = exp2_approx(y.x);
+                        y.y = exp2_approx(y.y);
+                        sum[i & 1] = pair_add<true>(sum[i & 1], y);
+                        p[i] = pack_pair<T>(y.x, y.y);
                     }
-                    tmem_store32(s_at + h * 32, p);
+                    tmem_store16(s_at + c * 16, p);
+                    if (c == 1) {  // the first half of the values' product can start
+                        tmem_wait_store();
+                        fence_before();
+                        bar_arrive(p_half + w);
+                    }
                 }
                 tmem_wait_store();
                 fence_before();
                 bar_arrive(p_full + w);
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!ok) break;
             ok = bar_wait(o_full + w, o_uses++ & 1, gave_up);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             fence_after();
+            int token, head;
+            const bool real = attn_row(s, place.q.q0, place.q.n, place.cur.head, place.cur.row_tile, r, &token, &head);
             const bool whole = g.first == 0 && g.last == g.units;
             const float inv = attn_inverse(l);
             float *part = attn_slot(s, cta, g.first == 0 ? 1 : 0);
             T *dst = (T *)a.out + token * a.out_token_stride + head * a.out_head_stride;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kDim / 32; ++c) {
                 uint32_t o[32];
                 tmem_load32(o, o_at + c * 32);
@@ -489,15 +566,15 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             }
             if (!whole && g.first == 0 && threadIdx.x == 0) {
                 AttnJoin j = {};
-                j.pieces = (int32_t)(attn_owner(cur, cur.at + g.units - 1) - cta + 1);
-                j.seq = cur.seq;
-                j.head = cur.head;
-                j.row_tile = cur.row_tile;
-                j.q0 = q.q0;
-                j.q_len = q.n;
+                j.pieces = (int32_t)(attn_owner(place.cur, place.cur.at + g.units - 1) - cta + 1);
+                j.seq = place.cur.seq;
+                j.head = place.cur.head;
+                j.row_tile = place.cur.row_tile;
+                j.q0 = place.q.q0;
+                j.q_len = place.q.n;
                 attn_joins(s, ctas)[cta] = j;
             }
-            more = next_segment(s, cur, q, g);
+            more = next_segment(s, place, g.last - g.first);
         }
     }
     __syncwarp();
