@@ -3,17 +3,17 @@
 //
 // A CTA works on a row tile of 256 query rows, two tiles of 128 that share every 128-key step of
 // the cache: S = Q K^T and O += P V are tcgen05.mma with S, P and O in tensor memory, which they
-// fill exactly (two 128-column S, over which P is written, two 128-column O). Twelve warps:
-//   warps 0-3, 4-7  softmax of tile 0 and 1, one row per thread (no shuffles): S to registers,
-//                   running maximum, exponentials, P back to tensor memory; at the end of a row
-//                   tile O to the output or the workspace;
-//   warps 8 and 10  issue the matrix instructions of tile 0 and 1: P V in two halves as P comes,
-//                   then Q K(next), which overwrites S and P behind it in order;
-//   warp 9          copies pages to shared memory by TMA, one lane per page and 64 columns;
-//   warp 11         clears value rows behind a sequence's last key.
-// While one tile is in its softmax, the matrix instructions of the other run. O is rescaled by the softmax warps, and only when a row's
-// maximum has grown by more than 2^8: until then the old maximum stays the row's base, which changes
-// nothing in the quotient and keeps P below 256.
+// fill exactly (two 128-column S, over which P is written, two 128-column O). Twenty warps:
+//   warps 0-7, 8-15  softmax of tile 0 and 1, two threads a row (no shuffles): S to registers, running
+//                    maximum, exponentials, P back to tensor memory; at the end of a row tile O to the
+//                    output or the workspace;
+//   warps 16 and 18  issue the matrix instructions of tile 0 and 1: P V, then Q K(next), which
+//                    overwrites S and P behind it in order;
+//   warp 17          copies pages to shared memory by TMA, one lane per page and 64 columns;
+//   warp 19          clears value rows behind a sequence's last key.
+// While one tile is in its softmax, the matrix instructions of the other run. O is rescaled by the
+// softmax warps, and only when a row's maximum has grown by more than 2^8: until then the old maximum
+// stays the row's base, which changes nothing in the quotient and keeps P below 256.
 //
 // Bound by the tensor cores for long chunks (2 * 128 * 128 * 2 * dim operations a step and tile).
 // For few rows of a tile it is a stream of the cache like the 16-row kernel's.
@@ -30,10 +30,12 @@ namespace {
 constexpr int kTile = 128;         // rows of a matrix tile
 constexpr int kRows = 2 * kTile;   // rows of a row tile
 constexpr int kKeys = 128;         // keys of a step
-constexpr int kSoftmaxThreads = 256, kThreads = kSoftmaxThreads + 128;
-// Registers: 384 threads launch with 168 each; the softmax warpgroups take 232 (128 scores a thread and
-// their probabilities), the third keeps 40: 128 * (232 + 232 + 40) = 384 * 168.
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kTileThreads = 2 * kTile;  // softmax threads of a tile: two a row, 64 keys each
+constexpr int kSoftmaxWarps = 2 * kTileThreads / 32, kThreads = 2 * kTileThreads + 128;
+constexpr int kMma = kSoftmaxWarps, kCopy = kMma + 1, kTail = kMma + 3;  // the other warps (kMma + 2: see there)
+// Registers: 640 threads launch with 96 each; the softmax warpgroups take 104 (64 scores a thread and
+// their probabilities), the last keeps 64.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr int kHalfBytes = kKeys * 128;  // 128 rows of 64 values
 constexpr float kGrowth = 8.0f;    // log2 of how far a row's maximum may pass its base
 
@@ -135,6 +137,13 @@ __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// One arrival for the warp: 32 arrivals of lanes would be worked off one after the other, in shared
+// memory that the matrix instructions read from (measured: a fifth of the kernel's time).
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) bar_arrive(bar);
+}
+
 // Waits for phase `parity`; false when the wait's limit passed or another role gave up. The role
 // then leaves its loop: everybody meets at the kernel's end, with the fault word set.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up) {
@@ -152,6 +161,21 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
+// The same by a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up) {
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, gave_up));
+}
+
+// Lane 0's value, which the compiler then knows to be the same in all lanes: what the matrix
+// instructions are given stays in uniform registers.
+__device__ __forceinline__ int warp_uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
     uint32_t w;
@@ -165,11 +189,48 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
     return w;
 }
 
+__device__ __forceinline__ void tmem_store1(uint32_t addr, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(__float_as_uint(v)) : "memory");
+}
+__device__ __forceinline__ float tmem_load1(uint32_t addr) {
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(addr));
+    tmem_wait_load();
+    return __uint_as_float(v);
+}
+
+// Barrier of the softmax threads of tile w, plain or telling whether any of them says yes.
+__device__ __forceinline__ void tile_sync(int w) {
+    asm volatile("bar.sync %0, %1;" ::"r"(w + 1), "n"(kTileThreads) : "memory");
+}
+__device__ __forceinline__ bool tile_any(int w, bool yes) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, %3, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)yes), "r"(w + 1), "n"(kTileThreads)
+        : "memory");
+    return any != 0;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+
+// A place in the ring of tiles and the phase of its barriers there.
+template <int kStages>
+struct RingAt {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // The part of a CTA's work that one row tile is: the same for all roles.
 struct Segment {
@@ -208,12 +269,21 @@ __device__ __forceinline__ bool next_segment(const AttnArgs &s, Place &p, int st
     return p.cur.left > 0;
 }
 
+// The same for the softmax threads of tile w, which share a place.
+__device__ __forceinline__ bool next_tile_segment(const AttnArgs &s, Place &p, int steps, int w) {
+    tile_sync(w);
+    if (threadIdx.x % kTileThreads == 0) (void)next_segment<false>(s, p, steps);
+    tile_sync(w);
+    return p.cur.left > 0;
+}
+
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUtensorMap k_map,
                const __grid_constant__ CUtensorMap v_map) {
     using C = Tc<kDim>;
-    static_assert(128 * (2 * kSoftmaxRegs + kOtherRegs) <= kThreads * 168, "the split draws on the launch's registers");
+    static_assert(2 * kTileThreads * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
+                  "the split draws on the launch's registers");
     extern __shared__ uint8_t raw[];
     const ks_attention_args_t &a = s.a;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
@@ -222,30 +292,31 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (2 + C::kStages) * C::kTileBytes);
     uint64_t *full = bars, *empty = bars + C::kStages;
     uint64_t *q_full = empty + C::kStages, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 2;
-    uint64_t *p_half = o_full + 2, *done = p_half + 2, *tail = done + 2;
+    uint64_t *turn = o_full + 2, *done = turn + 2, *tail = done + 2;
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile uint32_t *gave_up = tmem_at + 1;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = warp_uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int cta = blockIdx.x, ctas = gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, 3);  // warps 8, 10 and 11
+            mbar_init(empty + i, 3);  // the issuing warps and the one that clears tails
             mbar_init(tail + i, 1);
         }
         for (int w = 0; w < 2; ++w) {
-            mbar_init(q_full + w, kTile);
+            mbar_init(q_full + w, kTileThreads / 32);
             mbar_init(s_full + w, 1);
-            mbar_init(p_full + w, kTile);
+            mbar_init(p_full + w, kTileThreads / 32);
             mbar_init(o_full + w, 1);
-            mbar_init(p_half + w, kTile);
+            mbar_init(turn + w, 1);
             mbar_init(done + w, 1);
         }
+        bar_arrive(turn);  // tile 0 begins
         *gave_up = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == kMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_at))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -253,26 +324,26 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = warp_uniform(*tmem_at);
     grid_dependency_wait();
     allow_dependents_launch();
     if (threadIdx.x == 0) attn_joins(s, ctas)[cta].pieces = 0;
-    __shared__ Place places[kThreads / 32];
-    Place &place = places[warp];
+    __shared__ Place places[6];
+    Place &place = places[warp < kSoftmaxWarps ? warp / 8 : warp - kSoftmaxWarps + 2];
     bool more;
     {
         const AttnCursor c = attn_begin<kThreads>(s, cta, ctas);
         more = c.left > 0;
-        if (lane == 0 && more) {
+        if (more && lane == 0 && (warp >= kSoftmaxWarps || warp % 8 == 0)) {
             place.cur = c;
             place.q = attn_seq(a, c.seq);
         }
-        __syncwarp();
+        __syncthreads();
     }
 
-    if (warp >= 8) {
+    if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 9) {
+    if (warp == kCopy) {
         // ---- copies
         const int page_size = (int)a.page_size, in_tile = min(page_size, kKeys);  // keys of a copy
         const int part = lane / C::kHalves, half = lane % C::kHalves;
@@ -312,19 +383,22 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         // nothing of this CTA's is in flight when it ends, also after a wait that gave up
         const uint32_t from = at > (uint32_t)C::kStages ? at - C::kStages : 0;
         for (uint32_t i = from; i < at; ++i) (void)mbar_wait_bounded(full + i % C::kStages, i / C::kStages & 1);
-    } else if (warp != 11) {
-        // ---- matrix instructions of tile w: one thread issues them
-        const int w = warp == 8 ? 0 : 1;
+    } else if (warp == kMma || warp == kMma + 2) {
+        // ---- matrix instructions of tile w, issued by one thread: for each step P V, then Q K of the
+        // next step. The two warps take turns, a whole batch each: the other tile's softmax runs beside
+        // a batch, and a warp has done its waiting when its turn comes. (Without turns the batches
+        // interleave, both softmaxes run at once and the tensor cores wait for them; one warp for both
+        // tiles spends a third of its time on barriers while the few instructions it can issue ahead
+        // run out. Measured at 8192 tokens over 16384 keys: both 1.2 to 1.4 ms.)
+        const int w = warp == kMma ? 0 : 1;
         constexpr uint32_t qk = mma_shape<T>(kKeys, false), pv = mma_shape<T>(kDim, true);
         const uint32_t s_at = tmem + w * 128, o_at = tmem + C::kO + w * 128;
         const uint32_t q_low = desc_low(q_addr + w * C::kTileBytes, 16);
-        uint32_t at = 0, q_uses = 0, p_uses = 0;
-        uint32_t tails = 0;  // phase of each stage's tail barrier, a bit each
-        auto stage_addr = [&](uint32_t i) { return ring + i % C::kStages * C::kTileBytes; };
-        auto wait_tile = [&](uint32_t i) { return bar_wait(full + i % C::kStages, i / C::kStages & 1, gave_up); };
-        auto free_tile = [&](uint32_t i) { mma_commit(smem_addr(empty + i % C::kStages)); };
-        auto issue_qk = [&](uint32_t k_tile) {
-            const uint32_t k_low = desc_low(k_tile, 16);
+        RingAt<C::kStages> k_at, v_at;  // the next step's keys, this step's values
+        uint32_t q_uses = 0, p_uses = 0, turns = 0;
+        uint32_t tails = 0;             // phase of each stage's tail barrier, a bit each
+        auto issue_qk = [&](uint32_t stage) {
+            const uint32_t k_low = desc_low(ring + stage * C::kTileBytes, 16);
             mma_ss<false>(s_at, q_low, k_low, qk);
 #pragma unroll
             for (int i = 1; i < kDim / 16; ++i) {
@@ -333,62 +407,72 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             }
             mma_commit(smem_addr(s_full + w));
         };
-        while (lane == 0 && more) {
+        while (more) {
             const Segment g = segment(s, place.cur, place.q);
-            const int keys = place.q.keys;
-            bool ok;
-            if (w == 1 && !g.two) {  // this tile has no rows: its share of the stages is given back
-                ok = true;
-                for (int i = 2 * (g.last - g.first); i > 0 && ok; --i, ++at) {
-                    ok = wait_tile(at);
-                    if (ok) bar_arrive(empty + at % C::kStages);
+            const int first = warp_uniform(g.first), end = warp_uniform(g.last);
+            const int keys = warp_uniform(place.q.keys);
+            const bool two = warp_uniform(g.two) != 0;
+            bool ok = true;
+            if (w == 1 && !two) {  // this tile has no rows: its share of the stages is given back
+                for (int i = 2 * (end - first); i > 0 && ok; --i) {
+                    ok = bar_wait_warp(full + k_at.stage, k_at.phase, gave_up);
+                    if (i == 1 && keys < end * kKeys) tails ^= 1u << k_at.stage;
+                    if (ok && lane == 0) bar_arrive(empty + k_at.stage);
+                    k_at.next();
                 }
-                if (keys < g.last * kKeys) tails ^= 1u << (at - 1) % C::kStages;
-                more = ok && next_segment<false>(s, place, g.last - g.first);
+                more = ok && next_segment(s, place, end - first);
                 continue;
             }
-            ok = bar_wait(q_full + w, q_uses++ & 1, gave_up) && wait_tile(at);
+            ok = bar_wait_warp(full + k_at.stage, k_at.phase, gave_up) &&
+                 bar_wait_warp(q_full + w, q_uses++ & 1, gave_up) &&
+                 (!two || bar_wait_warp(turn + w, turns++ & 1, gave_up));
             if (!ok) break;
             fence_after();
-            issue_qk(stage_addr(at));
-            free_tile(at);
-            for (int j = g.first; j < g.last; ++j, at += 2) {
-                ok = wait_tile(at + 1);
-                if (ok && keys < (j + 1) * kKeys) {
-                    const uint32_t v_stage = (at + 1) % C::kStages;
-                    ok = bar_wait(tail + v_stage, tails >> v_stage & 1, gave_up);
-                    tails ^= 1u << v_stage;
-                }
-                ok = ok && bar_wait(p_half + w, p_uses & 1, gave_up);
-                if (!ok) break;
-                fence_after();
-                const uint32_t v_low = desc_low(stage_addr(at + 1), kHalfBytes);
-                mma_ts(o_at, s_at, v_low, pv, j > g.first);
-#pragma unroll
-                for (int i = 1; i < kKeys / 32; ++i) mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
-                ok = bar_wait(p_full + w, p_uses++ & 1, gave_up);
-                if (!ok) break;
-                fence_after();
-#pragma unroll
-                for (int i = kKeys / 32; i < kKeys / 16; ++i) mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
-                free_tile(at + 1);
-                if (j + 1 == g.last) {
-                    mma_commit(smem_addr(o_full + w));
-                } else {
-                    ok = wait_tile(at + 2);
-                    if (!ok) break;
-                    issue_qk(stage_addr(at + 2));
-                    free_tile(at + 2);
-                }
+            if (elect_one()) {
+                issue_qk(k_at.stage);
+                if (two) bar_arrive(turn + 1 - w);
+                mma_commit(smem_addr(empty + k_at.stage));
             }
-            more = ok && next_segment<false>(s, place, g.last - g.first);
+            __syncwarp();
+            v_at = k_at;
+            v_at.next();
+            for (int j = first; j < end; ++j) {
+                const bool last = j + 1 == end;
+                k_at = v_at;
+                k_at.next();
+                ok = bar_wait_warp(full + v_at.stage, v_at.phase, gave_up);
+                if (ok && keys < (j + 1) * kKeys) {
+                    ok = bar_wait_warp(tail + v_at.stage, tails >> v_at.stage & 1, gave_up);
+                    tails ^= 1u << v_at.stage;
+                }
+                if (!last) ok = ok && bar_wait_warp(full + k_at.stage, k_at.phase, gave_up);
+                ok = ok && bar_wait_warp(p_full + w, p_uses++ & 1, gave_up);
+                if (two) ok = ok && bar_wait_warp(turn + w, turns++ & 1, gave_up);
+                if (!ok) break;
+                fence_after();
+                if (elect_one()) {
+                    const uint32_t v_low = desc_low(ring + v_at.stage * C::kTileBytes, kHalfBytes);
+                    mma_ts(o_at, s_at, v_low, pv, j > first);
+#pragma unroll
+                    for (int i = 1; i < kKeys / 16; ++i) mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
+                    if (last) mma_commit(smem_addr(o_full + w));
+                    else issue_qk(k_at.stage);
+                    if (two) bar_arrive(turn + 1 - w);
+                    mma_commit(smem_addr(empty + v_at.stage));
+                    if (!last) mma_commit(smem_addr(empty + k_at.stage));
+                }
+                __syncwarp();
+                v_at = k_at;
+                v_at.next();
+            }
+            // k_at is the tile after the row tile's last values: the next row tile's first keys
+            more = ok && next_segment(s, place, end - first);
         }
         // every instruction and arrival of this warp is done when it ends, also after a wait that gave up
-        if (lane == 0) {
-            mma_commit(smem_addr(done + w));
-            (void)mbar_wait_bounded(done + w, 0);
-        }
-    } else {
+        if (elect_one()) mma_commit(smem_addr(done + w));
+        __syncwarp();
+        (void)mbar_wait_bounded(done + w, 0);
+    } else if (warp == kTail) {
         // ---- the step a sequence ends in: value rows behind its last key hold anything, and a product
         // with their probability 0 would let a NaN through, so they are set to 0. This warp follows every
         // tile through the ring (a barrier's phases can be told apart one apart, no further).
@@ -418,25 +502,27 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        // ---- softmax
-        const int w = warp / 4, row = threadIdx.x % kTile;
+        // ---- softmax: two threads a row, `half` having the first or last 64 keys of a step, and the first
+        // or last half of the output's columns
+        const int w = warp / 8, half = warp / 4 % 2, row = warp % 4 * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
-        const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + C::kO + w * 128;
+        const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + C::kO + w * 128 + half * (kDim / 2);
+        // One number goes to the row's other thread through a column of S that P leaves free.
+        const uint32_t mine = s_at + 126 + half, theirs = s_at + 127 - half;
         const int dim = (int)a.head_dim;
         const bool causal = (a.flags & KS_ATTENTION_CAUSAL) != 0;
         // The products run with |scale|: a negative one turns the query's signs. 0 becomes the least
         // normal number, whose products with finite scores vanish and which leaves -inf as it is.
         const float scale = fmaxf(fabsf(s.scale_log2), 1.17549435e-38f);
-        const uint32_t sign = s.scale_log2 < 0.0f ? 0x80008000u : 0u;
         uint32_t s_uses = 0, o_uses = 0;
         const int r = w * kTile + row;
         while (more) {
             const Segment g = segment(s, place.cur, place.q);
             if (w == 1 && !g.two) {
-                more = next_segment(s, place, g.last - g.first);
+                more = next_tile_segment(s, place, g.last - g.first, w);
                 continue;
             }
-            int limit, all_see;  // keys this thread's row sees, and all rows of the tile
+            int limit, all_see;  // keys of a step's half that this thread's row sees, and all rows of the tile
             {
                 const AttnSeq q = place.q;
                 const int row_tile = place.cur.row_tile;
@@ -444,8 +530,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 const bool real = attn_row(s, q.q0, q.n, place.cur.head, row_tile, r, &token, &head);
                 const T *src = (const T *)a.q + token * a.q_token_stride + head * a.q_head_stride;
                 uint8_t *dst = smem + w * C::kTileBytes + row * 128;
+                const uint32_t sign = s.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-                for (int c = 0; c < kDim / 8; ++c) {
+                for (int i = 0; i < kDim / 16; ++i) {
+                    const int c = half * (kDim / 16) + i;
                     uint4 x = make_uint4(0, 0, 0, 0);
                     if (real && c * 8 < dim) x = *reinterpret_cast<const uint4 *>(src + c * 8);
                     x.x ^= sign;
@@ -456,11 +544,11 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 }
                 fence_async_smem();
                 fence_before();
-                bar_arrive(q_full + w);
+                warp_arrive(q_full + w);
                 const int sees = attn_tile_keys(s, q, row_tile);
                 const int first = q.keys - q.n + row_tile * s.tile_tokens + 1;
-                limit = causal ? min(sees, first + r / s.tile_heads) : sees;
-                all_see = causal ? min(sees, first + w * kTile / s.tile_heads) : sees;
+                limit = (causal ? min(sees, first + r / s.tile_heads) : sees) - half * 64;
+                all_see = (causal ? min(sees, first + w * kTile / s.tile_heads) : sees) - half * 64;
             }
 
             float m = -INFINITY, l = 0.0f;
@@ -468,41 +556,51 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             for (int j = g.first; j < g.last; ++j) {
                 ok = bar_wait(s_full + w, s_uses++ & 1, gave_up);
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
                 fence_after();
-                uint32_t x[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_load32(x[c], s_at + c * 32);
+                uint32_t x[2][32];
+                tmem_load32(x[0], s_at + half * 64);
+                tmem_load32(x[1], s_at + half * 64 + 32);
                 tmem_wait_load();
                 const int key0 = j * kKeys;
-                if (key0 + kKeys > all_see) {
+                if (key0 + 64 > all_see) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (key0 + c * 32 + i >= limit) x[c][i] = 0xFF800000u;  // -inf
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 32; i += 2)
+                for (int i = 0; i < 32; i += 4)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        top[c] = max3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                        top[c] = max3(top[c], __uint_as_float(x[c / 2][i + c % 2 * 2]), __uint_as_float(x[c / 2][i + c % 2 * 2 + 1]));
                 const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-                if (j == g.first) {
-                    m = best;
-                } else if (__any_sync(0xFFFFFFFFu, best > m + kGrowth)) {
-                    const float to = best > m + kGrowth ? best : m;
+                fence_before();
+                // Past this barrier both halves have read their scores, and P may overwrite them.
+                if (tile_any(w, !ok || best > m + kGrowth)) {
+                    tmem_store1(mine, best);
+                    tmem_wait_store();
+                    fence_before();
+                    if (tile_any(w, !ok)) {  // a wait gave up: all threads of the tile leave here
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const float row_best = fmaxf(best, tmem_load1(theirs));
+                    const float to = row_best > m + kGrowth ? row_best : m;
                     const float f = exp2_approx(m - attn_base(to));
-                    l *= f;
                     m = to;
+                    l *= f;
+                    if (j > g.first) {
 #pragma unroll 1
-                    for (int c = 0; c < kDim / 16; ++c) tmem_scale16(o_at + c * 16, f);
+                        for (int c = 0; c < kDim / 32; ++c) tmem_scale16(o_at + c * 16, f);
+                    }
                 }
                 const float2 mul = make_float2(scale, scale), off = make_float2(-attn_base(m), -attn_base(m));
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -513,23 +611,23 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                         sum[i & 1] = pair_add<true>(sum[i & 1], y);
                         p[i] = pack_pair<T>(y.x, y.y);
                     }
-                    tmem_store16(s_at + c * 16, p);
-                    if (c == 1) {  // the first half of the values' product can start
-                        tmem_wait_store();
-                        fence_before();
-                        bar_arrive(p_half + w);
-                    }
+                    tmem_store16(s_at + half * 32 + c * 16, p);
                 }
                 tmem_wait_store();
                 fence_before();
-                bar_arrive(p_full + w);
+                warp_arrive(p_full + w);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!ok) break;
             ok = bar_wait(o_full + w, o_uses++ & 1, gave_up);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
             fence_after();
+            tmem_store1(mine, l);
+            tmem_wait_store();
+            fence_before();
+            if (tile_any(w, !ok)) break;
+            fence_after();
+            l += tmem_load1(theirs);
             int token, head;
             const bool real = attn_row(s, place.q.q0, place.q.n, place.cur.head, place.cur.row_tile, r, &token, &head);
             const bool whole = g.first == 0 && g.last == g.units;
@@ -537,9 +635,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             float *part = attn_slot(s, cta, g.first == 0 ? 1 : 0);
             T *dst = (T *)a.out + token * a.out_token_stride + head * a.out_head_stride;
 #pragma unroll 1
-            for (int c = 0; c < kDim / 32; ++c) {
+            for (int c = half * (kDim / 64); c < (half + 1) * (kDim / 64); ++c) {
                 uint32_t o[32];
-                tmem_load32(o, o_at + c * 32);
+                tmem_load32(o, o_at + c * 32 - half * (kDim / 2));
                 tmem_wait_load();
                 if (real && whole) {
 #pragma unroll
@@ -560,7 +658,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 __syncwarp();
             }
             fence_before();  // O is read before the next row tile's first product overwrites it
-            if (!whole && real) {
+            if (!whole && real && half == 0) {
                 part[kRows * dim + r] = m;
                 part[kRows * dim + kRows + r] = l;
             }
@@ -574,14 +672,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 j.q_len = place.q.n;
                 attn_joins(s, ctas)[cta] = j;
             }
-            more = next_segment(s, place, g.last - g.first);
+            more = next_tile_segment(s, place, g.last - g.first, w);
         }
     }
     __syncwarp();
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == 8)
+    if (warp == kMma)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
