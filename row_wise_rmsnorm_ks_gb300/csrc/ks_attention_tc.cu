@@ -4,9 +4,9 @@
 // A CTA works on a row tile of 256 query rows, two tiles of 128 that share every 128-key step of
 // the cache: S = Q K^T and O += P V are tcgen05.mma with S, P and O in tensor memory, which they
 // fill exactly (two 128-column S, over which P is written, two 128-column O). Twenty warps:
-//   warps 0-7, 8-15  softmax of tile 0 and 1, two threads a row (no shuffles): S to registers, running
-//                    maximum, exponentials, P back to tensor memory; at the end of a row tile O to the
-//                    output or the workspace;
+//   warps 0-7, 8-15  softmax of tile 0 and 1, 16 rows a warp: S to registers, running maximum,
+//                    exponentials, P back to tensor memory; at the end of a row tile O to the output or
+//                    the workspace;
 //   warps 16 and 18  issue the matrix instructions of tile 0 and 1: P V, then Q K(next), which
 //                    overwrites S and P behind it in order;
 //   warp 17          copies pages to shared memory by TMA, one lane per page and 64 columns;
@@ -30,7 +30,7 @@ namespace {
 constexpr int kTile = 128;         // rows of a matrix tile
 constexpr int kRows = 2 * kTile;   // rows of a row tile
 constexpr int kKeys = 128;         // keys of a step
-constexpr int kTileThreads = 2 * kTile;  // softmax threads of a tile: two a row, 64 keys each
+constexpr int kTileThreads = 2 * kTile;  // softmax threads of a tile: 16 rows a warp
 constexpr int kSoftmaxWarps = 2 * kTileThreads / 32, kThreads = 2 * kTileThreads + 128;
 constexpr int kMma = kSoftmaxWarps, kCopy = kMma + 1, kTail = kMma + 3;  // the other warps (kMma + 2: see there)
 // Registers: 640 threads launch with 96 each; the softmax warpgroups take 104 (64 scores a thread and
@@ -93,17 +93,28 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 #define KS_R4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
 #define KS_W4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
 
-// 32 columns of this warp's 32 lanes, a lane's row in one thread's registers.
-__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr) {
+// 16 rows of tensor memory: the quad lane / 4 has rows lane / 4 and lane / 4 + 8. Of every 8 columns a
+// lane has columns 2 (lane % 4) and the next of the first row, then those of the second. 64 columns.
+__device__ __forceinline__ void tmem_load_rows32(uint32_t (&r)[32], uint32_t addr) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : KS_W4(r, 0), KS_W4(r, 4), KS_W4(r, 8), KS_W4(r, 12), KS_W4(r, 16), KS_W4(r, 20), KS_W4(r, 24), KS_W4(r, 28)
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+// 32 columns.
+__device__ __forceinline__ void tmem_load_rows16(uint32_t (&r)[16], uint32_t addr) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : KS_W4(r, 0), KS_W4(r, 4), KS_W4(r, 8), KS_W4(r, 12)
+        : "r"(addr));
+}
+// 32 columns of two 16-bit values each: of every 4, a lane has column lane % 4 of both rows, which is
+// where the pairs it loaded belong.
+__device__ __forceinline__ void tmem_store_rows16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16};" ::"r"(addr),
         KS_R4(r, 0), KS_R4(r, 4), KS_R4(r, 8), KS_R4(r, 12)
         : "memory");
@@ -111,18 +122,18 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 16 columns of the lane's row times f, in place.
-__device__ __forceinline__ void tmem_scale16(uint32_t addr, float f) {
+// 32 columns of the lane's two rows times f and g, in place.
+__device__ __forceinline__ void tmem_scale_rows(uint32_t addr, float f, float g) {
     uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : KS_W4(r, 0), KS_W4(r, 4), KS_W4(r, 8), KS_W4(r, 12)
-        : "r"(addr));
+    tmem_load_rows16(r, addr);
     tmem_wait_load();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-    tmem_store16(addr, r);
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (i & 2 ? g : f));
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr),
+        KS_R4(r, 0), KS_R4(r, 4), KS_R4(r, 8), KS_R4(r, 12)
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int col, int slot, int head, int page,
@@ -189,31 +200,6 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
     return w;
 }
 
-__device__ __forceinline__ void tmem_store1(uint32_t addr, float v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(__float_as_uint(v)) : "memory");
-}
-__device__ __forceinline__ float tmem_load1(uint32_t addr) {
-    uint32_t v;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(addr));
-    tmem_wait_load();
-    return __uint_as_float(v);
-}
-
-// Barrier of the softmax threads of tile w, plain or telling whether any of them says yes.
-__device__ __forceinline__ void tile_sync(int w) {
-    asm volatile("bar.sync %0, %1;" ::"r"(w + 1), "n"(kTileThreads) : "memory");
-}
-__device__ __forceinline__ bool tile_any(int w, bool yes) {
-    uint32_t any;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, %3, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(any)
-        : "r"((uint32_t)yes), "r"(w + 1), "n"(kTileThreads)
-        : "memory");
-    return any != 0;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -269,14 +255,6 @@ __device__ __forceinline__ bool next_segment(const AttnArgs &s, Place &p, int st
     return p.cur.left > 0;
 }
 
-// The same for the softmax threads of tile w, which share a place.
-__device__ __forceinline__ bool next_tile_segment(const AttnArgs &s, Place &p, int steps, int w) {
-    tile_sync(w);
-    if (threadIdx.x % kTileThreads == 0) (void)next_segment<false>(s, p, steps);
-    tile_sync(w);
-    return p.cur.left > 0;
-}
-
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUtensorMap k_map,
@@ -328,17 +306,17 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     grid_dependency_wait();
     allow_dependents_launch();
     if (threadIdx.x == 0) attn_joins(s, ctas)[cta].pieces = 0;
-    __shared__ Place places[6];
-    Place &place = places[warp < kSoftmaxWarps ? warp / 8 : warp - kSoftmaxWarps + 2];
+    __shared__ Place places[kThreads / 32];
+    Place &place = places[warp];
     bool more;
     {
-        const AttnCursor c = attn_begin<kThreads>(s, cta, ctas);
+        const AttnCursor &c = attn_begin<kThreads>(s, cta, ctas);
         more = c.left > 0;
-        if (more && lane == 0 && (warp >= kSoftmaxWarps || warp % 8 == 0)) {
+        if (more && lane == 0) {
             place.cur = c;
             place.q = attn_seq(a, c.seq);
         }
-        __syncthreads();
+        __syncwarp();
     }
 
     if (warp >= kSoftmaxWarps) {
@@ -454,7 +432,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                     const uint32_t v_low = desc_low(ring + v_at.stage * C::kTileBytes, kHalfBytes);
                     mma_ts(o_at, s_at, v_low, pv, j > first);
 #pragma unroll
-                    for (int i = 1; i < kKeys / 16; ++i) mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
+                    for (int i = 1; i < kKeys / 16; ++i)
+                        mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
                     if (last) mma_commit(smem_addr(o_full + w));
                     else issue_qk(k_at.stage);
                     if (two) bar_arrive(turn + 1 - w);
@@ -502,32 +481,32 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        // ---- softmax: two threads a row, `half` having the first or last 64 keys of a step, and the first
-        // or last half of the output's columns
-        const int w = warp / 8, half = warp / 4 % 2, row = warp % 4 * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
-        const uint32_t s_at = tmem + lanes + w * 128, o_at = tmem + lanes + C::kO + w * 128 + half * (kDim / 2);
-        // One number goes to the row's other thread through a column of S that P leaves free.
-        const uint32_t mine = s_at + 126 + half, theirs = s_at + 127 - half;
+        // ---- softmax: a warp has 16 rows, a quad of lanes a row pair (r0, r0 + 8): the layout in which the
+        // 16-row loads of tensor memory hand out scores, so that maxima and sums need two shuffles and
+        // warps nothing of each other
+        const int w = warp / 8, sub = warp % 4 * 32 + warp / 4 % 2 * 16, quad = lane % 4;
+        const uint32_t s_at = tmem + ((uint32_t)sub << 16) + w * 128, o_at = s_at - w * 128 + C::kO + w * 128;
+        const int r0 = w * kTile + sub + lane / 4;
         const int dim = (int)a.head_dim;
         const bool causal = (a.flags & KS_ATTENTION_CAUSAL) != 0;
         // The products run with |scale|: a negative one turns the query's signs. 0 becomes the least
         // normal number, whose products with finite scores vanish and which leaves -inf as it is.
         const float scale = fmaxf(fabsf(s.scale_log2), 1.17549435e-38f);
         uint32_t s_uses = 0, o_uses = 0;
-        const int r = w * kTile + row;
         while (more) {
             const Segment g = segment(s, place.cur, place.q);
             if (w == 1 && !g.two) {
-                more = next_tile_segment(s, place, g.last - g.first, w);
+                more = next_segment(s, place, g.last - g.first);
                 continue;
             }
-            int limit, all_see;  // keys of a step's half that this thread's row sees, and all rows of the tile
+            int limit[2], all_see;  // keys that this thread's rows see, and all rows of the tile
             {
                 const AttnSeq q = place.q;
                 const int row_tile = place.cur.row_tile;
+                // the query: half a row per thread
+                const int row = threadIdx.x % kTile, half = threadIdx.x / kTile % 2;
                 int token, head;
-                const bool real = attn_row(s, q.q0, q.n, place.cur.head, row_tile, r, &token, &head);
+                const bool real = attn_row(s, q.q0, q.n, place.cur.head, row_tile, w * kTile + row, &token, &head);
                 const T *src = (const T *)a.q + token * a.q_token_stride + head * a.q_head_stride;
                 uint8_t *dst = smem + w * C::kTileBytes + row * 128;
                 const uint32_t sign = s.scale_log2 < 0.0f ? 0x80008000u : 0u;
@@ -547,57 +526,62 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 warp_arrive(q_full + w);
                 const int sees = attn_tile_keys(s, q, row_tile);
                 const int first = q.keys - q.n + row_tile * s.tile_tokens + 1;
-                limit = (causal ? min(sees, first + r / s.tile_heads) : sees) - half * 64;
-                all_see = (causal ? min(sees, first + w * kTile / s.tile_heads) : sees) - half * 64;
+                limit[0] = causal ? min(sees, first + r0 / s.tile_heads) : sees;
+                limit[1] = causal ? min(sees, first + (r0 + 8) / s.tile_heads) : sees;
+                all_see = causal ? min(sees, first + w * kTile / s.tile_heads) : sees;
             }
 
-            float m = -INFINITY, l = 0.0f;
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
             bool ok = true;
             for (int j = g.first; j < g.last; ++j) {
-                ok = bar_wait(s_full + w, s_uses++ & 1, gave_up);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                ok = bar_wait_warp(s_full + w, s_uses++ & 1, gave_up);
+                if (!ok) break;
                 fence_after();
-                uint32_t x[2][32];
-                tmem_load32(x[0], s_at + half * 64);
-                tmem_load32(x[1], s_at + half * 64 + 32);
+                uint32_t x[2][32];  // [64 keys][8 keys: two of each row, ...]
+                tmem_load_rows32(x[0], s_at);
+                tmem_load_rows32(x[1], s_at + 64);
                 tmem_wait_load();
                 const int key0 = j * kKeys;
-                if (key0 + 64 > all_see) {
+                if (key0 + kKeys > all_see) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (key0 + c * 32 + i >= limit) x[c][i] = 0xFF800000u;  // -inf
+                            if (key0 + c * 64 + i / 4 * 8 + quad * 2 + i % 2 >= limit[i / 2 % 2]) x[c][i] = 0xFF800000u;  // -inf
                 }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float top[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        top[c] = max3(top[c], __uint_as_float(x[c / 2][i + c % 2 * 2]), __uint_as_float(x[c / 2][i + c % 2 * 2 + 1]));
-                const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-                fence_before();
-                // Past this barrier both halves have read their scores, and P may overwrite them.
-                if (tile_any(w, !ok || best > m + kGrowth)) {
-                    tmem_store1(mine, best);
-                    tmem_wait_store();
-                    fence_before();
-                    if (tile_any(w, !ok)) {  // a wait gave up: all threads of the tile leave here
-                        ok = false;
-                        break;
+                    for (int c = 0; c < 2; ++c) {
+                        top[0][c] = max3(top[0][c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                        top[1][c] = max3(top[1][c], __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
                     }
-                    fence_after();
-                    const float row_best = fmaxf(best, tmem_load1(theirs));
-                    const float to = row_best > m + kGrowth ? row_best : m;
-                    const float f = exp2_approx(m - attn_base(to));
-                    m = to;
-                    l *= f;
-                    if (j > g.first) {
-#pragma unroll 1
-                        for (int c = 0; c < kDim / 32; ++c) tmem_scale16(o_at + c * 16, f);
-                    }
+                float best[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    best[i] = fmaxf(top[i][0], top[i][1]);
+                    best[i] = fmaxf(best[i], __shfl_xor_sync(0xFFFFFFFFu, best[i], 1));
+                    best[i] = fmaxf(best[i], __shfl_xor_sync(0xFFFFFFFFu, best[i], 2)) * scale;
                 }
-                const float2 mul = make_float2(scale, scale), off = make_float2(-attn_base(m), -attn_base(m));
+                if (j == g.first) {
+                    m[0] = best[0];
+                    m[1] = best[1];
+                } else if (__any_sync(0xFFFFFFFFu, best[0] > m[0] + kGrowth || best[1] > m[1] + kGrowth)) {
+                    float f[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float to = best[i] > m[i] + kGrowth ? best[i] : m[i];
+                        f[i] = exp2_approx(m[i] - attn_base(to));
+                        l[i] *= f[i];
+                        m[i] = to;
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < kDim / 32; ++c) tmem_scale_rows(o_at + c * 32, f[0], f[1]);
+                }
+                const float2 mul = make_float2(scale, scale);
+                const float2 off[2] = {make_float2(-attn_base(m[0]), -attn_base(m[0])),
+                                       make_float2(-attn_base(m[1]), -attn_base(m[1]))};
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -605,63 +589,62 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 y = make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
-                        y = pair_fma<true>(y, mul, off);
+                        y = pair_fma<true>(y, mul, off[i & 1]);
                         y.x = exp2_approx(y.x);
                         y.y = exp2_approx(y.y);
                         sum[i & 1] = pair_add<true>(sum[i & 1], y);
                         p[i] = pack_pair<T>(y.x, y.y);
                     }
-                    tmem_store16(s_at + half * 32 + c * 16, p);
+                    tmem_store_rows16(s_at + c * 32, p);
                 }
                 tmem_wait_store();
                 fence_before();
                 warp_arrive(p_full + w);
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                l[0] += sum[0].x + sum[0].y;
+                l[1] += sum[1].x + sum[1].y;
             }
             if (!ok) break;
-            ok = bar_wait(o_full + w, o_uses++ & 1, gave_up);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+            ok = bar_wait_warp(o_full + w, o_uses++ & 1, gave_up);
+            if (!ok) break;
             fence_after();
-            tmem_store1(mine, l);
-            tmem_wait_store();
-            fence_before();
-            if (tile_any(w, !ok)) break;
-            fence_after();
-            l += tmem_load1(theirs);
-            int token, head;
-            const bool real = attn_row(s, place.q.q0, place.q.n, place.cur.head, place.cur.row_tile, r, &token, &head);
             const bool whole = g.first == 0 && g.last == g.units;
-            const float inv = attn_inverse(l);
+            float inv[2];
+            T *dst[2];
+            bool real[2];
             float *part = attn_slot(s, cta, g.first == 0 ? 1 : 0);
-            T *dst = (T *)a.out + token * a.out_token_stride + head * a.out_head_stride;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+                inv[i] = attn_inverse(l[i]);
+                int token, head;
+                real[i] = attn_row(s, place.q.q0, place.q.n, place.cur.head, place.cur.row_tile, r0 + 8 * i, &token, &head);
+                dst[i] = (T *)a.out + token * a.out_token_stride + head * a.out_head_stride;
+            }
 #pragma unroll 1
-            for (int c = half * (kDim / 64); c < (half + 1) * (kDim / 64); ++c) {
-                uint32_t o[32];
-                tmem_load32(o, o_at + c * 32 - half * (kDim / 2));
+            for (int c = 0; c < kDim / 32; ++c) {
+                uint32_t o[16];
+                tmem_load_rows16(o, o_at + c * 32);
                 tmem_wait_load();
-                if (real && whole) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            y[k] = pack_pair<T>(__uint_as_float(o[i + 2 * k]) * inv, __uint_as_float(o[i + 2 * k + 1]) * inv);
-                        if (c * 32 + i < dim)
-                            *reinterpret_cast<uint4 *>(dst + c * 32 + i) = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-                } else if (real) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        if (c * 32 + i < dim)
-                            *reinterpret_cast<uint4 *>(part + r * dim + c * 32 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                for (int i = 0; i < 16; i += 2) {
+                    const int k = i / 2 % 2, col = c * 32 + i / 4 * 8 + quad * 2;
+                    if (!real[k] || col >= dim) continue;
+                    if (whole)
+                        *reinterpret_cast<uint32_t *>(dst[k] + col) =
+                            pack_pair<T>(__uint_as_float(o[i]) * inv[k], __uint_as_float(o[i + 1]) * inv[k]);
+                    else
+                        *reinterpret_cast<uint2 *>(part + (r0 + 8 * k) * dim + col) = make_uint2(o[i], o[i + 1]);
                 }
                 __syncwarp();
             }
             fence_before();  // O is read before the next row tile's first product overwrites it
-            if (!whole && real && half == 0) {
-                part[kRows * dim + r] = m;
-                part[kRows * dim + kRows + r] = l;
-            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (!whole && real[i] && quad == 0) {
+                    part[kRows * dim + r0 + 8 * i] = m[i];
+                    part[kRows * dim + kRows + r0 + 8 * i] = l[i];
+                }
             if (!whole && g.first == 0 && threadIdx.x == 0) {
                 AttnJoin j = {};
                 j.pieces = (int32_t)(attn_owner(place.cur, place.cur.at + g.units - 1) - cta + 1);
@@ -672,7 +655,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 j.q_len = place.q.n;
                 attn_joins(s, ctas)[cta] = j;
             }
-            more = next_tile_segment(s, place, g.last - g.first, w);
+            more = next_segment(s, place, g.last - g.first);
         }
     }
     __syncwarp();
