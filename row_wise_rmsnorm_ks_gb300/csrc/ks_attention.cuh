@@ -56,7 +56,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const ks_attention_args_t &a, int b)
 }
 
 // a / b for a, b >= 0: by 32 bits where they fit (a fifth of the time of the 64-bit routine).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+__device__ inline int64_t quotient(int64_t a, int64_t b) {
     if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
     return a / b;
 }

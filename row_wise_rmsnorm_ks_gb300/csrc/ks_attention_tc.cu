@@ -11,9 +11,10 @@
 //                    overwrites S and P behind it in order;
 //   warp 17          copies pages to shared memory by TMA, one lane per page and 64 columns;
 //   warp 19          clears value rows behind a sequence's last key.
-// While one tile is in its softmax, the matrix instructions of the other run. O is rescaled by the
-// softmax warps, and only when a row's maximum has grown by more than 2^8: until then the old maximum
-// stays the row's base, which changes nothing in the quotient and keeps P below 256.
+// While one tile is in its softmax, the matrix instructions of the other run. A row's base is the
+// maximum of the first scores it saw until later probabilities pass 2^14 (of which fp16 holds 65504):
+// only then is it raised and O scaled. The quotient does not depend on the base, and FP32 sums and
+// 16-bit probabilities keep their relative precision at any size.
 //
 // Bound by the tensor cores for long chunks (2 * 128 * 128 * 2 * dim operations a step and tile).
 // For few rows of a tile it is a stream of the cache like the 16-row kernel's.
@@ -37,7 +38,7 @@ constexpr int kMma = kSoftmaxWarps, kCopy = kMma + 1, kTail = kMma + 3;  // the 
 // their probabilities), the last keeps 64.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr int kHalfBytes = kKeys * 128;  // 128 rows of 64 values
-constexpr float kGrowth = 8.0f;    // log2 of how far a row's maximum may pass its base
+constexpr float kGrowth = 16384.0f;  // the most that a lane's probabilities to an old base may sum to
 
 template <int kDim>
 struct Tc {
@@ -198,12 +199,6 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
         memcpy(&w, &h, 4);
     }
     return w;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 
 // A place in the ring of tiles and the phase of its barriers there.
@@ -537,71 +532,74 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 ok = bar_wait_warp(s_full + w, s_uses++ & 1, gave_up);
                 if (!ok) break;
                 fence_after();
-                uint32_t x[2][32];  // [64 keys][8 keys: two of each row, ...]
-                tmem_load_rows32(x[0], s_at);
-                tmem_load_rows32(x[1], s_at + 64);
-                tmem_wait_load();
                 const int key0 = j * kKeys;
-                if (key0 + kKeys > all_see) {
+                uint32_t p[2][16];
+                float2 sum[2];
+                // The exponentials are taken to the rows' old base at once; their sums tell whether a score
+                // has outgrown it (a maximum over the scores would take as long as the exponentials). Then,
+                // and for the first step and rows that saw no key yet, the maxima are taken and the
+                // exponentials again: the scores are still in tensor memory.
+                bool rebase = __any_sync(0xFFFFFFFFu, m[0] == -INFINITY || m[1] == -INFINITY);
+                while (true) {
+                    uint32_t x[2][32];  // [64 keys][of 8 keys two of each row, ...]
+                    tmem_load_rows32(x[0], s_at);
+                    tmem_load_rows32(x[1], s_at + 64);
+                    tmem_wait_load();
+                    if (key0 + kKeys > all_see) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (key0 + c * 64 + i / 4 * 8 + quad * 2 + i % 2 >= limit[i / 2 % 2]) x[c][i] = 0xFF800000u;  // -inf
+                    }
+                    if (rebase) {
+                        float f[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float best = m[k];
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int i = 2 * k; i < 32; i += 4)
+                                    best = fmaxf(best, fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])) * scale);
+                            best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, 1));
+                            best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, 2));
+                            f[k] = exp2_approx(m[k] - attn_base(best));
+                            l[k] *= f[k];
+                            m[k] = best;
+                        }
+                        if (j > g.first) {
+#pragma unroll 1
+                            for (int c = 0; c < kDim / 32; ++c) tmem_scale_rows(o_at + c * 32, f[0], f[1]);
+                        }
+                    }
+                    const float2 mul = make_float2(scale, scale);
+                    const float2 off[2] = {make_float2(-attn_base(m[0]), -attn_base(m[0])),
+                                           make_float2(-attn_base(m[1]), -attn_base(m[1]))};
+                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (key0 + c * 64 + i / 4 * 8 + quad * 2 + i % 2 >= limit[i / 2 % 2]) x[c][i] = 0xFF800000u;  // -inf
+                        for (int i = 0; i < 16; ++i) {
+                            float2 y = make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
+                            y = pair_fma<true>(y, mul, off[i & 1]);
+                            y.x = exp2_approx(y.x);
+                            y.y = exp2_approx(y.y);
+                            sum[i & 1] = pair_add<true>(sum[i & 1], y);
+                            p[c][i] = pack_pair<T>(y.x, y.y);
+                        }
+                    sum[0].x += sum[0].y;
+                    sum[1].x += sum[1].y;
+                    if (rebase || !__any_sync(0xFFFFFFFFu, !(sum[0].x <= kGrowth && sum[1].x <= kGrowth))) break;
+                    rebase = true;
                 }
-                float top[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        top[0][c] = max3(top[0][c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-                        top[1][c] = max3(top[1][c], __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
-                    }
-                float best[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    best[i] = fmaxf(top[i][0], top[i][1]);
-                    best[i] = fmaxf(best[i], __shfl_xor_sync(0xFFFFFFFFu, best[i], 1));
-                    best[i] = fmaxf(best[i], __shfl_xor_sync(0xFFFFFFFFu, best[i], 2)) * scale;
-                }
-                if (j == g.first) {
-                    m[0] = best[0];
-                    m[1] = best[1];
-                } else if (__any_sync(0xFFFFFFFFu, best[0] > m[0] + kGrowth || best[1] > m[1] + kGrowth)) {
-                    float f[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float to = best[i] > m[i] + kGrowth ? best[i] : m[i];
-                        f[i] = exp2_approx(m[i] - attn_base(to));
-                        l[i] *= f[i];
-                        m[i] = to;
-                    }
-#pragma unroll 1
-                    for (int c = 0; c < kDim / 32; ++c) tmem_scale_rows(o_at + c * 32, f[0], f[1]);
-                }
-                const float2 mul = make_float2(scale, scale);
-                const float2 off[2] = {make_float2(-attn_base(m[0]), -attn_base(m[0])),
-                                       make_float2(-attn_base(m[1]), -attn_base(m[1]))};
-                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 y = make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
-                        y = pair_fma<true>(y, mul, off[i & 1]);
-                        y.x = exp2_approx(y.x);
-                        y.y = exp2_approx(y.y);
-                        sum[i & 1] = pair_add<true>(sum[i & 1], y);
-                        p[i] = pack_pair<T>(y.x, y.y);
-                    }
-                    tmem_store_rows16(s_at + c * 32, p);
-                }
+                tmem_store_rows16(s_at, p[0]);
+                tmem_store_rows16(s_at + 32, p[1]);
                 tmem_wait_store();
                 fence_before();
                 warp_arrive(p_full + w);
-                l[0] += sum[0].x + sum[0].y;
-                l[1] += sum[1].x + sum[1].y;
+                l[0] += sum[0].x;
+                l[1] += sum[1].x;
             }
             if (!ok) break;
             ok = bar_wait_warp(o_full + w, o_uses++ & 1, gave_up);
