@@ -19,7 +19,7 @@ namespace {
 constexpr int kRows = 16;                 // rows of a tile: one mma.m16n8k16 tile
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kSub = 16;                  // keys of a warp's step
-constexpr int kUnit = kWarps * kSub;      // keys of a unit: a step of each warp
+constexpr int kUnit = kWarps * kSub;      // keys of a unit: a step of each warp (a power of two)
 
 // Few rows make this a stream of the cache: per key of 128 values 512 bytes, 16 query rows cost
 // two 16x8x16 matrix instructions, a tenth of the time its bytes take. Each warp therefore runs
@@ -437,7 +437,9 @@ void attn_plan(const ks_attention_args_t &a, bool tc, int sms, AttnPlan *p) {
     p->s.group = (int32_t)(a.q_heads / a.kv_heads);
     p->s.scale_log2 = a.scale * 1.4426950408889634f;
     p->s.rows = tc ? attn_tc_rows() : kRows;
-    p->s.unit = tc ? attn_tc_unit() : kUnit;
+    const int unit = tc ? attn_tc_unit() : kUnit;
+    p->s.unit_shift = 0;
+    while (1 << p->s.unit_shift < unit) ++p->s.unit_shift;
     int per_sm = 1;
     p->smem = 0;
     p->kernel = nullptr;
@@ -448,7 +450,7 @@ void attn_plan(const ks_attention_args_t &a, bool tc, int sms, AttnPlan *p) {
     p->s.tile_tokens = p->s.head_splits > 1 ? 1 : p->s.rows / p->s.tile_heads;
     // No more CTAs than the call can have units.
     const int64_t tiles = ceil_to(a.tokens, p->s.tile_tokens) + a.seqs;
-    const int64_t tile_units = ceil_to(a.table_pages * a.page_size, p->s.unit) + 1;
+    const int64_t tile_units = ceil_to(a.table_pages * a.page_size, unit) + 1;
     const int64_t heads = a.kv_heads * p->s.head_splits;
     int64_t ctas = (int64_t)sms * per_sm;
     if (tile_units < ctas && tiles < ctas && heads < ctas && tile_units * tiles * heads < ctas)

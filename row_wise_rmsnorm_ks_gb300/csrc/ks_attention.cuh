@@ -22,7 +22,7 @@ struct AttnArgs {
     int32_t tile_heads;  // heads of a group in a row tile
     int32_t head_splits; // row tiles a token's group is cut into (1 unless group > M)
     int32_t tile_tokens; // tokens in a row tile
-    int32_t unit;        // keys per unit (TN)
+    int32_t unit_shift;  // log2 of the keys per unit (TN)
     int32_t rows;        // rows of a tile (M)
     float scale_log2;    // scale * log2(e)
 };
@@ -61,30 +61,36 @@ __device__ inline int64_t quotient(int64_t a, int64_t b) {
     return a / b;
 }
 
-// sum over i in [0, n) of floor((a i + b) / m), for m > 0 and a n + b below 2^32: the whole multiples
-// of m in a and b sum in closed form; for what is left (a, b < m), the points under the line are
-// counted along the other axis, which is the same sum with a and m changed over.
-__device__ inline int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-    int64_t total = 0;
-    while (n > 0) {
+// sum over i in [0, n) of floor((a i + b) / 2^shift), for a n + b below 2^32: the whole multiples of the
+// divisor in a and b sum in closed form; for what is left, the points under the line are counted along
+// the other axis, which is the same sum with a and the divisor changed over.
+__device__ inline int64_t floor_sum(uint32_t n, int shift, uint32_t a, uint32_t b) {
+    uint32_t m = 1u << shift;
+    int64_t total = (int64_t)(a >> shift) * ((int64_t)n * (n - 1) / 2) + (int64_t)(b >> shift) * n;
+    a &= m - 1;
+    b &= m - 1;
+    uint32_t top = a * n + b;  // m times the line's height at n
+    if (top < m) return total;
+    n = top >> shift;
+    b = top & (m - 1);
+    while (true) {
+        const uint32_t t = a;  // axes changed over
+        a = m;
+        m = t;
         const uint32_t qa = a / m, qb = b / m;
         total += (int64_t)qa * ((int64_t)n * (n - 1) / 2) + (int64_t)qb * n;
         a -= qa * m;
         b -= qb * m;
-        const uint32_t top = a * n + b;  // m times the line's height at n
-        if (top < m) break;
+        top = a * n + b;
+        if (top < m) return total;
         n = top / m;
         b = top - n * m;
-        const uint32_t t = a;
-        a = m;
-        m = t;
     }
-    return total;
 }
 
 // Row tiles of a sequence for one head (head splits aside).
 __device__ __forceinline__ int attn_row_tiles(const AttnArgs &s, const AttnSeq &q) {
-    return (q.n + s.tile_tokens - 1) / s.tile_tokens;
+    return q.n <= s.tile_tokens ? q.n > 0 : (q.n + s.tile_tokens - 1) / s.tile_tokens;
 }
 
 // Keys that the last token of row tile `rt` sees (the most any row of it sees), 0 if none.
@@ -96,14 +102,13 @@ __device__ __forceinline__ int attn_tile_keys(const AttnArgs &s, const AttnSeq &
 
 // Units of row tile `rt`: at least one, so that a tile that sees nothing still writes its zeros.
 __device__ __forceinline__ int attn_tile_units(const AttnArgs &s, const AttnSeq &q, int rt) {
-    return max(1, (attn_tile_keys(s, q, rt) + s.unit - 1) / s.unit);
+    return max(1, (int)(((uint32_t)attn_tile_keys(s, q, rt) + (1u << s.unit_shift) - 1) >> s.unit_shift));
 }
 
-// Units of the row tiles [0, k) of one head.
-__device__ inline int64_t attn_units_before(const AttnArgs &s, const AttnSeq &q, int k) {
+// Units of the row tiles [0, k) of one head, of `tiles` in all.
+__device__ __forceinline__ int64_t attn_units_before(const AttnArgs &s, const AttnSeq &q, int tiles, int k) {
     if (k <= 0) return 0;
     if (k == 1) return attn_tile_units(s, q, 0);
-    const int tiles = attn_row_tiles(s, q);
     if (!(s.a.flags & KS_ATTENTION_CAUSAL)) return (int64_t)k * attn_tile_units(s, q, 0);
     int64_t total = 0;
     if (k == tiles) {  // the last tile is cut off at the last token: by itself
@@ -111,11 +116,12 @@ __device__ inline int64_t attn_units_before(const AttnArgs &s, const AttnSeq &q,
         --k;
     }
     // tile i < tiles - 1 sees past + (i + 1) tile_tokens keys; up to one unit of them counts as one
-    const int64_t past = (int64_t)q.keys - q.n, tt = s.tile_tokens, un = s.unit;
-    int64_t one = past >= un ? 0 : quotient(un - past, tt);  // tiles i with past + (i + 1) tt <= un
-    one = min(one, (int64_t)k);
-    return total + one + floor_sum((uint32_t)(k - one), (uint32_t)un, (uint32_t)tt,
-                                   (uint32_t)(past + (one + 1) * tt + un - 1));
+    const int past = q.keys - q.n, tt = s.tile_tokens, un = 1 << s.unit_shift;
+    int one = 0;  // tiles i with past + (i + 1) tt <= un
+    if (past < un) one = (int)min((uint32_t)k, ((uint32_t)un - (uint32_t)past) / (uint32_t)tt);
+    if (one == k) return total + k;
+    return total + one + floor_sum((uint32_t)(k - one), s.unit_shift, (uint32_t)tt,
+                                   (uint32_t)(past + (one + 1) * (int64_t)tt + un - 1));
 }
 
 // A CTA's place in the call's units.
@@ -134,82 +140,92 @@ __device__ __forceinline__ int64_t attn_owner(const AttnCursor &c, int64_t u) {
 
 // Finds the CTA's first unit: the sequences' units are summed by the block (a contiguous run of
 // sequences per thread, a scan over the threads), the thread whose run holds the CTA's first unit
-// walks it, and one warp then searches the sequence's row tiles, 32 places at a time. All threads of
-// the block call it; kThreads a multiple of 32, at most 1024. The result is in shared memory.
+// names its sequence, and one warp searches that sequence's row tiles, 32 places at a time. All threads
+// of the block call it; kThreads a multiple of 32, at most 1024. The result is in shared memory.
+// It is one chain of latencies (2 to 3 us, most of it fetching code that no cache holds yet), which is
+// why it divides by shifts where it can and computes nothing twice.
 template <int kThreads>
 __device__ inline const AttnCursor &attn_begin(const AttnArgs &s, int cta, int ctas) {
-    __shared__ int64_t warp_units[kThreads / 32];
-    __shared__ int32_t found_seq;
-    __shared__ int64_t found_before;
+    constexpr int kWarps = kThreads / 32;
+    __shared__ int64_t warp_units[kWarps];
+    __shared__ int64_t found_before, found_per_head;
     __shared__ AttnCursor result;
-    const int t = threadIdx.x, seqs = (int)s.a.seqs;
-    const int per = (seqs + kThreads - 1) / kThreads;
-    const int64_t heads = s.a.kv_heads * s.head_splits;
+    const int t = threadIdx.x, lane = t & 31, seqs = (int)s.a.seqs;
+    const int per = seqs <= kThreads ? 1 : (seqs + kThreads - 1) / kThreads;
+    const int64_t heads = (int64_t)s.a.kv_heads * s.head_splits;
     const int lo = min(seqs, t * per), hi = min(seqs, lo + per);
-    int64_t mine = 0;
+    int64_t mine = 0, per_head = 0;
     for (int b = lo; b < hi; ++b) {
         const AttnSeq q = attn_seq(s.a, b);
-        mine += heads * attn_units_before(s, q, attn_row_tiles(s, q));
+        const int tiles = attn_row_tiles(s, q);
+        per_head = attn_units_before(s, q, tiles, tiles);
+        mine += heads * per_head;
     }
     int64_t upto = mine;
-    const int lane = t & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
         if (lane >= o) upto += v;
     }
     if (lane == 31) warp_units[t / 32] = upto;
-    if (t == 0) found_seq = -1;
     __syncthreads();
-    int64_t units = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w == t / 32) upto += units;
-        units += warp_units[w];
+    int64_t sums = lane < kWarps ? warp_units[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sums, o);
+        if (lane >= o) sums += v;
     }
     AttnCursor c = {};
-    c.units = units;
+    c.units = __shfl_sync(0xFFFFFFFFu, sums, kWarps - 1);
+    const int64_t warps_before = __shfl_sync(0xFFFFFFFFu, sums, max(t / 32 - 1, 0));
+    if (t >= 32) upto += warps_before;
     // with fewer units than CTAs, the first CTAs take one each: a row tile's pieces are then always
     // those of consecutive CTAs
-    c.ctas = (int32_t)min((int64_t)ctas, units);
-    if (cta < c.ctas) {
-        c.at = quotient(units * cta, c.ctas);
-        c.left = quotient(units * (cta + 1), c.ctas) - c.at;
+    c.ctas = (int32_t)min((int64_t)ctas, c.units);
+    if (cta >= c.ctas) {  // the whole block
+        if (t == 0) result = c;
+        __syncthreads();
+        return result;
     }
+    c.at = quotient(c.units * cta, c.ctas);
+    c.left = quotient(c.units * (cta + 1), c.ctas) - c.at;
     int64_t before = upto - mine;
-    if (c.left > 0 && before <= c.at && c.at < upto) {
-        for (int b = lo; b < hi; ++b) {
+    if (before <= c.at && c.at < upto) {  // one thread, since some sequence has the unit
+        c.seq = lo;
+        for (int b = lo; per > 1; ++b) {
             const AttnSeq q = attn_seq(s.a, b);
-            const int64_t n = heads * attn_units_before(s, q, attn_row_tiles(s, q));
-            if (c.at < before + n) {
-                found_seq = b;
-                found_before = before;
-                break;
-            }
-            before += n;
+            const int tiles = attn_row_tiles(s, q);
+            per_head = attn_units_before(s, q, tiles, tiles);
+            c.seq = b;
+            if (c.at < before + heads * per_head) break;
+            before += heads * per_head;
         }
+        result = c;
+        found_before = before;
+        found_per_head = per_head;
     }
     __syncthreads();
     if (t < 32) {
-        if (found_seq < 0) c.left = 0;
-        if (c.left > 0) {
-            c.seq = found_seq;
-            const AttnSeq q = attn_seq(s.a, c.seq);
-            int low = 0, size = attn_row_tiles(s, q);  // the wanted tile is one of size from low on
-            const int64_t per_head = attn_units_before(s, q, size);
-            int64_t u = c.at - found_before;
-            c.head = (int32_t)quotient(u, per_head);
-            u -= c.head * per_head;
-            while (size > 1) {  // the last tile that begins at or before u
-                const int step = (size + 31) / 32;
-                const bool yes = lane * step < size && attn_units_before(s, q, low + lane * step) <= u;
-                const int place = __popc(__ballot_sync(0xFFFFFFFFu, yes)) - 1;
-                low += place * step;
-                size = min(step, size - place * step);
-            }
-            c.row_tile = low;
-            c.unit = (int32_t)(u - attn_units_before(s, q, low));
+        const AttnSeq q = attn_seq(s.a, result.seq);
+        const int tiles = attn_row_tiles(s, q);
+        const int64_t begin = c.at - found_before;
+        const int head = (int)quotient(begin, found_per_head);
+        const int64_t u = begin - head * found_per_head;
+        int low = 0, size = tiles;  // the wanted tile, the last that begins at or before u, is one of size from low on
+        int64_t begins = 0;         // units before `low`
+        while (size > 1) {
+            const int step = (size + 31) >> 5;
+            const int64_t mine_begins = lane * step < size ? attn_units_before(s, q, tiles, low + lane * step) : u + 1;
+            const int place = __popc(__ballot_sync(0xFFFFFFFFu, mine_begins <= u)) - 1;
+            begins = __shfl_sync(0xFFFFFFFFu, mine_begins, place);
+            low += place * step;
+            size = min(step, size - place * step);
         }
-        if (lane == 0) result = c;
+        if (lane == 0) {
+            result.head = head;
+            result.row_tile = low;
+            result.unit = (int32_t)(u - begins);
+        }
     }
     __syncthreads();
     return result;

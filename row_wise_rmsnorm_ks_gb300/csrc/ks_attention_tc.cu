@@ -156,13 +156,23 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     if (threadIdx.x % 32 == 0) bar_arrive(bar);
 }
 
+// One try that may sleep up to 20 us: warps that wait take no issue slots from those that compute.
+__device__ __forceinline__ bool bar_sleep(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return done != 0;
+}
+
 // Waits for phase `parity`; false when the wait's limit passed or another role gave up. The role
 // then leaves its loop: everybody meets at the kernel's end, with the fault word set.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up) {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!bar_sleep(bar, parity)) {
         if (*gave_up) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             atomicOr(&g_fault_flags, kFaultWaitTimeout);
