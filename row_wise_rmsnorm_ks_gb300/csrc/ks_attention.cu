@@ -308,34 +308,38 @@ attn_rows16_kernel(const __grid_constant__ AttnArgs s) {
         __syncthreads();
         const bool whole = first == 0 && last == units;
         float *part = attn_slot(s, cta, first == 0 ? 1 : 0);
-        for (int i = threadIdx.x; i < kRows * (kDim / 4); i += kThreads) {
-            const int r = i / (kDim / 4), c = (i % (kDim / 4)) * 4;
-            if (c >= dim) continue;
-            float mm = -INFINITY, ll = 0.0f, acc[4] = {};
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mw[w * kRows + r]);
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2_approx(mw[w * kRows + r] - attn_base(mm));
-                ll += f * mw[(kWarps + w) * kRows + r];
-                const float4 x = *reinterpret_cast<const float4 *>(ow + (w * kRows + r) * kPitch + c);
-                acc[0] += f * x.x;
-                acc[1] += f * x.y;
-                acc[2] += f * x.z;
-                acc[3] += f * x.w;
-            }
-            if (whole) {
-                int token, head;
-                if (attn_row(s, q.q0, q.n, cur.head, cur.row_tile, r, &token, &head)) {
-                    const float inv = attn_inverse(ll);
-                    uint2 y = make_uint2(pack16<T>(acc[0] * inv, acc[1] * inv), pack16<T>(acc[2] * inv, acc[3] * inv));
-                    *reinterpret_cast<uint2 *>((T *)a.out + token * a.out_token_stride + head * a.out_head_stride + c) = y;
+        for (int g = warp; g < chunks; g += kWarps) {  // 8 columns
+            float ll[2], mm[2], acc[4];
+            const float *src = ow + (lane / 4) * kPitch + g * 8 + (lane % 4) * 2;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = lane / 4 + 8 * k;
+                mm[k] = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mm[k] = fmaxf(mm[k], mw[w * kRows + r]);
+                ll[k] = acc[2 * k] = acc[2 * k + 1] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = exp2_approx(mw[w * kRows + r] - attn_base(mm[k]));
+                    const float2 x = *reinterpret_cast<const float2 *>(src + (w * kRows + 8 * k) * kPitch);
+                    ll[k] += f * mw[(kWarps + w) * kRows + r];
+                    acc[2 * k] += f * x.x;
+                    acc[2 * k + 1] += f * x.y;
                 }
-            } else {
-                // 8-byte stores: the slots are only known to begin on 8 bytes
-                *reinterpret_cast<float2 *>(part + r * dim + c) = make_float2(acc[0], acc[1]);
-                *reinterpret_cast<float2 *>(part + r * dim + c + 2) = make_float2(acc[2], acc[3]);
-                if (c == 0) {
-                    part[kRows * dim + r] = mm;
-                    part[kRows * dim + kRows + r] = ll;
+            }
+            if (!whole) *attn_part(s, part, 0, g, lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = lane / 4 + 8 * k;
+                int token, head;
+                if (whole && attn_row(s, q.q0, q.n, cur.head, cur.row_tile, r, &token, &head)) {
+                    const float inv = attn_inverse(ll[k]);
+                    *reinterpret_cast<uint32_t *>((T *)a.out + token * a.out_token_stride + head * a.out_head_stride +
+                                                  g * 8 + lane % 4 * 2) = pack16<T>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+                }
+                if (!whole && g == 0 && lane % 4 == 0) {
+                    part[kRows * dim + r] = mm[k];
+                    part[kRows * dim + kRows + r] = ll[k];
                 }
             }
         }
@@ -357,41 +361,92 @@ attn_rows16_kernel(const __grid_constant__ AttnArgs s) {
     }
 }
 
-// Joins the row tiles that several CTAs shared: block (c, y) takes rows y, y + gridDim.y, ... of
-// the tile that CTA c began. The pieces are added in the order of their keys.
+// A piece of a row, its output to base pm and its sum, added to what there is.
+__device__ __forceinline__ void attn_add(float &m, float &l, float &x, float &y, float pm, float pl, float px, float py) {
+    const float top = fmaxf(m, pm), base = attn_base(top);
+    const float f = exp2_approx(m - base), g = exp2_approx(pm - base);
+    m = top;
+    l = l * f + pl * g;
+    x = x * f + px * g;
+    y = y * f + py * g;
+}
+
+// Joins the row tiles that several CTAs shared: blocks (c, y) take the tile that CTA c began, a warp 16
+// rows and 8 columns at a time, a lane two columns of two rows. Where there are many pieces the block's
+// warps share them out; either way the pieces are added in one fixed order. It is a chain of two loads,
+// so each warp has four pieces in flight.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
 attn_join_kernel(const __grid_constant__ AttnArgs s, int ctas) {
+    constexpr int kJoinWarps = kJoinThreads / 32;
+    __shared__ float shared[kJoinWarps][32][8];  // outputs, maxima and sums of a warp's share
     grid_dependency_wait();
     allow_dependents_launch();
     const ks_attention_args_t &a = s.a;
-    const int c = blockIdx.x, dim = (int)a.head_dim;
+    const int c = blockIdx.x, dim = (int)a.head_dim, groups = dim / 8;
     const AttnJoin j = attn_joins(s, ctas)[c];
     if (j.pieces <= 0) return;
-    const int quads = dim / 4, per = kJoinThreads / quads;  // rows a block handles at once
-    const int col = (threadIdx.x % quads) * 4, sub = threadIdx.x / quads;
-    if (sub >= per) return;
-    for (int r = blockIdx.y * per + sub; r < s.rows; r += gridDim.y * per) {
-        int token, head;
-        if (!attn_row(s, j.q0, j.q_len, j.head, j.row_tile, r, &token, &head)) continue;
-        float mm = -INFINITY, ll = 0.0f, acc[4] = {};
-        for (int i = 0; i < j.pieces; ++i) {
-            const float *part = attn_slot(s, c + i, i == 0 ? 1 : 0);
-            const float pm = part[s.rows * dim + r], pl = part[s.rows * dim + s.rows + r];
-            const float2 x = *reinterpret_cast<const float2 *>(part + r * dim + col);
-            const float2 y = *reinterpret_cast<const float2 *>(part + r * dim + col + 2);
-            const float top = fmaxf(mm, pm), base = attn_base(top);
-            const float f = exp2_approx(mm - base), g = exp2_approx(pm - base);
-            mm = top;
-            ll = ll * f + pl * g;
-            acc[0] = acc[0] * f + x.x * g;
-            acc[1] = acc[1] * f + x.y * g;
-            acc[2] = acc[2] * f + y.x * g;
-            acc[3] = acc[3] * f + y.y * g;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    int shares = 1;  // warps that share the pieces of one item
+    while (shares < kJoinWarps && shares * 4 < j.pieces) shares *= 2;
+    const int share = warp % shares, at_once = kJoinWarps / shares;
+    const int rows = min(s.tile_tokens, j.q_len - j.row_tile * s.tile_tokens) * s.tile_heads;
+    const int items = (rows + 15) / 16 * groups;
+    for (int first = blockIdx.y * at_once; first < items; first += gridDim.y * at_once) {
+        const int item = first + warp / shares, group = item / groups, col = item % groups;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, acc[4] = {};
+        if (item < items) {
+            const int r = group * 16 + lane / 4;
+            for (int i0 = share; i0 < j.pieces; i0 += 4 * shares) {
+                float4 x[4];
+                float pm[4][2], pl[4][2];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + u * shares;
+                    if (i >= j.pieces) continue;
+                    float *part = attn_slot(s, c + i, i == 0 ? 1 : 0);
+                    x[u] = *attn_part(s, part, group, col, lane);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        pm[u][k] = part[s.rows * dim + r + 8 * k];
+                        pl[u][k] = part[s.rows * dim + s.rows + r + 8 * k];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (i0 + u * shares >= j.pieces) continue;
+                    const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) attn_add(m[k], l[k], acc[2 * k], acc[2 * k + 1], pm[u][k], pl[u][k], v[2 * k], v[2 * k + 1]);
+                }
+            }
         }
-        const float inv = attn_inverse(ll);
-        const uint2 y = make_uint2(pack16<T>(acc[0] * inv, acc[1] * inv), pack16<T>(acc[2] * inv, acc[3] * inv));
-        *reinterpret_cast<uint2 *>((T *)a.out + token * a.out_token_stride + head * a.out_head_stride + col) = y;
+        if (shares > 1) {
+            float *mine = shared[warp][lane];
+            for (int k = 0; k < 4; ++k) mine[k] = acc[k];
+            for (int k = 0; k < 2; ++k) {
+                mine[4 + k] = m[k];
+                mine[6 + k] = l[k];
+            }
+            __syncthreads();
+            if (share == 0)
+                for (int w = 1; w < shares; ++w) {
+                    const float *other = shared[warp + w][lane];
+                    for (int k = 0; k < 2; ++k)
+                        attn_add(m[k], l[k], acc[2 * k], acc[2 * k + 1], other[4 + k], other[6 + k], other[2 * k], other[2 * k + 1]);
+                }
+            __syncthreads();
+        }
+        if (share == 0 && item < items) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                int token, head;
+                if (!attn_row(s, j.q0, j.q_len, j.head, j.row_tile, group * 16 + lane / 4 + 8 * k, &token, &head)) continue;
+                const float inv = attn_inverse(l[k]);
+                *reinterpret_cast<uint32_t *>((T *)a.out + token * a.out_token_stride + head * a.out_head_stride + col * 8 +
+                                              lane % 4 * 2) = pack16<T>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+            }
+        }
     }
 }
 
@@ -577,13 +632,13 @@ ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stre
     }
     if (ce == cudaSuccess && p.ctas > 1) {
         // The join is scheduled while the last CTAs finish and waits for them on the device.
-        const int per = kJoinThreads / (int)(args->head_dim / 4);
         void *jp[] = {&p.s, &p.ctas};
         const void *f = args->dtype == KS_DTYPE_BF16 ? (const void *)attn_join_kernel<__nv_bfloat16>
                                                      : (const void *)attn_join_kernel<__half>;
-        const int row_blocks = (p.s.rows + per - 1) / per;
-        ce = launch_kernel(f, dim3((unsigned)p.ctas, (unsigned)(row_blocks < 16 ? row_blocks : 16)), dim3(kJoinThreads), 0,
-                           jp, s, true);
+        // a warp or two for each of a tile's items, without more blocks than start quickly
+        const int items = p.s.rows / 16 * (int)(args->head_dim / 8);
+        ce = launch_kernel(f, dim3((unsigned)p.ctas, (unsigned)(items / 4 < 1 ? 1 : items / 4 < 16 ? items / 4 : 16)),
+                           dim3(kJoinThreads), 0, jp, s, true);
     }
     if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));
     return KS_SUCCESS;

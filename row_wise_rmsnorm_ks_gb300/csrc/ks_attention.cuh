@@ -255,8 +255,10 @@ __device__ __forceinline__ bool attn_row(const AttnArgs &s, int q0, int n, int h
     return i < s.tile_tokens && in_seq < n && g < s.group;
 }
 
-// Workspace: per CTA two slots of rows * (dim + 2) floats (outputs, maxima, sums), then an
-// AttnJoin per CTA.
+// Workspace: per CTA two slots of rows * (dim + 2) floats (outputs, maxima, sums), then an AttnJoin per
+// CTA. Outputs lie as the matrix instructions hand them out, so that a warp reads and writes 512 bytes
+// in a row: by 16 rows and 8 columns, then four floats a lane, columns 2 (lane % 4) and the next of row
+// lane / 4, then of row lane / 4 + 8.
 __host__ __device__ inline int64_t attn_slot_floats(int64_t rows, int64_t dim) {
     return rows * (dim + 2);
 }
@@ -280,6 +282,10 @@ __device__ __forceinline__ float attn_inverse(float l) { return l == 0.0f ? 0.0f
 
 // A maximum that can be subtracted: of a row that saw nothing yet, 0.
 __device__ __forceinline__ float attn_base(float m) { return m == -INFINITY ? 0.0f : m; }
+
+__device__ __forceinline__ float4 *attn_part(const AttnArgs &s, float *slot, int row_group, int col_group, int lane) {
+    return reinterpret_cast<float4 *>(slot) + (row_group * ((int)s.a.head_dim / 8) + col_group) * 32 + lane;
+}
 
 // The tensor-core kernel (ks_attention_tc.cu): whether it takes a call's sizes, and its strides too,
 // the rows and keys of its tiles, and its launch.

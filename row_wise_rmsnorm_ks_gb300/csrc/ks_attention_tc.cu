@@ -504,7 +504,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 more = next_segment(s, place, g.last - g.first);
                 continue;
             }
-            int limit[2], all_see;  // keys that this thread's rows see, and all rows of the tile
+            int limit[2], all_see;  // keys that this thread's rows see, and all rows of the warp
             {
                 const AttnSeq q = place.q;
                 const int row_tile = place.cur.row_tile;
@@ -533,7 +533,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 const int first = q.keys - q.n + row_tile * s.tile_tokens + 1;
                 limit[0] = causal ? min(sees, first + r0 / s.tile_heads) : sees;
                 limit[1] = causal ? min(sees, first + (r0 + 8) / s.tile_heads) : sees;
-                all_see = causal ? min(sees, first + w * kTile / s.tile_heads) : sees;
+                all_see = causal ? min(sees, first + (w * kTile + sub) / s.tile_heads) : sees;
             }
 
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
@@ -557,10 +557,12 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                     tmem_wait_load();
                     if (key0 + kKeys > all_see) {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                        for (int g8 = 0; g8 < kKeys / 8; ++g8) {
+                            if (key0 + g8 * 8 + 8 <= all_see) continue;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (key0 + c * 64 + i / 4 * 8 + quad * 2 + i % 2 >= limit[i / 2 % 2]) x[c][i] = 0xFF800000u;  // -inf
+                            for (int i = 0; i < 4; ++i)
+                                if (key0 + g8 * 8 + quad * 2 + i % 2 >= limit[i / 2]) x[g8 / 8][g8 % 8 * 4 + i] = 0xFF800000u;  // -inf
+                        }
                     }
                     if (rebase) {
                         float f[2];
@@ -635,21 +637,27 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 tmem_load_rows16(o, o_at + c * 32);
                 tmem_wait_load();
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const int k = i / 2 % 2, col = c * 32 + i / 4 * 8 + quad * 2;
-                    if (!real[k] || col >= dim) continue;
-                    if (whole)
-                        *reinterpret_cast<uint32_t *>(dst[k] + col) =
-                            pack_pair<T>(__uint_as_float(o[i]) * inv[k], __uint_as_float(o[i + 1]) * inv[k]);
-                    else
-                        *reinterpret_cast<uint2 *>(part + (r0 + 8 * k) * dim + col) = make_uint2(o[i], o[i + 1]);
+                for (int i = 0; i < 16; i += 4) {
+                    const int col = c * 32 + i * 2;  // of the group's 8
+                    if (col >= dim) continue;
+                    if (!whole) {
+                        *attn_part(s, part, r0 / 16, col / 8, lane) =
+                            make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                        __uint_as_float(o[i + 3]));
+                        continue;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (real[k])
+                            *reinterpret_cast<uint32_t *>(dst[k] + col + quad * 2) =
+                                pack_pair<T>(__uint_as_float(o[i + 2 * k]) * inv[k], __uint_as_float(o[i + 2 * k + 1]) * inv[k]);
                 }
                 __syncwarp();
             }
             fence_before();  // O is read before the next row tile's first product overwrites it
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (!whole && real[i] && quad == 0) {
+                if (!whole && quad == 0) {
                     part[kRows * dim + r0 + 8 * i] = m[i];
                     part[kRows * dim + kRows + r0 + 8 * i] = l[i];
                 }
