@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kRows = 16;                 // rows of a tile: one mma.m16n8k16 tile
 constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kTileCost = 2;              // units that beginning and ending a row tile costs
 constexpr int kSub = 16;                  // keys of a warp's step
 constexpr int kUnit = kWarps * kSub;      // keys of a unit: a step of each warp (a power of two)
 
@@ -120,8 +121,9 @@ attn_rows16_kernel(const __grid_constant__ AttnArgs s) {
     const int page_size = (int)a.page_size;
 
     while (true) {
-        const int units = attn_tile_units(s, q, cur.row_tile);
-        const int first = cur.unit, last = (int)min((int64_t)units, first + cur.left);
+        const AttnSpan span = attn_span(s, cur, q);
+        const int units = span.units, first = span.first, last = span.last;
+        if (first >= last) break;  // the share ends in the tile's extra cost
         const int sees = attn_tile_keys(s, q, cur.row_tile);
         const int kv_head = cur.head / s.head_splits;
         const T *k_base = (const T *)a.k_pages + kv_head * a.k_head_stride;
@@ -345,7 +347,7 @@ attn_rows16_kernel(const __grid_constant__ AttnArgs s) {
         }
         if (!whole && first == 0 && threadIdx.x == 0) {
             AttnJoin j = {};
-            j.pieces = (int32_t)(attn_owner(cur, cur.at + units - 1) - cta + 1);
+            j.pieces = attn_pieces(s, cur, span, cta);
             j.seq = cur.seq;
             j.head = cur.head;
             j.row_tile = cur.row_tile;
@@ -353,8 +355,8 @@ attn_rows16_kernel(const __grid_constant__ AttnArgs s) {
             j.q_len = q.n;
             attn_joins(s, ctas)[cta] = j;
         }
-        cur.at += last - first;
-        cur.left -= last - first;
+        cur.at += span.cost;
+        cur.left -= span.cost;
         if (cur.left <= 0) break;
         attn_next(s, cur, q);
         __syncthreads();  // the join's reads are done before the ring is filled again
@@ -492,6 +494,7 @@ void attn_plan(const ks_attention_args_t &a, bool tc, int sms, AttnPlan *p) {
     p->s.group = (int32_t)(a.q_heads / a.kv_heads);
     p->s.scale_log2 = a.scale * 1.4426950408889634f;
     p->s.rows = tc ? attn_tc_rows() : kRows;
+    p->s.tile_cost = tc ? attn_tc_tile_cost() : kTileCost;
     const int unit = tc ? attn_tc_unit() : kUnit;
     p->s.unit_shift = 0;
     while (1 << p->s.unit_shift < unit) ++p->s.unit_shift;
@@ -505,7 +508,7 @@ void attn_plan(const ks_attention_args_t &a, bool tc, int sms, AttnPlan *p) {
     p->s.tile_tokens = p->s.head_splits > 1 ? 1 : p->s.rows / p->s.tile_heads;
     // No more CTAs than the call can have units.
     const int64_t tiles = ceil_to(a.tokens, p->s.tile_tokens) + a.seqs;
-    const int64_t tile_units = ceil_to(a.table_pages * a.page_size, unit) + 1;
+    const int64_t tile_units = ceil_to(a.table_pages * a.page_size, unit) + 1 + p->s.tile_cost;
     const int64_t heads = a.kv_heads * p->s.head_splits;
     int64_t ctas = (int64_t)sms * per_sm;
     if (tile_units < ctas && tiles < ctas && heads < ctas && tile_units * tiles * heads < ctas)

@@ -3,12 +3,12 @@
 //
 // Division of the work. The queries of one sequence and one key/value head (all heads of its
 // group, token after token) are cut into row tiles of at most M rows, and the keys a row tile sees
-// into units of TN keys. All units of a call, in the order sequence, head, row tile, unit, are
-// shared out evenly: CTA c of G takes units [U c / G, U (c + 1) / G)
-// (G no more than U). A row tile whose units fall
-// to several CTAs is split over its long axis; each of them leaves its running maximum, sum and
-// unnormalised output in the workspace and a second kernel joins them in a fixed order, so results
-// do not depend on timing. The lengths are read on the device: the launch depends on host-known
+// into units of TN keys. A row tile costs its units and a few more for its beginning and end
+// (tile_cost). All cost of a call, in the order sequence, head, row tile, unit, is shared out evenly:
+// CTA c of G takes [U c / G, U (c + 1) / G), G no more than U. A row tile whose units fall to several
+// CTAs is split over its long axis; each of them leaves its running maximum, sum and unnormalised
+// output in the workspace and a second kernel joins them in a fixed order, so results do not depend
+// on timing. The lengths are read on the device: the launch depends on host-known
 // sizes only, and a captured graph may be replayed with other lengths.
 #pragma once
 
@@ -24,6 +24,7 @@ struct AttnArgs {
     int32_t tile_tokens; // tokens in a row tile
     int32_t unit_shift;  // log2 of the keys per unit (TN)
     int32_t rows;        // rows of a tile (M)
+    int32_t tile_cost;   // units that a row tile costs beside its own
     float scale_log2;    // scale * log2(e)
 };
 
@@ -105,14 +106,14 @@ __device__ __forceinline__ int attn_tile_units(const AttnArgs &s, const AttnSeq 
     return max(1, (int)(((uint32_t)attn_tile_keys(s, q, rt) + (1u << s.unit_shift) - 1) >> s.unit_shift));
 }
 
-// Units of the row tiles [0, k) of one head, of `tiles` in all.
-__device__ __forceinline__ int64_t attn_units_before(const AttnArgs &s, const AttnSeq &q, int tiles, int k) {
+// Cost of the row tiles [0, k) of one head, of `tiles` in all.
+__device__ __forceinline__ int64_t attn_cost_before(const AttnArgs &s, const AttnSeq &q, int tiles, int k) {
     if (k <= 0) return 0;
-    if (k == 1) return attn_tile_units(s, q, 0);
-    if (!(s.a.flags & KS_ATTENTION_CAUSAL)) return (int64_t)k * attn_tile_units(s, q, 0);
-    int64_t total = 0;
+    if (k == 1) return attn_tile_units(s, q, 0) + s.tile_cost;
+    if (!(s.a.flags & KS_ATTENTION_CAUSAL)) return (int64_t)k * (attn_tile_units(s, q, 0) + s.tile_cost);
+    int64_t total = (int64_t)k * s.tile_cost;
     if (k == tiles) {  // the last tile is cut off at the last token: by itself
-        total = attn_tile_units(s, q, tiles - 1);
+        total += attn_tile_units(s, q, tiles - 1);
         --k;
     }
     // tile i < tiles - 1 sees past + (i + 1) tile_tokens keys; up to one unit of them counts as one
@@ -126,14 +127,31 @@ __device__ __forceinline__ int64_t attn_units_before(const AttnArgs &s, const At
 
 // A CTA's place in the call's units.
 struct AttnCursor {
-    int32_t seq, head, row_tile, unit;  // head: key/value head * head_splits + split
-    int64_t left;                       // units this CTA still has to do
-    int64_t at;                         // index of the current unit among all
-    int64_t units;                      // all units of the call
-    int32_t ctas;                       // CTAs that have units
+    int32_t seq, head, row_tile;  // head: key/value head * head_splits + split
+    int32_t pos;                  // place in the row tile's cost: tile_cost, then its units
+    int64_t left;                 // cost this CTA still has to do
+    int64_t at;                   // place in the call's cost
+    int64_t units;                // the call's cost
+    int32_t ctas;                 // CTAs that have some
 };
 
-// The CTA that has unit u: the last c with U c / G < u + 1.
+// The CTA's part of the row tile it is at: units [first, last) of `units`, none if first == last (its
+// share ends in the tile's extra cost: the next CTA begins the tile).
+struct AttnSpan {
+    int32_t first, last, units, cost;
+};
+
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs &s, const AttnCursor &c, const AttnSeq &q) {
+    AttnSpan p;
+    p.units = attn_tile_units(s, q, c.row_tile);
+    const int end = (int)min((int64_t)p.units + s.tile_cost, c.pos + c.left);
+    p.first = max(0, c.pos - s.tile_cost);
+    p.last = max(0, end - s.tile_cost);
+    p.cost = end - c.pos;
+    return p;
+}
+
+// The CTA that has place u of the cost U: the last c with U c / G < u + 1.
 __device__ __forceinline__ int64_t attn_owner(const AttnCursor &c, int64_t u) {
     return quotient((u + 1) * c.ctas - 1, c.units);
 }
@@ -158,7 +176,7 @@ __device__ inline const AttnCursor &attn_begin(const AttnArgs &s, int cta, int c
     for (int b = lo; b < hi; ++b) {
         const AttnSeq q = attn_seq(s.a, b);
         const int tiles = attn_row_tiles(s, q);
-        per_head = attn_units_before(s, q, tiles, tiles);
+        per_head = attn_cost_before(s, q, tiles, tiles);
         mine += heads * per_head;
     }
     int64_t upto = mine;
@@ -195,7 +213,7 @@ __device__ inline const AttnCursor &attn_begin(const AttnArgs &s, int cta, int c
         for (int b = lo; per > 1; ++b) {
             const AttnSeq q = attn_seq(s.a, b);
             const int tiles = attn_row_tiles(s, q);
-            per_head = attn_units_before(s, q, tiles, tiles);
+            per_head = attn_cost_before(s, q, tiles, tiles);
             c.seq = b;
             if (c.at < before + heads * per_head) break;
             before += heads * per_head;
@@ -215,7 +233,7 @@ __device__ inline const AttnCursor &attn_begin(const AttnArgs &s, int cta, int c
         int64_t begins = 0;         // units before `low`
         while (size > 1) {
             const int step = (size + 31) >> 5;
-            const int64_t mine_begins = lane * step < size ? attn_units_before(s, q, tiles, low + lane * step) : u + 1;
+            const int64_t mine_begins = lane * step < size ? attn_cost_before(s, q, tiles, low + lane * step) : u + 1;
             const int place = __popc(__ballot_sync(0xFFFFFFFFu, mine_begins <= u)) - 1;
             begins = __shfl_sync(0xFFFFFFFFu, mine_begins, place);
             low += place * step;
@@ -224,7 +242,7 @@ __device__ inline const AttnCursor &attn_begin(const AttnArgs &s, int cta, int c
         if (lane == 0) {
             result.head = head;
             result.row_tile = low;
-            result.unit = (int32_t)(u - begins);
+            result.pos = (int32_t)(u - begins);
         }
     }
     __syncthreads();
@@ -233,7 +251,7 @@ __device__ inline const AttnCursor &attn_begin(const AttnArgs &s, int cta, int c
 
 // Moves to the next row tile with units (called only while units are left).
 __device__ __forceinline__ void attn_next(const AttnArgs &s, AttnCursor &c, AttnSeq &q) {
-    c.unit = 0;
+    c.pos = 0;
     if (++c.row_tile < attn_row_tiles(s, q)) return;
     c.row_tile = 0;
     if (++c.head < s.a.kv_heads * s.head_splits) return;
@@ -253,6 +271,11 @@ __device__ __forceinline__ bool attn_row(const AttnArgs &s, int q0, int n, int h
     *token = q0 + in_seq;
     *q_head = (head / s.head_splits) * s.group + g;
     return i < s.tile_tokens && in_seq < n && g < s.group;
+}
+
+// Pieces of the row tile that the CTA begins: up to the CTA that has its last unit.
+__device__ __forceinline__ int attn_pieces(const AttnArgs &s, const AttnCursor &c, const AttnSpan &p, int cta) {
+    return (int)(attn_owner(c, c.at - c.pos + s.tile_cost + p.units - 1) - cta + 1);
 }
 
 // Workspace: per CTA two slots of rows * (dim + 2) floats (outputs, maxima, sums), then an AttnJoin per
@@ -293,6 +316,7 @@ bool attn_tc_sizes(const ks_attention_args_t &a);
 bool attn_tc_fits(const ks_attention_args_t &a);
 int attn_tc_rows();
 int attn_tc_unit();
+int attn_tc_tile_cost();
 cudaError_t attn_tc_launch(const AttnArgs &s, int ctas, cudaStream_t stream, bool pdl);
 
 }  // namespace ks

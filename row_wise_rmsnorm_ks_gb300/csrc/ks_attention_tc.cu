@@ -9,7 +9,8 @@
 //                    the workspace;
 //   warps 16 and 18  issue the matrix instructions of tile 0 and 1: P V, then Q K(next), which
 //                    overwrites S and P behind it in order;
-//   warp 17          copies pages to shared memory by TMA, one lane per page and 64 columns;
+//   warp 17          copies queries and pages to shared memory by TMA, for pages one lane per page and
+//                    64 columns;
 //   warp 19          clears value rows behind a sequence's last key.
 // While one tile is in its softmax, the matrix instructions of the other run. A row's base is the
 // maximum of the first scores it saw until later probabilities pass 2^14 (of which fp16 holds 65504):
@@ -38,6 +39,7 @@ constexpr int kMma = kSoftmaxWarps, kCopy = kMma + 1, kTail = kMma + 3;  // the 
 // their probabilities), the last keeps 64.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr int kHalfBytes = kKeys * 128;  // 128 rows of 64 values
+constexpr int kTileCost = 3;       // steps that beginning and ending a row tile costs
 constexpr float kGrowth = 16384.0f;  // the most that a lane's probabilities to an old base may sum to
 
 template <int kDim>
@@ -145,6 +147,13 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -211,6 +220,29 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
     return w;
 }
 
+// Word i of lane q of a quad becomes word q of lane i.
+__device__ __forceinline__ void quad_transpose(uint32_t (&y)[4], int q) {
+    // pairs of words between lanes two apart, then words between neighbours
+    const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, q & 2 ? y[0] : y[2], 2);
+    const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, q & 2 ? y[1] : y[3], 2);
+    if (q & 2) {
+        y[0] = a;
+        y[1] = b;
+    } else {
+        y[2] = a;
+        y[3] = b;
+    }
+    const uint32_t c = __shfl_xor_sync(0xFFFFFFFFu, q & 1 ? y[0] : y[1], 1);
+    const uint32_t d = __shfl_xor_sync(0xFFFFFFFFu, q & 1 ? y[2] : y[3], 1);
+    if (q & 1) {
+        y[0] = c;
+        y[2] = d;
+    } else {
+        y[1] = c;
+        y[3] = d;
+    }
+}
+
 // A place in the ring of tiles and the phase of its barriers there.
 template <int kStages>
 struct RingAt {
@@ -223,47 +255,34 @@ struct RingAt {
     }
 };
 
-// The part of a CTA's work that one row tile is: the same for all roles.
-struct Segment {
-    int first, last;   // units (128-key steps)
-    int units;         // of the row tile
-    bool two;          // the second tile has rows
-};
-
-// Each warp keeps its place in the CTA's work in shared memory: between row tiles it is needed
-// once, and the softmax has no registers to spare for it.
+// Each warp keeps its place in the CTA's work in shared memory: it is needed once per row tile, and the
+// softmax has no registers to spare for it.
 struct Place {
     AttnCursor cur;
     AttnSeq q;
 };
 
-__device__ __forceinline__ Segment segment(const AttnArgs &s, const AttnCursor &c, const AttnSeq &q) {
-    Segment g;
-    g.units = attn_tile_units(s, q, c.row_tile);
-    g.first = c.unit;
-    g.last = (int)min((int64_t)g.units, g.first + c.left);
-    g.two = min(s.tile_tokens, q.n - c.row_tile * s.tile_tokens) * s.tile_heads > kTile;
-    return g;
+// Whether the row tile's second tile has rows.
+__device__ __forceinline__ bool second_tile(const AttnArgs &s, const Place &p) {
+    return min(s.tile_tokens, p.q.n - p.cur.row_tile * s.tile_tokens) * s.tile_heads > kTile;
 }
 
-// Goes on to the CTA's next row tile; false when its share is done. All lanes of the
-// warp call it, or (kWarp false) the one that works.
-template <bool kWarp = true>
-__device__ __forceinline__ bool next_segment(const AttnArgs &s, Place &p, int steps) {
-    if (kWarp) __syncwarp();
-    if (!kWarp || threadIdx.x % 32 == 0) {
-        p.cur.at += steps;
-        p.cur.left -= steps;
+// Goes on to the CTA's next row tile; false when its share is done. All lanes of the warp call it.
+__device__ __forceinline__ bool next_tile(const AttnArgs &s, Place &p, int cost) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) {
+        p.cur.at += cost;
+        p.cur.left -= cost;
         if (p.cur.left > 0) attn_next(s, p.cur, p.q);
     }
-    if (kWarp) __syncwarp();
+    __syncwarp();
     return p.cur.left > 0;
 }
 
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUtensorMap k_map,
-               const __grid_constant__ CUtensorMap v_map) {
+attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUtensorMap q_map,
+               const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = Tc<kDim>;
     static_assert(2 * kTileThreads * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
                   "the split draws on the launch's registers");
@@ -274,7 +293,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     const uint32_t q_addr = base, ring = base + 2 * C::kTileBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (2 + C::kStages) * C::kTileBytes);
     uint64_t *full = bars, *empty = bars + C::kStages;
-    uint64_t *q_full = empty + C::kStages, *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *q_full = empty + C::kStages, *q_free = q_full + 1, *s_full = q_full + 2, *p_full = s_full + 2;
+    uint64_t *o_full = p_full + 2;
     uint64_t *turn = o_full + 2, *done = turn + 2, *tail = done + 2;
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile uint32_t *gave_up = tmem_at + 1;
@@ -288,13 +308,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             mbar_init(tail + i, 1);
         }
         for (int w = 0; w < 2; ++w) {
-            mbar_init(q_full + w, kTileThreads / 32);
             mbar_init(s_full + w, 1);
             mbar_init(p_full + w, kTileThreads / 32);
             mbar_init(o_full + w, 1);
             mbar_init(turn + w, 1);
             mbar_init(done + w, 1);
         }
+        mbar_init(q_full, 1);
+        mbar_init(q_free, 2);
         bar_arrive(turn);  // tile 0 begins
         *gave_up = 0;
         fence_mbar_init();
@@ -331,12 +352,13 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         const int page_size = (int)a.page_size, in_tile = min(page_size, kKeys);  // keys of a copy
         const int part = lane / C::kHalves, half = lane % C::kHalves;
         uint32_t at = 0;  // tiles copied so far: K and V of each step in turn
+        uint32_t queries = 0;
         while (more) {
-            const Segment g = segment(s, place.cur, place.q);
+            const AttnSpan span = attn_span(s, place.cur, place.q);
             const int head = place.cur.head / s.head_splits, keys = place.q.keys;
             const int32_t *table = a.page_table + (int64_t)place.cur.seq * a.table_stride;
             bool ok = true;
-            for (int j = g.first; j < g.last && ok; ++j) {
+            for (int j = span.first; j < span.last && ok; ++j) {
                 const int key = j * kKeys + part * in_tile;
                 const bool wanted = part * in_tile < kKeys && key < keys;
                 int page = 0, slot = 0;
@@ -351,8 +373,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, wanted)) * in_tile * 128;
                 for (int v = 0; v < 2 && ok; ++v, ++at) {
                     const uint32_t stage = at % C::kStages;
-                    ok = bar_wait(empty + stage, (at / C::kStages & 1) ^ 1, gave_up);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    ok = bar_wait_warp(empty + stage, (at / C::kStages & 1) ^ 1, gave_up);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(full + stage, bytes);
                     __syncwarp();
@@ -360,9 +381,25 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                         tma_load(ring + stage * C::kTileBytes + half * kHalfBytes + part * in_tile * 128,
                                  v ? &v_map : &k_map, half * 64, slot, head, page, smem_addr(full + stage));
                 }
+                if (ok && j == span.first) {
+                    // The row tile's queries, as soon as the tile before has had its last product with
+                    // its own: a box of tile_heads heads and tile_tokens tokens comes in the rows' order.
+                    // Rows behind the sequence hold other tokens' queries (or zeros behind the last);
+                    // no row touches another.
+                    ok = bar_wait_warp(q_free, (queries++ & 1) ^ 1, gave_up);
+                    if (ok && lane == 0) {
+                        mbar_arrive_expect_tx(q_full, C::kHalves * s.tile_heads * s.tile_tokens * 128);
+                        const int first_head = head * s.group + place.cur.head % s.head_splits * s.tile_heads;
+                        const int token = place.q.q0 + place.cur.row_tile * s.tile_tokens;
+                        for (int h = 0; h < C::kHalves; ++h)
+                            tma_load3(q_addr + h * kRows * 128, &q_map, h * 64, first_head, token, smem_addr(q_full));
+                    }
+                    __syncwarp();
+                }
             }
-            more = ok && next_segment(s, place, g.last - g.first);
+            more = ok && next_tile(s, place, span.cost);
         }
+        if (queries) (void)mbar_wait_bounded(q_full, (queries - 1) & 1);
         // nothing of this CTA's is in flight when it ends, also after a wait that gave up
         const uint32_t from = at > (uint32_t)C::kStages ? at - C::kStages : 0;
         for (uint32_t i = from; i < at; ++i) (void)mbar_wait_bounded(full + i % C::kStages, i / C::kStages & 1);
@@ -376,7 +413,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         const int w = warp == kMma ? 0 : 1;
         constexpr uint32_t qk = mma_shape<T>(kKeys, false), pv = mma_shape<T>(kDim, true);
         const uint32_t s_at = tmem + w * 128, o_at = tmem + C::kO + w * 128;
-        const uint32_t q_low = desc_low(q_addr + w * C::kTileBytes, 16);
+        const uint32_t q_low = desc_low(q_addr + w * kTile * 128, 16);
         RingAt<C::kStages> k_at, v_at;  // the next step's keys, this step's values
         uint32_t q_uses = 0, p_uses = 0, turns = 0;
         uint32_t tails = 0;             // phase of each stage's tail barrier, a bit each
@@ -384,30 +421,30 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             const uint32_t k_low = desc_low(ring + stage * C::kTileBytes, 16);
             mma_ss<false>(s_at, q_low, k_low, qk);
 #pragma unroll
-            for (int i = 1; i < kDim / 16; ++i) {
-                const uint32_t off = (i / 4 * kHalfBytes + i % 4 * 32) >> 4;
-                mma_ss<true>(s_at, q_low + off, k_low + off, qk);
-            }
+            for (int i = 1; i < kDim / 16; ++i)
+                mma_ss<true>(s_at, q_low + ((i / 4 * kRows * 128 + i % 4 * 32) >> 4),
+                             k_low + ((i / 4 * kHalfBytes + i % 4 * 32) >> 4), qk);
             mma_commit(smem_addr(s_full + w));
         };
         while (more) {
-            const Segment g = segment(s, place.cur, place.q);
-            const int first = warp_uniform(g.first), end = warp_uniform(g.last);
+            const AttnSpan span = attn_span(s, place.cur, place.q);
+            const int first = warp_uniform(span.first), end = warp_uniform(span.last);
             const int keys = warp_uniform(place.q.keys);
-            const bool two = warp_uniform(g.two) != 0;
-            bool ok = true;
+            const bool two = warp_uniform(second_tile(s, place)) != 0;
+            if (first >= end) break;  // the share ends in the tile's extra cost
+            bool ok = bar_wait_warp(q_full, q_uses++ & 1, gave_up);
             if (w == 1 && !two) {  // this tile has no rows: its share of the stages is given back
+                if (ok && lane == 0) bar_arrive(q_free);
                 for (int i = 2 * (end - first); i > 0 && ok; --i) {
                     ok = bar_wait_warp(full + k_at.stage, k_at.phase, gave_up);
                     if (i == 1 && keys < end * kKeys) tails ^= 1u << k_at.stage;
                     if (ok && lane == 0) bar_arrive(empty + k_at.stage);
                     k_at.next();
                 }
-                more = ok && next_segment(s, place, end - first);
+                more = ok && next_tile(s, place, span.cost);
                 continue;
             }
-            ok = bar_wait_warp(full + k_at.stage, k_at.phase, gave_up) &&
-                 bar_wait_warp(q_full + w, q_uses++ & 1, gave_up) &&
+            ok = ok && bar_wait_warp(full + k_at.stage, k_at.phase, gave_up) &&
                  (!two || bar_wait_warp(turn + w, turns++ & 1, gave_up));
             if (!ok) break;
             fence_after();
@@ -415,6 +452,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 issue_qk(k_at.stage);
                 if (two) bar_arrive(turn + 1 - w);
                 mma_commit(smem_addr(empty + k_at.stage));
+                if (first + 1 == end) mma_commit(smem_addr(q_free));
             }
             __syncwarp();
             v_at = k_at;
@@ -437,20 +475,20 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                     const uint32_t v_low = desc_low(ring + v_at.stage * C::kTileBytes, kHalfBytes);
                     mma_ts(o_at, s_at, v_low, pv, j > first);
 #pragma unroll
-                    for (int i = 1; i < kKeys / 16; ++i)
-                        mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
+                    for (int i = 1; i < kKeys / 16; ++i) mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
                     if (last) mma_commit(smem_addr(o_full + w));
                     else issue_qk(k_at.stage);
                     if (two) bar_arrive(turn + 1 - w);
                     mma_commit(smem_addr(empty + v_at.stage));
                     if (!last) mma_commit(smem_addr(empty + k_at.stage));
+                    if (j + 2 == end) mma_commit(smem_addr(q_free));
                 }
                 __syncwarp();
                 v_at = k_at;
                 v_at.next();
             }
             // k_at is the tile after the row tile's last values: the next row tile's first keys
-            more = ok && next_segment(s, place, end - first);
+            more = ok && next_tile(s, place, span.cost);
         }
         // every instruction and arrival of this warp is done when it ends, also after a wait that gave up
         if (elect_one()) mma_commit(smem_addr(done + w));
@@ -462,13 +500,12 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         // tile through the ring (a barrier's phases can be told apart one apart, no further).
         uint32_t at = 0;
         while (more) {
-            const Segment g = segment(s, place.cur, place.q);
-            const int valid = place.q.keys - (g.last - 1) * kKeys;
+            const AttnSpan span = attn_span(s, place.cur, place.q);
+            const int valid = place.q.keys - (span.last - 1) * kKeys;
             bool ok = true;
-            for (uint32_t end = at + 2 * (g.last - g.first); at < end && ok; ++at) {
+            for (uint32_t end = at + 2 * (span.last - span.first); at < end && ok; ++at) {
                 const uint32_t stage = at % C::kStages;
-                ok = bar_wait(full + stage, at / C::kStages & 1, gave_up);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                ok = bar_wait_warp(full + stage, at / C::kStages & 1, gave_up);
                 if (!ok) break;
                 if (at + 1 == end && valid < kKeys) {  // the row tile's last values
                     uint8_t *v_tile = smem + (2 + stage) * C::kTileBytes;
@@ -481,7 +518,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 }
                 if (lane == 0) bar_arrive(empty + stage);
             }
-            more = ok && next_segment(s, place, g.last - g.first);
+            more = ok && next_tile(s, place, span.cost);
         }
     }
     } else {
@@ -494,51 +531,39 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         const int r0 = w * kTile + sub + lane / 4;
         const int dim = (int)a.head_dim;
         const bool causal = (a.flags & KS_ATTENTION_CAUSAL) != 0;
-        // The products run with |scale|: a negative one turns the query's signs. 0 becomes the least
+        // The exponents are made with |scale|: a negative one turns the scores' signs. 0 becomes the least
         // normal number, whose products with finite scores vanish and which leaves -inf as it is.
         const float scale = fmaxf(fabsf(s.scale_log2), 1.17549435e-38f);
+        const bool negative = s.scale_log2 < 0.0f;
         uint32_t s_uses = 0, o_uses = 0;
         while (more) {
-            const Segment g = segment(s, place.cur, place.q);
-            if (w == 1 && !g.two) {
-                more = next_segment(s, place, g.last - g.first);
+            const AttnSpan span = attn_span(s, place.cur, place.q);
+            if (span.first >= span.last) break;  // the share ends in the tile's extra cost
+            if (w == 1 && !second_tile(s, place)) {
+                more = next_tile(s, place, span.cost);
                 continue;
             }
-            int limit[2], all_see;  // keys that this thread's rows see, and all rows of the warp
+            // keys that this thread's rows see, and all rows of the warp; the threads' rows in the output
+            int limit[2], all_see;
+            T *dst[2];
+            bool real[2];
             {
                 const AttnSeq q = place.q;
-                const int row_tile = place.cur.row_tile;
-                // the query: half a row per thread
-                const int row = threadIdx.x % kTile, half = threadIdx.x / kTile % 2;
-                int token, head;
-                const bool real = attn_row(s, q.q0, q.n, place.cur.head, row_tile, w * kTile + row, &token, &head);
-                const T *src = (const T *)a.q + token * a.q_token_stride + head * a.q_head_stride;
-                uint8_t *dst = smem + w * C::kTileBytes + row * 128;
-                const uint32_t sign = s.scale_log2 < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-                for (int i = 0; i < kDim / 16; ++i) {
-                    const int c = half * (kDim / 16) + i;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (real && c * 8 < dim) x = *reinterpret_cast<const uint4 *>(src + c * 8);
-                    x.x ^= sign;
-                    x.y ^= sign;
-                    x.z ^= sign;
-                    x.w ^= sign;
-                    *reinterpret_cast<uint4 *>(dst + c / 8 * kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = x;
-                }
-                fence_async_smem();
-                fence_before();
-                warp_arrive(q_full + w);
-                const int sees = attn_tile_keys(s, q, row_tile);
+                const int row_tile = place.cur.row_tile, sees = attn_tile_keys(s, q, row_tile);
                 const int first = q.keys - q.n + row_tile * s.tile_tokens + 1;
-                limit[0] = causal ? min(sees, first + r0 / s.tile_heads) : sees;
-                limit[1] = causal ? min(sees, first + (r0 + 8) / s.tile_heads) : sees;
                 all_see = causal ? min(sees, first + (w * kTile + sub) / s.tile_heads) : sees;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    int token, head;
+                    real[i] = attn_row(s, q.q0, q.n, place.cur.head, row_tile, r0 + 8 * i, &token, &head);
+                    limit[i] = causal ? min(sees, first + (r0 + 8 * i) / s.tile_heads) : sees;
+                    dst[i] = (T *)a.out + token * a.out_token_stride + head * a.out_head_stride;
+                }
             }
 
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
             bool ok = true;
-            for (int j = g.first; j < g.last; ++j) {
+            for (int j = span.first; j < span.last; ++j) {
                 ok = bar_wait_warp(s_full + w, s_uses++ & 1, gave_up);
                 if (!ok) break;
                 fence_after();
@@ -549,12 +574,19 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 // has outgrown it (a maximum over the scores would take as long as the exponentials). Then,
                 // and for the first step and rows that saw no key yet, the maxima are taken and the
                 // exponentials again: the scores are still in tensor memory.
-                bool rebase = __any_sync(0xFFFFFFFFu, m[0] == -INFINITY || m[1] == -INFINITY);
+                bool rebase = j == span.first ||
+                              __any_sync(0xFFFFFFFFu, (real[0] && m[0] == -INFINITY) || (real[1] && m[1] == -INFINITY));
                 while (true) {
                     uint32_t x[2][32];  // [64 keys][of 8 keys two of each row, ...]
                     tmem_load_rows32(x[0], s_at);
                     tmem_load_rows32(x[1], s_at + 64);
                     tmem_wait_load();
+                    if (negative) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[c][i] ^= 0x80000000u;
+                    }
                     if (key0 + kKeys > all_see) {
 #pragma unroll
                         for (int g8 = 0; g8 < kKeys / 8; ++g8) {
@@ -580,7 +612,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                             l[k] *= f[k];
                             m[k] = best;
                         }
-                        if (j > g.first) {
+                        if (j > span.first) {
 #pragma unroll 1
                             for (int c = 0; c < kDim / 32; ++c) tmem_scale_rows(o_at + c * 32, f[0], f[1]);
                         }
@@ -602,7 +634,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                         }
                     sum[0].x += sum[0].y;
                     sum[1].x += sum[1].y;
-                    if (rebase || !__any_sync(0xFFFFFFFFu, !(sum[0].x <= kGrowth && sum[1].x <= kGrowth))) break;
+                    if (rebase || !__any_sync(0xFFFFFFFFu, (real[0] && !(sum[0].x <= kGrowth)) ||
+                                                               (real[1] && !(sum[1].x <= kGrowth))))
+                        break;
                     rebase = true;
                 }
                 tmem_store_rows16(s_at, p[0]);
@@ -614,56 +648,23 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 l[1] += sum[1].x;
             }
             if (!ok) break;
-            ok = bar_wait_warp(o_full + w, o_uses++ & 1, gave_up);
-            if (!ok) break;
-            fence_after();
-            const bool whole = g.first == 0 && g.last == g.units;
+            // What is left to do without the output is done before the wait for it.
+            const bool whole = span.first == 0 && span.last == span.units;
+            float *part = attn_slot(s, cta, span.first == 0 ? 1 : 0);
             float inv[2];
-            T *dst[2];
-            bool real[2];
-            float *part = attn_slot(s, cta, g.first == 0 ? 1 : 0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
                 inv[i] = attn_inverse(l[i]);
-                int token, head;
-                real[i] = attn_row(s, place.q.q0, place.q.n, place.cur.head, place.cur.row_tile, r0 + 8 * i, &token, &head);
-                dst[i] = (T *)a.out + token * a.out_token_stride + head * a.out_head_stride;
-            }
-#pragma unroll 1
-            for (int c = 0; c < kDim / 32; ++c) {
-                uint32_t o[16];
-                tmem_load_rows16(o, o_at + c * 32);
-                tmem_wait_load();
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const int col = c * 32 + i * 2;  // of the group's 8
-                    if (col >= dim) continue;
-                    if (!whole) {
-                        *attn_part(s, part, r0 / 16, col / 8, lane) =
-                            make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
-                                        __uint_as_float(o[i + 3]));
-                        continue;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (real[k])
-                            *reinterpret_cast<uint32_t *>(dst[k] + col + quad * 2) =
-                                pack_pair<T>(__uint_as_float(o[i + 2 * k]) * inv[k], __uint_as_float(o[i + 2 * k + 1]) * inv[k]);
-                }
-                __syncwarp();
-            }
-            fence_before();  // O is read before the next row tile's first product overwrites it
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
                 if (!whole && quad == 0) {
                     part[kRows * dim + r0 + 8 * i] = m[i];
                     part[kRows * dim + kRows + r0 + 8 * i] = l[i];
                 }
-            if (!whole && g.first == 0 && threadIdx.x == 0) {
+            }
+            if (!whole && span.first == 0 && threadIdx.x == 0) {
                 AttnJoin j = {};
-                j.pieces = (int32_t)(attn_owner(place.cur, place.cur.at + g.units - 1) - cta + 1);
+                j.pieces = attn_pieces(s, place.cur, span, cta);
                 j.seq = place.cur.seq;
                 j.head = place.cur.head;
                 j.row_tile = place.cur.row_tile;
@@ -671,7 +672,38 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 j.q_len = place.q.n;
                 attn_joins(s, ctas)[cta] = j;
             }
-            more = next_segment(s, place, g.last - g.first);
+            more = next_tile(s, place, span.cost);
+            ok = bar_wait_warp(o_full + w, o_uses++ & 1, gave_up);
+            if (!ok) break;
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kDim / 32; ++c) {
+                uint32_t o[16];
+                tmem_load_rows16(o, o_at + c * 32);
+                tmem_wait_load();
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c * 32 + i * 8 < dim)
+                            *attn_part(s, part, r0 / 16, c * 4 + i, lane) =
+                                make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    continue;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    // A lane has two columns of each of the chunk's four groups of 8; after the exchange
+                    // lane q of the quad has the 8 columns of group q, 16 bytes.
+                    uint32_t y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[i] = pack_pair<T>(__uint_as_float(o[4 * i + 2 * k]) * inv[k], __uint_as_float(o[4 * i + 2 * k + 1]) * inv[k]);
+                    quad_transpose(y, quad);
+                    const int col = c * 32 + quad * 8;
+                    if (real[k] && col < dim) *reinterpret_cast<uint4 *>(dst[k] + col) = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
+            fence_before();  // O is read before the next row tile's first product overwrites it
         }
     }
     __syncwarp();
@@ -721,6 +753,23 @@ bool pool_map(CUtensorMap *map, const ks_attention_args_t &a, const void *p, int
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as columns, heads, tokens; boxes of 64 columns, a row tile's heads and its tokens.
+bool query_map(CUtensorMap *map, const AttnArgs &s) {
+    const ks_attention_args_t &a = s.a;
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t row = 16 * ((a.head_dim + 7) / 8);
+    const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.q_heads, (cuuint64_t)a.tokens};
+    const cuuint64_t strides[2] = {a.q_heads > 1 ? (cuuint64_t)a.q_head_stride * 2 : row,
+                                   a.tokens > 1 ? (cuuint64_t)a.q_token_stride * 2 : row};
+    const cuuint32_t box[3] = {64, (cuuint32_t)s.tile_heads, (cuuint32_t)s.tile_tokens};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return encode(map, a.dtype == KS_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<void *>(a.q), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T>
 const void *tc_kernel(int dim, int *smem) {
     *smem = dim <= 64 ? Tc<64>::kSmem : Tc<128>::kSmem;
@@ -737,28 +786,31 @@ bool attn_tc_sizes(const ks_attention_args_t &a) {
 bool attn_tc_fits(const ks_attention_args_t &a) {
     if (!attn_tc_sizes(a)) return false;
     // the tensor map's strides are below 2^40 bytes and not zero
-    const int64_t strides[6] = {a.k_page_stride, a.k_slot_stride, a.k_head_stride, a.v_page_stride, a.v_slot_stride, a.v_head_stride};
-    const int64_t counts[6] = {a.pages, a.page_size, a.kv_heads, a.pages, a.page_size, a.kv_heads};
-    for (int i = 0; i < 6; ++i)
+    const int64_t strides[8] = {a.k_page_stride, a.k_slot_stride, a.k_head_stride, a.v_page_stride,
+                                a.v_slot_stride, a.v_head_stride, a.q_token_stride, a.q_head_stride};
+    const int64_t counts[8] = {a.pages, a.page_size, a.kv_heads, a.pages, a.page_size, a.kv_heads, a.tokens, a.q_heads};
+    for (int i = 0; i < 8; ++i)
         if (counts[i] > 1 && (strides[i] == 0 || strides[i] >= (1ll << 39))) return false;
     return a.pages > 0;
 }
 
 int attn_tc_rows() { return kRows; }
 int attn_tc_unit() { return kKeys; }
+int attn_tc_tile_cost() { return kTileCost; }
 
 cudaError_t attn_tc_launch(const AttnArgs &s, int ctas, cudaStream_t stream, bool pdl) {
     const ks_attention_args_t &a = s.a;
     AttnArgs args = s;
-    CUtensorMap k_map, v_map;
-    if (!pool_map(&k_map, a, a.k_pages, a.k_page_stride, a.k_slot_stride, a.k_head_stride) ||
+    CUtensorMap q_map, k_map, v_map;
+    if (!query_map(&q_map, s) ||
+        !pool_map(&k_map, a, a.k_pages, a.k_page_stride, a.k_slot_stride, a.k_head_stride) ||
         !pool_map(&v_map, a, a.v_pages, a.v_page_stride, a.v_slot_stride, a.v_head_stride))
         return cudaErrorInvalidValue;
     int smem = 0;
     const void *f = a.dtype == KS_DTYPE_BF16 ? tc_kernel<__nv_bfloat16>((int)a.head_dim, &smem)
                                              : tc_kernel<__half>((int)a.head_dim, &smem);
     if (!allow_smem(f, (size_t)smem)) return cudaErrorInvalidConfiguration;
-    void *kp[] = {&args, &k_map, &v_map};
+    void *kp[] = {&args, &q_map, &k_map, &v_map};
     return launch_kernel(f, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, kp, stream, pdl);
 }
 
