@@ -268,21 +268,21 @@ def ks_layer_norm_planned(out: int, x: int, weight: int | None, bias: int | None
 
 
 def ks_rotary(args: bytes | None, stream: int | None) -> int:
-    return load().ks_rotary(args, stream)
+    return (_lib or load()).ks_rotary(args, stream)
 
 
 def ks_rotary_to_pages(args: bytes | None, stream: int | None) -> int:
-    return load().ks_rotary_to_pages(args, stream)
+    return (_lib or load()).ks_rotary_to_pages(args, stream)
 
 
 def ks_paged_attention(args: bytes | None, stream: int | None) -> int:
-    return load().ks_paged_attention(args, stream)
+    return (_lib or load()).ks_paged_attention(args, stream)
 
 
 def ks_paged_attention_workspace(args: bytes | None) -> tuple[int, int]:
     """(status, bytes) for a call of these sizes on the current device."""
     need = ctypes.c_int64(0)
-    st = load().ks_paged_attention_workspace(args, ctypes.byref(need))
+    st = (_lib or load()).ks_paged_attention_workspace(args, ctypes.byref(need))
     return st, need.value
 
 

@@ -70,8 +70,21 @@ def rotary_steps(rotary_dim: int, base: float = 10000.0, *, scaling: str | None 
     return torch.tensor(steps, dtype=torch.int64, device=device)
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+# A decode step is a few microseconds of GPU time, so the calls keep their own time on the host small:
+# the stream comes as its handle, and the device is only changed where it is not the current one.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
+def _launch(call, args: bytes, device: torch.device) -> None:
+    index = device.index
+    if _current_device() == index:
+        status = call(args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = call(args, _raw_stream(index))
+    if status:
+        _abi.check(status)
 
 
 def _rows(t, name, dtype, device):
@@ -184,8 +197,7 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, ste
         0, 0, 0, 0, 0, 0, 0, 0, scale,
         (_abi.KS_ROTARY_INTERLEAVED if interleaved else 0) | (_abi.KS_ROTARY_INVERSE if inverse else 0),
         _DTYPES[dt], 0)
-    with torch.cuda.device(dev):
-        _abi.check(_abi.ks_rotary(args, _stream(dev)))
+    _launch(_abi.ks_rotary, args, dev)
     return qo, ko
 
 
@@ -239,8 +251,7 @@ def rotary_to_pages(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
         k_pages.shape[1], qos[0], qos[1], qs[0], qs[1], 0, 0, ks_[0], ks_[1], vs[0], vs[1],
         kp[0], kp[1], kp[2], vp[0], vp[1], vp[2], scale,
         _abi.KS_ROTARY_INTERLEAVED if interleaved else 0, _DTYPES[dt], 0)
-    with torch.cuda.device(dev):
-        _abi.check(_abi.ks_rotary_to_pages(args, _stream(dev)))
+    _launch(_abi.ks_rotary_to_pages, args, dev)
     return out
 
 
@@ -325,12 +336,18 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     tail = (tokens, seqs, hq, hk, dim, k_pages.shape[0], k_pages.shape[1], page_table.shape[1],
             page_table.stride(0), max_q_len or 0, os_[0], os_[1], qs[0], qs[1], kp[0], kp[1], kp[2],
             vp[0], vp[1], vp[2], scale, _abi.KS_ATTENTION_CAUSAL if causal else 0, _DTYPES[dt], 0)
-    with torch.cuda.device(dev):
-        if workspace is None:
+    if workspace is None:
+        if _current_device() == dev.index:
             st, need = _abi.ks_paged_attention_workspace(_abi.ATTENTION_ARGS.pack(*head, 0, 0, *tail))
+        else:
+            with torch.cuda.device(dev):
+                st, need = _abi.ks_paged_attention_workspace(_abi.ATTENTION_ARGS.pack(*head, 0, 0, *tail))
+        if st:
             _abi.check(st)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = need
+    else:
         ws_bytes = workspace.numel() * workspace.element_size()
-        args = _abi.ATTENTION_ARGS.pack(*head, workspace.data_ptr(), ws_bytes, *tail)
-        _abi.check(_abi.ks_paged_attention(args, _stream(dev)))
+    _launch(_abi.ks_paged_attention,
+            _abi.ATTENTION_ARGS.pack(*head, workspace.data_ptr(), ws_bytes, *tail), dev)
     return out
