@@ -10,8 +10,9 @@
 // position 2^19. The rotation runs in FP32 and is rounded once.
 //
 // Layout. A CTA takes one token (and, where there are fewer tokens than SMs, a part of its heads):
-// its threads first issue the loads of their first vectors, then compute the token's rotary_dim/2
-// sines and cosines once into shared memory, then rotate every head with them. A thread keeps one
+// its threads first issue every load that does not hang on another (position, slot, step and their
+// first vectors), then compute the token's rotary_dim/2 sines and cosines once into shared memory,
+// then rotate every head with them. A thread keeps one
 // column of the head (a 16-byte vector, or the two vectors of a half-split pair), so no index
 // division is left in the loop. Bound by memory: each value is read once and written once.
 #include <cuda_runtime.h>
@@ -44,86 +45,99 @@ __device__ __forceinline__ float2 turn_cos_sin(uint64_t t, float scale) {
     return make_float2((neg_c ? -cc : cc) * scale, (neg_s ? -ss : ss) * scale);
 }
 
-// Where a head slot's row is read and written. Slots 0 .. q_heads-1 are the query's heads, then
-// the keys', then (with a cache) the values'. dst is NULL for a row that is not written.
+// Where a head slot's row is read and written. Slots 0 .. q_heads-1 are the query's heads, then the
+// keys', then (with a cache) the values', which are not rotated.
 template <typename T>
-struct RotRow {
-    const T *src;
-    T *dst;
-    bool rotate;
+__device__ __forceinline__ const T *rot_src(const ks_rotary_args_t &a, int64_t token, int slot) {
+    if (slot < a.q_heads) return (const T *)a.q + token * a.q_token_stride + slot * a.q_head_stride;
+    const int64_t h = slot - a.q_heads;
+    if (h < a.kv_heads) return (const T *)a.k + token * a.k_token_stride + h * a.k_head_stride;
+    return (const T *)a.v + token * a.v_token_stride + (h - a.kv_heads) * a.v_head_stride;
+}
+
+// The token's rows in the cache: NULL where they are not written (a negative slot, or one past the
+// pool, which is also reported in the fault word).
+template <typename T>
+struct RotPage {
+    T *k, *v;
 };
 
-template <typename T, bool kPages>
-__device__ __forceinline__ RotRow<T> rot_row(const ks_rotary_args_t &a, int64_t token, int slot,
-                                             int64_t page, int64_t in_page) {
-    RotRow<T> r;
-    r.rotate = true;
-    if (slot < a.q_heads) {
-        r.src = (const T *)a.q + token * a.q_token_stride + slot * a.q_head_stride;
-        r.dst = (T *)a.q_out + token * a.q_out_token_stride + slot * a.q_out_head_stride;
-        return r;
+template <typename T>
+__device__ __forceinline__ RotPage<T> rot_page(const ks_rotary_args_t &a, int64_t slot) {
+    RotPage<T> p = {nullptr, nullptr};
+    const int64_t size = a.page_size;
+    if (slot < 0) return p;
+    int64_t page, in_page;
+    if (((uint64_t)slot | (uint64_t)size) >> 32 == 0) {  // a 32-bit division takes a fifth of the time
+        page = (uint32_t)slot / (uint32_t)size;
+        in_page = (uint32_t)slot - (uint32_t)page * (uint32_t)size;
+    } else {
+        page = slot / size;
+        in_page = slot - page * size;
     }
-    int64_t h = slot - a.q_heads;
-    if (h < a.kv_heads) {
-        r.src = (const T *)a.k + token * a.k_token_stride + h * a.k_head_stride;
-        if (kPages)
-            r.dst = page < 0 ? nullptr
-                             : (T *)a.k_pages + page * a.k_page_stride + in_page * a.k_slot_stride +
-                                   h * a.k_pages_head_stride;
-        else
-            r.dst = (T *)a.k_out + token * a.k_out_token_stride + h * a.k_out_head_stride;
-        return r;
-    }
-    h -= a.kv_heads;
-    r.rotate = false;
-    r.src = (const T *)a.v + token * a.v_token_stride + h * a.v_head_stride;
-    r.dst = page < 0 ? nullptr
-                     : (T *)a.v_pages + page * a.v_page_stride + in_page * a.v_slot_stride +
-                           h * a.v_pages_head_stride;
-    return r;
-}
-
-// The token's page and place in it; page -1 where its rows are not written (a negative slot, or
-// one past the pool, which is also reported in the fault word).
-__device__ __forceinline__ void rot_slot(const ks_rotary_args_t &a, int64_t token, int64_t *page,
-                                         int64_t *in_page) {
-    const int64_t slot = a.slots[token];
-    *page = -1;
-    *in_page = 0;
-    if (slot >= a.pages * a.page_size) {
+    if (page >= a.pages) {
         if (threadIdx.x == 0) atomicOr(&g_fault_flags, kFaultBadIndex);
-    } else if (slot >= 0) {
-        *page = slot / a.page_size;
-        *in_page = slot - *page * a.page_size;
+        return p;
     }
+    p.k = (T *)a.k_pages + page * a.k_page_stride + in_page * a.k_slot_stride;
+    p.v = (T *)a.v_pages + page * a.v_page_stride + in_page * a.v_slot_stride;
+    return p;
 }
 
-__device__ __forceinline__ void rot_table(const ks_rotary_args_t &a, int64_t token, float2 *cs) {
-    if (a.rotary_dim == 0) return;  // nothing is turned: positions and steps may be NULL
-    const uint64_t pos = (uint64_t)a.positions[token];
-    const uint64_t *steps = (const uint64_t *)a.steps;
+template <typename T, bool kPages>
+__device__ __forceinline__ T *rot_dst(const ks_rotary_args_t &a, int64_t token, int slot, const RotPage<T> &p) {
+    if (slot < a.q_heads) return (T *)a.q_out + token * a.q_out_token_stride + slot * a.q_out_head_stride;
+    const int64_t h = slot - a.q_heads;
+    if (!kPages) return (T *)a.k_out + token * a.k_out_token_stride + h * a.k_out_head_stride;
+    if (!p.k) return nullptr;
+    if (h < a.kv_heads) return p.k + h * a.k_pages_head_stride;
+    return p.v + (h - a.kv_heads) * a.v_pages_head_stride;
+}
+
+// What a token's work hangs on, all loaded at once: its position, its slot, and the step of the angle
+// that this thread computes.
+struct RotToken {
+    uint64_t position, step;
+    int64_t slot;
+};
+
+template <bool kPages>
+__device__ __forceinline__ RotToken rot_token(const ks_rotary_args_t &a, int64_t token) {
+    RotToken t = {0, 0, -1};
+    if (a.rotary_dim > 0) {  // otherwise nothing is turned, and positions and steps may be NULL
+        t.position = (uint64_t)a.positions[token];
+        if (threadIdx.x < a.rotary_dim / 2) t.step = (uint64_t)a.steps[threadIdx.x];
+    }
+    if (kPages) t.slot = a.slots[token];
+    return t;
+}
+
+__device__ __forceinline__ void rot_table(const ks_rotary_args_t &a, const RotToken &t, float2 *cs) {
     const bool inverse = (a.flags & KS_ROTARY_INVERSE) != 0;
+    uint64_t step = t.step;
     for (int j = threadIdx.x; j < (int)(a.rotary_dim / 2); j += blockDim.x) {
-        uint64_t t = pos * steps[j];
-        if (inverse) t = 0 - t;
-        cs[j] = turn_cos_sin(t, a.scale);
+        if (j != threadIdx.x) step = (uint64_t)a.steps[j];
+        const uint64_t angle = t.position * step;
+        cs[j] = turn_cos_sin(inverse ? 0 - angle : angle, a.scale);
     }
 }
 
 // 16-byte vectors. kHalf: pair (j, j + rotary_dim/2); otherwise pair (2j, 2j + 1). kU: vectors
-// (or pairs of them) a thread has in flight.
+// (or pairs of them) a thread has in flight; measured (us): 1, 2 and 3 of them, 16384 tokens of 64 + 8
+// heads 88.4, 88.0, 87.1; 8192 tokens of 56 + 8 + 8 into the cache, where addresses take more registers,
+// 52.6, 48.9, 51.9.
 template <typename T, bool kHalf, bool kPages>
 __global__ void __launch_bounds__(kRotThreads)
 rotary_vec_kernel(const __grid_constant__ RotaryArgs args) {
     constexpr int V = Elem<T>::kPerVec;
-    constexpr int kU = 3;
+    constexpr int kU = kPages ? 2 : 3;
     __shared__ float2 cs[kRotMaxDim / 2];
     const ks_rotary_args_t &a = args.a;
     grid_dependency_wait();
     allow_dependents_launch();
     const int64_t token = blockIdx.x;
     const int column = threadIdx.x % args.columns, lane = threadIdx.x / args.columns;
-    const int lanes = kRotThreads / args.columns;
+    const int lanes = blockDim.x / args.columns;
     const int total = (int)(a.q_heads + a.kv_heads * (kPages ? 2 : 1));
     const int first = blockIdx.y * args.heads_per_y;
     const int last = min(total, first + args.heads_per_y);
@@ -134,8 +148,6 @@ rotary_vec_kernel(const __grid_constant__ RotaryArgs args) {
     const int at = (!kHalf || mine) ? column * V : (column + pairs) * V;
     const int at2 = at + pairs * V;
 
-    int64_t page = -1, in_page = 0;
-    if (kPages) rot_slot(a, token, &page, &in_page);
     uint4 x[kU], y[kU];
     const bool active = lane < lanes;
     auto load = [&](int base) {
@@ -143,14 +155,17 @@ rotary_vec_kernel(const __grid_constant__ RotaryArgs args) {
         for (int u = 0; u < kU; ++u) {
             const int slot = base + u * lanes;
             if (active && slot < last) {
-                const RotRow<T> r = rot_row<T, kPages>(a, token, slot, page, in_page);
-                x[u] = *reinterpret_cast<const uint4 *>(r.src + at);
-                if (kHalf && mine) y[u] = *reinterpret_cast<const uint4 *>(r.src + at2);
+                const T *src = rot_src<T>(a, token, slot);
+                x[u] = *reinterpret_cast<const uint4 *>(src + at);
+                if (kHalf && mine) y[u] = *reinterpret_cast<const uint4 *>(src + at2);
             }
         }
     };
+    const RotToken t = rot_token<kPages>(a, token);
     load(first + lane);
-    rot_table(a, token, cs);
+    rot_table(a, t, cs);
+    RotPage<T> page = {};
+    if (kPages) page = rot_page<T>(a, t.slot);
     __syncthreads();
     float2 turn[V];
     if (mine) {
@@ -166,9 +181,9 @@ rotary_vec_kernel(const __grid_constant__ RotaryArgs args) {
         for (int u = 0; u < kU; ++u) {
             const int slot = base + u * lanes;
             if (!active || slot >= last) break;
-            const RotRow<T> r = rot_row<T, kPages>(a, token, slot, page, in_page);
-            if (kPages && r.dst == nullptr) continue;
-            if (mine && r.rotate) {
+            T *dst = rot_dst<T, kPages>(a, token, slot, page);
+            if (kPages && dst == nullptr) continue;
+            if (mine && (!kPages || slot < a.q_heads + a.kv_heads)) {
                 float p[V];
                 Elem<T>::unpack(x[u], p);
                 if (kHalf) {
@@ -191,8 +206,8 @@ rotary_vec_kernel(const __grid_constant__ RotaryArgs args) {
                 }
                 x[u] = Elem<T>::pack(p);
             }
-            *reinterpret_cast<uint4 *>(r.dst + at) = x[u];
-            if (kHalf && mine) *reinterpret_cast<uint4 *>(r.dst + at2) = y[u];
+            *reinterpret_cast<uint4 *>(dst + at) = x[u];
+            if (kHalf && mine) *reinterpret_cast<uint4 *>(dst + at2) = y[u];
         }
     }
 }
@@ -209,31 +224,33 @@ rotary_scalar_kernel(const __grid_constant__ RotaryArgs args) {
     const int total = (int)(a.q_heads + a.kv_heads * (kPages ? 2 : 1));
     const int first = blockIdx.y * args.heads_per_y;
     const int last = min(total, first + args.heads_per_y);
-    int64_t page = -1, in_page = 0;
-    if (kPages) rot_slot(a, token, &page, &in_page);
-    rot_table(a, token, cs);
+    const RotToken t = rot_token<kPages>(a, token);
+    RotPage<T> page = {};
+    if (kPages) page = rot_page<T>(a, t.slot);
+    rot_table(a, t, cs);
     __syncthreads();
     const int pairs = (int)(a.rotary_dim / 2);
     const int n = (last - first) * args.columns;
-    for (int i = threadIdx.x; i < n; i += kRotThreads) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int slot = first + i / args.columns, column = i % args.columns;
-        const RotRow<T> r = rot_row<T, kPages>(a, token, slot, page, in_page);
-        if (kPages && r.dst == nullptr) continue;
+        const T *src = rot_src<T>(a, token, slot);
+        T *dst = rot_dst<T, kPages>(a, token, slot, page);
+        if (kPages && dst == nullptr) continue;
         if (column >= pairs) {  // not rotated
-            r.dst[column + pairs] = r.src[column + pairs];
+            dst[column + pairs] = src[column + pairs];
             continue;
         }
         const int i0 = kHalf ? column : 2 * column, i1 = kHalf ? column + pairs : 2 * column + 1;
-        const T x = r.src[i0], y = r.src[i1];
-        if (!r.rotate) {
-            r.dst[i0] = x;
-            r.dst[i1] = y;
+        const T x = src[i0], y = src[i1];
+        if (kPages && slot >= a.q_heads + a.kv_heads) {
+            dst[i0] = x;
+            dst[i1] = y;
             continue;
         }
         const float c = cs[column].x, s = cs[column].y;
         const float m = Elem<T>::load1(&x, 0), k = Elem<T>::load1(&y, 0);
-        Elem<T>::store1(r.dst, i0, fmaf(m, c, -k * s));
-        Elem<T>::store1(r.dst, i1, fmaf(k, c, m * s));
+        Elem<T>::store1(dst, i0, fmaf(m, c, -k * s));
+        Elem<T>::store1(dst, i1, fmaf(k, c, m * s));
     }
 }
 
@@ -407,6 +424,14 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
     parts = parts > most ? most : parts;
     k_args.heads_per_y = (total + parts - 1) / parts;
     parts = (total + k_args.heads_per_y - 1) / k_args.heads_per_y;
+    // As many threads as do the CTA's heads in equal rounds: with 72 heads of 8 columns, 3 rounds of 192
+    // threads, not 2 of 256 and a third of 64.
+    int threads = kRotThreads;
+    if (vec) {
+        const int rounds = (k_args.heads_per_y + lanes - 1) / lanes;
+        threads = ((k_args.heads_per_y + rounds - 1) / rounds * k_args.columns + 31) / 32 * 32;
+        threads = threads < 64 ? 64 : threads;
+    }
     const void *f;
     switch (a.dtype) {
     case KS_DTYPE_BF16: f = pages ? rotary_pick<__nv_bfloat16, true>(vec, half) : rotary_pick<__nv_bfloat16, false>(vec, half); break;
@@ -414,7 +439,7 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
     default: f = pages ? rotary_pick<float, true>(vec, half) : rotary_pick<float, false>(vec, half); break;
     }
     void *kp[] = {&k_args};
-    cudaError_t ce = launch_kernel(f, dim3((unsigned)T, (unsigned)parts), dim3(kRotThreads), 0, kp,
+    cudaError_t ce = launch_kernel(f, dim3((unsigned)T, (unsigned)parts), dim3((unsigned)threads), 0, kp,
                                    static_cast<cudaStream_t>(stream), launch_pdl_enabled());
     if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));
     return KS_SUCCESS;
