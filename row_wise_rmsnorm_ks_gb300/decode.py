@@ -71,9 +71,14 @@ def rotary_steps(rotary_dim: int, base: float = 10000.0, *, scaling: str | None 
 
 
 # A decode step is a few microseconds of GPU time, so the calls keep their own time on the host small:
-# the stream comes as its handle, and the device is only changed where it is not the current one.
+# each first asks everything in one expression, and goes through the checks one by one, which name what
+# is wrong, only if that fails; the stream comes as its handle; the device is only changed where it is
+# not the current one.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch.cuda.current_device
+_grad = torch.is_grad_enabled
+_I32, _I64 = torch.int32, torch.int64
+_INF = math.inf
 
 
 def _launch(call, args: bytes, device: torch.device) -> None:
@@ -151,14 +156,7 @@ def _turns(positions, steps, tokens, dim, device, scale):
     return positions.data_ptr(), steps.data_ptr(), 2 * steps.shape[0]
 
 
-def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, steps: torch.Tensor, *,
-           interleaved: bool = False, inverse: bool = False, scale: float = 1.0,
-           out: tuple | None = None) -> tuple:
-    """Rotates the first 2 * len(steps) values of every head of q and k (None: q alone) by each
-    token's position; the rest is copied. Pairs are (j, j + half), or neighbours with `interleaved`.
-    `inverse` turns back, which is also the gradient's turn. `out`: (q_out, k_out), each a tensor of
-    its input's shape that is the input itself (in place) or shares nothing with the inputs.
-    Returns (q_out, k_out)."""
+def _check_rotary(q, k, positions, steps, scale, out):
     _first(q, "q")
     dev, dt = q.device, q.dtype
     _rows(q, "q", dt, dev)
@@ -168,48 +166,76 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, ste
         if k.shape[0] != tokens or k.shape[2] != dim:
             raise ValueError("k must have q's tokens and head_dim")
     _inference(q, k)
-    pos_p, steps_p, rot = _turns(positions, steps, tokens, dim, dev, scale)
-    if out is None:
-        qo = torch.empty((tokens, hq, dim), dtype=dt, device=dev)
-        ko = None if k is None else torch.empty(tuple(k.shape), dtype=dt, device=dev)
-    else:
+    _turns(positions, steps, tokens, dim, dev, scale)
+    if out is not None:
         if not isinstance(out, (tuple, list)) or len(out) != 2 or (out[1] is None) != (k is None):
             raise ValueError("out must be (q_out, k_out), k_out None where k is")
-        qo, ko = out
-        for t, s, n in ((qo, q, "q_out"), (ko, k, "k_out")):
+        for t, s, n in ((out[0], q, "q_out"), (out[1], k, "k_out")):
             if s is not None:
                 _rows(t, n, dt, dev)
                 if t.shape != s.shape:
                     raise ValueError(f"{n} must have its input's shape")
-        _inference(qo, ko)
-    if dim == 0 or tokens == 0 or (hq == 0 and (k is None or k.shape[1] == 0)):
-        return qo, ko
-    hk = 0 if k is None else k.shape[1]
-    qs, qos = q.stride(), qo.stride()
-    if hk:
-        ks_, kos, k_p, ko_p = k.stride(), ko.stride(), k.data_ptr(), ko.data_ptr()
+        _inference(*out)
+
+
+def _turned(positions, steps, tokens, dim, dev):
+    """Whether positions and steps are as they must be, in one go."""
+    return (positions.dtype is _I64 and steps.dtype is _I64 and positions.shape == (tokens,)
+            and steps.dim() == 1 and 2 * steps.shape[0] <= dim and positions.device == dev
+            and steps.device == dev and positions.is_contiguous() and steps.is_contiguous())
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, steps: torch.Tensor, *,
+           interleaved: bool = False, inverse: bool = False, scale: float = 1.0,
+           out: tuple | None = None) -> tuple:
+    """Rotates the first 2 * len(steps) values of every head of q and k (None: q alone) by each
+    token's position; the rest is copied. Pairs are (j, j + half), or neighbours with `interleaved`.
+    `inverse` turns back, which is also the gradient's turn. `out`: (q_out, k_out), each a tensor of
+    its input's shape that is the input itself (in place) or shares nothing with the inputs.
+    Returns (q_out, k_out)."""
+    try:
+        dt, dev, code = q.dtype, q.device, _DTYPES[q.dtype]
+        tokens, hq, dim = q.shape
+        qs = q.stride()
+        fine = (out is None and k is not None and q.is_cuda and qs[2] == 1 and k.dtype is dt
+                and k.device == dev and -_INF < scale < _INF
+                and _turned(positions, steps, tokens, dim, dev)
+                and not (_grad() and (q.requires_grad or k.requires_grad)))
+        if fine:
+            kt, hk, kd = k.shape
+            ks_ = k.stride()
+            fine = kt == tokens and kd == dim and ks_[2] == 1
+    except (AttributeError, KeyError, ValueError, TypeError):
+        fine = False
+    if not fine:
+        _check_rotary(q, k, positions, steps, scale, out)
+        hk, ks_ = (k.shape[1], k.stride()) if k is not None else (0, (0, 0))
+    if out is None:
+        qo = torch.empty((tokens, hq, dim), dtype=dt, device=dev)
+        ko = None if k is None else torch.empty((tokens, hk, dim), dtype=dt, device=dev)
     else:
-        ks_ = kos = (0, 0)
-        k_p = ko_p = 0
-    args = _abi.ROTARY_ARGS.pack(
+        qo, ko = out
+    if dim == 0 or tokens == 0 or hq + hk == 0:
+        return qo, ko
+    if steps is None:
+        pos_p = steps_p = rot = 0
+    else:
+        pos_p, steps_p, rot = positions.data_ptr(), steps.data_ptr(), 2 * steps.shape[0]
+    qos = qo.stride()
+    if hk:
+        kos, k_p, ko_p = ko.stride(), k.data_ptr(), ko.data_ptr()
+    else:
+        kos, k_p, ko_p = (0, 0), 0, 0
+    _launch(_abi.ks_rotary, _abi.ROTARY_ARGS.pack(
         qo.data_ptr(), q.data_ptr(), ko_p, k_p, 0, pos_p, steps_p, 0, 0, 0,
         tokens, hq, hk, dim, rot, 0, 1, qos[0], qos[1], qs[0], qs[1], kos[0], kos[1], ks_[0], ks_[1],
         0, 0, 0, 0, 0, 0, 0, 0, scale,
         (_abi.KS_ROTARY_INTERLEAVED if interleaved else 0) | (_abi.KS_ROTARY_INVERSE if inverse else 0),
-        _DTYPES[dt], 0)
-    _launch(_abi.ks_rotary, args, dev)
+        code, 0), dev)
     return qo, ko
 
 
-def rotary_to_pages(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
-                    positions: torch.Tensor | None, steps: torch.Tensor | None,
-                    k_pages: torch.Tensor, v_pages: torch.Tensor, slots: torch.Tensor, *,
-                    interleaved: bool = False, scale: float = 1.0,
-                    out: torch.Tensor | None = None) -> torch.Tensor | None:
-    """rotary() with the keys and values landing in their cache: token t's rotated key and its value
-    go to slot slots[t] (page slots[t] // page_size, place slots[t] % page_size); a negative slot
-    writes neither. Slots of one call must differ. steps None: nothing is rotated; q None: only the
-    cache is written. Returns q_out (`out`, a new tensor, or None without q)."""
+def _check_to_pages(q, k, v, positions, steps, k_pages, v_pages, slots, scale, out):
     _first(k, "k")
     dev, dt = k.device, k.dtype
     _rows(k, "k", dt, dev)
@@ -229,29 +255,67 @@ def rotary_to_pages(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
         raise ValueError("k_pages and v_pages must have one shape")
     _index(slots, "slots", torch.int64, dev, (tokens,))
     _inference(q, k, v, k_pages, v_pages, out)
-    pos_p, steps_p, rot = _turns(positions, steps, tokens, dim, dev, scale)
+    _turns(positions, steps, tokens, dim, dev, scale)
     if q is None:
         if out is not None:
             raise ValueError("out without q")
-        hq, q_p, o_p, qs, qos = 0, 0, 0, (0, 0), (0, 0)
-    else:
-        if out is None:
-            out = torch.empty(tuple(q.shape), dtype=dt, device=dev)
-        else:
-            _rows(out, "out", dt, dev)
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-        hq, q_p, o_p, qs, qos = q.shape[1], q.data_ptr(), out.data_ptr(), q.stride(), out.stride()
+    elif out is not None:
+        _rows(out, "out", dt, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+
+
+def rotary_to_pages(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                    positions: torch.Tensor | None, steps: torch.Tensor | None,
+                    k_pages: torch.Tensor, v_pages: torch.Tensor, slots: torch.Tensor, *,
+                    interleaved: bool = False, scale: float = 1.0,
+                    out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """rotary() with the keys and values landing in their cache: token t's rotated key and its value
+    go to slot slots[t] (page slots[t] // page_size, place slots[t] % page_size); a negative slot
+    writes neither. Slots of one call must differ. steps None: nothing is rotated; q None: only the
+    cache is written. Returns q_out (`out`, a new tensor, or None without q)."""
+    try:
+        dt, dev, code = k.dtype, k.device, _DTYPES[k.dtype]
+        tokens, hk, dim = k.shape
+        ks_, vs, kp, vp = k.stride(), v.stride(), k_pages.stride(), v_pages.stride()
+        pages, page_size, pool_heads, pool_dim = shape = k_pages.shape
+        fine = (q is not None and out is None and k.is_cuda and hk > 0 and dim > 0 and page_size > 0
+                and v.shape == k.shape and pool_heads == hk and pool_dim == dim
+                and v_pages.shape == shape and ks_[2] == vs[2] == kp[3] == vp[3] == 1
+                and q.dtype is dt and v.dtype is dt and k_pages.dtype is dt and v_pages.dtype is dt
+                and q.device == dev and v.device == dev and k_pages.device == dev
+                and v_pages.device == dev and slots.dtype is _I64 and slots.device == dev
+                and slots.shape == (tokens,) and slots.is_contiguous() and -_INF < scale < _INF
+                and _turned(positions, steps, tokens, dim, dev)
+                and not (_grad() and (q.requires_grad or k.requires_grad or v.requires_grad
+                                      or k_pages.requires_grad or v_pages.requires_grad)))
+        if fine:
+            qt, hq, qd = q.shape
+            qs = q.stride()
+            fine = qt == tokens and qd == dim and qs[2] == 1
+    except (AttributeError, KeyError, ValueError, TypeError):
+        fine = False
+    if not fine:
+        _check_to_pages(q, k, v, positions, steps, k_pages, v_pages, slots, scale, out)
+        hq, qs = (q.shape[1], q.stride()) if q is not None else (0, (0, 0))
+    if q is not None and out is None:
+        out = torch.empty((tokens, hq, dim), dtype=dt, device=dev)
     if tokens == 0:
         return out
-    ks_, vs, kp, vp = k.stride(), v.stride(), k_pages.stride(), v_pages.stride()
-    args = _abi.ROTARY_ARGS.pack(
+    if q is None:
+        q_p, o_p, qos = 0, 0, (0, 0)
+    else:
+        q_p, o_p, qos = q.data_ptr(), out.data_ptr(), out.stride()
+    if steps is None:
+        pos_p = steps_p = rot = 0
+    else:
+        pos_p, steps_p, rot = positions.data_ptr(), steps.data_ptr(), 2 * steps.shape[0]
+    _launch(_abi.ks_rotary_to_pages, _abi.ROTARY_ARGS.pack(
         o_p, q_p, 0, k.data_ptr(), v.data_ptr(), pos_p, steps_p, k_pages.data_ptr(),
-        v_pages.data_ptr(), slots.data_ptr(), tokens, hq, hk, dim, rot, k_pages.shape[0],
-        k_pages.shape[1], qos[0], qos[1], qs[0], qs[1], 0, 0, ks_[0], ks_[1], vs[0], vs[1],
+        v_pages.data_ptr(), slots.data_ptr(), tokens, hq, hk, dim, rot, pages, page_size,
+        qos[0], qos[1], qs[0], qs[1], 0, 0, ks_[0], ks_[1], vs[0], vs[1],
         kp[0], kp[1], kp[2], vp[0], vp[1], vp[2], scale,
-        _abi.KS_ROTARY_INTERLEAVED if interleaved else 0, _DTYPES[dt], 0)
-    _launch(_abi.ks_rotary_to_pages, args, dev)
+        _abi.KS_ROTARY_INTERLEAVED if interleaved else 0, code, 0), dev)
     return out
 
 
@@ -272,24 +336,8 @@ def paged_attention_workspace(tokens: int, seqs: int, q_heads: int, kv_heads: in
     return need
 
 
-def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
-                    page_table: torch.Tensor, kv_lens: torch.Tensor, q_starts: torch.Tensor, *,
-                    scale: float | None = None, causal: bool = True, max_q_len: int | None = None,
-                    out: torch.Tensor | None = None,
-                    workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """Attention of new tokens over their sequences' pages (float16 or bfloat16).
-
-    q [tokens, q_heads, head_dim] holds the new tokens of all sequences, sequence b's being
-    q_starts[b] .. q_starts[b + 1] - 1; its keys and values, the new tokens' included, are the first
-    kv_lens[b] places of the pages in page_table[b]. page_table [seqs, n], kv_lens [seqs] and
-    q_starts [seqs + 1] are int32. Causal: the i-th of n new tokens sees kv_lens[b] - n + i + 1 keys;
-    a row that sees none comes out 0. scale: 1 / sqrt(head_dim) unless given.
-
-    max_q_len: the most new tokens of any sequence, where the caller knows it (1 for a decode step);
-    it only picks the kernel. `out`: a tensor of q's shape that shares nothing with q (rows outside
-    every sequence are left as they were; in a new tensor they are undefined). `workspace`: a uint8
-    CUDA tensor of at least paged_attention_workspace(...) bytes, for callers that keep one; calls
-    that may run at once need their own. Without it one is taken from torch's allocator per call."""
+def _check_attention(q, k_pages, v_pages, page_table, kv_lens, q_starts, scale, max_q_len, out,
+                     workspace):
     _first(q, "q")
     dev, dt = q.device, q.dtype
     if dt == torch.float32:
@@ -313,41 +361,90 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     _index(kv_lens, "kv_lens", torch.int32, dev, (seqs,))
     _index(q_starts, "q_starts", torch.int32, dev, (seqs + 1,))
     _inference(q, k_pages, v_pages, out)
-    if scale is None:
-        scale = 1.0 / math.sqrt(dim) if dim else 1.0
-    elif not (isinstance(scale, (int, float)) and math.isfinite(scale)):
+    if scale is not None and not (isinstance(scale, (int, float)) and math.isfinite(scale)):
         raise ValueError("scale must be finite")
     if max_q_len is not None and (not isinstance(max_q_len, int) or max_q_len < 0):
         raise ValueError("max_q_len must be a non-negative int")
-    if out is None:
-        out = torch.empty((tokens, hq, dim), dtype=dt, device=dev)
-    else:
+    if out is not None:
         _rows(out, "out", dt, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.device != dev
                                   or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+
+
+# Workspace sizes by device and sizes: asking the library takes longer than looking them up.
+_workspace_sizes: dict = {}
+
+
+def _workspace_size(dev, tokens, seqs, hq, hk, dim, page_size, table_pages, dtype, max_q_len):
+    key = (dev.index, tokens, seqs, hq, hk, dim, page_size, table_pages, dtype, max_q_len)
+    need = _workspace_sizes.get(key)
+    if need is None:
+        if len(_workspace_sizes) >= 4096:
+            _workspace_sizes.clear()
+        need = _workspace_sizes[key] = paged_attention_workspace(
+            tokens, seqs, hq, hk, dim, page_size, table_pages, dtype, max_q_len=max_q_len, device=dev)
+    return need
+
+
+def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                    page_table: torch.Tensor, kv_lens: torch.Tensor, q_starts: torch.Tensor, *,
+                    scale: float | None = None, causal: bool = True, max_q_len: int | None = None,
+                    out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of new tokens over their sequences' pages (float16 or bfloat16).
+
+    q [tokens, q_heads, head_dim] holds the new tokens of all sequences, sequence b's being
+    q_starts[b] .. q_starts[b + 1] - 1; its keys and values, the new tokens' included, are the first
+    kv_lens[b] places of the pages in page_table[b]. page_table [seqs, n], kv_lens [seqs] and
+    q_starts [seqs + 1] are int32. Causal: the i-th of n new tokens sees kv_lens[b] - n + i + 1 keys;
+    a row that sees none comes out 0. scale: 1 / sqrt(head_dim) unless given.
+
+    max_q_len: the most new tokens of any sequence, where the caller knows it (1 for a decode step);
+    it only picks the kernel. `out`: a tensor of q's shape that shares nothing with q (rows outside
+    every sequence are left as they were; in a new tensor they are undefined). `workspace`: a uint8
+    CUDA tensor of at least paged_attention_workspace(...) bytes, for callers that keep one; calls
+    that may run at once need their own. Without it one is taken from torch's allocator per call."""
+    try:
+        dt, dev, code = q.dtype, q.device, _DTYPES[q.dtype]
+        tokens, hq, dim = q.shape
+        pages, page_size, hk, pool_dim = shape = k_pages.shape
+        seqs, width = page_table.shape
+        qs, kp, vp = q.stride(), k_pages.stride(), v_pages.stride()
+        table_stride, in_row = page_table.stride()
+        fine = (out is None and workspace is None and code and q.is_cuda and hk > 0 and hq > 0
+                and hq % hk == 0 and pool_dim == dim and page_size > 0 and v_pages.shape == shape
+                and qs[2] == kp[3] == vp[3] == in_row == 1 and k_pages.dtype is dt
+                and v_pages.dtype is dt and page_table.dtype is _I32 and kv_lens.dtype is _I32
+                and q_starts.dtype is _I32 and k_pages.device == dev and v_pages.device == dev
+                and page_table.device == dev and kv_lens.device == dev and q_starts.device == dev
+                and kv_lens.shape == (seqs,) and q_starts.shape == (seqs + 1,)
+                and kv_lens.is_contiguous() and q_starts.is_contiguous()
+                and (scale is None or -_INF < scale < _INF) and (max_q_len is None or max_q_len >= 0)
+                and not (_grad() and (q.requires_grad or k_pages.requires_grad or v_pages.requires_grad)))
+    except (AttributeError, KeyError, ValueError, TypeError):
+        fine = False
+    if not fine or type(max_q_len) not in (int, type(None)):
+        _check_attention(q, k_pages, v_pages, page_table, kv_lens, q_starts, scale, max_q_len, out,
+                         workspace)
+    if scale is None:
+        scale = dim ** -0.5 if dim else 1.0
+    if out is None:
+        out = torch.empty((tokens, hq, dim), dtype=dt, device=dev)
     if tokens == 0 or seqs == 0:
         return out
-    qs, os_, kp, vp = q.stride(), out.stride(), k_pages.stride(), v_pages.stride()
-    head = (out.data_ptr(), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            page_table.data_ptr(), kv_lens.data_ptr(), q_starts.data_ptr())
-    tail = (tokens, seqs, hq, hk, dim, k_pages.shape[0], k_pages.shape[1], page_table.shape[1],
-            page_table.stride(0), max_q_len or 0, os_[0], os_[1], qs[0], qs[1], kp[0], kp[1], kp[2],
-            vp[0], vp[1], vp[2], scale, _abi.KS_ATTENTION_CAUSAL if causal else 0, _DTYPES[dt], 0)
     if workspace is None:
-        if _current_device() == dev.index:
-            st, need = _abi.ks_paged_attention_workspace(_abi.ATTENTION_ARGS.pack(*head, 0, 0, *tail))
-        else:
-            with torch.cuda.device(dev):
-                st, need = _abi.ks_paged_attention_workspace(_abi.ATTENTION_ARGS.pack(*head, 0, 0, *tail))
-        if st:
-            _abi.check(st)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_bytes = need
+        ws_bytes = _workspace_size(dev, tokens, seqs, hq, hk, dim, page_size, width, dt, max_q_len)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
-    _launch(_abi.ks_paged_attention,
-            _abi.ATTENTION_ARGS.pack(*head, workspace.data_ptr(), ws_bytes, *tail), dev)
+    os_ = out.stride()
+    _launch(_abi.ks_paged_attention, _abi.ATTENTION_ARGS.pack(
+        out.data_ptr(), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        kv_lens.data_ptr(), q_starts.data_ptr(), workspace.data_ptr(), ws_bytes, tokens, seqs, hq, hk,
+        dim, pages, page_size, width, table_stride, max_q_len or 0, os_[0], os_[1], qs[0], qs[1],
+        kp[0], kp[1], kp[2], vp[0], vp[1], vp[2], scale, _abi.KS_ATTENTION_CAUSAL if causal else 0,
+        code, 0), dev)
     return out
