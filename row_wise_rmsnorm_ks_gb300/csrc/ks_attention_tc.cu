@@ -347,180 +347,180 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
 
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kCopy) {
-        // ---- copies
-        const int page_size = (int)a.page_size, in_tile = min(page_size, kKeys);  // keys of a copy
-        const int part = lane / C::kHalves, half = lane % C::kHalves;
-        uint32_t at = 0;  // tiles copied so far: K and V of each step in turn
-        uint32_t queries = 0;
-        while (more) {
-            const AttnSpan span = attn_span(s, place.cur, place.q);
-            const int head = place.cur.head / s.head_splits, keys = place.q.keys;
-            const int32_t *table = a.page_table + (int64_t)place.cur.seq * a.table_stride;
-            bool ok = true;
-            for (int j = span.first; j < span.last && ok; ++j) {
-                const int key = j * kKeys + part * in_tile;
-                const bool wanted = part * in_tile < kKeys && key < keys;
-                int page = 0, slot = 0;
-                if (wanted) {
-                    page = __ldg(table + key / page_size);
-                    slot = key % page_size;
-                    if ((uint32_t)page >= (uint64_t)a.pages) {  // past the pool: the copy fills zeros
-                        atomicOr(&g_fault_flags, kFaultBadIndex);
-                        page = (int)a.pages;
+        if (warp == kCopy) {
+            // ---- copies
+            const int page_size = (int)a.page_size, in_tile = min(page_size, kKeys);  // keys of a copy
+            const int part = lane / C::kHalves, half = lane % C::kHalves;
+            uint32_t at = 0;  // tiles copied so far: K and V of each step in turn
+            uint32_t queries = 0;
+            while (more) {
+                const AttnSpan span = attn_span(s, place.cur, place.q);
+                const int head = place.cur.head / s.head_splits, keys = place.q.keys;
+                const int32_t *table = a.page_table + (int64_t)place.cur.seq * a.table_stride;
+                bool ok = true;
+                for (int j = span.first; j < span.last && ok; ++j) {
+                    const int key = j * kKeys + part * in_tile;
+                    const bool wanted = part * in_tile < kKeys && key < keys;
+                    int page = 0, slot = 0;
+                    if (wanted) {
+                        page = __ldg(table + key / page_size);
+                        slot = key % page_size;
+                        if ((uint32_t)page >= (uint64_t)a.pages) {  // past the pool: the copy fills zeros
+                            atomicOr(&g_fault_flags, kFaultBadIndex);
+                            page = (int)a.pages;
+                        }
                     }
-                }
-                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, wanted)) * in_tile * 128;
-                for (int v = 0; v < 2 && ok; ++v, ++at) {
-                    const uint32_t stage = at % C::kStages;
-                    ok = bar_wait_warp(empty + stage, (at / C::kStages & 1) ^ 1, gave_up);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(full + stage, bytes);
-                    __syncwarp();
-                    if (wanted)
-                        tma_load(ring + stage * C::kTileBytes + half * kHalfBytes + part * in_tile * 128,
-                                 v ? &v_map : &k_map, half * 64, slot, head, page, smem_addr(full + stage));
-                }
-                if (ok && j == span.first) {
-                    // The row tile's queries, as soon as the tile before has had its last product with
-                    // its own: a box of tile_heads heads and tile_tokens tokens comes in the rows' order.
-                    // Rows behind the sequence hold other tokens' queries (or zeros behind the last);
-                    // no row touches another.
-                    ok = bar_wait_warp(q_free, (queries++ & 1) ^ 1, gave_up);
-                    if (ok && lane == 0) {
-                        mbar_arrive_expect_tx(q_full, C::kHalves * s.tile_heads * s.tile_tokens * 128);
-                        const int first_head = head * s.group + place.cur.head % s.head_splits * s.tile_heads;
-                        const int token = place.q.q0 + place.cur.row_tile * s.tile_tokens;
-                        for (int h = 0; h < C::kHalves; ++h)
-                            tma_load3(q_addr + h * kRows * 128, &q_map, h * 64, first_head, token, smem_addr(q_full));
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, wanted)) * in_tile * 128;
+                    for (int v = 0; v < 2 && ok; ++v, ++at) {
+                        const uint32_t stage = at % C::kStages;
+                        ok = bar_wait_warp(empty + stage, (at / C::kStages & 1) ^ 1, gave_up);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(full + stage, bytes);
+                        __syncwarp();
+                        if (wanted)
+                            tma_load(ring + stage * C::kTileBytes + half * kHalfBytes + part * in_tile * 128,
+                                     v ? &v_map : &k_map, half * 64, slot, head, page, smem_addr(full + stage));
                     }
-                    __syncwarp();
-                }
-            }
-            more = ok && next_tile(s, place, span.cost);
-        }
-        if (queries) (void)mbar_wait_bounded(q_full, (queries - 1) & 1);
-        // nothing of this CTA's is in flight when it ends, also after a wait that gave up
-        const uint32_t from = at > (uint32_t)C::kStages ? at - C::kStages : 0;
-        for (uint32_t i = from; i < at; ++i) (void)mbar_wait_bounded(full + i % C::kStages, i / C::kStages & 1);
-    } else if (warp == kMma || warp == kMma + 2) {
-        // ---- matrix instructions of tile w, issued by one thread: for each step P V, then Q K of the
-        // next step. The two warps take turns, a whole batch each: the other tile's softmax runs beside
-        // a batch, and a warp has done its waiting when its turn comes. (Without turns the batches
-        // interleave, both softmaxes run at once and the tensor cores wait for them; one warp for both
-        // tiles spends a third of its time on barriers while the few instructions it can issue ahead
-        // run out. Measured at 8192 tokens over 16384 keys: both 1.2 to 1.4 ms.)
-        const int w = warp == kMma ? 0 : 1;
-        constexpr uint32_t qk = mma_shape<T>(kKeys, false), pv = mma_shape<T>(kDim, true);
-        const uint32_t s_at = tmem + w * 128, o_at = tmem + C::kO + w * 128;
-        const uint32_t q_low = desc_low(q_addr + w * kTile * 128, 16);
-        RingAt<C::kStages> k_at, v_at;  // the next step's keys, this step's values
-        uint32_t q_uses = 0, p_uses = 0, turns = 0;
-        uint32_t tails = 0;             // phase of each stage's tail barrier, a bit each
-        auto issue_qk = [&](uint32_t stage) {
-            const uint32_t k_low = desc_low(ring + stage * C::kTileBytes, 16);
-            mma_ss<false>(s_at, q_low, k_low, qk);
-#pragma unroll
-            for (int i = 1; i < kDim / 16; ++i)
-                mma_ss<true>(s_at, q_low + ((i / 4 * kRows * 128 + i % 4 * 32) >> 4),
-                             k_low + ((i / 4 * kHalfBytes + i % 4 * 32) >> 4), qk);
-            mma_commit(smem_addr(s_full + w));
-        };
-        while (more) {
-            const AttnSpan span = attn_span(s, place.cur, place.q);
-            const int first = warp_uniform(span.first), end = warp_uniform(span.last);
-            const int keys = warp_uniform(place.q.keys);
-            const bool two = warp_uniform(second_tile(s, place)) != 0;
-            if (first >= end) break;  // the share ends in the tile's extra cost
-            bool ok = bar_wait_warp(q_full, q_uses++ & 1, gave_up);
-            if (w == 1 && !two) {  // this tile has no rows: its share of the stages is given back
-                if (ok && lane == 0) bar_arrive(q_free);
-                for (int i = 2 * (end - first); i > 0 && ok; --i) {
-                    ok = bar_wait_warp(full + k_at.stage, k_at.phase, gave_up);
-                    if (i == 1 && keys < end * kKeys) tails ^= 1u << k_at.stage;
-                    if (ok && lane == 0) bar_arrive(empty + k_at.stage);
-                    k_at.next();
+                    if (ok && j == span.first) {
+                        // The row tile's queries, as soon as the tile before has had its last product with
+                        // its own: a box of tile_heads heads and tile_tokens tokens comes in the rows' order.
+                        // Rows behind the sequence hold other tokens' queries (or zeros behind the last);
+                        // no row touches another.
+                        ok = bar_wait_warp(q_free, (queries++ & 1) ^ 1, gave_up);
+                        if (ok && lane == 0) {
+                            mbar_arrive_expect_tx(q_full, C::kHalves * s.tile_heads * s.tile_tokens * 128);
+                            const int first_head = head * s.group + place.cur.head % s.head_splits * s.tile_heads;
+                            const int token = place.q.q0 + place.cur.row_tile * s.tile_tokens;
+                            for (int h = 0; h < C::kHalves; ++h)
+                                tma_load3(q_addr + h * kRows * 128, &q_map, h * 64, first_head, token, smem_addr(q_full));
+                        }
+                        __syncwarp();
+                    }
                 }
                 more = ok && next_tile(s, place, span.cost);
-                continue;
             }
-            ok = ok && bar_wait_warp(full + k_at.stage, k_at.phase, gave_up) &&
-                 (!two || bar_wait_warp(turn + w, turns++ & 1, gave_up));
-            if (!ok) break;
-            fence_after();
-            if (elect_one()) {
-                issue_qk(k_at.stage);
-                if (two) bar_arrive(turn + 1 - w);
-                mma_commit(smem_addr(empty + k_at.stage));
-                if (first + 1 == end) mma_commit(smem_addr(q_free));
-            }
-            __syncwarp();
-            v_at = k_at;
-            v_at.next();
-            for (int j = first; j < end; ++j) {
-                const bool last = j + 1 == end;
-                k_at = v_at;
-                k_at.next();
-                ok = bar_wait_warp(full + v_at.stage, v_at.phase, gave_up);
-                if (ok && keys < (j + 1) * kKeys) {
-                    ok = bar_wait_warp(tail + v_at.stage, tails >> v_at.stage & 1, gave_up);
-                    tails ^= 1u << v_at.stage;
+            if (queries) (void)mbar_wait_bounded(q_full, (queries - 1) & 1);
+            // nothing of this CTA's is in flight when it ends, also after a wait that gave up
+            const uint32_t from = at > (uint32_t)C::kStages ? at - C::kStages : 0;
+            for (uint32_t i = from; i < at; ++i) (void)mbar_wait_bounded(full + i % C::kStages, i / C::kStages & 1);
+        } else if (warp == kMma || warp == kMma + 2) {
+            // ---- matrix instructions of tile w, issued by one thread: for each step P V, then Q K of the
+            // next step. The two warps take turns, a whole batch each: the other tile's softmax runs beside
+            // a batch, and a warp has done its waiting when its turn comes. (Without turns the batches
+            // interleave, both softmaxes run at once and the tensor cores wait for them; one warp for both
+            // tiles spends a third of its time on barriers while the few instructions it can issue ahead
+            // run out. Measured at 8192 tokens over 16384 keys: both 1.2 to 1.4 ms.)
+            const int w = warp == kMma ? 0 : 1;
+            constexpr uint32_t qk = mma_shape<T>(kKeys, false), pv = mma_shape<T>(kDim, true);
+            const uint32_t s_at = tmem + w * 128, o_at = tmem + C::kO + w * 128;
+            const uint32_t q_low = desc_low(q_addr + w * kTile * 128, 16);
+            RingAt<C::kStages> k_at, v_at;  // the next step's keys, this step's values
+            uint32_t q_uses = 0, p_uses = 0, turns = 0;
+            uint32_t tails = 0;             // phase of each stage's tail barrier, a bit each
+            auto issue_qk = [&](uint32_t stage) {
+                const uint32_t k_low = desc_low(ring + stage * C::kTileBytes, 16);
+                mma_ss<false>(s_at, q_low, k_low, qk);
+#pragma unroll
+                for (int i = 1; i < kDim / 16; ++i)
+                    mma_ss<true>(s_at, q_low + ((i / 4 * kRows * 128 + i % 4 * 32) >> 4),
+                                 k_low + ((i / 4 * kHalfBytes + i % 4 * 32) >> 4), qk);
+                mma_commit(smem_addr(s_full + w));
+            };
+            while (more) {
+                const AttnSpan span = attn_span(s, place.cur, place.q);
+                const int first = warp_uniform(span.first), end = warp_uniform(span.last);
+                const int keys = warp_uniform(place.q.keys);
+                const bool two = warp_uniform(second_tile(s, place)) != 0;
+                if (first >= end) break;  // the share ends in the tile's extra cost
+                bool ok = bar_wait_warp(q_full, q_uses++ & 1, gave_up);
+                if (w == 1 && !two) {  // this tile has no rows: its share of the stages is given back
+                    if (ok && lane == 0) bar_arrive(q_free);
+                    for (int i = 2 * (end - first); i > 0 && ok; --i) {
+                        ok = bar_wait_warp(full + k_at.stage, k_at.phase, gave_up);
+                        if (i == 1 && keys < end * kKeys) tails ^= 1u << k_at.stage;
+                        if (ok && lane == 0) bar_arrive(empty + k_at.stage);
+                        k_at.next();
+                    }
+                    more = ok && next_tile(s, place, span.cost);
+                    continue;
                 }
-                if (!last) ok = ok && bar_wait_warp(full + k_at.stage, k_at.phase, gave_up);
-                ok = ok && bar_wait_warp(p_full + w, p_uses++ & 1, gave_up);
-                if (two) ok = ok && bar_wait_warp(turn + w, turns++ & 1, gave_up);
+                ok = ok && bar_wait_warp(full + k_at.stage, k_at.phase, gave_up) &&
+                     (!two || bar_wait_warp(turn + w, turns++ & 1, gave_up));
                 if (!ok) break;
                 fence_after();
                 if (elect_one()) {
-                    const uint32_t v_low = desc_low(ring + v_at.stage * C::kTileBytes, kHalfBytes);
-                    mma_ts(o_at, s_at, v_low, pv, j > first);
-#pragma unroll
-                    for (int i = 1; i < kKeys / 16; ++i) mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
-                    if (last) mma_commit(smem_addr(o_full + w));
-                    else issue_qk(k_at.stage);
+                    issue_qk(k_at.stage);
                     if (two) bar_arrive(turn + 1 - w);
-                    mma_commit(smem_addr(empty + v_at.stage));
-                    if (!last) mma_commit(smem_addr(empty + k_at.stage));
-                    if (j + 2 == end) mma_commit(smem_addr(q_free));
+                    mma_commit(smem_addr(empty + k_at.stage));
+                    if (first + 1 == end) mma_commit(smem_addr(q_free));
                 }
                 __syncwarp();
                 v_at = k_at;
                 v_at.next();
-            }
-            // k_at is the tile after the row tile's last values: the next row tile's first keys
-            more = ok && next_tile(s, place, span.cost);
-        }
-        // every instruction and arrival of this warp is done when it ends, also after a wait that gave up
-        if (elect_one()) mma_commit(smem_addr(done + w));
-        __syncwarp();
-        (void)mbar_wait_bounded(done + w, 0);
-    } else if (warp == kTail) {
-        // ---- the step a sequence ends in: value rows behind its last key hold anything, and a product
-        // with their probability 0 would let a NaN through, so they are set to 0. This warp follows every
-        // tile through the ring (a barrier's phases can be told apart one apart, no further).
-        uint32_t at = 0;
-        while (more) {
-            const AttnSpan span = attn_span(s, place.cur, place.q);
-            const int valid = place.q.keys - (span.last - 1) * kKeys;
-            bool ok = true;
-            for (uint32_t end = at + 2 * (span.last - span.first); at < end && ok; ++at) {
-                const uint32_t stage = at % C::kStages;
-                ok = bar_wait_warp(full + stage, at / C::kStages & 1, gave_up);
-                if (!ok) break;
-                if (at + 1 == end && valid < kKeys) {  // the row tile's last values
-                    uint8_t *v_tile = smem + (2 + stage) * C::kTileBytes;
-                    for (int h = 0; h < C::kHalves; ++h)
-                        for (uint32_t b = (uint32_t)max(valid, 0) * 128 + lane * 16; b < (uint32_t)kHalfBytes; b += 512)
-                            *reinterpret_cast<uint4 *>(v_tile + h * kHalfBytes + b) = make_uint4(0, 0, 0, 0);
-                    fence_async_smem();
+                for (int j = first; j < end; ++j) {
+                    const bool last = j + 1 == end;
+                    k_at = v_at;
+                    k_at.next();
+                    ok = bar_wait_warp(full + v_at.stage, v_at.phase, gave_up);
+                    if (ok && keys < (j + 1) * kKeys) {
+                        ok = bar_wait_warp(tail + v_at.stage, tails >> v_at.stage & 1, gave_up);
+                        tails ^= 1u << v_at.stage;
+                    }
+                    if (!last) ok = ok && bar_wait_warp(full + k_at.stage, k_at.phase, gave_up);
+                    ok = ok && bar_wait_warp(p_full + w, p_uses++ & 1, gave_up);
+                    if (two) ok = ok && bar_wait_warp(turn + w, turns++ & 1, gave_up);
+                    if (!ok) break;
+                    fence_after();
+                    if (elect_one()) {
+                        const uint32_t v_low = desc_low(ring + v_at.stage * C::kTileBytes, kHalfBytes);
+                        mma_ts(o_at, s_at, v_low, pv, j > first);
+#pragma unroll
+                        for (int i = 1; i < kKeys / 16; ++i) mma_ts(o_at, s_at + i * 8, v_low + i * (2048 >> 4), pv, 1u);
+                        if (last) mma_commit(smem_addr(o_full + w));
+                        else issue_qk(k_at.stage);
+                        if (two) bar_arrive(turn + 1 - w);
+                        mma_commit(smem_addr(empty + v_at.stage));
+                        if (!last) mma_commit(smem_addr(empty + k_at.stage));
+                        if (j + 2 == end) mma_commit(smem_addr(q_free));
+                    }
                     __syncwarp();
-                    if (lane == 0) bar_arrive(tail + stage);
+                    v_at = k_at;
+                    v_at.next();
                 }
-                if (lane == 0) bar_arrive(empty + stage);
+                // k_at is the tile after the row tile's last values: the next row tile's first keys
+                more = ok && next_tile(s, place, span.cost);
             }
-            more = ok && next_tile(s, place, span.cost);
+            // every instruction and arrival of this warp is done when it ends, also after a wait that gave up
+            if (elect_one()) mma_commit(smem_addr(done + w));
+            __syncwarp();
+            (void)mbar_wait_bounded(done + w, 0);
+        } else if (warp == kTail) {
+            // ---- the step a sequence ends in: value rows behind its last key hold anything, and a product
+            // with their probability 0 would let a NaN through, so they are set to 0. This warp follows every
+            // tile through the ring (a barrier's phases can be told apart one apart, no further).
+            uint32_t at = 0;
+            while (more) {
+                const AttnSpan span = attn_span(s, place.cur, place.q);
+                const int valid = place.q.keys - (span.last - 1) * kKeys;
+                bool ok = true;
+                for (uint32_t end = at + 2 * (span.last - span.first); at < end && ok; ++at) {
+                    const uint32_t stage = at % C::kStages;
+                    ok = bar_wait_warp(full + stage, at / C::kStages & 1, gave_up);
+                    if (!ok) break;
+                    if (at + 1 == end && valid < kKeys) {  // the row tile's last values
+                        uint8_t *v_tile = smem + (2 + stage) * C::kTileBytes;
+                        for (int h = 0; h < C::kHalves; ++h)
+                            for (uint32_t b = (uint32_t)max(valid, 0) * 128 + lane * 16; b < (uint32_t)kHalfBytes; b += 512)
+                                *reinterpret_cast<uint4 *>(v_tile + h * kHalfBytes + b) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(tail + stage);
+                    }
+                    if (lane == 0) bar_arrive(empty + stage);
+                }
+                more = ok && next_tile(s, place, span.cost);
+            }
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---- softmax: a warp has 16 rows, a quad of lanes a row pair (r0, r0 + 8): the layout in which the

@@ -439,6 +439,51 @@ def test_paged_attention_non_finite_keys_stay_in_their_sequence(cuda_device):
         check_rows(out[b:b + 1], st["q"][b:b + 1], st["k"][b], st["v"][b], 100, True, 64 ** -0.5, "neighbour")
 
 
+def test_chunks_beside_non_finite_neighbours(cuda_device):
+    """Row tiles reach into the next sequence's queries, and steps past a sequence's keys: what is not
+    finite there stays there."""
+    st = build([40, 7, 90], [150, 100, 200], 8, 2, 128, BF16, 16, cuda_device, seed=12)
+    st["q"][40:47] = math.nan
+    st["kp"][int(st["table"][1, 2]), 3] = math.inf
+    st["vp"][int(st["table"][1, 2]), 3] = math.nan
+    out = attend(st, max_q_len=90)
+    assert bool(out[40:47].isnan().all())
+    for b in (0, 2):
+        lo, n = st["s"][b], st["q_lens"][b]
+        check_rows(out[lo:lo + n], st["q"][lo:lo + n], st["k"][b], st["v"][b], st["kv_lens"][b], True,
+                   128 ** -0.5, "neighbour")
+
+
+@pytest.mark.parametrize("q_lens, kv_lens, hq, hk, dim, page_size", [
+    ([2000], [2000], 4, 1, 128, 128),          # many row tiles of one sequence, split among the CTAs
+    ([40, 3], [700, 2900], 320, 1, 64, 32),    # a group of more heads than a row tile has rows
+    ([1] * 40 + [600], [3000] * 40 + [900], 8, 4, 128, 64),
+    ([33], [33], 1, 1, 96, 8), ([17, 18, 19], [128, 256, 384], 2, 2, 112, 384),
+])
+def test_paged_attention_shapes_of_work(cuda_device, q_lens, kv_lens, hq, hk, dim, page_size):
+    st = build(q_lens, kv_lens, hq, hk, dim, BF16, page_size, cuda_device, seed=30)
+    check_all(attend(st, max_q_len=max(q_lens)), st)
+
+
+def test_broadcast_queries(cuda_device):
+    """A head stride of 0: one row for every head of the group."""
+    st = build([1, 30], [100, 200], 4, 2, 64, BF16, 16, cuda_device, seed=13)
+    row = st["q"][:, :1].clone()
+    st["q"] = row.expand(31, 4, 64)
+    check_all(attend(st), st)
+    pos = torch.arange(31)
+    y, _ = ks.rotary(st["q"], None, pos.to(cuda_device), ks.rotary_steps(64, device=cuda_device))
+    close(y, *rotated(st["q"], pos, freqs(64), False), "expanded")
+
+
+def test_workspace_never_grows_with_less(cuda_device):
+    def need(tokens, seqs, width, most):
+        return ks.paged_attention_workspace(tokens, seqs, 8, 2, 128, 16, width, BF16, max_q_len=most, device=cuda_device)
+    sizes = [need(t, s, w, m) for t, s, w, m in ((4096, 64, 512, 4096), (1000, 64, 512, 1000), (1000, 8, 512, 1000),
+                                                 (1000, 8, 5, 1000), (20, 8, 5, 20), (8, 8, 5, 1), (1, 1, 1, 1))]
+    assert sizes == sorted(sizes, reverse=True) and sizes[-1] > 0
+
+
 def test_paged_attention_bad_indices_are_reported(cuda_device):
     """A page outside the pool reads as zeros; lengths and starts are brought into range."""
     st = build([1, 2], [40, 30], 2, 1, 64, BF16, 16, cuda_device, seed=4, spoil=False)
