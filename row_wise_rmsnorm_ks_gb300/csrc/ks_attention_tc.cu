@@ -147,6 +147,9 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
@@ -301,6 +304,11 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     const int warp = warp_uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int cta = blockIdx.x, ctas = gridDim.x;
 
+    if (threadIdx.x == kThreads - 1) {  // the maps' descriptors, which the first copies would wait for
+        prefetch_map(&q_map);
+        prefetch_map(&k_map);
+        prefetch_map(&v_map);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(full + i, 1);
@@ -353,11 +361,30 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             const int part = lane / C::kHalves, half = lane % C::kHalves;
             uint32_t at = 0;  // tiles copied so far: K and V of each step in turn
             uint32_t queries = 0;
+            // A row tile's queries, as soon as the tile before has had its last product with its own: a
+            // box of tile_heads heads and tile_tokens tokens comes in the rows' order. Rows behind the
+            // sequence hold other tokens' queries (or zeros behind the last); no row touches another.
+            auto copy_queries = [&](int head) {
+                if (!bar_wait_warp(q_free, (queries++ & 1) ^ 1, gave_up)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, C::kHalves * s.tile_heads * s.tile_tokens * 128);
+                    const int first_head = head * s.group + place.cur.head % s.head_splits * s.tile_heads;
+                    const int token = place.q.q0 + place.cur.row_tile * s.tile_tokens;
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_load3(q_addr + h * kRows * 128, &q_map, h * 64, first_head, token, smem_addr(q_full));
+                }
+                __syncwarp();
+                return true;
+            };
             while (more) {
                 const AttnSpan span = attn_span(s, place.cur, place.q);
                 const int head = place.cur.head / s.head_splits, keys = place.q.keys;
                 const int32_t *table = a.page_table + (int64_t)place.cur.seq * a.table_stride;
                 bool ok = true;
+                // The first row tile's queries are copied before all else, later ones behind their first keys
+                // and values, which need not wait.
+                const uint32_t tile = queries;
+                if (tile == 0 && span.first < span.last) ok = copy_queries(head);
                 for (int j = span.first; j < span.last && ok; ++j) {
                     const int key = j * kKeys + part * in_tile;
                     const bool wanted = part * in_tile < kKeys && key < keys;
@@ -381,21 +408,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                             tma_load(ring + stage * C::kTileBytes + half * kHalfBytes + part * in_tile * 128,
                                      v ? &v_map : &k_map, half * 64, slot, head, page, smem_addr(full + stage));
                     }
-                    if (ok && j == span.first) {
-                        // The row tile's queries, as soon as the tile before has had its last product with
-                        // its own: a box of tile_heads heads and tile_tokens tokens comes in the rows' order.
-                        // Rows behind the sequence hold other tokens' queries (or zeros behind the last);
-                        // no row touches another.
-                        ok = bar_wait_warp(q_free, (queries++ & 1) ^ 1, gave_up);
-                        if (ok && lane == 0) {
-                            mbar_arrive_expect_tx(q_full, C::kHalves * s.tile_heads * s.tile_tokens * 128);
-                            const int first_head = head * s.group + place.cur.head % s.head_splits * s.tile_heads;
-                            const int token = place.q.q0 + place.cur.row_tile * s.tile_tokens;
-                            for (int h = 0; h < C::kHalves; ++h)
-                                tma_load3(q_addr + h * kRows * 128, &q_map, h * 64, first_head, token, smem_addr(q_full));
-                        }
-                        __syncwarp();
-                    }
+                    if (tile > 0 && j == span.first) ok = ok && copy_queries(head);
                 }
                 more = ok && next_tile(s, place, span.cost);
             }
@@ -535,6 +548,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         // normal number, whose products with finite scores vanish and which leaves -inf as it is.
         const float scale = fmaxf(fabsf(s.scale_log2), 1.17549435e-38f);
         const bool negative = s.scale_log2 < 0.0f;
+        // the thread's rows' tokens and heads within a row tile
+        const int r_token[2] = {r0 / s.tile_heads, (r0 + 8) / s.tile_heads};
+        const int r_head[2] = {r0 % s.tile_heads, (r0 + 8) % s.tile_heads};
+        const int warp_token = (w * kTile + sub) / s.tile_heads;
         uint32_t s_uses = 0, o_uses = 0;
         while (more) {
             const AttnSpan span = attn_span(s, place.cur, place.q);
@@ -551,13 +568,19 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 const AttnSeq q = place.q;
                 const int row_tile = place.cur.row_tile, sees = attn_tile_keys(s, q, row_tile);
                 const int first = q.keys - q.n + row_tile * s.tile_tokens + 1;
-                all_see = causal ? min(sees, first + (w * kTile + sub) / s.tile_heads) : sees;
+                all_see = causal ? min(sees, first + warp_token) : sees;
+                int kv_head = place.cur.head, split = 0;
+                if (s.head_splits > 1) {
+                    kv_head /= s.head_splits;
+                    split = place.cur.head - kv_head * s.head_splits;
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    int token, head;
-                    real[i] = attn_row(s, q.q0, q.n, place.cur.head, row_tile, r0 + 8 * i, &token, &head);
-                    limit[i] = causal ? min(sees, first + (r0 + 8 * i) / s.tile_heads) : sees;
-                    dst[i] = (T *)a.out + token * a.out_token_stride + head * a.out_head_stride;
+                    const int in_seq = row_tile * s.tile_tokens + r_token[i], in_group = split * s.tile_heads + r_head[i];
+                    real[i] = r_token[i] < s.tile_tokens && in_seq < q.n && in_group < s.group;
+                    limit[i] = causal ? min(sees, first + r_token[i]) : sees;
+                    dst[i] = (T *)a.out + (q.q0 + in_seq) * a.out_token_stride +
+                             (kv_head * s.group + in_group) * a.out_head_stride;
                 }
             }
 
@@ -676,20 +699,24 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             ok = bar_wait_warp(o_full + w, o_uses++ & 1, gave_up);
             if (!ok) break;
             fence_after();
-#pragma unroll 1
-            for (int c = 0; c < kDim / 32; ++c) {
-                uint32_t o[16];
-                tmem_load_rows16(o, o_at + c * 32);
-                tmem_wait_load();
-                if (!whole) {
+            uint32_t o[kDim / 64][32];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (c * 32 + i * 8 < dim)
-                            *attn_part(s, part, r0 / 16, c * 4 + i, lane) =
-                                make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-                    continue;
-                }
+            for (int c = 0; c < kDim / 64; ++c) tmem_load_rows32(o[c], o_at + c * 64);
+            tmem_wait_load();
+            fence_before();  // O is read before the next row tile's first product overwrites it
+            if (!whole) {
+#pragma unroll
+                for (int c = 0; c < kDim / 8; ++c)
+                    if (c * 8 < dim) {
+                        const uint32_t *y = o[c / 8] + c % 8 * 4;
+                        *attn_part(s, part, r0 / 16, c, lane) = make_float4(__uint_as_float(y[0]), __uint_as_float(y[1]),
+                                                                            __uint_as_float(y[2]), __uint_as_float(y[3]));
+                    }
+                continue;
+            }
+#pragma unroll
+            for (int c = 0; c < kDim / 32; ++c) {
+                const uint32_t *x = o[c / 2] + c % 2 * 16;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     // A lane has two columns of each of the chunk's four groups of 8; after the exchange
@@ -697,13 +724,13 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                     uint32_t y[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        y[i] = pack_pair<T>(__uint_as_float(o[4 * i + 2 * k]) * inv[k], __uint_as_float(o[4 * i + 2 * k + 1]) * inv[k]);
+                        y[i] = pack_pair<T>(__uint_as_float(x[4 * i + 2 * k]) * inv[k],
+                                            __uint_as_float(x[4 * i + 2 * k + 1]) * inv[k]);
                     quad_transpose(y, quad);
                     const int col = c * 32 + quad * 8;
                     if (real[k] && col < dim) *reinterpret_cast<uint4 *>(dst[k] + col) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
             }
-            fence_before();  // O is read before the next row tile's first product overwrites it
         }
     }
     __syncwarp();
