@@ -467,8 +467,8 @@ ks_status_t ks_rotary_to_pages(const ks_rotary_args_t *args, ks_stream_t stream)
  *
  * Errors: KS_ERR_UNSUPPORTED_DTYPE for KS_DTYPE_F32; KS_ERR_INVALID_ARGUMENT for sizes, NULL
  * pointers, data or strides that are not multiples of 16 bytes, a workspace that is too small;
- * KS_ERR_OVERLAP when out shares memory with q or the cache. tokens == 0 or seqs == 0 launches
- * nothing.
+ * KS_ERR_OVERLAP when out's bytes, first to last, cross those of q, the cache or the workspace.
+ * tokens == 0 or seqs == 0 launches nothing.
  */
 #define KS_ATTENTION_CAUSAL 1
 typedef struct ks_attention_args {

@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kRows = 16;                 // rows of a tile: one mma.m16n8k16 tile
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTileCost = 2;              // units that beginning and ending a row tile costs
+constexpr int kTileCost = 4;              // units that beginning and ending a row tile costs
 constexpr int kSub = 16;                  // keys of a warp's step
 constexpr int kUnit = kWarps * kSub;      // keys of a unit: a step of each warp (a power of two)
 
@@ -543,7 +543,8 @@ ks_status_t attn_check_sizes(const ks_attention_args_t &a) {
 
 ks_status_t attn_check_tensors(const ks_attention_args_t &a) {
     const int e = 2;
-    if (!std::isfinite(a.scale)) return fail(KS_ERR_INVALID_ARGUMENT, "scale must be finite");
+    if (!std::isfinite(a.scale * 1.4426950408889634f))
+        return fail(KS_ERR_INVALID_ARGUMENT, "scale (times log2 e) must be finite");
     if (a.tokens == 0 || a.seqs == 0) return KS_SUCCESS;
     if (!a.out || !a.q || !a.kv_lens || !a.q_starts || (a.table_pages > 0 && !a.page_table) ||
         (a.pages > 0 && (!a.k_pages || !a.v_pages)))
@@ -624,6 +625,10 @@ ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stre
     if (args->workspace_bytes < need)
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace has %lld bytes, %lld are needed",
                     (long long)args->workspace_bytes, (long long)need);
+    const int64_t out_bytes = ((args->tokens - 1) * args->out_token_stride + (args->q_heads - 1) * args->out_head_stride +
+                               args->head_dim) * 2;
+    if (overlaps(args->workspace, need, args->out, out_bytes))
+        return fail(KS_ERR_OVERLAP, "the workspace and out overlap");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t ce;
     if (p.kernel) {

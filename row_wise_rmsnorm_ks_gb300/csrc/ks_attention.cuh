@@ -37,6 +37,7 @@ struct AttnJoin {
 };
 
 constexpr int kJoinThreads = 128;
+constexpr int kMaxKeys = 0x7ffffc00;  // keys of a sequence: indices a few steps behind them still fit 31 bits
 
 // A sequence's new tokens [q0, q0 + n) and key count, brought into range (and reported) where the
 // given indices are not: nothing outside the tensors is ever addressed.
@@ -45,7 +46,7 @@ struct AttnSeq {
 };
 
 __device__ __forceinline__ AttnSeq attn_seq(const ks_attention_args_t &a, int b) {
-    const int64_t tokens = a.tokens, room = min(a.table_pages * a.page_size, (int64_t)0x7fffffff);
+    const int64_t tokens = a.tokens, room = min(a.table_pages * a.page_size, (int64_t)kMaxKeys);
     const int32_t q0 = a.q_starts[b], q1 = a.q_starts[b + 1], keys = a.kv_lens[b];
     AttnSeq s;
     s.q0 = (int32_t)min(max((int64_t)q0, (int64_t)0), tokens);

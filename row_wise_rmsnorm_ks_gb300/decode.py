@@ -78,7 +78,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch.cuda.current_device
 _grad = torch.is_grad_enabled
 _I32, _I64 = torch.int32, torch.int64
-_INF = math.inf
+_BIG = 2.0 ** 127  # what a scale may be: finite in 32 bits, times log2(e) too
 
 
 def _launch(call, args: bytes, device: torch.device) -> None:
@@ -142,8 +142,8 @@ def _first(t, name):
 
 def _turns(positions, steps, tokens, dim, device, scale):
     """Checks the positions and steps; returns their addresses and the rotated dimension."""
-    if not (isinstance(scale, (int, float)) and math.isfinite(scale)):
-        raise ValueError("scale must be finite")
+    if not (isinstance(scale, (int, float)) and -_BIG < scale < _BIG):
+        raise ValueError("scale must be finite (below 2^127)")
     if steps is None:
         return 0, 0, 0
     _index(positions, "positions", torch.int64, device, (tokens,))
@@ -198,7 +198,7 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, ste
         tokens, hq, dim = q.shape
         qs = q.stride()
         fine = (out is None and k is not None and q.is_cuda and qs[2] == 1 and k.dtype is dt
-                and k.device == dev and -_INF < scale < _INF
+                and k.device == dev and -_BIG < scale < _BIG
                 and _turned(positions, steps, tokens, dim, dev)
                 and not (_grad() and (q.requires_grad or k.requires_grad)))
         if fine:
@@ -285,7 +285,7 @@ def rotary_to_pages(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
                 and q.dtype is dt and v.dtype is dt and k_pages.dtype is dt and v_pages.dtype is dt
                 and q.device == dev and v.device == dev and k_pages.device == dev
                 and v_pages.device == dev and slots.dtype is _I64 and slots.device == dev
-                and slots.shape == (tokens,) and slots.is_contiguous() and -_INF < scale < _INF
+                and slots.shape == (tokens,) and slots.is_contiguous() and -_BIG < scale < _BIG
                 and _turned(positions, steps, tokens, dim, dev)
                 and not (_grad() and (q.requires_grad or k.requires_grad or v.requires_grad
                                       or k_pages.requires_grad or v_pages.requires_grad)))
@@ -361,10 +361,10 @@ def _check_attention(q, k_pages, v_pages, page_table, kv_lens, q_starts, scale, 
     _index(kv_lens, "kv_lens", torch.int32, dev, (seqs,))
     _index(q_starts, "q_starts", torch.int32, dev, (seqs + 1,))
     _inference(q, k_pages, v_pages, out)
-    if scale is not None and not (isinstance(scale, (int, float)) and math.isfinite(scale)):
-        raise ValueError("scale must be finite")
-    if max_q_len is not None and (not isinstance(max_q_len, int) or max_q_len < 0):
-        raise ValueError("max_q_len must be a non-negative int")
+    if scale is not None and not (isinstance(scale, (int, float)) and -_BIG < scale < _BIG):
+        raise ValueError("scale must be finite (below 2^127)")
+    if max_q_len is not None and not (isinstance(max_q_len, int) and 0 <= max_q_len < 2 ** 31):
+        raise ValueError("max_q_len must be an int in 0 .. 2^31 - 1")
     if out is not None:
         _rows(out, "out", dt, dev)
         if out.shape != q.shape:
@@ -422,7 +422,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                 and page_table.device == dev and kv_lens.device == dev and q_starts.device == dev
                 and kv_lens.shape == (seqs,) and q_starts.shape == (seqs + 1,)
                 and kv_lens.is_contiguous() and q_starts.is_contiguous()
-                and (scale is None or -_INF < scale < _INF) and (max_q_len is None or max_q_len >= 0)
+                and (scale is None or -_BIG < scale < _BIG)
+                and (max_q_len is None or 0 <= max_q_len < 2 ** 31)
                 and not (_grad() and (q.requires_grad or k_pages.requires_grad or v_pages.requires_grad)))
     except (AttributeError, KeyError, ValueError, TypeError):
         fine = False

@@ -98,7 +98,8 @@ def test_rotary_to_pages_refuses(change, status):
     (dict(head_dim=264), INVALID), (dict(q_heads=3), INVALID), (dict(kv_heads=0), INVALID),
     (dict(q_heads=0), INVALID), (dict(page_size=0), INVALID), (dict(pages=-1), INVALID),
     (dict(table_pages=-1), INVALID), (dict(table_stride=-4), INVALID), (dict(max_q_len=-1), INVALID),
-    (dict(flags=2), INVALID), (dict(scale=math.nan), INVALID), (dict(out=0), INVALID), (dict(q=0), INVALID),
+    (dict(flags=2), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=3e38), INVALID), (dict(out=0), INVALID),
+    (dict(q=0), INVALID),
     (dict(k_pages=0), INVALID), (dict(v_pages=0), INVALID), (dict(page_table=0), INVALID),
     (dict(kv_lens=0), INVALID), (dict(q_starts=0), INVALID), (dict(kv_lens=6 * FAKE + 2), INVALID),
     (dict(workspace=0), INVALID), (dict(workspace=8 * FAKE + 8), INVALID), (dict(q=2 * FAKE + 2), INVALID),

@@ -196,7 +196,7 @@ def test_rotary_empty_and_refusals(cuda_device):
                 lambda: ks.rotary(q, q, i, ks.rotary_steps(10, device=cuda_device)),
                 lambda: ks.rotary(q[0], None, i, steps), lambda: ks.rotary(q, None, i.cpu(), steps),
                 lambda: ks.rotary(q.transpose(1, 2), None, i, steps),
-                lambda: ks.rotary(q, None, i, steps, scale=math.inf),
+                lambda: ks.rotary(q, None, i, steps, scale=math.inf), lambda: ks.rotary(q, None, i, steps, scale=1e39),
                 lambda: ks.rotary(q, None, i, steps, out=(q, q)), lambda: ks.rotary(q, None, i, steps, out=q)):
         with pytest.raises(ValueError):
             bad()
@@ -577,8 +577,13 @@ def test_paged_attention_refusals(cuda_device):
     with pytest.raises(_abi.KsError):  # head rows that no 16-byte load reaches
         wide = torch.zeros(3, 4 * 64 + 4, dtype=BF16, device=cuda_device)
         attend({**st, "q": wide[:, 4:].view(3, 4, 64)})
-    with pytest.raises(ValueError):
-        attend(st, scale=math.nan)
+    for bad in (dict(scale=math.nan), dict(scale=1e39), dict(scale=-math.inf), dict(max_q_len=-1), dict(max_q_len=2 ** 40)):
+        with pytest.raises(ValueError):
+            attend(st, **bad)
+    with pytest.raises(_abi.KsError):  # the workspace over the output
+        need = ks.paged_attention_workspace(3, 2, 4, 2, 64, 16, st["table"].shape[1], BF16, device=cuda_device)
+        buf = torch.zeros(need + 4096, dtype=torch.uint8, device=cuda_device)
+        attend(st, workspace=buf, out=buf[:3 * 4 * 64 * 2].view(BF16).view(3, 4, 64))
     with pytest.raises(RuntimeError):
         attend({**st, "q": st["q"].clone().requires_grad_()})
 
@@ -659,6 +664,29 @@ def test_decoder_step_run(cuda_device):
         # the projection of other row counts may add up in another order: one more rounding step
         close(kp[pg, pl], want, tol + 2 * torch.finfo(BF16).eps * (want.abs() + 1), "keys")
         check_rows(torch.cat(outs[b]), torch.cat(qs[b]), kp[pg, pl], vp[pg, pl], n, True, dim ** -0.5, f"sequence {b}")
+
+
+def test_with_programmatic_dependent_launch(cuda_device):
+    """A chain of steps with every launch scheduled early: each kernel waits for the one before."""
+    st = build([1, 30, 2], [300, 200, 80], 8, 2, 128, BF16, 16, cuda_device, seed=9)
+    pos = torch.arange(33, device=cuda_device)
+    steps = ks.rotary_steps(128, device=cuda_device)
+
+    def chain():
+        x, got = st["q"], []
+        for _ in range(6):
+            x, _ = ks.rotary(x, None, pos, steps)
+            x = attend({**st, "q": x}, max_q_len=30)
+            got.append(x)
+        return got
+    want = chain()
+    assert _abi.ks_set_launch_options(_abi.KS_LAUNCH_PDL) == _abi.KS_SUCCESS
+    try:
+        got = chain()
+        torch.cuda.synchronize()
+    finally:
+        _abi.ks_set_launch_options(0)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_calls_on_another_stream(cuda_device):
