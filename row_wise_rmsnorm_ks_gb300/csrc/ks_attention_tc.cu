@@ -17,8 +17,11 @@
 // only then is it raised and O scaled. The quotient does not depend on the base, and FP32 sums and
 // 16-bit probabilities keep their relative precision at any size.
 //
-// Bound by the tensor cores for long chunks (2 * 128 * 128 * 2 * dim operations a step and tile).
-// For few rows of a tile it is a stream of the cache like the 16-row kernel's.
+// Bound by the tensor cores for long chunks: a step of both tiles is 32 instructions of 64 cycles at
+// dim 128. Measured: 8192 tokens over 16384 keys, 32 query and 8 key/value heads of 128, bf16, 0.96 ms
+// or 1.71 PFLOP/s (2650 cycles a step; the softmax of a tile is 850 to 1100 of them, beside the other
+// tile's products). Few rows of a tile make it a stream of the cache: 64 contexts of 6000 keys, 20 rows,
+// 296 us or 5.3 TB/s, by the copies that the five 32 KB tiles of shared memory let be in flight.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
