@@ -26,7 +26,8 @@ constexpr int kUnit = kWarps * kSub;      // keys of a unit: a step of each warp
 // two 16x8x16 matrix instructions, a tenth of the time its bytes take. Each warp therefore runs
 // alone on every fourth 16-key step, with its own ring of asynchronous 16-byte copies in shared
 // memory (no barrier in the loop), its own maximum, sum and output registers; the four are joined
-// when the row tile ends.
+// when the row tile ends. Bound by DRAM: 64 contexts of 700 to 8100 keys, 8 heads of 128, one token of
+// 64 query heads each, 201 us or 6.3 TB/s; 4 of 131000 keys 317 us or 6.6 TB/s.
 template <int kDim>
 struct Rows16 {
     static constexpr int kStages = kDim == 64 ? 4 : 3;
