@@ -390,11 +390,21 @@ attn_join_kernel(const __grid_constant__ AttnArgs s, int ctas) {
     const AttnJoin j = attn_joins(s, ctas)[c];
     if (j.pieces <= 0) return;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    int shares = 1;  // warps that share the pieces of one item
-    while (shares < kJoinWarps && shares * 4 < j.pieces) shares *= 2;
-    const int share = warp % shares, at_once = kJoinWarps / shares;
     const int rows = min(s.tile_tokens, j.q_len - j.row_tile * s.tile_tokens) * s.tile_heads;
     const int items = (rows + 15) / 16 * groups;
+    // Warps that share the pieces of one item: what leaves a warp the fewest chains of loads, its items
+    // times the fours of pieces that it takes of each.
+    int shares = 1, chains = 0x7fffffff;
+#pragma unroll
+    for (int n = 1; n <= kJoinWarps; n *= 2) {
+        const int at_once = gridDim.y * (kJoinWarps / n), fours = (j.pieces + 4 * n - 1) / (4 * n);
+        const int mine = (items + at_once - 1) / at_once * fours;
+        if (mine < chains) {
+            chains = mine;
+            shares = n;
+        }
+    }
+    const int share = warp % shares, at_once = kJoinWarps / shares;
     for (int first = blockIdx.y * at_once; first < items; first += gridDim.y * at_once) {
         const int item = first + warp / shares, group = item / groups, col = item % groups;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, acc[4] = {};
