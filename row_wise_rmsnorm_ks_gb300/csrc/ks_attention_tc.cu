@@ -483,8 +483,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                         tails ^= 1u << v_at.stage;
                     }
                     if (!last) ok = ok && bar_wait_warp(full + k_at.stage, k_at.phase, gave_up);
-                    ok = ok && bar_wait_warp(p_full + w, p_uses++ & 1, gave_up);
+                    // the probabilities last: they come later than the turn, and the products wait for them
                     if (two) ok = ok && bar_wait_warp(turn + w, turns++ & 1, gave_up);
+                    ok = ok && bar_wait_warp(p_full + w, p_uses++ & 1, gave_up);
                     if (!ok) break;
                     fence_after();
                     if (elect_one()) {
