@@ -242,7 +242,8 @@ ks_status_t ks_fused_add_rms_norm_planned(void *x, void *residual, const void *w
  * KS_FAULT_WAIT_TIMEOUT: a staged kernel gave up waiting for a bulk copy after about 2 s, left
  * its row loop and returned; its outputs are then incomplete; bit 1, KS_FAULT_BAD_INDEX: a slot,
  * page or length that ks_rotary_to_pages or ks_paged_attention read on the device was out of range
- * and its access was left out). Reading synchronises with the device. clear != 0 zeroes the words after reading. KS_ERR_CUDA if the read fails.
+ * and its access was left out). Reading synchronises with the device. clear != 0 zeroes the words
+ * after reading. KS_ERR_CUDA if the read fails.
  */
 #define KS_FAULT_WAIT_TIMEOUT 1
 #define KS_FAULT_BAD_INDEX 2
@@ -401,8 +402,9 @@ ks_status_t ks_layer_norm_planned(void *out, const void *x, const void *weight, 
  * be absent (its head count 0). ks_rotary_to_pages rotates q into q_out and k into the cache, and
  * copies v into it: token t's rows go to slot slots[t], that is page slots[t] / page_size, place
  * slots[t] % page_size. A negative slot writes neither row (a padding token); a slot past the pool
- * is left out too and sets KS_FAULT_BAD_INDEX. Slots of a call must differ: of two tokens with one
- * slot, either's values are left. rotary_dim 0 only writes the cache (steps and positions unread).
+ * is left out too and sets KS_FAULT_BAD_INDEX. Slots of a call must differ: where two tokens have
+ * one slot, a mixture of their values may be left. rotary_dim 0 only writes the cache (steps and
+ * positions unread).
  *
  * Errors as for ks_rms_norm: KS_ERR_INVALID_ARGUMENT for sizes, strides, alignment to the element
  * (indices: 8 bytes) or NULL pointers; KS_ERR_OVERLAP as above, and when the cache shares memory
@@ -446,7 +448,8 @@ ks_status_t ks_rotary_to_pages(const ks_rotary_args_t *args, ks_stream_t stream)
  * Sequence b has the packed tokens q_starts[b] .. q_starts[b + 1] - 1 and the first kv_lens[b]
  * keys of the pages that row b of the page table lists: key j is place j % page_size of page
  * page_table[b * table_stride + j / page_size]. With KS_ATTENTION_CAUSAL the i-th of n new tokens
- * sees the keys j < kv_lens[b] - n + i + 1, without it all of them; a row that sees none is 0.
+ * sees the keys j < kv_lens[b] - n + i + 1, without it all of them; a row that sees none, or whose
+ * scores are all -inf, is 0.
  * Query head h reads key/value head h / (q_heads / kv_heads). The same entry serves single
  * tokens, chunks of a prompt and batches of both; sequences may have no new token or no key.
  *
@@ -462,12 +465,14 @@ ks_status_t ks_rotary_to_pages(const ks_rotary_args_t *args, ks_stream_t stream)
  *
  * The workspace is device memory, 16-byte aligned, of at least the bytes that
  * ks_paged_attention_workspace gives for the same sizes on the current device (it reads the
- * struct's sizes, flags and dtype alone); its contents do not matter. Calls that may run at once need workspaces of their own. A captured call may be
- * replayed with other contents of kv_lens, q_starts and page_table.
+ * struct's sizes, flags and dtype alone); its contents do not matter. Calls that may run at once
+ * need workspaces of their own. A captured call may be replayed with other contents of kv_lens,
+ * q_starts and page_table.
  *
  * Errors: KS_ERR_UNSUPPORTED_DTYPE for KS_DTYPE_F32; KS_ERR_INVALID_ARGUMENT for sizes, NULL
  * pointers, data or strides that are not multiples of 16 bytes, a workspace that is too small;
- * KS_ERR_OVERLAP when out's bytes, first to last, cross those of q, the cache or the workspace.
+ * KS_ERR_OVERLAP when out's bytes, first to last, cross those of q, the cache or the workspace, or
+ * the workspace's those of q or the cache.
  * tokens == 0 or seqs == 0 launches nothing.
  */
 #define KS_ATTENTION_CAUSAL 1

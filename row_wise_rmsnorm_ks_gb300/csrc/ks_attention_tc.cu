@@ -19,7 +19,7 @@
 //
 // Bound by the tensor cores for long chunks: a step of both tiles is 32 instructions of 64 cycles at
 // dim 128. Measured: 8192 tokens over 16384 keys, 32 query and 8 key/value heads of 128, bf16, 0.92 ms
-// or 1.79 PFLOP/s (2500 cycles a step; the softmax of a tile is 850 to 1100 of them, beside the other
+// or 1.79 PFLOP/s (2580 cycles a step; the softmax of a tile is 850 to 1100 of them, beside the other
 // tile's products). Few rows of a tile make it a stream of the cache: 64 contexts of 6000 keys, 20 rows,
 // 296 us or 5.3 TB/s, by the copies that the five 32 KB tiles of shared memory let be in flight.
 #include <cuda.h>

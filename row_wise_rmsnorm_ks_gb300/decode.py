@@ -272,8 +272,8 @@ def rotary_to_pages(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
                     out: torch.Tensor | None = None) -> torch.Tensor | None:
     """rotary() with the keys and values landing in their cache: token t's rotated key and its value
     go to slot slots[t] (page slots[t] // page_size, place slots[t] % page_size); a negative slot
-    writes neither. Slots of one call must differ. steps None: nothing is rotated; q None: only the
-    cache is written. Returns q_out (`out`, a new tensor, or None without q)."""
+    writes neither. Slots of one call must differ (where two are one, a mixture of both tokens may be
+    left there). steps None: nothing is rotated; q None: only the cache is written. Returns q_out (`out`, a new tensor, or None without q)."""
     try:
         dt, dev, code = k.dtype, k.device, _DTYPES[k.dtype]
         tokens, hk, dim = k.shape

@@ -584,6 +584,12 @@ def test_paged_attention_refusals(cuda_device):
         need = ks.paged_attention_workspace(3, 2, 4, 2, 64, 16, st["table"].shape[1], BF16, device=cuda_device)
         buf = torch.zeros(need + 4096, dtype=torch.uint8, device=cuda_device)
         attend(st, workspace=buf, out=buf[:3 * 4 * 64 * 2].view(BF16).view(3, 4, 64))
+    for name in ("q", "kp", "vp"):  # and over what the call reads
+        size = st[name].numel() * 2
+        buf = torch.zeros(need + size, dtype=torch.uint8, device=cuda_device)
+        inside = buf[need - 16:need - 16 + size].view(BF16).view(st[name].shape)
+        with pytest.raises(_abi.KsError):
+            attend({**st, name: inside}, workspace=buf[:need])
     with pytest.raises(RuntimeError):
         attend({**st, "q": st["q"].clone().requires_grad_()})
 
