@@ -588,6 +588,8 @@ ks_status_t attn_check_tensors(const ks_attention_args_t &a) {
         if (counts[i] > 1 && strides[i] % 8)
             return fail(KS_ERR_INVALID_ARGUMENT, "strides must be multiples of 8 elements (16 bytes)");
     }
+    if ((__int128)a.table_stride * a.seqs > ((__int128)1 << 60))
+        return fail(KS_ERR_INVALID_ARGUMENT, "the page table is too large");
     if (((uintptr_t)a.q | (uintptr_t)a.out | (uintptr_t)a.k_pages | (uintptr_t)a.v_pages) & 15u)
         return fail(KS_ERR_INVALID_ARGUMENT, "q, out and the cache must be aligned to 16 bytes");
     const int64_t D = a.head_dim, T = a.tokens;

@@ -187,3 +187,8 @@ def test_cpu_tensors_are_refused():
         ks.paged_attention(q.half(), pool.half(), pool.half(), i.view(1, 2).int(), i[:1].int(), i.int())
     with pytest.raises(TypeError):
         ks.rotary(q.double(), None, i, ks.rotary_steps(8))
+
+
+@pytest.mark.parametrize("stride", [1 << 60, (1 << 63) - 1])
+def test_paged_attention_refuses_tables_beyond_64_bits(stride):
+    assert _abi.ks_paged_attention(attention_args(table_stride=stride), None) == INVALID
