@@ -192,3 +192,29 @@ def test_cpu_tensors_are_refused():
 @pytest.mark.parametrize("stride", [1 << 60, (1 << 63) - 1])
 def test_paged_attention_refuses_tables_beyond_64_bits(stride):
     assert _abi.ks_paged_attention(attention_args(table_stride=stride), None) == INVALID
+
+
+@pytest.mark.parametrize("change", [
+    dict(out=5 * FAKE), dict(out=6 * FAKE), dict(out=7 * FAKE),
+    dict(out=7 * FAKE - 1520),                               # q_starts lies in out's last row
+    dict(out=5 * FAKE + 4096, page_table=5 * FAKE, table_stride=1024),  # the table's second row
+])
+def test_paged_attention_refuses_outputs_over_its_indices(change):
+    """The kernels read lengths and tables while they write: other blocks would see other lengths."""
+    assert _abi.ks_paged_attention(attention_args(**change), None) == OVERLAP
+
+
+@pytest.mark.parametrize("change", [
+    dict(q_out=6 * FAKE), dict(q_out=7 * FAKE - 448), dict(k_out=6 * FAKE - 248), dict(k_out=7 * FAKE),
+])
+def test_rotary_refuses_outputs_over_its_indices(change):
+    assert _abi.ks_rotary(rotary_args(**change), None) == OVERLAP
+
+
+@pytest.mark.parametrize("change", [
+    dict(q_out=6 * FAKE), dict(q_out=7 * FAKE), dict(q_out=10 * FAKE), dict(k_pages=6 * FAKE),
+    dict(k_pages=10 * FAKE - 2040), dict(v_pages=7 * FAKE), dict(v_pages=10 * FAKE),
+    dict(v_pages=10 * FAKE, rotary_dim=0),
+])
+def test_rotary_to_pages_refuses_outputs_over_its_indices(change):
+    assert _abi.ks_rotary_to_pages(rotary_args(**change), None) == OVERLAP

@@ -705,3 +705,21 @@ def test_calls_on_another_stream(cuda_device):
     more = [attend(st) for _ in range(4)]  # at the same time on this one
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got + more)
+
+
+def test_paged_attention_refuses_a_workspace_over_its_indices(cuda_device):
+    st = build([1, 2], [40, 30], 2, 1, 64, BF16, 16, cuda_device, seed=14)
+    need = ks.paged_attention_workspace(3, 2, 2, 1, 64, 16, st["table"].shape[1], BF16, device=cuda_device)
+    for name in ("table", "kv", "starts"):
+        size = st[name].numel() * 4
+        for at in (0, need // 2 // 16 * 16, need - 16):
+            buf = torch.zeros(need + size, dtype=torch.uint8, device=cuda_device)
+            inside = buf[at:at + size].view(torch.int32).view(st[name].shape)
+            inside.copy_(st[name])
+            with pytest.raises(_abi.KsError):
+                attend({**st, name: inside}, workspace=buf[:need])
+        # behind the bytes that the call needs, in the same allocation, they are its own business
+        buf = torch.zeros(need + size, dtype=torch.uint8, device=cuda_device)
+        behind = buf[need:].view(torch.int32).view(st[name].shape)
+        behind.copy_(st[name])
+        check_all(attend({**st, name: behind}, workspace=buf), st, name=name)
