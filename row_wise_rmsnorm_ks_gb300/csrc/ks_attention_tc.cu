@@ -11,7 +11,7 @@
 //                    overwrites S and P behind it in order;
 //   warp 17          copies queries and pages to shared memory by TMA, for pages one lane per page and
 //                    64 columns;
-//   warp 19          clears value rows behind a sequence's last key.
+//   warp 19          clears value rows behind the last key that the row tile sees.
 // While one tile is in its softmax, the matrix instructions of the other run. A row's base is the
 // maximum of the first scores it saw until later probabilities pass 2^14 (of which fp16 holds 65504):
 // only then is it raised and O scaled. The quotient does not depend on the base, and FP32 sums and
@@ -445,7 +445,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             while (more) {
                 const AttnSpan span = attn_span(s, place.cur, place.q);
                 const int first = warp_uniform(span.first), end = warp_uniform(span.last);
-                const int keys = warp_uniform(place.q.keys);
+                const int keys = warp_uniform(attn_tile_keys(s, place.q, place.cur.row_tile));
                 const bool two = warp_uniform(second_tile(s, place)) != 0;
                 if (first >= end) break;  // the share ends in the tile's extra cost
                 bool ok = bar_wait_warp(q_full, q_uses++ & 1, gave_up);
@@ -512,13 +512,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             __syncwarp();
             (void)mbar_wait_bounded(done + w, 0);
         } else if (warp == kTail) {
-            // ---- the step a sequence ends in: value rows behind its last key hold anything, and a product
-            // with their probability 0 would let a NaN through, so they are set to 0. This warp follows every
-            // tile through the ring (a barrier's phases can be told apart one apart, no further).
+            // ---- the step a row tile's keys end in: value rows behind the last key that a row of it sees may
+            // hold anything (later tokens' values, or no token's), and a product with their probability 0 would
+            // let a NaN through, so they are set to 0. This warp follows every tile through the ring (a
+            // barrier's phases can be told apart one apart, no further).
             uint32_t at = 0;
             while (more) {
                 const AttnSpan span = attn_span(s, place.cur, place.q);
-                const int valid = place.q.keys - (span.last - 1) * kKeys;
+                const int valid = attn_tile_keys(s, place.q, place.cur.row_tile) - (span.last - 1) * kKeys;
                 bool ok = true;
                 for (uint32_t end = at + 2 * (span.last - span.first); at < end && ok; ++at) {
                     const uint32_t stage = at % C::kStages;

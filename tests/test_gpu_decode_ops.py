@@ -723,3 +723,29 @@ def test_paged_attention_refuses_a_workspace_over_its_indices(cuda_device):
         behind = buf[need:].view(torch.int32).view(st[name].shape)
         behind.copy_(st[name])
         check_all(attend({**st, name: behind}, workspace=buf), st, name=name)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("hq, hk, dim, n, keys", [
+    (32, 1, 128, 40, 100), (32, 1, 64, 40, 1000), (8, 2, 128, 200, 1003), (4, 4, 64, 700, 730), (300, 1, 64, 9, 140),
+])
+def test_keys_behind_a_row_tile_may_hold_anything(cuda_device, dtype, hq, hk, dim, n, keys):
+    """Later tokens' keys and values that are not finite reach no row tile before them, whichever kernel
+    the hint picks."""
+    st = build([n, 3], [keys, 50], hq, hk, dim, dtype, 16, cuda_device, seed=15)
+    group = hq // hk
+    for hint in (n, 1):
+        # tokens of a row tile: 256 rows, or 16 where the hinted tokens' rows fit them
+        tile = max(1, (16 if hint * group <= 16 else 256) // group)
+        for m in {tile, (n - 1) // tile * tile}:
+            if m >= n:
+                continue
+            bad = {**st, "kp": st["kp"].clone(), "vp": st["vp"].clone()}
+            seen = keys - n + m  # keys that the first m tokens see
+            for j in range(seen, keys):
+                page = int(st["table"][0, j // 16])
+                bad["kp"][page, j % 16], bad["vp"][page, j % 16] = (math.inf, math.nan) if j % 2 else (math.nan, -math.inf)
+            out = attend(bad, max_q_len=hint)
+            check_rows(out[:m], st["q"][:m], st["k"][0][:seen], st["v"][0][:seen], seen, True, dim ** -0.5,
+                       f"hint {hint}, {m} of {n} tokens")
+            check_rows(out[n:], st["q"][n:], st["k"][1], st["v"][1], 50, True, dim ** -0.5, "neighbour")
