@@ -455,7 +455,8 @@ ks_status_t ks_rotary_to_pages(const ks_rotary_args_t *args, ks_stream_t stream)
  * tokens, chunks of a prompt and batches of both; sequences may have no new token or no key.
  *
  * FP32 scores, maxima, sums and outputs, one rounding at the end; the probabilities are rounded
- * to the 16-bit type for the product with the values. Results are the same from run to run; a
+ * to the 16-bit type for the product with the values (in fp16 those below 2^-22 of a row's largest to
+ * multiples of 2^-32 of it). Results are the same from run to run; a
  * call of other sizes (or another max_q_len) may add up in another order.
  *
  * What is not part of a sequence is not read: table entries past its last page, and cache places

@@ -5,11 +5,14 @@
 //   m = max s_j, l = sum exp(s_j - m), o = sum exp(s_j - m) v_j / l
 // in one pass with a running maximum: when m grows, l and o are scaled by exp(m_old - m_new).
 // Scores, maxima, sums and outputs are FP32. The probabilities are rounded to the inputs' 16-bit
-// type for the second matrix product (relative error 2^-9 for bf16, 2^-12 for fp16, averaged over
-// the keys); the sum l adds them before that rounding.
+// type for the second matrix product, at most half a step relative to each (2^-9 for bf16, 2^-12 for
+// fp16); the sum l adds them before that rounding. fp16 is normal down to 2^-14 only, so that its
+// probabilities are taken 2^15 times as large as they are (l and o with them, which the quotient does
+// not depend on): they keep their precision down to 2^-29 of the row's largest and end at 2^-40.
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "ks_attention.cuh"
 
@@ -21,6 +24,8 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTileCost = 4;              // units that beginning and ending a row tile costs
 constexpr int kSub = 16;                  // keys of a warp's step
 constexpr int kUnit = kWarps * kSub;      // keys of a unit: a step of each warp (a power of two)
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 32768.0f : 1.0f;  // what a row's largest probability counts
 
 // Few rows make this a stream of the cache: per key of 128 values 512 bytes, 16 query rows cost
 // two 16x8x16 matrix instructions, a tenth of the time its bytes take. Each warp therefore runs
@@ -263,8 +268,8 @@ attn_rows16_kernel(const __grid_constant__ AttnArgs s) {
                 uint32_t p[4];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const float x0 = exp2_approx(sc[t][0] - b0), x1 = exp2_approx(sc[t][1] - b0);
-                    const float x2 = exp2_approx(sc[t][2] - b1), x3 = exp2_approx(sc[t][3] - b1);
+                    const float x0 = exp2_approx(sc[t][0] - b0) * kLift<T>, x1 = exp2_approx(sc[t][1] - b0) * kLift<T>;
+                    const float x2 = exp2_approx(sc[t][2] - b1) * kLift<T>, x3 = exp2_approx(sc[t][3] - b1) * kLift<T>;
                     l[0] += x0 + x1;
                     l[1] += x2 + x3;
                     p[2 * t] = pack16<T>(x0, x1);

@@ -749,3 +749,35 @@ def test_keys_behind_a_row_tile_may_hold_anything(cuda_device, dtype, hq, hk, di
             check_rows(out[:m], st["q"][:m], st["k"][0][:seen], st["v"][0][:seen], seen, True, dim ** -0.5,
                        f"hint {hint}, {m} of {n} tokens")
             check_rows(out[n:], st["q"][n:], st["k"][1], st["v"][1], 50, True, dim ** -0.5, "neighbour")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("tokens, seqs, dim", [(1, 640, 64), (1, 320, 256), (20, 160, 64), (20, 160, 128)])
+@pytest.mark.parametrize("at", [0, 5000, 15999])
+@pytest.mark.parametrize("below", [10.0, 14.0, 16.0, 17.4, 20.0])
+def test_many_small_probabilities_beside_a_large_one(cuda_device, dtype, tokens, seqs, dim, at, below):
+    """One key draws most of the attention, the others' scores lie `below` under it: what they weigh
+    together is kept. So many sequences (over the same pages) that a block has whole row tiles, all keys
+    to one base. Tolerance as in check_rows, but for fp16 with probabilities that count 2^8 at the
+    least for the largest: those below 2^-14 are off by 2^-25 at most, 2^-33 of the largest."""
+    keys, heads, page = 16000, 8, 64
+    kp = torch.zeros(keys // page, page, 1, dim, dtype=dtype, device=cuda_device)
+    vp = torch.ones_like(kp)
+    q = torch.zeros(seqs * tokens, heads, dim, dtype=dtype, device=cuda_device)
+    q[..., 0] = 4.0
+    kp[at // page, at % page, 0, 0] = below / 4
+    vp[at // page, at % page] = 0.0
+    table = torch.arange(keys // page, dtype=torch.int32, device=cuda_device).expand(seqs, -1)
+    lens = torch.full((seqs,), keys, dtype=torch.int32, device=cuda_device)
+    starts = torch.arange(0, (seqs + 1) * tokens, tokens, dtype=torch.int32, device=cuda_device)
+    out = ks.paged_attention(q, kp, vp, table, lens, starts, scale=1.0, causal=False, max_q_len=tokens)
+    score = 4.0 * float(kp[at // page, at % page, 0, 0])
+    rest = (keys - 1) * math.exp(-score)
+    want = rest / (1 + rest)
+    u = torch.finfo(dtype).eps / 2
+    tol = want * (u + 2 * ((dim + 8) * 2.0 ** -23 * score + 2.0 ** -21) + 4 * keys * 2.0 ** -23)
+    if dtype == F16:
+        tol += keys * 2.0 ** -33 / (1 + rest) + 2.0 ** -25
+    tol += u * (want + tol)
+    full = torch.full(out.shape, want, dtype=torch.float64, device=cuda_device)
+    close(out, full, torch.full_like(full, tol), f"{below} below")
