@@ -781,3 +781,27 @@ def test_many_small_probabilities_beside_a_large_one(cuda_device, dtype, tokens,
     tol += u * (want + tol)
     full = torch.full(out.shape, want, dtype=torch.float64, device=cuda_device)
     close(out, full, torch.full_like(full, tol), f"{below} below")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("negative", [False, True])
+@pytest.mark.parametrize("powers", [5, 7, 7.9, 8.1, 9, 13.9, 14.1, 15, 15.9, 16.1, 17, 24, 60])
+def test_scores_that_outgrow_the_first_keys(cuda_device, dtype, dim, negative, powers):
+    """Scores rise by that many powers of two behind the first keys, and fall again: bases that have
+    to be raised, just not, and probabilities at the ends of fp16."""
+    n, keys = 20, 400
+    st = build([n, 1], [keys, keys], 8, 2, dim, dtype, 16, cuda_device, seed=16, spoil=False)
+    ramp = torch.cat([torch.zeros(130), torch.linspace(0, 1, 150), torch.linspace(1, 0.2, 120)]) * powers * math.log(2)
+    st["q"][..., 0] = 4.0
+    for b in range(2):
+        k = st["k"][b]
+        k[..., 0] = (ramp[:, None] / 4).to(cuda_device).to(dtype)
+        k[..., 1:] *= 0.1
+        if negative:
+            k.neg_()
+        for c in range(keys // 16):
+            st["kp"][int(st["table"][b, c])] = k[16 * c:16 * c + 16]
+    scale = -1.0 if negative else 1.0
+    for hint in (n, 1):
+        check_all(attend(st, scale=scale, max_q_len=hint), st, scale=scale, name=f"hint {hint}")
