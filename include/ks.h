@@ -396,7 +396,8 @@ ks_status_t ks_layer_norm_planned(void *out, const void *x, const void *weight, 
  *
  * Tensors are [tokens, heads, head_dim] with contiguous head rows; strides are in elements. An
  * output may be exactly its input (in place); otherwise it must not share memory with any input.
- * The parts of one fused projection (one token stride) count as apart.
+ * Views of the same strides may alternate at any level (the parts of one fused projection, per token or
+ * per head); with different strides what lies between the first and the last byte counts as shared.
  *
  * ks_rotary writes q_out and k_out (v, the cache and slots are not looked at); either side may
  * be absent (its head count 0). ks_rotary_to_pages rotates q into q_out and k into the cache, and

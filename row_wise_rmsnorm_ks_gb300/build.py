@@ -22,7 +22,8 @@ LIB = os.path.join(OUT_DIR, "libks.so")
 SOURCES = ["ks_abi.cu", "ks_host.cu", "ks_noalloc.cu", "ks_ops.cu", "ks_launch_bf16.cu",
            "ks_launch_f16.cu", "ks_launch_f32.cu", "ks_rotary.cu", "ks_attention.cu",
            "ks_attention_tc.cu"]
-HEADERS = ["ks_kernels.cuh", "ks_internal.h", "ks_ptx.cuh", "ks_attention.cuh", "ks_decode.cuh"]
+HEADERS = ["ks_kernels.cuh", "ks_internal.h", "ks_ptx.cuh", "ks_attention.cuh", "ks_decode.cuh",
+           "ks_strided.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -22,6 +22,7 @@
 #include <cmath>
 
 #include "ks_decode.cuh"
+#include "ks_strided.h"
 
 namespace ks {
 namespace {
@@ -279,28 +280,8 @@ bool view_span(const View &v, int64_t tokens, int64_t dim, int e, int64_t *span)
     return true;
 }
 
-// Rows of an output must not share elements: tokens outside heads or heads outside tokens.
-bool distinct_rows(const View &v, int64_t tokens, int64_t dim) {
-    const bool heads_inner = (v.heads == 1 || v.head >= dim) &&
-                             (tokens == 1 || v.token >= (v.heads - 1) * v.head + dim);
-    const bool tokens_inner = (tokens == 1 || v.token >= dim) &&
-                              (v.heads == 1 || v.head >= (tokens - 1) * v.token + dim);
-    return heads_inner || tokens_inner;
-}
-
-// Whether two views share memory. Byte ranges that cross may still interleave, as the parts of
-// one fused projection do: with one token stride, each token's parts are compared.
-bool views_cross(const View &x, const View &y, int64_t tokens, int64_t dim, int e) {
-    int64_t nx = 0, ny = 0;
-    view_span(x, tokens, dim, e, &nx);
-    view_span(y, tokens, dim, e, &ny);
-    if (!overlaps(x.p, nx, y.p, ny)) return false;
-    const int64_t row = x.token * e;
-    const int64_t wx = ((x.heads - 1) * x.head + dim) * e, wy = ((y.heads - 1) * y.head + dim) * e;
-    if (x.token != y.token || tokens == 1 || wx > row || wy > row) return true;
-    int64_t d = (int64_t)((intptr_t)y.p - (intptr_t)x.p) % row;
-    if (d < 0) d += row;
-    return !(d >= wx && row - d >= wy);
+Strided strided(const View &v, int64_t tokens, int64_t dim, int e) {
+    return {v.p, dim * e, {tokens, v.heads, 1}, {v.token * e, v.head * e, 0}};
 }
 
 struct PoolView {
@@ -316,8 +297,7 @@ bool pool_span(const PoolView &v, const ks_rotary_args_t &a, int e, int64_t *spa
     if (last * e > ((__int128)1 << 62)) return false;
     *span = (int64_t)last * e;
     if (a.pages > 1 && v.page < in) return false;
-    const View rows = {v.p, v.slot, v.head, a.kv_heads};
-    return distinct_rows(rows, a.page_size, a.head_dim);
+    return strided_rows_apart({v.p, a.head_dim * e, {a.page_size, a.kv_heads, 1}, {v.slot * e, v.head * e, 0}});
 }
 
 // Whether n bytes at p cross the positions, the steps or the slots that the call reads. Every CTA reads
@@ -374,7 +354,7 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
     }
     for (int i = 0; i < 2; ++i) {
         if (!out[i]) continue;
-        if (!distinct_rows(*out[i], T, D))
+        if (!strided_rows_apart(strided(*out[i], T, D, e)))
             return fail(KS_ERR_OVERLAP, "rows of an output share storage");
         view_span(*out[i], T, D, e, &span);
         if (crosses_indices(a, pages, out[i]->p, span))
@@ -383,11 +363,11 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
             if (!in[j]) continue;
             const bool same = i == j && out[i]->p == in[j]->p && (T == 1 || out[i]->token == in[j]->token) &&
                               (out[i]->heads == 1 || out[i]->head == in[j]->head);
-            if (!same && views_cross(*out[i], *in[j], T, D, e))
+            if (!same && strided_cross(strided(*out[i], T, D, e), strided(*in[j], T, D, e)))
                 return fail(KS_ERR_OVERLAP, "an output overlaps an input without being exactly it");
         }
     }
-    if (out[0] && out[1] && views_cross(qo, ko, T, D, e))
+    if (out[0] && out[1] && strided_cross(strided(qo, T, D, e), strided(ko, T, D, e)))
         return fail(KS_ERR_OVERLAP, "q_out and k_out storage overlap");
     if (pages && a.pages > 0) {
         const PoolView pools[2] = {{a.k_pages, a.k_page_stride, a.k_slot_stride, a.k_pages_head_stride},

@@ -1,6 +1,8 @@
 """The decode operators' refusals and host-side parts on CPU: every call below fails its checks
 before any CUDA call (addresses are never read), and rotary_steps is plain arithmetic."""
 import math
+import os
+import subprocess
 
 import pytest
 import torch
@@ -218,3 +220,22 @@ def test_rotary_refuses_outputs_over_its_indices(change):
 ])
 def test_rotary_to_pages_refuses_outputs_over_its_indices(change):
     assert _abi.ks_rotary_to_pages(rotary_args(**change), None) == OVERLAP
+
+
+def test_strided_tensors_are_told_apart(tmp_path):
+    """The host's overlap checks against counting bytes (strided_check.cpp)."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = tmp_path / "strided_check"
+    subprocess.run(["g++", "-std=c++17", "-O2", "-Wall", "-Wextra", "-Werror", f"-I{ks_build.CSRC}",
+                    os.path.join(here, "strided_check.cpp"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+
+
+@pytest.mark.parametrize("change", [
+    # [tokens, heads, 2, dim] projections whose parts cross by one element, from either side
+    dict(q_out=2 * FAKE + 4 * 15, qo_t=64, qo_h=32, q_t=64, q_h=32), dict(q_out=2 * FAKE - 4 * 15, qo_t=64, qo_h=32, q_t=64, q_h=32),
+    dict(k_out=2 * FAKE + 4 * 17, ko_t=64, ko_h=32, q_t=64, q_h=32),
+])
+def test_rotary_refuses_alternating_parts_that_cross(change):
+    assert _abi.ks_rotary(rotary_args(**change), None) == OVERLAP

@@ -805,3 +805,28 @@ def test_scores_that_outgrow_the_first_keys(cuda_device, dtype, dim, negative, p
     scale = -1.0 if negative else 1.0
     for hint in (n, 1):
         check_all(attend(st, scale=scale, max_q_len=hint), st, scale=scale, name=f"hint {hint}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens", [1, 23])
+@pytest.mark.parametrize("order", ["parts_inside_heads", "heads_inside_parts", "head_major"])
+def test_rotary_in_place_on_parts_that_alternate(cuda_device, dtype, tokens, order):
+    """q, k and v interleaved in one projection, per head or per token: views that share no element."""
+    heads, dim = 6, 64
+    if order == "parts_inside_heads":
+        both = normal((tokens, heads, 3, dim), dtype, 1, cuda_device)
+        q, k, v = both.unbind(2)
+    elif order == "heads_inside_parts":
+        both = normal((tokens, 3, heads, dim), dtype, 1, cuda_device)
+        q, k, v = both.unbind(1)
+    else:
+        both = normal((heads, tokens, 3, dim), dtype, 1, cuda_device)
+        q, k, v = (t.transpose(0, 1) for t in both.unbind(2))
+    pos = torch.arange(tokens) * 77 + 5
+    steps = ks.rotary_steps(dim, device=cuda_device)
+    (wq, tq), (wk, tk) = rotated(q, pos, freqs(dim), False), rotated(k, pos, freqs(dim), False)
+    before = v.clone()
+    ks.rotary(q, k, pos.to(cuda_device), steps, out=(q, k))
+    close(q, wq, tq, "q")
+    close(k, wk, tk, "k")
+    assert torch.equal(v, before)
