@@ -289,15 +289,18 @@ struct PoolView {
     int64_t page, slot, head;
 };
 
-// The pool's span, and that its rows are apart: head and slot strides in either order inside a page.
+Strided strided(const PoolView &v, const ks_rotary_args_t &a, int e) {
+    return {v.p, a.head_dim * e, {a.pages, a.page_size, a.kv_heads}, {v.page * e, v.slot * e, v.head * e}};
+}
+
+// The pool's span, and that its rows are apart, whatever the order of its axes.
 bool pool_span(const PoolView &v, const ks_rotary_args_t &a, int e, int64_t *span) {
     if (v.page < 0 || v.slot < 0 || v.head < 0) return false;
-    const __int128 in = (__int128)(a.page_size - 1) * v.slot + (__int128)(a.kv_heads - 1) * v.head + a.head_dim;
-    const __int128 last = (__int128)(a.pages - 1) * v.page + in;
+    const __int128 last = (__int128)(a.pages - 1) * v.page + (__int128)(a.page_size - 1) * v.slot +
+                          (__int128)(a.kv_heads - 1) * v.head + a.head_dim;
     if (last * e > ((__int128)1 << 62)) return false;
     *span = (int64_t)last * e;
-    if (a.pages > 1 && v.page < in) return false;
-    return strided_rows_apart({v.p, a.head_dim * e, {a.page_size, a.kv_heads, 1}, {v.slot * e, v.head * e, 0}});
+    return strided_rows_apart(strided(v, a, e));
 }
 
 // Whether n bytes at p cross the positions, the steps or the slots that the call reads. Every CTA reads

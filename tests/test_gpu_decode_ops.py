@@ -830,3 +830,45 @@ def test_rotary_in_place_on_parts_that_alternate(cuda_device, dtype, tokens, ord
     close(q, wq, tq, "q")
     close(k, wk, tk, "k")
     assert torch.equal(v, before)
+
+
+def write_and_read_pools(device, order, page_size, heads):
+    """Pools of that memory order, written by rotary_to_pages and read by the attention over them."""
+    pages, dim = 12, 64
+    shape = {"page_parts": (pages, 2, page_size, heads, dim), "slot_parts": (pages, page_size, 2, heads, dim),
+             "head_parts": (pages, page_size, heads, 2, dim), "dim_parts": (pages, page_size, heads, 2 * dim),
+             "heads_outermost": (2, heads, pages, page_size, dim), "slots_outermost": (2, page_size, pages, heads, dim),
+             "layers": (pages, 3, 2, heads, page_size, dim)}[order]
+    both = normal(shape, F16, 1, device)
+    kp, vp = {"page_parts": lambda: both.unbind(1), "slot_parts": lambda: both.unbind(2),
+              "head_parts": lambda: both.unbind(3), "dim_parts": lambda: both.split(dim, 3),
+              "heads_outermost": lambda: [t.permute(1, 2, 0, 3) for t in both],
+              "slots_outermost": lambda: [t.transpose(0, 1) for t in both],
+              "layers": lambda: [both[:, 1, i].transpose(1, 2) for i in range(2)]}[order]()
+    assert kp.shape == vp.shape == (pages, page_size, heads, dim)
+    before = both.clone()
+    n = min(40, pages * page_size - 2)
+    k, v, q = (normal((n, h, dim), F16, 2 + i, device) for i, h in enumerate((heads, heads, 2 * heads)))
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(4)).int()[None].to(device)
+    t = torch.arange(n, device=device)
+    slots = table[0].long()[t // page_size] * page_size + t % page_size
+    ks.rotary_to_pages(None, k, v, None, None, kp, vp, slots)
+    assert torch.equal(kp[slots // page_size, slots % page_size], k)
+    assert torch.equal(vp[slots // page_size, slots % page_size], v)
+    i32 = dict(dtype=torch.int32, device=device)
+    for hint in (1, n):
+        out = ks.paged_attention(q, kp, vp, table, torch.tensor([n], **i32), torch.tensor([0, n], **i32), max_q_len=hint)
+        check_rows(out, q, k, v, n, True, dim ** -0.5, f"{order} hint {hint}")
+    kp[slots // page_size, slots % page_size] = 0
+    vp[slots // page_size, slots % page_size] = 0
+    after = both.clone()
+    both.copy_(before)
+    kp[slots // page_size, slots % page_size] = 0
+    vp[slots // page_size, slots % page_size] = 0
+    assert torch.equal(both, after), "nothing else was written"
+
+
+@pytest.mark.parametrize("order", ["heads_outermost", "slots_outermost"])
+@pytest.mark.parametrize("page_size, heads", [(16, 2), (1, 3), (5, 1)])
+def test_pools_whose_pages_are_not_the_outermost_axis(cuda_device, order, page_size, heads):
+    write_and_read_pools(cuda_device, order, page_size, heads)
