@@ -405,7 +405,7 @@ ks_status_t ks_layer_norm_planned(void *out, const void *x, const void *weight, 
  * slots[t] % page_size. A negative slot writes neither row (a padding token); a slot past the pool
  * is left out too and sets KS_FAULT_BAD_INDEX. Slots of a call must differ: where two tokens have
  * one slot, a mixture of their values may be left. rotary_dim 0 only writes the cache (steps and
- * positions unread).
+ * positions unread). k_pages and v_pages may alternate at any level, as the other views may.
  *
  * Errors as for ks_rms_norm: KS_ERR_INVALID_ARGUMENT for sizes, strides, alignment to the element
  * (indices: 8 bytes) or NULL pointers; KS_ERR_OVERLAP as above, when the cache shares memory

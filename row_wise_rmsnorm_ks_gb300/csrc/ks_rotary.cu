@@ -392,16 +392,8 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
                     return fail(KS_ERR_OVERLAP, "the cache overlaps q, k, v or q_out");
             }
         }
-        const bool one = a.k_page_stride == a.v_page_stride && a.k_slot_stride == a.v_slot_stride;
-        if (overlaps(a.k_pages, n[0], a.v_pages, n[1])) {
-            // keys and values of one page side by side: apart within the page stride
-            const int64_t row = a.k_page_stride * e;
-            const int64_t in_page = n[0] - (a.pages - 1) * row, in_page_v = n[1] - (a.pages - 1) * row;
-            int64_t d = row > 0 ? (int64_t)((intptr_t)a.v_pages - (intptr_t)a.k_pages) % row : 0;
-            if (d < 0) d += row;
-            if (!one || a.pages == 1 || !(d >= in_page && row - d >= in_page_v))
-                return fail(KS_ERR_OVERLAP, "k_pages and v_pages storage overlap");
-        }
+        if (strided_cross(strided(pools[0], a, e), strided(pools[1], a, e)))
+            return fail(KS_ERR_OVERLAP, "k_pages and v_pages storage overlap");
     }
 
     const int V = 16 / e;

@@ -239,3 +239,14 @@ def test_strided_tensors_are_told_apart(tmp_path):
 ])
 def test_rotary_refuses_alternating_parts_that_cross(change):
     assert _abi.ks_rotary(rotary_args(**change), None) == OVERLAP
+
+
+@pytest.mark.parametrize("change", [
+    # [pages, page_size, 2, heads, head_dim]: one element too near, and a whole place apart
+    dict(v_pages=8 * FAKE + 4 * 15, kp_p=256, vp_p=256, kp_s=32, vp_s=32),
+    dict(v_pages=8 * FAKE + 4 * 32, kp_p=256, vp_p=256, kp_s=32, vp_s=32),
+    # keys and values of a page of other strides, half a page apart
+    dict(v_pages=8 * FAKE + 4 * 64, kp_p=256, vp_p=256, kp_s=16, vp_s=24),
+])
+def test_rotary_to_pages_refuses_alternating_pools_that_cross(change):
+    assert _abi.ks_rotary_to_pages(rotary_args(**change), None) == OVERLAP

@@ -872,3 +872,9 @@ def write_and_read_pools(device, order, page_size, heads):
 @pytest.mark.parametrize("page_size, heads", [(16, 2), (1, 3), (5, 1)])
 def test_pools_whose_pages_are_not_the_outermost_axis(cuda_device, order, page_size, heads):
     write_and_read_pools(cuda_device, order, page_size, heads)
+
+
+@pytest.mark.parametrize("order", ["page_parts", "slot_parts", "head_parts", "dim_parts", "layers"])
+@pytest.mark.parametrize("page_size, heads", [(16, 2), (1, 3), (5, 1)])
+def test_pools_of_keys_and_values_that_alternate(cuda_device, order, page_size, heads):
+    write_and_read_pools(cuda_device, order, page_size, heads)
