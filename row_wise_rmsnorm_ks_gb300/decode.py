@@ -74,7 +74,7 @@ def rotary_steps(rotary_dim: int, base: float = 10000.0, *, scaling: str | None 
 # each first asks everything in one expression, and goes through the checks one by one, which name what
 # is wrong, only if that fails; the stream comes as its handle; the device is only changed where it is
 # not the current one.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # torch without CUDA has none, nor CUDA tensors
 _current_device = torch.cuda.current_device
 _grad = torch.is_grad_enabled
 _I32, _I64 = torch.int32, torch.int64

@@ -3,6 +3,7 @@ before any CUDA call (addresses are never read), and rotary_steps is plain arith
 import math
 import os
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -250,3 +251,14 @@ def test_rotary_refuses_alternating_parts_that_cross(change):
 ])
 def test_rotary_to_pages_refuses_alternating_pools_that_cross(change):
     assert _abi.ks_rotary_to_pages(rotary_args(**change), None) == OVERLAP
+
+
+def test_imports_on_a_torch_without_cuda():
+    """torch built without CUDA lacks the stream function that the calls use; importing needs no GPU."""
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'): del torch._C._cuda_getCurrentRawStream\n"
+            "import row_wise_rmsnorm_ks_gb300 as ks\n"
+            "assert ks.rotary_steps(8).shape == (4,)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
