@@ -489,7 +489,8 @@ typedef struct ks_attention_args {
     const int32_t *q_starts;     /* [seqs + 1], non-decreasing */
     void *workspace;
     int64_t workspace_bytes;
-    int64_t tokens, seqs, q_heads, kv_heads, head_dim; /* head_dim: a multiple of 8, at most 256 */
+    int64_t tokens, seqs, q_heads, kv_heads, head_dim; /* head_dim: a multiple of 8, at most 256;
+                                    tokens at most 2^31 - 1024, seqs at most 2^30 */
     int64_t pages, page_size, table_pages, table_stride;
     int64_t max_q_len;           /* most new tokens of a sequence, 0 if unknown: picks the kernel
                                     only; any value gives right results */

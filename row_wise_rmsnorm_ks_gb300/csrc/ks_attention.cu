@@ -542,8 +542,8 @@ ks_status_t attn_check_sizes(const ks_attention_args_t &a) {
         return fail(KS_ERR_UNSUPPORTED_DTYPE, "paged attention takes float16 and bfloat16 (its products run on the tensor cores)");
     const int e = elem_bytes((ks_dtype_t)a.dtype);
     if (e == 0) return fail(KS_ERR_UNSUPPORTED_DTYPE, "dtype code %d is not a ks_dtype_t", (int)a.dtype);
-    if (a.tokens < 0 || a.tokens > 0x7fffffff || a.seqs < 0 || a.seqs > 0x7ffffffe)
-        return fail(KS_ERR_INVALID_ARGUMENT, "tokens and seqs must be in 0 .. 2^31-1");
+    if (a.tokens < 0 || a.tokens > kMaxTokens || a.seqs < 0 || a.seqs > kMaxSeqs)
+        return fail(KS_ERR_INVALID_ARGUMENT, "tokens must be in 0 .. %d and seqs in 0 .. %d", kMaxTokens, kMaxSeqs);
     if (a.head_dim < 8 || a.head_dim > 256 || a.head_dim % 8)
         return fail(KS_ERR_INVALID_ARGUMENT, "head_dim must be a multiple of 8 in 8 .. 256 (got %lld)", (long long)a.head_dim);
     if (a.kv_heads < 1 || a.q_heads < 1 || a.q_heads > 65536 || a.q_heads % a.kv_heads)

@@ -38,6 +38,8 @@ struct AttnJoin {
 
 constexpr int kJoinThreads = 128;
 constexpr int kMaxKeys = 0x7ffffc00;  // keys of a sequence: indices a few steps behind them still fit 31 bits
+constexpr int kMaxTokens = 0x7ffffc00;  // the same for a row tile's rows behind the last token
+constexpr int kMaxSeqs = 1 << 30;       // and for the last thread's share of the sequences
 
 // A sequence's new tokens [q0, q0 + n) and key count, brought into range (and reported) where the
 // given indices are not: nothing outside the tensors is ever addressed.

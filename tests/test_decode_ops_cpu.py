@@ -262,3 +262,13 @@ def test_imports_on_a_torch_without_cuda():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("change", [
+    dict(tokens=(1 << 31) - 1), dict(tokens=(1 << 31) - 1023), dict(seqs=(1 << 30) + 1), dict(seqs=(1 << 31) - 2),
+])
+def test_paged_attention_refuses_sizes_its_indices_do_not_hold(change):
+    """Tokens and sequences are numbered in 32 bits, a row tile's and a thread's share past the last."""
+    args = attention_args(out=1 << 50, workspace=1 << 51, **change)
+    assert _abi.ks_paged_attention(args, None) == INVALID
+    assert _abi.ks_paged_attention_workspace(args)[0] == INVALID
