@@ -272,3 +272,32 @@ def test_paged_attention_refuses_sizes_its_indices_do_not_hold(change):
     args = attention_args(out=1 << 50, workspace=1 << 51, **change)
     assert _abi.ks_paged_attention(args, None) == INVALID
     assert _abi.ks_paged_attention_workspace(args)[0] == INVALID
+
+
+@pytest.mark.parametrize("rotary_dim, base, factor, length, low, high", [
+    (64, 500000.0, 4.0, 8192, 1.0, 4.0), (128, 10000.0, 32.0, 4096, 1.0, 32.0), (30, 1e6, 2.5, 1000, 0.5, 2.0),
+])
+def test_rotary_steps_between_the_bands(rotary_dim, base, factor, length, low, high):
+    """The blend's weight is linear in the turns over the original length, 0 at `low` and 1 at `high`."""
+    got = turns_to_angle(ks.rotary_steps(rotary_dim, base, scaling="bands", factor=factor, original_length=length,
+                                         low=low, high=high))
+    blended = 0
+    for j, f in enumerate(got):
+        plain = base ** (-2 * j / rotary_dim)
+        turns = length * plain / (2 * math.pi)
+        if low < turns < high:
+            blended += 1
+            # f = plain (1 - w) / factor + plain w
+            w = (f / plain - 1 / factor) / (1 - 1 / factor)
+            assert w == pytest.approx((turns - low) / (high - low), abs=1e-9)
+        else:
+            assert f == pytest.approx(plain if turns >= high else plain / factor, rel=1e-12)
+    assert blended >= 2
+
+
+@pytest.mark.parametrize("rotary_dim, base, factor", [(64, 500000.0, 4.0), (128, 10000.0, 8.0), (6, 100.0, 1.5)])
+def test_rotary_steps_of_a_raised_base(rotary_dim, base, factor):
+    """Every frequency: divided by factor^(j / (rotary_dim / 2 - 1)), from 1 for the fastest to factor."""
+    got = turns_to_angle(ks.rotary_steps(rotary_dim, base, scaling="base", factor=factor))
+    for j, f in enumerate(got):
+        assert f == pytest.approx(base ** (-2 * j / rotary_dim) / factor ** (j / (rotary_dim / 2 - 1)), rel=1e-12)
