@@ -32,7 +32,7 @@ constexpr float kLift = std::is_same<T, __half>::value ? 32768.0f : 1.0f;  // wh
 // alone on every fourth 16-key step, with its own ring of asynchronous 16-byte copies in shared
 // memory (no barrier in the loop), its own maximum, sum and output registers; the four are joined
 // when the row tile ends. Bound by DRAM: 64 contexts of 700 to 8100 keys, 8 heads of 128, one token of
-// 64 query heads each, 201 us or 6.3 TB/s; 4 of 131000 keys 317 us or 6.6 TB/s.
+// 64 query heads each, 198 to 207 us or 6.1 to 6.4 TB/s; 4 of 131000 keys 315 to 327 us or 6.4 to 6.7 TB/s.
 template <int kDim>
 struct Rows16 {
     static constexpr int kStages = kDim == 64 ? 4 : 3;

@@ -13,17 +13,19 @@
 //                    64 columns;
 //   warp 19          clears value rows behind the last key that the row tile sees.
 // While one tile is in its softmax, the matrix instructions of the other run. A row's base is the
-// maximum of the first scores it saw until later probabilities outgrow it (kGrowth): only then is it raised and O
-// scaled. The quotient does not depend on the base, and FP32 sums and bf16 probabilities keep their
-// relative precision at any size. fp16 ends at 65504 and is normal down to 2^-14: a probability to the
+// maximum of the first scores it saw until later probabilities outgrow it (kGrowth): only then is it
+// raised and O scaled. The quotient does not depend on the base, and FP32 sums and bf16 probabilities
+// keep their relative precision at any size. fp16 ends at 65504 and is normal down to 2^-14: a probability to the
 // base counts 2^8 there (kLift), which leaves the base to be outgrown by 2^8, keeps the precision of
 // probabilities down to 2^-22 of the row's largest and loses none above 2^-33 of it.
 //
 // Bound by the tensor cores for long chunks: a step of both tiles is 32 instructions of 64 cycles at
 // dim 128. Measured: 8192 tokens over 16384 keys, 32 query and 8 key/value heads of 128, bf16, 0.92 ms
 // or 1.79 PFLOP/s (2580 cycles a step; the softmax of a tile is 850 to 1100 of them, beside the other
-// tile's products). Few rows of a tile make it a stream of the cache: 64 contexts of 6000 keys, 20 rows,
-// 296 us or 5.3 TB/s, by the copies that the five 32 KB tiles of shared memory let be in flight.
+// tile's products); called back to back, at the power limit's clock, 1.01 ms. Few rows of a tile make it a
+// stream of the cache: 64 contexts of 6000 keys, 20 rows, 296 us or 5.3 TB/s, 4 of 30000 103 us or 4.8. What
+// holds these below the copy rate is not known: 152 rings of 160 KB are 3.7 us of that rate, more than a
+// copy's latency, but a step's page numbers are read only when its turn to be copied has come.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -10,7 +10,8 @@ and attention over it.
 Tokens of all sequences are packed: q is [tokens, q_heads, head_dim], k and v are [tokens, kv_heads,
 head_dim]. The cache is two pools of pages, [pages, page_size, kv_heads, head_dim] (any stride order,
 so [pages, kv_heads, page_size, head_dim] pools come as their transpose(1, 2)). Head rows are
-contiguous; the other strides are free, so q, k and v may be views of one fused projection.
+contiguous; the other strides are free, so q, k and v may be views of one fused projection, and the two
+pools views of one tensor.
 
 Checks are those of the other operators: CUDA tensors of one dtype on one device, inference only;
 what they find raises TypeError, ValueError or RuntimeError, and the library's own checks raise
@@ -273,7 +274,8 @@ def rotary_to_pages(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
     """rotary() with the keys and values landing in their cache: token t's rotated key and its value
     go to slot slots[t] (page slots[t] // page_size, place slots[t] % page_size); a negative slot
     writes neither. Slots of one call must differ (where two are one, a mixture of both tokens may be
-    left there). steps None: nothing is rotated; q None: only the cache is written. Returns q_out (`out`, a new tensor, or None without q)."""
+    left there). steps None: nothing is rotated; q None: only the cache is written. Returns q_out (`out`,
+    a new tensor, or None without q)."""
     try:
         dt, dev, code = k.dtype, k.device, _DTYPES[k.dtype]
         tokens, hk, dim = k.shape
@@ -402,9 +404,14 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     q_starts [seqs + 1] are int32. Causal: the i-th of n new tokens sees kv_lens[b] - n + i + 1 keys;
     a row that sees none comes out 0. scale: 1 / sqrt(head_dim) unless given.
 
+    Scores, sums and outputs are FP32; the probabilities are rounded to q's type for the product with the
+    values (half a step relative to each; in float16 those below 2^-22 of a row's largest to multiples of
+    2^-32 of it).
+
     max_q_len: the most new tokens of any sequence, where the caller knows it (1 for a decode step);
-    it only picks the kernel. `out`: a tensor of q's shape that shares nothing with q (rows outside
-    every sequence are left as they were; in a new tensor they are undefined). `workspace`: a uint8
+    it only picks the kernel, and without it all tokens are taken for one sequence's, which costs a step
+    of many sequences a quarter of its time. `out`: a tensor of q's shape that shares nothing with what
+    the call reads (rows outside every sequence are left as they were; in a new tensor they are undefined). `workspace`: a uint8
     CUDA tensor of at least paged_attention_workspace(...) bytes, for callers that keep one; calls
     that may run at once need their own. Without it one is taken from torch's allocator per call."""
     try:
