@@ -409,9 +409,9 @@ ks_status_t ks_layer_norm_planned(void *out, const void *x, const void *weight, 
  *
  * Errors as for ks_rms_norm: KS_ERR_INVALID_ARGUMENT for sizes, strides, alignment to the element
  * (indices: 8 bytes) or NULL pointers; KS_ERR_OVERLAP as above, when the cache shares memory
- * with q, k, v or q_out, and when the bytes of an output or of the cache, first to last, cross those
- * of positions, steps or slots. tokens == 0 launches nothing. Rows and strides of 16 bytes take vector
- * kernels, anything else a scalar kernel of the same arithmetic.
+ * with q, k, v or q_out, and when an output or the cache shares memory with positions, steps or
+ * slots. tokens == 0 launches nothing. Rows and strides of 16 bytes take vector kernels, anything else
+ * a scalar kernel of the same arithmetic.
  */
 #define KS_ROTARY_INTERLEAVED 1
 #define KS_ROTARY_INVERSE 2
@@ -474,8 +474,9 @@ ks_status_t ks_rotary_to_pages(const ks_rotary_args_t *args, ks_stream_t stream)
  *
  * Errors: KS_ERR_UNSUPPORTED_DTYPE for KS_DTYPE_F32; KS_ERR_INVALID_ARGUMENT for sizes, NULL
  * pointers, data or strides that are not multiples of 16 bytes, a workspace that is too small;
- * KS_ERR_OVERLAP when out's bytes, first to last, cross those of q, the cache, the page table,
- * kv_lens, q_starts or the workspace, or the workspace's needed bytes those of what the call reads.
+ * KS_ERR_OVERLAP when out's bytes, first to last, cross those of q, the cache or the workspace, or the
+ * workspace's needed bytes those of q or the cache; and when either shares memory with the page table,
+ * kv_lens or q_starts.
  * tokens == 0 or seqs == 0 launches nothing.
  */
 #define KS_ATTENTION_CAUSAL 1

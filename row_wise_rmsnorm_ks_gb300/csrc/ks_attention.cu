@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "ks_attention.cuh"
+#include "ks_strided.h"
 
 namespace ks {
 namespace {
@@ -573,12 +574,14 @@ bool attn_crosses_inputs(const ks_attention_args_t &a, const void *p, int64_t n)
              overlaps(p, n, a.v_pages, attn_pool_bytes(a, a.v_page_stride, a.v_slot_stride, a.v_head_stride))));
 }
 
-// Whether n bytes at p cross the page table, the lengths or the starts. The kernels read them while other
-// blocks write the output and the workspace, and every block has to read the same.
-bool attn_crosses_indices(const ks_attention_args_t &a, const void *p, int64_t n) {
-    const int64_t table = a.table_pages > 0 ? ((a.seqs - 1) * a.table_stride + a.table_pages) * 4 : 0;
-    return (table > 0 && overlaps(p, n, a.page_table, table)) || overlaps(p, n, a.kv_lens, a.seqs * 4) ||
-           overlaps(p, n, a.q_starts, (a.seqs + 1) * 4);
+// Whether a tensor shares memory with the page table, the lengths or the starts. The kernels read them
+// while other blocks write the output and the workspace, and every block has to read the same.
+// (The table's rows are an axis that v does not have.)
+bool attn_crosses_indices(const ks_attention_args_t &a, const Strided &v) {
+    return (a.table_pages > 0 &&
+            strided_cross(v, {a.page_table, a.table_pages * 4, {1, 1, a.seqs}, {0, 0, a.table_stride * 4}})) ||
+           strided_cross(v, {a.kv_lens, a.seqs * 4, {1, 1, 1}, {0, 0, 0}}) ||
+           strided_cross(v, {a.q_starts, (a.seqs + 1) * 4, {1, 1, 1}, {0, 0, 0}});
 }
 
 ks_status_t attn_check_tensors(const ks_attention_args_t &a) {
@@ -613,7 +616,7 @@ ks_status_t attn_check_tensors(const ks_attention_args_t &a) {
     if (!heads_inner && !tokens_inner) return fail(KS_ERR_OVERLAP, "rows of out share storage");
     if (attn_crosses_inputs(a, a.out, attn_rows_bytes(a, a.out_token_stride, a.out_head_stride)))
         return fail(KS_ERR_OVERLAP, "out overlaps q or the cache");
-    if (attn_crosses_indices(a, a.out, attn_rows_bytes(a, a.out_token_stride, a.out_head_stride)))
+    if (attn_crosses_indices(a, {a.out, D * 2, {T, a.q_heads, 1}, {a.out_token_stride * 2, a.out_head_stride * 2, 0}}))
         return fail(KS_ERR_OVERLAP, "out overlaps the page table, kv_lens or q_starts");
     return KS_SUCCESS;
 }
@@ -662,7 +665,7 @@ ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stre
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace has %lld bytes, %lld are needed",
                     (long long)args->workspace_bytes, (long long)need);
     if (overlaps(args->workspace, need, args->out, attn_rows_bytes(*args, args->out_token_stride, args->out_head_stride)) ||
-        attn_crosses_inputs(*args, args->workspace, need) || attn_crosses_indices(*args, args->workspace, need))
+        attn_crosses_inputs(*args, args->workspace, need) || attn_crosses_indices(*args, {args->workspace, need, {1, 1, 1}, {0, 0, 0}}))
         return fail(KS_ERR_OVERLAP, "the workspace overlaps out or what the call reads");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t ce;

@@ -303,12 +303,12 @@ bool pool_span(const PoolView &v, const ks_rotary_args_t &a, int e, int64_t *spa
     return strided_rows_apart(strided(v, a, e));
 }
 
-// Whether n bytes at p cross the positions, the steps or the slots that the call reads. Every CTA reads
-// them for itself while others write.
-bool crosses_indices(const ks_rotary_args_t &a, bool pages, const void *p, int64_t n) {
-    return (a.rotary_dim > 0 && (overlaps(p, n, a.positions, a.tokens * 8) ||
-                                 overlaps(p, n, a.steps, a.rotary_dim / 2 * 8))) ||
-           (pages && overlaps(p, n, a.slots, a.tokens * 8));
+// Whether a tensor shares memory with the positions, the steps or the slots that the call reads. Every
+// CTA reads them for itself while others write.
+bool crosses_indices(const ks_rotary_args_t &a, bool pages, const Strided &v) {
+    auto crosses = [&](const void *p, int64_t n) { return strided_cross(v, {p, n, {1, 1, 1}, {0, 0, 0}}); };
+    return (a.rotary_dim > 0 && (crosses(a.positions, a.tokens * 8) || crosses(a.steps, a.rotary_dim / 2 * 8))) ||
+           (pages && crosses(a.slots, a.tokens * 8));
 }
 
 ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream) {
@@ -359,8 +359,7 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
         if (!out[i]) continue;
         if (!strided_rows_apart(strided(*out[i], T, D, e)))
             return fail(KS_ERR_OVERLAP, "rows of an output share storage");
-        view_span(*out[i], T, D, e, &span);
-        if (crosses_indices(a, pages, out[i]->p, span))
+        if (crosses_indices(a, pages, strided(*out[i], T, D, e)))
             return fail(KS_ERR_OVERLAP, "an output overlaps positions, steps or slots");
         for (int j = 0; j < 3; ++j) {
             if (!in[j]) continue;
@@ -383,7 +382,7 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
                 return fail(KS_ERR_INVALID_ARGUMENT, "the cache's strides are negative, too large or let rows share storage");
             align |= (uintptr_t)pools[i].p | (uintptr_t)(pools[i].page * e) | (uintptr_t)(pools[i].slot * e) |
                      (uintptr_t)(pools[i].head * e);
-            if (crosses_indices(a, pages, pools[i].p, n[i]))
+            if (crosses_indices(a, pages, strided(pools[i], a, e)))
                 return fail(KS_ERR_OVERLAP, "the cache overlaps positions, steps or slots");
             for (const View *w : {in[0], in[1], in[2], out[0]}) {
                 if (!w) continue;

@@ -878,3 +878,24 @@ def test_pools_whose_pages_are_not_the_outermost_axis(cuda_device, order, page_s
 @pytest.mark.parametrize("page_size, heads", [(16, 2), (1, 3), (5, 1)])
 def test_pools_of_keys_and_values_that_alternate(cuda_device, order, page_size, heads):
     write_and_read_pools(cuda_device, order, page_size, heads)
+
+
+def test_indices_between_an_outputs_rows(cuda_device):
+    """Outputs that are columns of a wider buffer, with the call's indices in the columns beside: nothing
+    is shared."""
+    tokens, heads, dim = 4, 2, 64
+    wide = torch.zeros(tokens, heads * dim + 64, dtype=BF16, device=cuda_device)
+    out = wide[:, :heads * dim].view(tokens, heads, dim)
+    beside = [wide[i, heads * dim:] for i in range(3)]  # 128 bytes each
+    q = normal((tokens, heads, dim), BF16, 1, cuda_device)
+    pos = beside[1].view(torch.int64)[:tokens]
+    pos.copy_(torch.tensor([3, 9, 1000, 5]))
+    steps = ks.rotary_steps(dim, device=cuda_device)
+    ks.rotary(q, None, pos, steps, out=(out, None))
+    close(out, *rotated(q, torch.tensor([3, 9, 1000, 5]), freqs(dim), False), "q")
+    st = build([3, 1], [40, 30], heads, 1, dim, BF16, 16, cuda_device, seed=17)
+    for name, where in zip(("table", "kv", "starts"), beside):
+        inside = where.view(torch.int32)[:st[name].numel()].view(st[name].shape)
+        inside.copy_(st[name])
+        st[name] = inside
+    check_all(attend(st, out=out), st)
