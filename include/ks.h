@@ -507,6 +507,94 @@ typedef struct ks_attention_args {
 ks_status_t ks_paged_attention_workspace(const ks_attention_args_t *args, int64_t *bytes);
 ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stream);
 
+/*
+ * A key/value cache held in 4 bits. A head's row of head_dim values (a multiple of 16) is cut into groups of 16. A
+ * group is held as 16 codes, a sign (bit 3) and the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 (e2m1), value 2i in the
+ * low half of byte i, and a scale s of 8 bits (e4m3, 0 .. 448). With the pool's factor g (2^-64 .. 2^64; 1 unless
+ * the values call for another) and the group's largest magnitude A:
+ *     s = A / (6 g), at most 448;   u = s g, in FP32;   code = x / u, at most 6 (0 where s is 0)
+ * s and the codes to the nearest, ties to the even code, as of real numbers: an FP32 result near a border is
+ * decided exactly. What is held is u * code. Infinities are held as the largest value; a group with a NaN gets
+ * the scale NaN.
+ */
+typedef struct ks_pages_4bit {
+    void *codes;                 /* [pages, page_size, kv_heads, head_dim / 2] bytes; address and strides
+                                    multiples of 8 */
+    void *scales;                /* [pages, page_size, kv_heads, head_dim / 16] bytes */
+    int64_t code_page_stride, code_slot_stride, code_head_stride;    /* bytes, any order */
+    int64_t scale_page_stride, scale_slot_stride, scale_head_stride;
+    float factor;
+    int32_t reserved;
+} ks_pages_4bit_t;
+
+/*
+ * ks_rotary_to_pages into 4-bit pools: q is rotated into q_out; k, rotated, and v are rounded to the pools' groups
+ * from the real values (not from values rounded to the 16-bit type). args->rotary is read as ks_rotary_to_pages
+ * reads it, except for k_pages and v_pages and their strides, which the pools stand for. head_dim: a multiple of
+ * 16. Pools may not share memory with each other or with what the call reads; errors otherwise as there, and
+ * KS_ERR_INVALID_ARGUMENT for a factor out of range.
+ */
+typedef struct ks_rotary_4bit_args {
+    ks_rotary_args_t rotary;
+    ks_pages_4bit_t k_pages, v_pages;
+} ks_rotary_4bit_args_t;
+ks_status_t ks_rotary_to_pages_4bit(const ks_rotary_4bit_args_t *args, ks_stream_t stream);
+
+/*
+ * Keys and values back from 4-bit pools: token t's rows, u * code rounded once to dtype, are read from slot slots[t].
+ * A negative slot gives rows of zeros (a padding token), one past the pool too and sets KS_FAULT_BAD_INDEX. Slots
+ * may be repeated. Errors as for ks_rotary; KS_ERR_OVERLAP when an output shares memory with the pools, the slots
+ * or the other output.
+ */
+typedef struct ks_pages_4bit_rows_args {
+    void *k_out, *v_out;         /* [tokens, kv_heads, head_dim], head rows contiguous; strides in elements */
+    const int64_t *slots;        /* [tokens] */
+    ks_pages_4bit_t k_pages, v_pages;
+    int64_t tokens, kv_heads, head_dim, pages, page_size;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int32_t dtype;
+    int32_t reserved;
+} ks_pages_4bit_rows_args_t;
+ks_status_t ks_pages_4bit_to_rows(const ks_pages_4bit_rows_args_t *args, ks_stream_t stream);
+
+/*
+ * ks_paged_attention over 4-bit pools. args->attention is read as there, except for k_pages and v_pages and their
+ * strides. Keys and values enter the products exactly as they are held. bfloat16 queries enter as fp16 after a
+ * row's largest magnitude is brought to 1 .. 2 by a power of two (values 2^-14 times as large and smaller lose
+ * at most 2^-25 of it), and probabilities as fp16 for either type. head_dim: a multiple of 16, at most 256. The
+ * workspace is that of ks_paged_attention_4bit_workspace.
+ */
+typedef struct ks_attention_4bit_args {
+    ks_attention_args_t attention;
+    ks_pages_4bit_t k_pages, v_pages;
+} ks_attention_4bit_args_t;
+ks_status_t ks_paged_attention_4bit_workspace(const ks_attention_4bit_args_t *args, int64_t *bytes);
+ks_status_t ks_paged_attention_4bit(const ks_attention_4bit_args_t *args, ks_stream_t stream);
+
+/*
+ * What lies between two blocks of a decoder that norms a block's output as well as its input, in place on both
+ * tensors, per row:
+ *     n = x * rsqrt(mean(x^2) + eps) * post_weight          (x itself without post_weight)
+ *     s = residual_scale * residual + block_scale * gate * n
+ *     residual = cast(s);   x = cast(s * rsqrt(mean(s^2) + eps) * weight)
+ * in FP32, the second norm from the unrounded s. gate holds a value for each of a row's `hidden` places
+ * (gate_column_stride 1) or one for the row (0); rows_per_gate consecutive rows share a row of it, gate_row_stride
+ * elements apart: rows_per_gate = rows with one vector for all (a learned scale per channel), a sequence's length
+ * with one per sequence, 1 with one per row.
+ *   x         [rows, hidden]: the block's output; on return the next block's input.
+ *   residual  [rows, hidden]; weight, post_weight [hidden], post_weight may be NULL; gate may be NULL (1).
+ * Errors as for ks_fused_add_rms_norm; residual_scale and block_scale are finite.
+ */
+typedef struct ks_gated_norm_args {
+    void *x, *residual;
+    const void *weight, *post_weight, *gate;
+    int64_t rows, hidden;
+    int64_t rows_per_gate, gate_row_stride, gate_column_stride;
+    float eps, residual_scale, block_scale;
+    int32_t dtype;
+} ks_gated_norm_args_t;
+ks_status_t ks_gated_add_rms_norm(const ks_gated_norm_args_t *args, ks_stream_t stream);
+
 /* Library version, major*10000 + minor*100 + patch. */
 int32_t ks_version(void);
 

@@ -38,6 +38,11 @@ KS_ATTENTION_CAUSAL = 1
 # the C argument.
 ROTARY_ARGS = struct.Struct("=10Q23qfiii")     # ks_rotary_args_t
 ATTENTION_ARGS = struct.Struct("=8Q21qfiii")   # ks_attention_args_t
+_POOL = "2Q6qfi"                                # ks_pages_4bit_t
+ROTARY_4BIT_ARGS = struct.Struct("=10Q23qfiii" + 2 * _POOL)     # ks_rotary_4bit_args_t
+ATTENTION_4BIT_ARGS = struct.Struct("=8Q21qfiii" + 2 * _POOL)   # ks_attention_4bit_args_t
+ROWS_4BIT_ARGS = struct.Struct("=3Q" + 2 * _POOL + "9qii")      # ks_pages_4bit_rows_args_t
+GATED_NORM_ARGS = struct.Struct("=5Q5qfffi")                    # ks_gated_norm_args_t
 
 # Every symbol include/ks.h declares (checked by the CPU test of the boundary).
 EXPORTED = ("ks_rms_norm", "ks_fused_add_rms_norm", "ks_status_string", "ks_last_error",
@@ -47,7 +52,9 @@ EXPORTED = ("ks_rms_norm", "ks_fused_add_rms_norm", "ks_status_string", "ks_last
             "ks_get_launch_options", "ks_silu_and_mul", "ks_softmax", "ks_layer_norm",
             "ks_silu_and_mul_planned", "ks_softmax_planned", "ks_layer_norm_planned",
             "ks_rotary", "ks_rotary_to_pages", "ks_paged_attention",
-            "ks_paged_attention_workspace", "ks_version")
+            "ks_paged_attention_workspace", "ks_rotary_to_pages_4bit", "ks_pages_4bit_to_rows",
+            "ks_paged_attention_4bit", "ks_paged_attention_4bit_workspace", "ks_gated_add_rms_norm",
+            "ks_version")
 
 
 class KsLibraryMissing(RuntimeError):
@@ -137,11 +144,13 @@ def load(path: str | None = None):
         lib.ks_softmax_planned.restype = ctypes.c_int
         lib.ks_layer_norm_planned.argtypes = [vp, vp, vp, vp, i64, i64, f32, ctypes.c_int, PP, vp]
         lib.ks_layer_norm_planned.restype = ctypes.c_int
-        for f in (lib.ks_rotary, lib.ks_rotary_to_pages, lib.ks_paged_attention):
+        for f in (lib.ks_rotary, lib.ks_rotary_to_pages, lib.ks_paged_attention, lib.ks_rotary_to_pages_4bit,
+                  lib.ks_pages_4bit_to_rows, lib.ks_paged_attention_4bit, lib.ks_gated_add_rms_norm):
             f.argtypes = [ctypes.c_char_p, vp]
             f.restype = ctypes.c_int
-        lib.ks_paged_attention_workspace.argtypes = [ctypes.c_char_p, ctypes.POINTER(i64)]
-        lib.ks_paged_attention_workspace.restype = ctypes.c_int
+        for f in (lib.ks_paged_attention_workspace, lib.ks_paged_attention_4bit_workspace):
+            f.argtypes = [ctypes.c_char_p, ctypes.POINTER(i64)]
+            f.restype = ctypes.c_int
         lib.ks_version.argtypes = []
         lib.ks_version.restype = i32
         _lib = lib
@@ -284,6 +293,29 @@ def ks_paged_attention_workspace(args: bytes | None) -> tuple[int, int]:
     need = ctypes.c_int64(0)
     st = (_lib or load()).ks_paged_attention_workspace(args, ctypes.byref(need))
     return st, need.value
+
+
+def ks_rotary_to_pages_4bit(args: bytes | None, stream: int | None) -> int:
+    return (_lib or load()).ks_rotary_to_pages_4bit(args, stream)
+
+
+def ks_pages_4bit_to_rows(args: bytes | None, stream: int | None) -> int:
+    return (_lib or load()).ks_pages_4bit_to_rows(args, stream)
+
+
+def ks_paged_attention_4bit(args: bytes | None, stream: int | None) -> int:
+    return (_lib or load()).ks_paged_attention_4bit(args, stream)
+
+
+def ks_paged_attention_4bit_workspace(args: bytes | None) -> tuple[int, int]:
+    """(status, bytes) for a call of these sizes on the current device."""
+    need = ctypes.c_int64(0)
+    st = (_lib or load()).ks_paged_attention_4bit_workspace(args, ctypes.byref(need))
+    return st, need.value
+
+
+def ks_gated_add_rms_norm(args: bytes | None, stream: int | None) -> int:
+    return (_lib or load()).ks_gated_add_rms_norm(args, stream)
 
 
 def ks_version() -> int:

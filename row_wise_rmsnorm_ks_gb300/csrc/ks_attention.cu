@@ -15,7 +15,6 @@
 #include <type_traits>
 
 #include "ks_attention.cuh"
-#include "ks_strided.h"
 
 namespace ks {
 namespace {
@@ -461,7 +460,7 @@ attn_join_kernel(const __grid_constant__ AttnArgs s, int ctas) {
             for (int k = 0; k < 2; ++k) {
                 int token, head;
                 if (!attn_row(s, j.q0, j.q_len, j.head, j.row_tile, group * 16 + lane / 4 + 8 * k, &token, &head)) continue;
-                const float inv = attn_inverse(l[k]);
+                const float inv = attn_inverse(l[k]) * s.out_scale;
                 *reinterpret_cast<uint32_t *>((T *)a.out + token * a.out_token_stride + head * a.out_head_stride + col * 8 +
                                               lane % 4 * 2) = pack16<T>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
             }
@@ -470,6 +469,8 @@ attn_join_kernel(const __grid_constant__ AttnArgs s, int ctas) {
 }
 
 // ------------------------------------------------------------------------------- host side
+
+int64_t ceil_to(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How a call is launched: the row-tile height, the keys of a unit and the CTAs. Depends on
 // host-known sizes only.
@@ -497,8 +498,6 @@ const void *rows16_kernel(int dim, int *smem, int *per_sm) {
     return (const void *)attn_rows16_kernel<T, 256>;
 }
 
-int64_t ceil_to(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // Up to 16 rows per key/value head fill one tile of the 16-row kernel; more go to the tensor-core
 // kernel where it takes the call's pages.
 bool attn_many_rows(const ks_attention_args_t &a) {
@@ -508,36 +507,46 @@ bool attn_many_rows(const ks_attention_args_t &a) {
 
 void attn_plan(const ks_attention_args_t &a, bool tc, int sms, AttnPlan *p) {
     p->s.a = a;
-    p->s.group = (int32_t)(a.q_heads / a.kv_heads);
     p->s.scale_log2 = a.scale * 1.4426950408889634f;
-    p->s.rows = tc ? attn_tc_rows() : kRows;
-    p->s.tile_cost = tc ? attn_tc_tile_cost() : kTileCost;
-    const int unit = tc ? attn_tc_unit() : kUnit;
-    p->s.unit_shift = 0;
-    while (1 << p->s.unit_shift < unit) ++p->s.unit_shift;
+    p->s.out_scale = 1.0f;
+    if (tc) attn_shape(&p->s, attn_tc_rows(), attn_tc_unit(), attn_tc_tile_cost());
+    else attn_shape(&p->s, kRows, kUnit, kTileCost);
     int per_sm = 1;
     p->smem = 0;
     p->kernel = nullptr;
     if (!tc) p->kernel = a.dtype == KS_DTYPE_BF16 ? rows16_kernel<__nv_bfloat16>((int)a.head_dim, &p->smem, &per_sm)
                                          : rows16_kernel<__half>((int)a.head_dim, &p->smem, &per_sm);
-    p->s.head_splits = (int32_t)ceil_to(p->s.group, p->s.rows);
-    p->s.tile_heads = (int32_t)ceil_to(p->s.group, p->s.head_splits);
-    p->s.tile_tokens = p->s.head_splits > 1 ? 1 : p->s.rows / p->s.tile_heads;
-    // No more CTAs than the call can have units.
-    const int64_t tiles = ceil_to(a.tokens, p->s.tile_tokens) + a.seqs;
-    const int64_t tile_units = ceil_to(a.table_pages * a.page_size, unit) + 1 + p->s.tile_cost;
-    const int64_t heads = a.kv_heads * p->s.head_splits;
-    int64_t ctas = (int64_t)sms * per_sm;
-    if (tile_units < ctas && tiles < ctas && heads < ctas && tile_units * tiles * heads < ctas)
-        ctas = tile_units * tiles * heads;
-    p->ctas = (int)ctas;
+    p->ctas = attn_ctas(p->s, (int64_t)sms * per_sm);
 }
 
-int64_t attn_workspace_bytes(const AttnPlan &p) {
-    return p.ctas * (2 * attn_slot_floats(p.s.rows, p.s.a.head_dim) * (int64_t)sizeof(float) + (int64_t)sizeof(AttnJoin));
+}  // namespace
+
+void attn_shape(AttnArgs *s, int rows, int unit, int tile_cost) {
+    const ks_attention_args_t &a = s->a;
+    s->group = (int32_t)(a.q_heads / a.kv_heads);
+    s->rows = rows;
+    s->tile_cost = tile_cost;
+    s->unit_shift = 0;
+    while (1 << s->unit_shift < unit) ++s->unit_shift;
+    s->head_splits = (int32_t)ceil_to(s->group, rows);
+    s->tile_heads = (int32_t)ceil_to(s->group, s->head_splits);
+    s->tile_tokens = s->head_splits > 1 ? 1 : rows / s->tile_heads;
 }
 
-// The checks of the sizes, and those of the tensors; neither needs a device.
+int attn_ctas(const AttnArgs &s, int64_t most) {
+    const ks_attention_args_t &a = s.a;
+    const int64_t tiles = ceil_to(a.tokens, s.tile_tokens) + a.seqs;
+    const int64_t tile_units = ceil_to(a.table_pages * a.page_size, 1 << s.unit_shift) + 1 + s.tile_cost;
+    const int64_t heads = a.kv_heads * s.head_splits;
+    if (tile_units < most && tiles < most && heads < most && tile_units * tiles * heads < most)
+        return (int)(tile_units * tiles * heads);
+    return (int)most;
+}
+
+int64_t attn_workspace_bytes(const AttnArgs &s, int ctas) {
+    return ctas * (2 * attn_slot_floats(s.rows, s.a.head_dim) * (int64_t)sizeof(float) + (int64_t)sizeof(AttnJoin));
+}
+
 ks_status_t attn_check_sizes(const ks_attention_args_t &a) {
     if (a.dtype == KS_DTYPE_F32)
         return fail(KS_ERR_UNSUPPORTED_DTYPE, "paged attention takes float16 and bfloat16 (its products run on the tensor cores)");
@@ -562,6 +571,17 @@ int64_t attn_rows_bytes(const ks_attention_args_t &a, int64_t token, int64_t hea
     return ((a.tokens - 1) * token + (a.q_heads - 1) * head + a.head_dim) * 2;
 }
 
+bool attn_out_apart(const ks_attention_args_t &a) {
+    const int64_t D = a.head_dim, T = a.tokens;
+    const bool heads_inner = (a.q_heads == 1 || a.out_head_stride >= D) &&
+                             (T == 1 || a.out_token_stride >= (a.q_heads - 1) * a.out_head_stride + D);
+    const bool tokens_inner = (T == 1 || a.out_token_stride >= D) &&
+                              (a.q_heads == 1 || a.out_head_stride >= (T - 1) * a.out_token_stride + D);
+    return heads_inner || tokens_inner;
+}
+
+namespace {
+
 int64_t attn_pool_bytes(const ks_attention_args_t &a, int64_t page, int64_t slot, int64_t head) {
     return a.pages > 0 ? ((a.pages - 1) * page + (a.page_size - 1) * slot + (a.kv_heads - 1) * head + a.head_dim) * 2 : 0;
 }
@@ -574,8 +594,10 @@ bool attn_crosses_inputs(const ks_attention_args_t &a, const void *p, int64_t n)
              overlaps(p, n, a.v_pages, attn_pool_bytes(a, a.v_page_stride, a.v_slot_stride, a.v_head_stride))));
 }
 
-// Whether a tensor shares memory with the page table, the lengths or the starts. The kernels read them
-// while other blocks write the output and the workspace, and every block has to read the same.
+}  // namespace
+
+// The kernels read these while other blocks write the output and the workspace, and every block has to
+// read the same.
 // (The table's rows are an axis that v does not have.)
 bool attn_crosses_indices(const ks_attention_args_t &a, const Strided &v) {
     return (a.table_pages > 0 &&
@@ -583,6 +605,8 @@ bool attn_crosses_indices(const ks_attention_args_t &a, const Strided &v) {
            strided_cross(v, {a.kv_lens, a.seqs * 4, {1, 1, 1}, {0, 0, 0}}) ||
            strided_cross(v, {a.q_starts, (a.seqs + 1) * 4, {1, 1, 1}, {0, 0, 0}});
 }
+
+namespace {
 
 ks_status_t attn_check_tensors(const ks_attention_args_t &a) {
     if (!std::isfinite(a.scale * 1.4426950408889634f))
@@ -608,20 +632,28 @@ ks_status_t attn_check_tensors(const ks_attention_args_t &a) {
         return fail(KS_ERR_INVALID_ARGUMENT, "the page table is too large");
     if (((uintptr_t)a.q | (uintptr_t)a.out | (uintptr_t)a.k_pages | (uintptr_t)a.v_pages) & 15u)
         return fail(KS_ERR_INVALID_ARGUMENT, "q, out and the cache must be aligned to 16 bytes");
-    const int64_t D = a.head_dim, T = a.tokens;
-    const bool heads_inner = (a.q_heads == 1 || a.out_head_stride >= D) &&
-                             (T == 1 || a.out_token_stride >= (a.q_heads - 1) * a.out_head_stride + D);
-    const bool tokens_inner = (T == 1 || a.out_token_stride >= D) &&
-                              (a.q_heads == 1 || a.out_head_stride >= (T - 1) * a.out_token_stride + D);
-    if (!heads_inner && !tokens_inner) return fail(KS_ERR_OVERLAP, "rows of out share storage");
+    if (!attn_out_apart(a)) return fail(KS_ERR_OVERLAP, "rows of out share storage");
     if (attn_crosses_inputs(a, a.out, attn_rows_bytes(a, a.out_token_stride, a.out_head_stride)))
         return fail(KS_ERR_OVERLAP, "out overlaps q or the cache");
-    if (attn_crosses_indices(a, {a.out, D * 2, {T, a.q_heads, 1}, {a.out_token_stride * 2, a.out_head_stride * 2, 0}}))
+    if (attn_crosses_indices(a, {a.out, a.head_dim * 2, {a.tokens, a.q_heads, 1}, {a.out_token_stride * 2, a.out_head_stride * 2, 0}}))
         return fail(KS_ERR_OVERLAP, "out overlaps the page table, kv_lens or q_starts");
     return KS_SUCCESS;
 }
 
 }  // namespace
+
+cudaError_t attn_join_launch(const AttnArgs &s, int ctas, cudaStream_t stream) {
+    // The join is scheduled while the last CTAs finish and waits for them on the device.
+    AttnArgs args = s;
+    void *jp[] = {&args, &ctas};
+    const void *f = s.a.dtype == KS_DTYPE_BF16 ? (const void *)attn_join_kernel<__nv_bfloat16>
+                                               : (const void *)attn_join_kernel<__half>;
+    // Half a block for each of a tile's items, without more blocks than start at once (measured, one
+    // token over 1000 keys: 11.6 us, with half as many blocks the same, with twice 13.3).
+    const int items = s.rows / 16 * (int)(s.a.head_dim / 8), blocks = items / 2 < 32 ? items / 2 : 32;
+    return launch_kernel(f, dim3((unsigned)ctas, (unsigned)(blocks < 1 ? 1 : blocks)), dim3(kJoinThreads), 0, jp, stream,
+                         true);
+}
 
 int fault_flags_attention(bool clear) { return fault_flags_t(clear); }
 
@@ -640,10 +672,10 @@ ks_status_t ks_paged_attention_workspace(const ks_attention_args_t *args, int64_
     if ((st = device_sms(&sms)) != KS_SUCCESS) return st;
     AttnPlan p;
     attn_plan(*args, false, sms, &p);
-    *bytes = attn_workspace_bytes(p);
+    *bytes = attn_workspace_bytes(p.s, p.ctas);
     if (attn_many_rows(*args) && attn_tc_sizes(*args)) {
         attn_plan(*args, true, sms, &p);
-        const int64_t more = attn_workspace_bytes(p);
+        const int64_t more = attn_workspace_bytes(p.s, p.ctas);
         *bytes = *bytes > more ? *bytes : more;
     }
     return KS_SUCCESS;
@@ -660,7 +692,7 @@ ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stre
     if ((st = device_sms(&sms)) != KS_SUCCESS) return st;
     AttnPlan p;
     attn_plan(*args, attn_many_rows(*args) && attn_tc_fits(*args), sms, &p);
-    const int64_t need = attn_workspace_bytes(p);
+    const int64_t need = attn_workspace_bytes(p.s, p.ctas);
     if (args->workspace_bytes < need)
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace has %lld bytes, %lld are needed",
                     (long long)args->workspace_bytes, (long long)need);
@@ -676,17 +708,7 @@ ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stre
     } else {
         ce = attn_tc_launch(p.s, p.ctas, s, launch_pdl_enabled());
     }
-    if (ce == cudaSuccess && p.ctas > 1) {
-        // The join is scheduled while the last CTAs finish and waits for them on the device.
-        void *jp[] = {&p.s, &p.ctas};
-        const void *f = args->dtype == KS_DTYPE_BF16 ? (const void *)attn_join_kernel<__nv_bfloat16>
-                                                     : (const void *)attn_join_kernel<__half>;
-        // Half a block for each of a tile's items, without more blocks than start at once (measured, one
-        // token over 1000 keys: 11.6 us, with half as many blocks the same, with twice 13.3).
-        const int items = p.s.rows / 16 * (int)(args->head_dim / 8), blocks = items / 2 < 32 ? items / 2 : 32;
-        ce = launch_kernel(f, dim3((unsigned)p.ctas, (unsigned)(blocks < 1 ? 1 : blocks)), dim3(kJoinThreads), 0, jp, s,
-                           true);
-    }
+    if (ce == cudaSuccess && p.ctas > 1) ce = attn_join_launch(p.s, p.ctas, s);
     if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));
     return KS_SUCCESS;
 }

@@ -13,6 +13,7 @@
 #pragma once
 
 #include "ks_decode.cuh"
+#include "ks_strided.h"
 
 namespace ks {
 
@@ -23,9 +24,10 @@ struct AttnArgs {
     int32_t head_splits; // row tiles a token's group is cut into (1 unless group > M)
     int32_t tile_tokens; // tokens in a row tile
     int32_t unit_shift;  // log2 of the keys per unit (TN)
-    int32_t rows;        // rows of a tile (M)
+    int32_t rows;        // rows of a partial slot: those of a tile (M), or more
     int32_t tile_cost;   // units that a row tile costs beside its own
     float scale_log2;    // scale * log2(e)
+    float out_scale;     // what the values count
 };
 
 // What a CTA left in its second partial slot: the beginning of a row tile that later CTAs finish.
@@ -57,12 +59,6 @@ __device__ __forceinline__ AttnSeq attn_seq(const ks_attention_args_t &a, int b)
     s.keys = (int32_t)min(max((int64_t)keys, (int64_t)0), room);
     if (s.q0 != q0 || end != q1 || s.keys != keys) atomicOr(&g_fault_flags, kFaultBadIndex);
     return s;
-}
-
-// a / b for a, b >= 0: by 32 bits where they fit (a fifth of the time of the 64-bit routine).
-__device__ inline int64_t quotient(int64_t a, int64_t b) {
-    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
 }
 
 // sum over i in [0, n) of floor((a i + b) / 2^shift), for a n + b below 2^32: the whole multiples of the
@@ -312,6 +308,23 @@ __device__ __forceinline__ float attn_base(float m) { return m == -INFINITY ? 0.
 __device__ __forceinline__ float4 *attn_part(const AttnArgs &s, float *slot, int row_group, int col_group, int lane) {
     return reinterpret_cast<float4 *>(slot) + (row_group * ((int)s.a.head_dim / 8) + col_group) * 32 + lane;
 }
+
+// ---- host side, shared with the attention over 4-bit pages
+
+// Fills in the division of a call's work: `rows` of a row tile, the keys of a unit and a tile's cost.
+void attn_shape(AttnArgs *s, int rows, int unit, int tile_cost);
+// No more CTAs than the call can have units.
+int attn_ctas(const AttnArgs &s, int64_t most);
+int64_t attn_workspace_bytes(const AttnArgs &s, int ctas);
+// The checks of a call's sizes, of which none needs a device.
+ks_status_t attn_check_sizes(const ks_attention_args_t &a);
+// Bytes from the first to past the last value of q, or of out, with these strides.
+int64_t attn_rows_bytes(const ks_attention_args_t &a, int64_t token, int64_t head);
+// Whether the rows of out are apart.
+bool attn_out_apart(const ks_attention_args_t &a);
+// Whether a tensor shares memory with the page table, the lengths or the starts.
+bool attn_crosses_indices(const ks_attention_args_t &a, const Strided &v);
+cudaError_t attn_join_launch(const AttnArgs &s, int ctas, cudaStream_t stream);
 
 // The tensor-core kernel (ks_attention_tc.cu): whether it takes a call's sizes, and its strides too,
 // the rows and keys of its tiles, and its launch.

@@ -1,0 +1,247 @@
+// The norm after a block, its gate, the scaled residual add and the norm before the next block, in one pass
+// (ks_gated_add_rms_norm). Per row, in FP32:
+//     n = x * rsqrt(mean(x^2) + eps) * post_weight,  s = residual_scale * r + block_scale * gate * n,
+//     r = cast(s),  x = cast(s * rsqrt(mean(s^2) + eps) * weight)
+// Two sums over the row, the second of what the first gives: the row has to stay at hand between them. Rows of up to
+// 4096 16-byte vectors lie in a CTA's registers, x and r each read and written once, which bounds the operator by
+// memory (4 values a place); wider rows, and rows that no vector fits, are read three times, the second and third
+// time mostly from L2.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "ks_kernels.cuh"
+
+namespace ks {
+namespace {
+
+struct GatedArgs {
+    ks_gated_norm_args_t a;
+    int64_t hv;  // vectors of a row
+};
+
+// The gate's row of a row, NULL without a gate.
+template <typename T>
+__device__ __forceinline__ const T *gate_row(const ks_gated_norm_args_t &a, int64_t row) {
+    if (!a.gate) return nullptr;
+    return (const T *)a.gate + (a.rows_per_gate == a.rows ? 0 : row / a.rows_per_gate) * a.gate_row_stride;
+}
+
+// s of some places, in place of x: `scale` is the first norm's (1 without one).
+template <int N>
+__device__ __forceinline__ void gated_sum(float (&x)[N], const float (&r)[N], float scale, const float (&post)[N], const float (&gate)[N],
+                                          float residual_scale, float block_scale) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = fmaf(r[i], residual_scale, x[i] * scale * post[i] * gate[i] * block_scale);
+}
+
+template <int N>
+__device__ __forceinline__ void fill(float (&f)[N], float v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = v;
+}
+
+// One CTA per row, V vectors a thread.
+template <typename T, int V>
+__global__ void __launch_bounds__(V == 4 ? 1024 : 512) gated_rows_kernel(const __grid_constant__ GatedArgs args) {
+    using E = Elem<T>;
+    constexpr int N = E::kPerVec;
+    __shared__ float red[2][32];
+    const ks_gated_norm_args_t &a = args.a;
+    const int g = blockDim.x, t = threadIdx.x;
+    const int64_t hv = args.hv;
+    const float hidden = (float)a.hidden;
+    grid_dependency_wait();
+    allow_dependents_launch();
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        uint4 *xr = (uint4 *)a.x + row * hv, *rr = (uint4 *)a.residual + row * hv;
+        uint4 xv[V], rv[V];
+        load_row<V>(xr, t, g, hv, xv);
+        load_row<V>(rr, t, g, hv, rv);
+        const T *gate = gate_row<T>(a, row);
+        float scale = 1.0f;
+        if (a.post_weight) {
+            SumSq acc;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                float f[N];
+                E::unpack(xv[k], f);
+                acc.add(f);
+            }
+            scale = row_scale(team_sum<0>(acc.total(), red[0]), hidden, a.eps);
+        }
+        float s[V][N];
+        SumSq acc;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int64_t c = t + (int64_t)k * g;
+            float r[N], post[N], gt[N];
+            E::unpack(xv[k], s[k]);
+            E::unpack(rv[k], r);
+            fill(post, 1.0f);
+            fill(gt, 1.0f);
+            if (c < hv) {
+                if (a.post_weight) E::unpack(__ldg((const uint4 *)a.post_weight + c), post);
+                if (gate) {
+                    if (a.gate_column_stride) E::unpack(__ldg((const uint4 *)gate + c), gt);
+                    else fill(gt, E::load1(gate, 0));
+                }
+            }
+            gated_sum(s[k], r, scale, post, gt, a.residual_scale, a.block_scale);
+            if (c < hv) {
+                __stcs(rr + c, E::pack(s[k]));
+                acc.add(s[k]);
+            }
+        }
+        const float out_scale = row_scale(team_sum<0>(acc.total(), red[1]), hidden, a.eps);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int64_t c = t + (int64_t)k * g;
+            if (c < hv) {
+                float w[N];
+                E::unpack(__ldg((const uint4 *)a.weight + c), w);
+#pragma unroll
+                for (int i = 0; i < N; ++i) s[k][i] = s[k][i] * out_scale * w[i];
+                __stcs(xr + c, E::pack(s[k]));
+            }
+        }
+    }
+}
+
+// Any width and alignment: the row read up to three times, vector by vector or value by value.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(512) gated_wide_kernel(const __grid_constant__ GatedArgs args) {
+    using E = Elem<T>;
+    constexpr int N = kVec ? E::kPerVec : 1;
+    __shared__ float red[2][32];
+    const ks_gated_norm_args_t &a = args.a;
+    const int64_t n = kVec ? args.hv : a.hidden;
+    const float hidden = (float)a.hidden;
+    grid_dependency_wait();
+    allow_dependents_launch();
+    auto load = [](const T *p, int64_t c, float (&f)[N]) {
+        if constexpr (kVec) E::unpack(reinterpret_cast<const uint4 *>(p)[c], f);
+        else f[0] = E::load1(p, c);
+    };
+    auto store = [](T *p, int64_t c, const float (&f)[N]) {
+        if constexpr (kVec) reinterpret_cast<uint4 *>(p)[c] = E::pack(f);
+        else E::store1(p, c, f[0]);
+    };
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        T *x = (T *)a.x + row * a.hidden, *r = (T *)a.residual + row * a.hidden;
+        const T *gate = gate_row<T>(a, row);
+        float scale = 1.0f;
+        if (a.post_weight) {
+            SumSq acc;
+            for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
+                float f[N];
+                load(x, c, f);
+                acc.add(f);
+            }
+            scale = row_scale(team_sum<0>(acc.total(), red[0]), hidden, a.eps);
+        }
+        auto sum = [&](int64_t c, float (&s)[N]) {
+            float rv[N], post[N], gt[N];
+            load(x, c, s);
+            load(r, c, rv);
+            fill(post, 1.0f);
+            fill(gt, 1.0f);
+            if (a.post_weight) load((const T *)a.post_weight, c, post);
+            if (gate) {
+                if (a.gate_column_stride) load(gate, c, gt);
+                else fill(gt, E::load1(gate, 0));
+            }
+            gated_sum(s, rv, scale, post, gt, a.residual_scale, a.block_scale);
+        };
+        SumSq acc;
+        for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
+            float s[N];
+            sum(c, s);
+            acc.add(s);
+        }
+        const float out_scale = row_scale(team_sum<0>(acc.total(), red[1]), hidden, a.eps);
+        for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
+            float s[N], w[N];
+            sum(c, s);
+            store(r, c, s);
+            load((const T *)a.weight, c, w);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = s[i] * out_scale * w[i];
+            store(x, c, s);
+        }
+    }
+}
+
+template <typename T>
+const void *pick(int v, bool vec) {
+    switch (v) {
+    case 1: return (const void *)gated_rows_kernel<T, 1>;
+    case 2: return (const void *)gated_rows_kernel<T, 2>;
+    case 4: return (const void *)gated_rows_kernel<T, 4>;
+    default: return vec ? (const void *)gated_wide_kernel<T, true> : (const void *)gated_wide_kernel<T, false>;
+    }
+}
+
+}  // namespace
+}  // namespace ks
+
+using namespace ks;
+
+extern "C" ks_status_t ks_gated_add_rms_norm(const ks_gated_norm_args_t *args, ks_stream_t stream) {
+    if (!args) return fail(KS_ERR_INVALID_ARGUMENT, "args is NULL");
+    const ks_gated_norm_args_t &a = *args;
+    const int e = elem_bytes((ks_dtype_t)a.dtype);
+    if (e == 0) return fail(KS_ERR_UNSUPPORTED_DTYPE, "dtype code %d is not a ks_dtype_t", (int)a.dtype);
+    if (a.hidden <= 0) return fail(KS_ERR_INVALID_ARGUMENT, "hidden must be > 0 (got %lld)", (long long)a.hidden);
+    if (a.rows < 0) return fail(KS_ERR_INVALID_ARGUMENT, "rows must be >= 0 (got %lld)", (long long)a.rows);
+    if (!std::isfinite(a.eps) || !(a.eps > 0.0f))
+        return fail(KS_ERR_INVALID_ARGUMENT, "eps must be finite and > 0 (got %g)", (double)a.eps);
+    if (!std::isfinite(a.residual_scale) || !std::isfinite(a.block_scale))
+        return fail(KS_ERR_INVALID_ARGUMENT, "residual_scale and block_scale must be finite");
+    if ((__int128)a.rows * a.hidden * e > ((__int128)1 << 62))
+        return fail(KS_ERR_INVALID_ARGUMENT, "rows*hidden*element size is too large");
+    if (a.rows == 0) return KS_SUCCESS;
+    if (!a.x || !a.residual || !a.weight) return fail(KS_ERR_INVALID_ARGUMENT, "NULL pointer with rows > 0");
+    if (misaligned(e, a.x, a.residual, a.weight) || misaligned(e, a.post_weight, a.gate))
+        return fail(KS_ERR_INVALID_ARGUMENT, "a pointer is not aligned to the %d-byte element", e);
+    const int64_t n = a.rows * a.hidden * e, w = a.hidden * e;
+    if (overlaps(a.x, n, a.residual, n)) return fail(KS_ERR_OVERLAP, "x and residual storage overlap");
+    uintptr_t align = (uintptr_t)a.x | (uintptr_t)a.residual | (uintptr_t)a.weight | (uintptr_t)a.post_weight;
+    int64_t gate_bytes = 0;
+    if (a.gate) {
+        if (a.rows_per_gate < 1 || a.gate_row_stride < 0 || a.gate_column_stride < 0 || a.gate_column_stride > 1)
+            return fail(KS_ERR_INVALID_ARGUMENT, "the gate needs rows_per_gate >= 1, a row stride >= 0 and a column stride of 0 or 1");
+        const int64_t gates = (a.rows - 1) / a.rows_per_gate + 1;
+        const __int128 last = (__int128)(gates - 1) * a.gate_row_stride + (a.hidden - 1) * a.gate_column_stride + 1;
+        if (last * e > ((__int128)1 << 62)) return fail(KS_ERR_INVALID_ARGUMENT, "the gate is too large");
+        gate_bytes = (int64_t)last * e;
+        if (a.gate_column_stride) align |= (uintptr_t)a.gate | (uintptr_t)(gates > 1 ? a.gate_row_stride * e : 0);
+    }
+    for (const void *p : {(const void *)a.x, (const void *)a.residual})
+        if (overlaps(p, n, a.weight, w) || (a.post_weight && overlaps(p, n, a.post_weight, w)) ||
+            (a.gate && overlaps(p, n, a.gate, gate_bytes)))
+            return fail(KS_ERR_OVERLAP, "x or residual overlaps a weight or the gate");
+    int sms = 0;
+    const ks_status_t st = device_sms(&sms);
+    if (st != KS_SUCCESS) return st;
+    GatedArgs k_args;
+    k_args.a = a;
+    const bool vec = (align & 15u) == 0 && w % 16 == 0;
+    k_args.hv = vec ? w / 16 : 0;
+    int v = 0, block = 512;
+    if (vec && k_args.hv <= 4096) {
+        v = k_args.hv <= 256 ? 1 : k_args.hv <= 1024 ? 2 : 4;
+        if (a.rows <= sms && k_args.hv <= 512) v = 1;
+        block = (int)((k_args.hv + v - 1) / v + 31) / 32 * 32;
+    }
+    const void *f = a.dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(v, vec)
+                    : a.dtype == KS_DTYPE_F16 ? pick<__half>(v, vec)
+                                              : pick<float>(v, vec);
+    const int64_t most = (int64_t)sms * (2048 / block > 32 ? 32 : 2048 / block);
+    const int64_t grid = a.rows < most ? a.rows : most;
+    void *kp[] = {&k_args};
+    const cudaError_t ce = launch_kernel(f, dim3((unsigned)grid), dim3((unsigned)block), 0, kp, static_cast<cudaStream_t>(stream),
+                                         launch_pdl_enabled());
+    if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));
+    return KS_SUCCESS;
+}

@@ -21,248 +21,31 @@
 
 #include <cmath>
 
-#include "ks_decode.cuh"
+#include "ks_rotary.cuh"
 #include "ks_strided.h"
 
 namespace ks {
 namespace {
 
-constexpr int kRotThreads = 256;
-constexpr int kRotMaxDim = 1024;  // head_dim limit: rotary_dim / 2 sines and cosines in shared memory
-
-struct RotaryArgs {
-    ks_rotary_args_t a;
-    int32_t columns;     // vectors, or pairs of vectors, per head
-    int32_t heads_per_y; // head slots per CTA (all of a token's, or a part)
-};
-
-// cos and sin of (t / 2^64) turns times scale, t taken mod 2^64.
-__device__ __forceinline__ float2 turn_cos_sin(uint64_t t, float scale) {
-    const uint32_t hi = (uint32_t)(t >> 32);
-    const uint32_t quadrant = (hi + 0x20000000u) >> 30;
-    const int32_t rest = (int32_t)(hi - (quadrant << 30));  // within an eighth of a turn
-    float s, c;
-    sincospif((float)rest * 4.656612873077393e-10f, &s, &c);  // rest / 2^31 half turns
-    const float cc = (quadrant & 1) ? s : c, ss = (quadrant & 1) ? c : s;
-    const bool neg_c = quadrant == 1 || quadrant == 2, neg_s = quadrant >= 2;
-    return make_float2((neg_c ? -cc : cc) * scale, (neg_s ? -ss : ss) * scale);
-}
-
-// Where a head slot's row is read and written. Slots 0 .. q_heads-1 are the query's heads, then the
-// keys', then (with a cache) the values', which are not rotated.
-template <typename T>
-__device__ __forceinline__ const T *rot_src(const ks_rotary_args_t &a, int64_t token, int slot) {
-    if (slot < a.q_heads) return (const T *)a.q + token * a.q_token_stride + slot * a.q_head_stride;
-    const int64_t h = slot - a.q_heads;
-    if (h < a.kv_heads) return (const T *)a.k + token * a.k_token_stride + h * a.k_head_stride;
-    return (const T *)a.v + token * a.v_token_stride + (h - a.kv_heads) * a.v_head_stride;
-}
-
-// The token's rows in the cache: NULL where they are not written (a negative slot, or one past the
-// pool, which is also reported in the fault word).
-template <typename T>
-struct RotPage {
-    T *k, *v;
-};
-
-template <typename T>
-__device__ __forceinline__ RotPage<T> rot_page(const ks_rotary_args_t &a, int64_t slot) {
-    RotPage<T> p = {nullptr, nullptr};
-    const int64_t size = a.page_size;
-    if (slot < 0) return p;
-    int64_t page, in_page;
-    if (((uint64_t)slot | (uint64_t)size) >> 32 == 0) {  // a 32-bit division takes a fifth of the time
-        page = (uint32_t)slot / (uint32_t)size;
-        in_page = (uint32_t)slot - (uint32_t)page * (uint32_t)size;
-    } else {
-        page = slot / size;
-        in_page = slot - page * size;
-    }
-    if (page >= a.pages) {
-        if (threadIdx.x == 0) atomicOr(&g_fault_flags, kFaultBadIndex);
-        return p;
-    }
-    p.k = (T *)a.k_pages + page * a.k_page_stride + in_page * a.k_slot_stride;
-    p.v = (T *)a.v_pages + page * a.v_page_stride + in_page * a.v_slot_stride;
-    return p;
-}
-
-template <typename T, bool kPages>
-__device__ __forceinline__ T *rot_dst(const ks_rotary_args_t &a, int64_t token, int slot, const RotPage<T> &p) {
-    if (slot < a.q_heads) return (T *)a.q_out + token * a.q_out_token_stride + slot * a.q_out_head_stride;
-    const int64_t h = slot - a.q_heads;
-    if (!kPages) return (T *)a.k_out + token * a.k_out_token_stride + h * a.k_out_head_stride;
-    if (!p.k) return nullptr;
-    if (h < a.kv_heads) return p.k + h * a.k_pages_head_stride;
-    return p.v + (h - a.kv_heads) * a.v_pages_head_stride;
-}
-
-// What a token's work hangs on, all loaded at once: its position, its slot, and the step of the angle
-// that this thread computes.
-struct RotToken {
-    uint64_t position, step;
-    int64_t slot;
-};
-
-template <bool kPages>
-__device__ __forceinline__ RotToken rot_token(const ks_rotary_args_t &a, int64_t token) {
-    RotToken t = {0, 0, -1};
-    if (a.rotary_dim > 0) {  // otherwise nothing is turned, and positions and steps may be NULL
-        t.position = (uint64_t)a.positions[token];
-        if (threadIdx.x < a.rotary_dim / 2) t.step = (uint64_t)a.steps[threadIdx.x];
-    }
-    if (kPages) t.slot = a.slots[token];
-    return t;
-}
-
-__device__ __forceinline__ void rot_table(const ks_rotary_args_t &a, const RotToken &t, float2 *cs) {
-    const bool inverse = (a.flags & KS_ROTARY_INVERSE) != 0;
-    uint64_t step = t.step;
-    for (int j = threadIdx.x; j < (int)(a.rotary_dim / 2); j += blockDim.x) {
-        if (j != threadIdx.x) step = (uint64_t)a.steps[j];
-        const uint64_t angle = t.position * step;
-        cs[j] = turn_cos_sin(inverse ? 0 - angle : angle, a.scale);
-    }
-}
-
-// 16-byte vectors. kHalf: pair (j, j + rotary_dim/2); otherwise pair (2j, 2j + 1). kU: vectors
-// (or pairs of them) a thread has in flight; measured (us): 1, 2 and 3 of them, 16384 tokens of 64 + 8
-// heads 88.4, 88.0, 87.1; 8192 tokens of 56 + 8 + 8 into the cache, where addresses take more registers,
-// 52.6, 48.9, 51.9.
-template <typename T, bool kHalf, bool kPages>
-__global__ void __launch_bounds__(kRotThreads)
-rotary_vec_kernel(const __grid_constant__ RotaryArgs args) {
-    constexpr int V = Elem<T>::kPerVec;
-    constexpr int kU = kPages ? 2 : 3;
+template <typename T, bool kHalf, bool kPages, bool kVec>
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryArgs args) {
     __shared__ float2 cs[kRotMaxDim / 2];
     const ks_rotary_args_t &a = args.a;
     grid_dependency_wait();
     allow_dependents_launch();
-    const int64_t token = blockIdx.x;
-    const int column = threadIdx.x % args.columns, lane = threadIdx.x / args.columns;
-    const int lanes = blockDim.x / args.columns;
     const int total = (int)(a.q_heads + a.kv_heads * (kPages ? 2 : 1));
     const int first = blockIdx.y * args.heads_per_y;
     const int last = min(total, first + args.heads_per_y);
-    // the column's first element, and its partner's for a half-split pair
-    const int pairs = (int)(a.rotary_dim / 2) / V;            // columns that are pairs (kHalf)
-    const int turned = kHalf ? pairs : (int)a.rotary_dim / V; // columns that are rotated
-    const bool mine = column < turned;
-    const int at = (!kHalf || mine) ? column * V : (column + pairs) * V;
-    const int at2 = at + pairs * V;
-
-    uint4 x[kU], y[kU];
-    const bool active = lane < lanes;
-    auto load = [&](int base) {
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int slot = base + u * lanes;
-            if (active && slot < last) {
-                const T *src = rot_src<T>(a, token, slot);
-                x[u] = *reinterpret_cast<const uint4 *>(src + at);
-                if (kHalf && mine) y[u] = *reinterpret_cast<const uint4 *>(src + at2);
-            }
-        }
-    };
-    const RotToken t = rot_token<kPages>(a, token);
-    load(first + lane);
-    rot_table(a, t, cs);
-    RotPage<T> page = {};
-    if (kPages) page = rot_page<T>(a, t.slot);
-    __syncthreads();
-    float2 turn[V];
-    if (mine) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (kHalf) turn[i] = cs[column * V + i];
-            else if (i < V / 2) turn[i] = cs[column * (V / 2) + i];
-        }
-    }
-    for (int base = first + lane; base < last; base += kU * lanes) {
-        if (base != first + lane) load(base);
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int slot = base + u * lanes;
-            if (!active || slot >= last) break;
-            T *dst = rot_dst<T, kPages>(a, token, slot, page);
-            if (kPages && dst == nullptr) continue;
-            if (mine && (!kPages || slot < a.q_heads + a.kv_heads)) {
-                float p[V];
-                Elem<T>::unpack(x[u], p);
-                if (kHalf) {
-                    float q[V];
-                    Elem<T>::unpack(y[u], q);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float c = turn[i].x, s = turn[i].y, m = p[i], n = q[i];
-                        p[i] = fmaf(m, c, -n * s);
-                        q[i] = fmaf(n, c, m * s);
-                    }
-                    y[u] = Elem<T>::pack(q);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V / 2; ++i) {
-                        const float c = turn[i].x, s = turn[i].y, m = p[2 * i], n = p[2 * i + 1];
-                        p[2 * i] = fmaf(m, c, -n * s);
-                        p[2 * i + 1] = fmaf(n, c, m * s);
-                    }
-                }
-                x[u] = Elem<T>::pack(p);
-            }
-            *reinterpret_cast<uint4 *>(dst + at) = x[u];
-            if (kHalf && mine) *reinterpret_cast<uint4 *>(dst + at2) = y[u];
-        }
-    }
-}
-
-// Element loads, any rotary_dim and alignment: a thread per pair, or per value that is not rotated.
-template <typename T, bool kHalf, bool kPages>
-__global__ void __launch_bounds__(kRotThreads)
-rotary_scalar_kernel(const __grid_constant__ RotaryArgs args) {
-    __shared__ float2 cs[kRotMaxDim / 2];
-    const ks_rotary_args_t &a = args.a;
-    grid_dependency_wait();
-    allow_dependents_launch();
-    const int64_t token = blockIdx.x;
-    const int total = (int)(a.q_heads + a.kv_heads * (kPages ? 2 : 1));
-    const int first = blockIdx.y * args.heads_per_y;
-    const int last = min(total, first + args.heads_per_y);
-    const RotToken t = rot_token<kPages>(a, token);
-    RotPage<T> page = {};
-    if (kPages) page = rot_page<T>(a, t.slot);
-    rot_table(a, t, cs);
-    __syncthreads();
-    const int pairs = (int)(a.rotary_dim / 2);
-    const int n = (last - first) * args.columns;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int slot = first + i / args.columns, column = i % args.columns;
-        const T *src = rot_src<T>(a, token, slot);
-        T *dst = rot_dst<T, kPages>(a, token, slot, page);
-        if (kPages && dst == nullptr) continue;
-        if (column >= pairs) {  // not rotated
-            dst[column + pairs] = src[column + pairs];
-            continue;
-        }
-        const int i0 = kHalf ? column : 2 * column, i1 = kHalf ? column + pairs : 2 * column + 1;
-        const T x = src[i0], y = src[i1];
-        if (kPages && slot >= a.q_heads + a.kv_heads) {
-            dst[i0] = x;
-            dst[i1] = y;
-            continue;
-        }
-        const float c = cs[column].x, s = cs[column].y;
-        const float m = Elem<T>::load1(&x, 0), k = Elem<T>::load1(&y, 0);
-        Elem<T>::store1(dst, i0, fmaf(m, c, -k * s));
-        Elem<T>::store1(dst, i1, fmaf(k, c, m * s));
-    }
+    if constexpr (kVec) rot_heads_vec<T, kHalf, kPages>(args, blockIdx.x, first, last, cs);
+    else rot_heads_scalar<T, kHalf, kPages>(args, blockIdx.x, first, last, cs);
 }
 
 template <typename T, bool kPages>
 const void *rotary_pick(bool vec, bool half) {
-    if (vec) return half ? (const void *)rotary_vec_kernel<T, true, kPages>
-                         : (const void *)rotary_vec_kernel<T, false, kPages>;
-    return half ? (const void *)rotary_scalar_kernel<T, true, kPages>
-                : (const void *)rotary_scalar_kernel<T, false, kPages>;
+    if (vec) return half ? (const void *)rotary_kernel<T, true, kPages, true>
+                         : (const void *)rotary_kernel<T, false, kPages, true>;
+    return half ? (const void *)rotary_kernel<T, true, kPages, false>
+                : (const void *)rotary_kernel<T, false, kPages, false>;
 }
 
 // One packed tensor [tokens, heads, head_dim]: what the host checks need of it.
@@ -311,7 +94,8 @@ bool crosses_indices(const ks_rotary_args_t &a, bool pages, const Strided &v) {
            (pages && crosses(a.slots, a.tokens * 8));
 }
 
-ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream) {
+// `four`: with `pages`, the 4-bit pools that the keys and values go to instead of args' own.
+ks_status_t rotary(const ks_rotary_args_t *args, bool pages, const ks_rotary_4bit_args_t *four, ks_stream_t stream) {
     if (!args) return fail(KS_ERR_INVALID_ARGUMENT, "args is NULL");
     const ks_rotary_args_t &a = *args;
     const int e = elem_bytes((ks_dtype_t)a.dtype);
@@ -329,10 +113,12 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
     if (!std::isfinite(a.scale)) return fail(KS_ERR_INVALID_ARGUMENT, "scale must be finite");
     if (pages && (a.kv_heads == 0 || a.page_size < 1 || a.pages < 0))
         return fail(KS_ERR_INVALID_ARGUMENT, "a cache needs kv_heads >= 1, page_size >= 1 and pages >= 0");
+    if (four && a.head_dim % 16)
+        return fail(KS_ERR_INVALID_ARGUMENT, "4-bit pages take head_dims of whole groups of 16 (got %lld)", (long long)a.head_dim);
     if (a.tokens == 0) return KS_SUCCESS;
     if ((a.rotary_dim > 0 && (!a.positions || !a.steps)) || (a.q_heads > 0 && (!a.q || !a.q_out)) ||
         (a.kv_heads > 0 && (!a.k || (!pages && !a.k_out))) || (pages && (!a.v || !a.slots)) ||
-        (pages && a.pages > 0 && (!a.k_pages || !a.v_pages)))
+        (pages && !four && a.pages > 0 && (!a.k_pages || !a.v_pages)))
         return fail(KS_ERR_INVALID_ARGUMENT, "NULL pointer with tokens > 0");
     if (misaligned(8, a.positions, a.steps, a.slots))
         return fail(KS_ERR_INVALID_ARGUMENT, "positions, steps and slots must be aligned to 8 bytes");
@@ -371,7 +157,24 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
     }
     if (out[0] && out[1] && strided_cross(strided(qo, T, D, e), strided(ko, T, D, e)))
         return fail(KS_ERR_OVERLAP, "q_out and k_out storage overlap");
-    if (pages && a.pages > 0) {
+    if (four) {
+        uintptr_t code_align = 0, scale_align = 0;
+        const ks_status_t st = check_pools4(four->k_pages, four->v_pages, a.pages, a.page_size, a.kv_heads, D, true,
+                                            &code_align, &scale_align);
+        if (st != KS_SUCCESS) return st;
+        if (a.pages > 0) {
+            for (const ks_pages_4bit_t *p : {&four->k_pages, &four->v_pages})
+                for (int part = 0; part < 2; ++part)
+                    if (crosses_indices(a, pages, strided4(*p, part != 0, a.pages, a.page_size, a.kv_heads, D)))
+                        return fail(KS_ERR_OVERLAP, "the cache overlaps positions, steps or slots");
+            for (const View *w : {in[0], in[1], in[2], out[0]}) {
+                if (!w) continue;
+                view_span(*w, T, D, e, &span);
+                if (crosses_pools4(four->k_pages, four->v_pages, a.pages, a.page_size, a.kv_heads, D, w->p, span))
+                    return fail(KS_ERR_OVERLAP, "the cache overlaps q, k, v or q_out");
+            }
+        }
+    } else if (pages && a.pages > 0) {
         const PoolView pools[2] = {{a.k_pages, a.k_page_stride, a.k_slot_stride, a.k_pages_head_stride},
                                    {a.v_pages, a.v_page_stride, a.v_slot_stride, a.v_pages_head_stride}};
         int64_t n[2] = {0, 0};
@@ -397,11 +200,12 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
 
     const int V = 16 / e;
     const bool half = (a.flags & KS_ROTARY_INTERLEAVED) == 0;
-    const bool vec = (align & 15u) == 0 && D % V == 0 && (half ? (a.rotary_dim / 2) % V == 0 : a.rotary_dim % V == 0);
+    bool vec = (align & 15u) == 0 && D % V == 0 && (half ? (a.rotary_dim / 2) % V == 0 : a.rotary_dim % V == 0);
+    if (four && half && a.rotary_dim % 32) vec = false;  // a group's partners are then not one group
     RotaryArgs k_args;
     k_args.a = a;
     k_args.columns = (int32_t)(vec ? (half ? (D - a.rotary_dim / 2) / V : D / V) : D - a.rotary_dim / 2);
-    const int total = (int)(a.q_heads + a.kv_heads * (pages ? 2 : 1));
+    const int total = (int)(a.q_heads + (four ? 0 : a.kv_heads * (pages ? 2 : 1)));
     // Few tokens: a token's heads are split over CTAs until the SMs are covered (each repeats the
     // token's sines, 64 of them for a head of 128).
     int sms = 0;
@@ -411,15 +215,20 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, ks_stream_t stream)
     int parts = (int)((sms + T - 1) / T);
     const int most = (total + lanes - 1) / lanes;
     parts = parts > most ? most : parts;
-    k_args.heads_per_y = (total + parts - 1) / parts;
-    parts = (total + k_args.heads_per_y - 1) / k_args.heads_per_y;
+    k_args.heads_per_y = parts ? (total + parts - 1) / parts : 0;  // no queries (4-bit pools alone): no parts
+    parts = parts ? (total + k_args.heads_per_y - 1) / k_args.heads_per_y : 0;
     // As many threads as do the CTA's heads in equal rounds: with 72 heads of 8 columns, 3 rounds of 192
     // threads, not 2 of 256 and a third of 64.
     int threads = kRotThreads;
-    if (vec) {
+    if (vec && parts) {
         const int rounds = (k_args.heads_per_y + lanes - 1) / lanes;
         threads = ((k_args.heads_per_y + rounds - 1) / rounds * k_args.columns + 31) / 32 * 32;
         threads = threads < 64 ? 64 : threads;
+    }
+    if (four) {
+        const cudaError_t ce = rotary_4bit_launch(k_args, *four, vec, half, parts, threads, static_cast<cudaStream_t>(stream));
+        if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));
+        return KS_SUCCESS;
     }
     const void *f;
     switch (a.dtype) {
@@ -443,11 +252,16 @@ int fault_flags_rotary(bool clear) { return fault_flags_t(clear); }
 extern "C" {
 
 ks_status_t ks_rotary(const ks_rotary_args_t *args, ks_stream_t stream) {
-    return ks::rotary(args, false, stream);
+    return ks::rotary(args, false, nullptr, stream);
 }
 
 ks_status_t ks_rotary_to_pages(const ks_rotary_args_t *args, ks_stream_t stream) {
-    return ks::rotary(args, true, stream);
+    return ks::rotary(args, true, nullptr, stream);
+}
+
+ks_status_t ks_rotary_to_pages_4bit(const ks_rotary_4bit_args_t *args, ks_stream_t stream) {
+    if (!args) return ks::fail(KS_ERR_INVALID_ARGUMENT, "args is NULL");
+    return ks::rotary(&args->rotary, true, args, stream);
 }
 
 }  // extern "C"

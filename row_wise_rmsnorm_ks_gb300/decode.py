@@ -353,6 +353,13 @@ def _check_attention(q, k_pages, v_pages, page_table, kv_lens, q_starts, scale, 
     _pool(v_pages, "v_pages", dt, dev, hk, dim)
     if k_pages.shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must have one shape")
+    _check_attention_rows(q, hk, page_table, kv_lens, q_starts, scale, max_q_len, out, workspace)
+    _inference(k_pages, v_pages)
+
+
+def _check_attention_rows(q, hk, page_table, kv_lens, q_starts, scale, max_q_len, out, workspace):
+    """The checks that do not look at the cache."""
+    dev, dt, hq = q.device, q.dtype, q.shape[1]
     if hk == 0 or hq == 0 or hq % hk:
         raise ValueError(f"q's {hq} heads must be a multiple of the cache's {hk}")
     if not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32:
@@ -362,7 +369,7 @@ def _check_attention(q, k_pages, v_pages, page_table, kv_lens, q_starts, scale, 
     seqs = page_table.shape[0]
     _index(kv_lens, "kv_lens", torch.int32, dev, (seqs,))
     _index(q_starts, "q_starts", torch.int32, dev, (seqs + 1,))
-    _inference(q, k_pages, v_pages, out)
+    _inference(q, out)
     if scale is not None and not (isinstance(scale, (int, float)) and -_BIG < scale < _BIG):
         raise ValueError("scale must be finite (below 2^127)")
     if max_q_len is not None and not (isinstance(max_q_len, int) and 0 <= max_q_len < 2 ** 31):

@@ -2,6 +2,8 @@
 
     rms_norm(x, weight, eps=1e-6) -> y
     fused_add_rms_norm(x, residual, weight, eps=1e-6) -> None   (x and residual updated in place)
+    gated_add_rms_norm(x, residual, weight, *, post_weight, gate, ...) -> None   (the same, with a norm
+                                                         of x before it, a gate and scales)
 
     rms_norm_host(x, weight, eps=1e-6, *, out=None, workspace=None) -> out
     fused_add_rms_norm_host(x, residual, weight, eps=1e-6, *, workspace=None) -> None
@@ -88,6 +90,67 @@ def fused_add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Te
         _abi.check(_abi.ks_fused_add_rms_norm(x.data_ptr(), residual.data_ptr(),
                                               weight.data_ptr(), rows, hidden, float(eps),
                                               _DTYPES[x.dtype], _stream(x.device)))
+    return None
+
+
+def _gate_rows(gate: torch.Tensor, x: torch.Tensor):
+    """(rows that share a row of the gate, its row stride, its column stride)."""
+    if not isinstance(gate, torch.Tensor) or gate.dtype != x.dtype:
+        raise TypeError(f"gate must be a tensor of {x.dtype}")
+    if gate.device != x.device or not gate.is_contiguous():
+        raise ValueError("gate must be contiguous, on x's device")
+    if torch.is_grad_enabled() and gate.requires_grad:
+        raise RuntimeError("these kernels are inference-only: inputs must not require grad")
+    hidden, lead = x.shape[-1], x.shape[:-1]
+    shape = (1,) * (x.dim() - gate.dim()) + tuple(gate.shape)
+    own = len(lead)  # leading dimensions that the gate has of its own: those up to its last that is not 1
+    while own > 0 and shape[own - 1] == 1:
+        own -= 1
+    if len(shape) != x.dim() or shape[-1] not in (1, hidden) or shape[:own] != tuple(lead[:own]):
+        raise ValueError(f"gate must have x's leading dimensions up to some point and ones behind it, and a last "
+                         f"dimension of {hidden} or 1; got {tuple(gate.shape)} for {tuple(x.shape)}")
+    return math.prod(lead[own:]), shape[-1], 1 if shape[-1] == hidden else 0
+
+
+def gated_add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, *,
+                       post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                       residual_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6) -> None:
+    """What lies between two blocks that norm their outputs too, in place, per row and in FP32:
+
+        n = x * rsqrt(mean(x^2) + eps) * post_weight       (x itself without post_weight)
+        s = residual_scale * residual + block_scale * gate * n
+        residual <- cast(s);  x <- cast(s * rsqrt(mean(s^2) + eps) * weight)
+
+    x is the block's output and becomes the next block's input. gate: (hidden,) for one vector, x's leading
+    dimensions up to some point and ones behind it for one per sequence or token ((B, 1, hidden) for an x of
+    (B, S, hidden)); a last dimension of 1 is one value for a row. weight and post_weight are (hidden,); all
+    tensors have x's dtype. Returns None."""
+    _check(x, weight, eps)
+    if not isinstance(residual, torch.Tensor) or residual.shape != x.shape:
+        raise ValueError("residual must have the same shape as x")
+    if residual.dtype != x.dtype or residual.device != x.device or not residual.is_contiguous():
+        raise ValueError("residual must be contiguous, with x's dtype and device")
+    if post_weight is not None:
+        _check(x, post_weight, eps, names=("x", "post_weight"))
+    if torch.is_grad_enabled() and residual.requires_grad:
+        raise RuntimeError("these kernels are inference-only: inputs must not require grad")
+    for v, n in ((residual_scale, "residual_scale"), (block_scale, "block_scale")):
+        if not (isinstance(v, (int, float)) and abs(v) < 2.0 ** 127):
+            raise ValueError(f"{n} must be finite (below 2^127)")
+    gate_p, per_gate, row_stride, column_stride = 0, 1, 0, 0
+    if gate is not None:
+        per_gate, row_stride, column_stride = _gate_rows(gate, x)
+        gate_p = gate.data_ptr()
+    hidden = x.shape[-1]
+    rows = x.numel() // hidden
+    if rows == 0:
+        return None
+    args = _abi.GATED_NORM_ARGS.pack(
+        x.data_ptr(), residual.data_ptr(), weight.data_ptr(), post_weight.data_ptr() if post_weight is not None else 0,
+        gate_p, rows, hidden, per_gate, row_stride, column_stride, float(eps), residual_scale, block_scale,
+        _DTYPES[x.dtype])
+    with torch.cuda.device(x.device):
+        _abi.check(_abi.ks_gated_add_rms_norm(args, _stream(x.device)))
     return None
 
 
