@@ -21,9 +21,11 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libks.so")
 SOURCES = ["ks_abi.cu", "ks_host.cu", "ks_noalloc.cu", "ks_ops.cu", "ks_launch_bf16.cu",
            "ks_launch_f16.cu", "ks_launch_f32.cu", "ks_rotary.cu", "ks_attention.cu",
-           "ks_attention_tc.cu", "ks_rotary_4bit.cu", "ks_attention_4bit.cu", "ks_gated_norm.cu"]
+           "ks_attention_tc.cu", "ks_rotary_4bit.cu", "ks_attention_4bit.cu",
+           "ks_attention_4bit_tc.cu", "ks_gated_norm.cu"]
 HEADERS = ["ks_kernels.cuh", "ks_internal.h", "ks_ptx.cuh", "ks_attention.cuh", "ks_decode.cuh",
-           "ks_strided.h", "ks_rotary.cuh", "ks_fp4.cuh"]
+           "ks_strided.h", "ks_rotary.cuh", "ks_fp4.cuh",
+           "ks_attention_tc.cuh", "ks_attention_4bit.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

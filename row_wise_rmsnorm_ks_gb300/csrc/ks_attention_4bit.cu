@@ -23,16 +23,9 @@
 #include <mutex>
 #include <unordered_map>
 
-#include "ks_attention.cuh"
-#include "ks_fp4.cuh"
+#include "ks_attention_4bit.cuh"
 
 namespace ks {
-
-struct Attn4Args {
-    AttnArgs s;
-    Pool4 k, v;
-};
-
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
@@ -466,7 +459,7 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
 struct Attn4Plan {
     Attn4Args args;
     int ctas;
-    const void *kernel;
+    const void *kernel;  // NULL: the tensor-core kernel
 };
 
 template <bool kWhole>
@@ -495,10 +488,13 @@ int resident(const void *f) {
     return n;
 }
 
-// Query rows of a tile, in eights: 16 where head_dim leaves the registers and a sequence may have more than 8.
+// Query rows of a tile, in eights: 16 where head_dim leaves the registers and a sequence may have more than 8; 32,
+// those of the tensor-core kernel, where it may have more than 16.
+constexpr int kTc = 32;
 int row_tiles(const ks_attention_args_t &a) {
     const int64_t q_len = a.max_q_len > 0 && a.max_q_len < a.tokens ? a.max_q_len : a.tokens;
-    return a.head_dim <= 128 && q_len * (a.q_heads / a.kv_heads) > 8 ? 2 : 1;
+    const int64_t rows = q_len * (a.q_heads / a.kv_heads);
+    return a.head_dim > 128 || rows <= 8 ? 1 : rows <= 16 ? 2 : kTc;
 }
 
 ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, uintptr_t code_align, uintptr_t scale_align, Attn4Plan *p) {
@@ -509,14 +505,20 @@ ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, uintptr_t code_a
     p->args.k = pool4(a.k_pages);
     p->args.v = pool4(a.v_pages);
     const int dim = (int)s.a.head_dim, r = (dim + 63) / 64;
+    int sms = 0;
+    const ks_status_t st = device_sms(&sms);
+    if (st != KS_SUCCESS) return st;
+    if (tiles == kTc) {
+        p->kernel = nullptr;
+        attn_shape(&s, attn_tc_rows(), attn_tc_unit(), attn_tc_tile_cost());
+        p->ctas = attn_ctas(s, sms);
+        return KS_SUCCESS;
+    }
     const uintptr_t codes = r % 4 == 0 || r == 2 ? 15 : 7, scales = r == 2 ? 1 : r == 4 ? 3 : 0;
     const bool whole = dim == 64 * r && (code_align & codes) == 0 && (scale_align & scales) == 0;
     p->kernel = whole ? rows_kernel<true>(r, tiles) : rows_kernel<false>(r, tiles);
     attn_shape(&s, 8 * tiles, kUnit, kTileCost);
     s.rows = kSlotRows;
-    int sms = 0;
-    const ks_status_t st = device_sms(&sms);
-    if (st != KS_SUCCESS) return st;
     const int per_sm = resident(p->kernel);
     if (per_sm <= 0) return fail(KS_ERR_CUDA, "the attention kernel cannot be resident");
     p->ctas = attn_ctas(s, (int64_t)sms * per_sm);
@@ -579,7 +581,7 @@ ks_status_t ks_paged_attention_4bit_workspace(const ks_attention_4bit_args_t *ar
     ks_status_t st = check_sizes4(args->attention);
     if (st != KS_SUCCESS || args->attention.tokens == 0 || args->attention.seqs == 0) return st;
     // whichever kernel the pools' alignment, or fewer tokens, pick
-    for (int tiles = row_tiles(args->attention); tiles > 0; --tiles)
+    for (int tiles = row_tiles(args->attention); tiles > 0; tiles = tiles == kTc ? 2 : tiles - 1)
         for (uintptr_t align : {(uintptr_t)0, (uintptr_t)8}) {
             Attn4Plan p;
             if ((st = plan4(*args, tiles, align, align ? 1 : 0, &p)) != KS_SUCCESS) return st;
@@ -599,7 +601,9 @@ ks_status_t ks_paged_attention_4bit(const ks_attention_4bit_args_t *args, ks_str
     if (!a.workspace || ((uintptr_t)a.workspace & 15u))
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace must be device memory aligned to 16 bytes");
     Attn4Plan p;
-    if ((st = plan4(*args, row_tiles(a), code_align, scale_align, &p)) != KS_SUCCESS) return st;
+    int tiles = row_tiles(a);
+    if (tiles == kTc && !attn4_tc_fits(a)) tiles = 2;
+    if ((st = plan4(*args, tiles, code_align, scale_align, &p)) != KS_SUCCESS) return st;
     const int64_t need = attn_workspace_bytes(p.args.s, p.ctas);
     if (a.workspace_bytes < need)
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace has %lld bytes, %lld are needed", (long long)a.workspace_bytes,
@@ -611,7 +615,8 @@ ks_status_t ks_paged_attention_4bit(const ks_attention_4bit_args_t *args, ks_str
         return fail(KS_ERR_OVERLAP, "the workspace overlaps out or what the call reads");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *kp[] = {&p.args};
-    cudaError_t ce = launch_kernel(p.kernel, dim3((unsigned)p.ctas), dim3(kThreads), 0, kp, s, launch_pdl_enabled());
+    cudaError_t ce = p.kernel ? launch_kernel(p.kernel, dim3((unsigned)p.ctas), dim3(kThreads), 0, kp, s, launch_pdl_enabled())
+                              : attn4_tc_launch(p.args, code_align, scale_align, p.ctas, s, launch_pdl_enabled());
     if (ce == cudaSuccess && p.ctas > 1) ce = attn_join_launch(p.args.s, p.ctas, s);
     if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));
     return KS_SUCCESS;

@@ -1,0 +1,19 @@
+// What the kernels of the attention over 4-bit pages share.
+#pragma once
+
+#include "ks_attention.cuh"
+#include "ks_fp4.cuh"
+
+namespace ks {
+
+struct Attn4Args {
+    AttnArgs s;
+    Pool4 k, v;
+};
+
+// The tensor-core kernel (ks_attention_4bit_tc.cu): whether it takes a call, and its launch.
+bool attn4_tc_fits(const ks_attention_args_t &a);
+cudaError_t attn4_tc_launch(const Attn4Args &args, uintptr_t code_align, uintptr_t scale_align, int ctas, cudaStream_t stream,
+                            bool pdl);
+
+}  // namespace ks

@@ -1,0 +1,40 @@
+// Paged attention over 4-bit pages on the fifth-generation tensor cores: the kernel of ks_attention_tc.cu with four more
+// warps, which make fp16 tiles of the pages instead of the copies by TMA.
+#include "ks_attention_tc.cuh"
+#include "ks_attention_4bit.cuh"
+
+namespace ks {
+
+bool attn4_tc_fits(const ks_attention_args_t &a) {
+    if (a.head_dim > 128 || a.pages <= 0) return false;
+    // the queries' tensor map takes strides below 2^40 bytes and not zero
+    const int64_t strides[2] = {a.q_token_stride, a.q_head_stride}, counts[2] = {a.tokens, a.q_heads};
+    for (int i = 0; i < 2; ++i)
+        if (counts[i] > 1 && (strides[i] == 0 || strides[i] >= (1ll << 39))) return false;
+    return true;
+}
+
+cudaError_t attn4_tc_launch(const Attn4Args &args, uintptr_t code_align, uintptr_t scale_align, int ctas, cudaStream_t stream,
+                            bool pdl) {
+    AttnArgs s = args.s;
+    CUtensorMap q_map;
+    if (!attn_query_map(&q_map, s)) return cudaErrorInvalidValue;
+    Pages4 pages;
+    pages.k = args.k;
+    pages.v = args.v;
+    const int dim = (int)s.a.head_dim;
+    pages.whole = (dim == 64 || dim == 128) && (code_align & 15) == 0 && (scale_align & 3) == 0;
+    const bool bf16 = s.a.dtype == KS_DTYPE_BF16;
+    const void *f = dim <= 64 ? (bf16 ? (const void *)attn_tc_kernel<__nv_bfloat16, 64, Pages4>
+                                      : (const void *)attn_tc_kernel<__half, 64, Pages4>)
+                              : (bf16 ? (const void *)attn_tc_kernel<__nv_bfloat16, 128, Pages4>
+                                      : (const void *)attn_tc_kernel<__half, 128, Pages4>);
+    const int smem = dim <= 64 ? Tc<64, true>::kSmem : Tc<128, true>::kSmem;
+    if (!allow_smem(f, (size_t)smem)) return cudaErrorInvalidConfiguration;
+    void *kp[] = {&s, &q_map, &pages};
+    return launch_kernel(f, dim3((unsigned)ctas), dim3(Split<true>::kThreads), (size_t)smem, kp, stream, pdl);
+}
+
+int fault_flags_attention_4bit_tc(bool clear) { return fault_flags_t(clear); }
+
+}  // namespace ks

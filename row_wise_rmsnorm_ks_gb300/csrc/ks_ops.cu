@@ -1625,7 +1625,7 @@ ks_status_t op_plan(int op, int64_t rows, int64_t hidden, ks_dtype_t dtype, bool
 int fault_flags_ops(bool clear) {
     const int parts[] = {fault_flags_t(clear), fault_flags_rotary(clear), fault_flags_attention(clear),
                          fault_flags_attention_tc(clear), fault_flags_rotary_4bit(clear),
-                         fault_flags_attention_4bit(clear)};
+                         fault_flags_attention_4bit(clear), fault_flags_attention_4bit_tc(clear)};
     int all = 0;
     for (int v : parts) {
         if (v < 0) return -1;
