@@ -9,14 +9,18 @@
 // Few rows make this a stream of the cache, 144 bytes per key of 128 values, and of the instructions that make fp16 of
 // it: each pair of codes is a conversion and a product with its group's scale. So the matrix instructions
 // take the cache as their 16-row operand, straight from registers, and the query rows as the 8 columns: S^T = K Q^T
-// and O^T += V^T P^T. Nothing passes through shared memory on the way:
+// and O^T += V^T P^T, fp16 values never leaving the registers:
 //   - K: a product's sum runs over any order of the dims, so the lane quad's member t takes dims t D / 4 and on of
-//     keys g and g + 8 (g = lane / 4): one contiguous load a key. Queries lie in registers in the same order.
-//   - V^T: rows may be any dims, so lane row g has dims g D / 8 and on, of the keys 2 t, 2 t + 1, 2 t + 8 and
-//     2 t + 9 that the operand's pairs want: the codes of two keys are merged by nibbles, and a conversion then
-//     gives a pair over keys.
+//     two keys: one contiguous load a key. Queries lie in registers in the same order.
+//   - V^T: rows may be any dims, so lane row g = lane / 4 has dims g D / 8 and on, of the four keys that the operand's
+//     pairs want: the codes of two keys are merged by nibbles, and a conversion then gives a pair over keys.
 //   - P^T comes from S^T by one 8x8 transposition of a matrix of 16-bit values for 8 keys.
-// A warp runs alone on every fourth 32-key step, and loads the next step's keys as soon as this step's are used.
+// Row 2 t + e of a product's first 8 is key t + 4 e of its block, and so for the last 8, so that the lanes of a load have
+// neighbouring keys.
+// A warp runs alone on every fourth 32-key step, with its own ring of asynchronous copies in shared memory (no barrier
+// in the loop; one ring for eight warps, which then wait for each other, takes 1.4 times as long; bulk copies, which
+// lanes issue one after the other, take as many instructions as these). Pools that copies cannot take are loaded to
+// registers a step ahead (kAny).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -33,10 +37,13 @@ constexpr int kStep = 32;                // keys of a warp's step
 constexpr int kUnit = kWarps * kStep;    // keys of a unit
 constexpr int kTileCost = 3;             // units that beginning and ending a row tile costs
 constexpr int kSlotRows = 16;            // rows of a partial slot
-constexpr float kLift = 32768.0f;        // what a row's largest probability counts
+// Exponentials are taken to a row's base, which lies kLift below the maximum of the scores when it was taken (in powers
+// of two). It stays until a lane's probabilities outgrow it: most steps need no maximum. fp16 ends at 65504 and is
+// normal down to 2^-14, so probabilities keep their precision down to 2^-25 of the row's largest and end at 2^-36.
+constexpr float kLift = 11.0f, kGrowth = 32768.0f;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -44,7 +51,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -71,51 +78,111 @@ __device__ __forceinline__ uint32_t pack16(float x, float y, bool bf16) {
     return w;
 }
 
-// kN words of codes. Whole: aligned to their size; otherwise in groups of two, those at and past `room` zeros.
-template <int kN, bool kWhole>
+// kN words of codes, in groups of two where kN is even; those at and past `room` are zeros.
+template <int kN>
 __device__ __forceinline__ void load_codes(uint32_t (&w)[kN], const uint8_t *p, int room) {
-    if constexpr (kWhole && kN % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < kN / 4; ++i) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-        }
-    } else if constexpr (kN % 2 == 0) {
+    if constexpr (kN % 2 == 0) {
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i) {
             uint2 x = make_uint2(0, 0);
-            if (kWhole || 2 * i < room) x = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+            if (2 * i < room) x = __ldg(reinterpret_cast<const uint2 *>(p) + i);
             w[2 * i] = x.x, w[2 * i + 1] = x.y;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) w[i] = kWhole || i < room ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0;
+        for (int i = 0; i < kN; ++i) w[i] = i < room ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0;
     }
 }
 
-// kN scales, one a byte of the result. Whole: aligned to kN bytes where kN is 2 or 4.
-template <int kN, bool kWhole>
+// kN scales, one a byte of the result.
+template <int kN>
 __device__ __forceinline__ uint32_t load_scales(const uint8_t *p, int room) {
-    if constexpr (kWhole && kN == 4) return __ldg(reinterpret_cast<const uint32_t *>(p));
-    if constexpr (kWhole && kN == 2) return __ldg(reinterpret_cast<const uint16_t *>(p));
     uint32_t x = 0;
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-        if (kWhole || i < room) x |= (uint32_t)__ldg(p + i) << (8 * i);
+        if (i < room) x |= (uint32_t)__ldg(p + i) << (8 * i);
     return x;
 }
 
-// kR: 64 dims each; kTiles: tiles of 8 query rows; kWhole: head_dim is 64 kR, and rows of codes and scales are aligned
-// to what a lane loads of them, and pages are whole blocks of 16 keys.
-template <int kR, int kTiles, bool kWhole>
-__global__ void __launch_bounds__(kThreads)
+// How pools lie:
+//   kAny     any strides and page sizes, rows of any number of groups: each key's page is looked up on its own
+//   kBlocks  head_dim is 64 kR, rows of codes and scales are aligned to what is copied of them at once, pages are whole
+//            blocks of 16 keys, both pools have the same strides, those of the scales an eighth of the codes': a
+//            block has one address. Copied by 16 bytes of codes and rows of scales.
+//   kRuns    kBlocks with a head's keys one behind the other: a warp copies 512 bytes of a block's codes at once
+enum { kAny, kBlocks, kRuns };
+
+// (of a row's m below 8; rows 8 on are 8 keys on)
+__device__ __forceinline__ int place(int m) { return (m >> 1) + 4 * (m & 1); }
+
+// A warp's ring of steps: keys' codes, values' codes, keys' scales, values' scales.
+template <int kR>
+struct Ring {
+    static constexpr int kStages = 3;
+    static constexpr int kRow = 32 * kR, kScaleRow = 4 * kR;  // bytes of a key
+    static constexpr int kCodes = kStep * kRow, kScales = kStep * kScaleRow;
+    static constexpr int kStageBytes = 2 * (kCodes + kScales);
+    // Byte of a 16-byte piece of a key's codes. Rows of 128 bytes all begin on one bank: where pieces are copied one by
+    // one, they change places.
+    template <int kPool>
+    __device__ __forceinline__ static uint32_t piece(int key, int c) {
+        return key * kRow + ((kR == 4 && kPool == kBlocks ? c ^ (key & 7) : c) << 4);
+    }
+};
+
+template <int kR, int kTiles, int kPool>
+struct Shared {
+    static constexpr int kPitch = 64 * kR + 4;
+    static constexpr int kJoin = kWarps * 8 * kTiles * kPitch * 4;  // the warps' outputs, over the rings
+    static constexpr int kRingBytes = kPool != kAny ? kWarps * Ring<kR>::kStages * Ring<kR>::kStageBytes : 0;
+    static constexpr int kBytes = kJoin > kRingBytes ? kJoin : kRingBytes;
+};
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int n) {  // n of them, zeros behind
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(n) : "memory");
+}
+
+template <int kN>
+__device__ __forceinline__ void shared_words(uint32_t (&w)[kN], const uint8_t *p) {
+    if constexpr (kN == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (kN == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+    }
+}
+template <int kN, bool kAligned = true>
+__device__ __forceinline__ uint32_t shared_bytes(const uint8_t *p) {
+    if constexpr (kN == 4) return *reinterpret_cast<const uint32_t *>(p);
+    if constexpr (kN == 2 && kAligned) return *reinterpret_cast<const uint16_t *>(p);
+    uint32_t x = 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) x |= (uint32_t)p[i] << (8 * i);
+    return x;
+}
+
+// kR: 64 dims each; kTiles: tiles of 8 query rows.
+template <int kR, int kTiles, int kPool>
+__global__ void __launch_bounds__(kThreads, kPool == kAny ? (kR * kTiles == 1 ? 4 : kR * kTiles == 2 ? 3 : 2)
+                                                          : (kR * kTiles <= 2 ? 4 : 2))
 attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
+    using C = Ring<kR>;
+    constexpr bool kWhole = kPool != kAny;
     constexpr int kWords = 2 * kR;                 // of a key's codes, for a quad's member
     constexpr int kVScales = (kR + 1) / 2;         // of a value's row, for a lane row
     constexpr int kRows = 8 * kTiles;
-    constexpr int kPitch = 64 * kR + 4;
-    __shared__ __align__(16) float ow[kWarps][kRows][kPitch];  // written and read in pairs
+    constexpr int kPitch = Shared<kR, kTiles, kPool>::kPitch;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float mw[kWarps][kRows], lw[kWarps][kRows];
+    float *ow = reinterpret_cast<float *>(smem);   // [kWarps][kRows][kPitch]
     const AttnArgs &s = args.s;
     const ks_attention_args_t &a = s.a;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -125,6 +192,7 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
     if (threadIdx.x == 0) attn_joins(s, ctas)[cta].pieces = 0;
     AttnCursor cur = attn_begin<kThreads>(s, cta, ctas);
     if (cur.left <= 0) return;
+    uint32_t stage = 0;  // of the next step in the warp's ring
     AttnSeq q = attn_seq(a, cur.seq);
 
     const int dim = (int)a.head_dim, page_size = (int)a.page_size;
@@ -133,6 +201,15 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
     const int v_first = g * kR;                    // its first word (8 dims) of a value
     const int k_room = 2 * (dim / 16 - k_first), v_room = dim / 8 - v_first;
     const int v_group = v_first / 2;
+    uint8_t *ring = smem + warp * C::kStages * C::kStageBytes;
+    const int64_t code_slot = args.k.code_slot;
+    // Where in a stage this lane's codes and scales of the first keys and values are.
+    const int k_row = place(g), v_row = t;
+    const uint32_t k_lane = k_row * C::kRow + (kR == 4 ? 0 : t * 8 * kR), v_lane = C::kCodes + v_row * C::kRow + (kR == 4 ? 0 : g * 4 * kR);
+    const uint32_t k_scale_lane = 2 * C::kCodes + k_row * C::kScaleRow + k_first;
+    const uint32_t v_scale_lane = 2 * C::kCodes + C::kScales + v_row * C::kScaleRow + v_group;
+    // kR 4: the 16-byte pieces, which change places by the key's low bits (8 and 4 keys on: all of them, and one)
+    auto piece = [&](int key, int c) { return (uint32_t)(kPool == kBlocks ? c ^ (key & 7) : c) << 4; };
 
     while (true) {
         const AttnSpan span = attn_span(s, cur, q);
@@ -140,64 +217,133 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
         if (first >= last) break;  // the share ends in the tile's extra cost
         const int sees = attn_tile_keys(s, q, cur.row_tile);
         const int kv_head = cur.head / s.head_splits;
-        const uint8_t *k_codes = args.k.codes + kv_head * args.k.code_head + k_first * 8;
-        const uint8_t *k_scales = args.k.scales + kv_head * args.k.scale_head + k_first;
-        const uint8_t *v_codes = args.v.codes + kv_head * args.v.code_head + v_first * 4;
-        const uint8_t *v_scales = args.v.scales + kv_head * args.v.scale_head + v_group;
+        const uint8_t *k_codes = args.k.codes + kv_head * args.k.code_head, *k_scales = args.k.scales + kv_head * args.k.scale_head;
+        const uint8_t *v_codes = args.v.codes + kv_head * args.v.code_head, *v_scales = args.v.scales + kv_head * args.v.scale_head;
+        if (!kWhole) {
+            k_codes += k_first * 8;
+            k_scales += k_first;
+            v_codes += v_first * 4;
+            v_scales += v_group;
+        }
         const int32_t *table = a.page_table + (int64_t)cur.seq * a.table_stride;
 
-        uint32_t kc[4][kWords], ks[4];             // keys g, g + 8, g + 16, g + 24
-        uint32_t vc[8][kR], vs[8];                 // values 2 t, 2 t + 1, 2 t + 8, 2 t + 9, then those 16 on
-        // The page and the place of key `lane` of a step; page -1: no such key, or its page is not in the pool.
-        auto look_up = [&](int key0, int &page, int &place) {
-            const int key = key0 + lane;
-            page = -1;
-            place = 0;
-            if (key < sees) {
-                const int index = key / page_size;
-                page = __ldg(table + index);
-                place = key - index * page_size;
-                if ((uint32_t)page >= (uint64_t)a.pages) {
-                    atomicOr(&g_fault_flags, kFaultBadIndex);
-                    page = -1;
+        uint32_t kc[kWhole ? 2 : 4][kWords], ks[kWhole ? 2 : 4];  // kAny: of a step; otherwise of a block of 16
+        uint32_t vc[kWhole ? 4 : 8][kR], vs[kWhole ? 4 : 8];
+        const bool whole = first == 0 && last == units;
+        const int end = min(sees, last * kUnit);  // steps at and past it are not this CTA's
+        // Where the keys of a step are. kAny: the page and the slot of key `lane`, page -1 where there is no such key or
+        // its page is not in the pool. Otherwise for each block of 16 the page as the table has it and the slot, -1 where
+        // there is no key.
+        struct Where {
+            int page[kWhole ? 2 : 1], slot[kWhole ? 2 : 1];
+        };
+        auto look_up = [&](int key_at) {
+            Where w;
+#pragma unroll
+            for (int b = 0; b < (kWhole ? 2 : 1); ++b) {
+                const int key = kWhole ? key_at + 16 * b : key_at + lane;
+                w.page[b] = w.slot[b] = -1;
+                if (kWhole ? key < end : key_at < end && key < sees) {
+                    int index;
+                    if (kWhole) index = (int)(__umulhi((uint32_t)key >> 3, args.page_magic) >> args.page_shift);
+                    else index = key / page_size;
+                    w.slot[b] = key - index * page_size;
+                    w.page[b] = __ldg(table + index);
+                    if (!kWhole && (uint32_t)w.page[b] >= (uint64_t)a.pages) {
+                        atomicOr(&g_fault_flags, kFaultBadIndex);
+                        w.page[b] = -1;
+                    }
+                }
+            }
+            return w;
+        };
+        // ---- copies of a step. Blocks whose page is not in the pool, and those without a key, come out as zeros.
+        auto copy_step = [&](const Where &w, uint32_t to_stage) {
+            const uint32_t to = smem_addr(ring) + to_stage * C::kStageBytes;
+            int64_t at[2];
+            int n[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const bool good = (uint32_t)w.page[b] < (uint64_t)a.pages;
+                if (!good && w.slot[b] >= 0) atomicOr(&g_fault_flags, kFaultBadIndex);
+                at[b] = good ? w.page[b] * args.k.code_page + w.slot[b] * code_slot : 0;
+                n[b] = good ? 16 : 0;
+#pragma unroll
+                for (int i = 0; i < kR; ++i) {
+                    const int in = i * 32 + lane, key = in / (2 * kR), c = in % (2 * kR);  // 16 bytes of a key's codes
+                    const int64_t off = at[b] + (kPool == kRuns ? in * 16 : key * code_slot + c * 16);
+                    const uint32_t dst = to + C::template piece<kPool>(16 * b + key, c);
+                    copy_async<16>(dst, k_codes + off, n[b]);
+                    copy_async<16>(dst + C::kCodes, v_codes + off, n[b]);
+                }
+            }
+            if constexpr (kPool == kRuns) {  // keys' scales of both blocks, then values': 16 bytes a lane
+#pragma unroll
+                for (int i = 0; i < (kR + 1) / 2; ++i) {
+                    const int in = i * 32 + lane, part = in / (4 * kR);
+                    const int64_t off = ((part & 1 ? at[1] : at[0]) >> 3) + in % (4 * kR) * 16;
+                    if (kR % 2 == 0 || in < 16 * kR)
+                        copy_async<16>(to + 2 * C::kCodes + in * 16, (part < 2 ? k_scales : v_scales) + off, part & 1 ? n[1] : n[0]);
+                }
+            } else {  // a key's row
+                constexpr int kBytes = kR == 3 ? 4 : C::kScaleRow;
+                const int64_t off = ((lane < 16 ? at[0] : at[1]) + lane % 16 * code_slot) >> 3;
+                const int of = (lane < 16 ? n[0] : n[1]) ? kBytes : 0;
+#pragma unroll
+                for (int i = 0; i < C::kScaleRow / kBytes; ++i) {
+                    const uint32_t dst = to + 2 * C::kCodes + lane * C::kScaleRow + i * kBytes;
+                    copy_async<kBytes>(dst, k_scales + off + i * kBytes, of);
+                    copy_async<kBytes>(dst + C::kScales, v_scales + off + i * kBytes, of);
                 }
             }
         };
-        auto load_keys = [&](int page, int place) {
+        auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+        // ---- kAny: loads of a step to registers
+        auto load_keys = [&](const Where &w) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = 8 * i + g;
-                const int64_t p = __shfl_sync(0xFFFFFFFFu, page, at), r = __shfl_sync(0xFFFFFFFFu, place, at);
+            for (int i = 0; i < (kWhole ? 0 : 4); ++i) {
+                const int at = 8 * i + place(g);
+                const int64_t p = __shfl_sync(0xFFFFFFFFu, w.page[0], at), r = __shfl_sync(0xFFFFFFFFu, w.slot[0], at);
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) kc[i][j] = 0;
                 ks[i] = 0;
                 if (p >= 0) {
-                    load_codes<kWords, kWhole>(kc[i], k_codes + p * args.k.code_page + r * args.k.code_slot, k_room);
-                    ks[i] = load_scales<kR, kWhole>(k_scales + p * args.k.scale_page + r * args.k.scale_slot, k_room / 2);
+                    load_codes<kWords>(kc[i], k_codes + p * args.k.code_page + r * args.k.code_slot, k_room);
+                    ks[i] = load_scales<kR>(k_scales + p * args.k.scale_page + r * args.k.scale_slot, k_room / 2);
                 }
             }
         };
-        auto load_values = [&](int page, int place) {
+        auto load_values = [&](const Where &w) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int at = 16 * (i / 4) + 8 * (i / 2 % 2) + 2 * t + i % 2;
-                const int64_t p = __shfl_sync(0xFFFFFFFFu, page, at), r = __shfl_sync(0xFFFFFFFFu, place, at);
+            for (int i = 0; i < (kWhole ? 0 : 8); ++i) {
+                const int at = 8 * (i / 2) + t + 4 * (i % 2);
+                const int64_t p = __shfl_sync(0xFFFFFFFFu, w.page[0], at), r = __shfl_sync(0xFFFFFFFFu, w.slot[0], at);
 #pragma unroll
                 for (int j = 0; j < kR; ++j) vc[i][j] = 0;
                 vs[i] = 0;
                 if (p >= 0) {
-                    load_codes<kR, kWhole>(vc[i], v_codes + p * args.v.code_page + r * args.v.code_slot, v_room);
-                    vs[i] = load_scales<kVScales, false>(v_scales + p * args.v.scale_page + r * args.v.scale_slot,
-                                                         kWhole ? kVScales : dim / 16 - v_group);
+                    load_codes<kR>(vc[i], v_codes + p * args.v.code_page + r * args.v.code_slot, v_room);
+                    vs[i] = load_scales<kVScales>(v_scales + p * args.v.scale_page + r * args.v.scale_slot,
+                                                         dim / 16 - v_group);
                 }
             }
         };
 
         int key0 = first * kUnit + warp * kStep;
-        int page, place;
-        look_up(key0, page, place);
-        load_keys(page, place);
-        load_values(page, place);
+        Where next = look_up(key0);
+        if constexpr (kWhole) {
+#pragma unroll
+            for (int i = 0; i < C::kStages - 1; ++i) {
+                const int at = key0 + i * kUnit;
+                const Where now = next;
+                next = look_up(at + kUnit);  // pages are asked for a step before their keys
+                copy_step(now, stage + i < C::kStages ? stage + i : stage + i - C::kStages);
+                commit();
+            }
+        } else {
+            load_keys(next);
+            load_values(next);
+        }
 
         // the query rows as the products' columns, zeros where the tile has none, and what their scores count
         uint32_t qf[kTiles][4 * kR][2];
@@ -260,14 +406,48 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
             for (int i = 0; i < 4 * kR; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
         }
 
-        for (int unit = first; unit < last; ++unit, key0 += kUnit) {
-            if (key0 >= sees) break;  // the tile's last unit may end before this warp's step
-            int next_page = -1, next_place = 0;
-            if (unit + 1 < last) look_up(key0 + kUnit, next_page, next_place);
-            // ---- scores of 32 keys: key 16 b + g (and 8 on), rows 2 t and 2 t + 1
+        for (; key0 < end; key0 += kUnit) {
+            const uint8_t *tile = ring + stage * C::kStageBytes;
+            if constexpr (kWhole) {
+                const int ahead = key0 + (C::kStages - 1) * kUnit;
+                const Where now = next;
+                next = look_up(ahead + kUnit);
+                if (ahead < end) copy_step(now, stage ? stage - 1 : C::kStages - 1);
+                commit();
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+                __syncwarp();
+                if (++stage == C::kStages) stage = 0;
+            } else {
+                next = look_up(key0 + kUnit);
+            }
+            // ---- scores of 32 keys: key place(g) of block b (and 8 on), rows 2 t and 2 t + 1
             float sc[2][kTiles][4];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
+                const int of = kWhole ? 0 : 2 * b;  // the block's keys among those in registers
+                if constexpr (kWhole) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint8_t *at = tile + k_lane + (16 * b + 8 * i) * C::kRow;
+                        if constexpr (kR == 4) {
+                            uint32_t x[4], y[4];
+                            shared_words(x, at + piece(k_row, 2 * t));
+                            shared_words(y, at + piece(k_row, 2 * t + 1));
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) kc[i][j] = x[j], kc[i][4 + j] = y[j];
+                        } else if constexpr (kR == 3) {
+#pragma unroll
+                            for (int j = 0; j < 3; ++j) {
+                                uint32_t x[2];
+                                shared_words(x, at + 8 * j);
+                                kc[i][2 * j] = x[0], kc[i][2 * j + 1] = x[1];
+                            }
+                        } else {
+                            shared_words(kc[i], at);
+                        }
+                        ks[i] = shared_bytes<kR>(tile + k_scale_lane + (16 * b + 8 * i) * C::kScaleRow);
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n) sc[b][n][0] = sc[b][n][1] = sc[b][n][2] = sc[b][n][3] = 0.0f;
 #pragma unroll
@@ -275,12 +455,11 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
                     uint32_t scale[2], h[2][8];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t byte = ks[2 * b + i] >> (8 * r) & 0xFF;
-                        scale[i] = e4m3_to_half(byte | byte << 8);
+                        scale[i] = e4m3_to_half(__byte_perm(ks[of + i], 0, r | r << 4));
                         uint32_t x[4];
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
-                            fp4_to_half(kc[2 * b + i][2 * r + w], x);
+                            fp4_to_half(kc[of + i][2 * r + w], x);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) h[i][4 * w + j] = half2_mul(x[j], scale[i]);
                         }
@@ -293,63 +472,105 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
                     }
                 }
             }
-            load_keys(next_page, next_place);
+            if (!kWhole) load_keys(next);
             // ---- probabilities
             const bool masked = key0 + kStep > all_see;
             uint32_t p[2][kTiles][2];
 #pragma unroll
             for (int n = 0; n < kTiles; ++n) {
-                float top[2] = {m[n][0], m[n][1]};
+                float sum[2];
+                // to the rows' old bases; again, with new ones, where a row has outgrown its base or has none yet
+                bool fresh = false;
+                while (true) {
+                    const float base[2] = {attn_base(m[n][0]), attn_base(m[n][1])};
+                    float x[2][4];
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                    for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = sc[b][n][i] * mul[n][i & 1];
-                        if (masked && key0 + 16 * b + 8 * (i / 2) + g >= limit[n][i & 1]) x = -INFINITY;
-                        sc[b][n][i] = x;
-                        top[i & 1] = fmaxf(top[i & 1], x);
+                        for (int i = 0; i < 4; ++i) x[b][i] = __fmaf_rn(sc[b][n][i], mul[n][i & 1], -base[i & 1]);
+                    if (masked) {
+                        __syncwarp();
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (key0 + 16 * b + 8 * (i / 2) + k_row >= limit[n][i & 1]) x[b][i] = -INFINITY;
                     }
+                    sum[0] = sum[1] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 4));
-                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 8));
-                    top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 16));
-                }
-                if (__any_sync(0xFFFFFFFFu, top[0] != m[n][0] || top[1] != m[n][1])) {
-                    const float f0 = exp2_approx(m[n][0] - attn_base(top[0])), f1 = exp2_approx(m[n][1] - attn_base(top[1]));
-                    l[n][0] *= f0;
-                    l[n][1] *= f1;
+                    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[b][i] = exp2_approx(x[b][i]);
+                            sum[i & 1] += x[b][i];
+                        }
+                        p[b][n][0] = pack_half(x[b][0], x[b][1]);
+                        p[b][n][1] = pack_half(x[b][2], x[b][3]);
+                    }
+                    if (fresh || !__any_sync(0xFFFFFFFFu, !(fmaxf(sum[0], sum[1]) <= kGrowth) ||
+                                                              fminf(m[n][0], m[n][1]) == -INFINITY))
+                        break;
+                    fresh = true;
+                    float f[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int i = k; i < 4; i += 2) {
+                                const float y = sc[b][n][i] * mul[n][k];
+                                if (!masked || key0 + 16 * b + 8 * (i / 2) + k_row < limit[n][k]) top = fmaxf(top, y);
+                            }
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                        top = fmaxf(m[n][k], fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16)) - kLift);
+                        f[k] = exp2_approx(m[n][k] - attn_base(top));
+                        l[n][k] *= f[k];
+                        m[n][k] = top;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4 * kR; ++i) {
-                        o[n][i][0] *= f0;
-                        o[n][i][1] *= f1;
-                        o[n][i][2] *= f0;
-                        o[n][i][3] *= f1;
+                        o[n][i][0] *= f[0];
+                        o[n][i][1] *= f[1];
+                        o[n][i][2] *= f[0];
+                        o[n][i][3] *= f[1];
                     }
-                    m[n][0] = top[0];
-                    m[n][1] = top[1];
                 }
-                const float b0 = attn_base(m[n][0]), b1 = attn_base(m[n][1]);
+                l[n][0] += sum[0];
+                l[n][1] += sum[1];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const float x0 = exp2_approx(sc[b][n][0] - b0) * kLift, x1 = exp2_approx(sc[b][n][1] - b1) * kLift;
-                    const float x2 = exp2_approx(sc[b][n][2] - b0) * kLift, x3 = exp2_approx(sc[b][n][3] - b1) * kLift;
-                    l[n][0] += x0 + x2;
-                    l[n][1] += x1 + x3;
-                    p[b][n][0] = transposed(pack_half(x0, x1));
-                    p[b][n][1] = transposed(pack_half(x2, x3));
+                    p[b][n][0] = transposed(p[b][n][0]);
+                    p[b][n][1] = transposed(p[b][n][1]);
                 }
             }
             // ---- outputs: dims 8 kR g + 2 j (and the next), rows 2 t and 2 t + 1
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
+                const int of = kWhole ? 0 : 4 * b;
+                if constexpr (kWhole) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = 16 * b + 8 * (i / 2) + 4 * (i % 2);  // and v_row on
+                        shared_words(vc[i], tile + v_lane + key * C::kRow + (kR == 4 ? piece(v_row + 4 * (i % 2), g) : 0));
+                        vs[i] = shared_bytes<kVScales, kR % 2 == 0>(tile + v_scale_lane + key * C::kScaleRow);
+                    }
+                    // A scale behind the last key that the tile sees may be anything, and a probability of 0 would let
+                    // a NaN through. (Its key's score is masked whatever it is.)
+                    if (key0 + kStep > sees) {
+                        __syncwarp();  // a branch, not selections in every step
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (key0 + 16 * b + 8 * (i / 2) + 4 * (i % 2) + v_row >= sees) vs[i] = 0;
+                    }
+                }
                 uint32_t scale[kVScales][2];
 #pragma unroll
                 for (int i = 0; i < kVScales; ++i)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        scale[i][k] = e4m3_to_half((vs[4 * b + 2 * k] >> (8 * i) & 0xFF) |
-                                                   (vs[4 * b + 2 * k + 1] >> (8 * i) & 0xFF) << 8);
+                        scale[i][k] = e4m3_to_half(__byte_perm(vs[of + 2 * k], vs[of + 2 * k + 1], i | (4 + i) << 4));
 #pragma unroll
                 for (int w = 0; w < kR; ++w) {
                     // the word's group among the lane's scales; with kR odd it depends on whether v_first is
@@ -357,7 +578,7 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
                     uint32_t h[2][2][4];  // [pair of keys][even, odd dims][byte]
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint32_t x = vc[4 * b + 2 * k][w], y = vc[4 * b + 2 * k + 1][w];
+                        const uint32_t x = vc[of + 2 * k][w], y = vc[of + 2 * k + 1][w];
                         const uint32_t u = i0 == i1 || !(v_first & 1) ? scale[i0 < kVScales ? i0 : 0][k]
                                                                       : scale[i1 < kVScales ? i1 : 0][k];
                         fp4_to_half((x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u), h[k][0]);
@@ -376,8 +597,10 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
                     }
                 }
             }
-            load_values(next_page, next_place);
+            if (kWhole) __syncwarp();  // all lanes have read the stage before it is refilled
+            else load_values(next);
         }
+        if (kWhole) asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
@@ -387,7 +610,8 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
                 l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], 16);
             }
 
-        // Join the four warps.
+        // Join the four warps, over the rings.
+        if (kWhole) __syncthreads();
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
@@ -395,14 +619,13 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
                 const int r = n * 8 + 2 * t + i;
 #pragma unroll
                 for (int j = 0; j < 4 * kR; ++j)
-                    *reinterpret_cast<float2 *>(&ow[warp][r][8 * kR * g + 2 * j]) = make_float2(o[n][j][i], o[n][j][2 + i]);
+                    *reinterpret_cast<float2 *>(ow + (warp * kRows + r) * kPitch + 8 * kR * g + 2 * j) = make_float2(o[n][j][i], o[n][j][2 + i]);
                 if (g == 0) {
                     mw[warp][r] = m[n][i];
                     lw[warp][r] = l[n][i];
                 }
             }
         __syncthreads();
-        const bool whole = first == 0 && last == units;
         float *part = attn_slot(s, cta, first == 0 ? 1 : 0);
         for (int c = warp; c < dim / 8; c += kWarps) {  // 8 columns
             float ll[2] = {}, mm[2] = {-INFINITY, -INFINITY}, acc[4] = {};
@@ -414,7 +637,7 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float f = exp2_approx(mw[w][r] - attn_base(mm[k]));
-                    const float2 x = *reinterpret_cast<const float2 *>(&ow[w][r][c * 8 + 2 * t]);
+                    const float2 x = *reinterpret_cast<const float2 *>(ow + (w * kRows + r) * kPitch + c * 8 + 2 * t);
                     ll[k] += f * lw[w][r];
                     acc[2 * k] += f * x.x;
                     acc[2 * k + 1] += f * x.y;
@@ -460,20 +683,27 @@ struct Attn4Plan {
     Attn4Args args;
     int ctas;
     const void *kernel;  // NULL: the tensor-core kernel
+    int smem;
 };
 
-template <bool kWhole>
-const void *rows_kernel(int r, int tiles) {
+template <int kR, int kTiles, int kPool>
+const void *rows_kernel(int *smem) {
+    *smem = Shared<kR, kTiles, kPool>::kBytes;
+    return (const void *)attn4_rows_kernel<kR, kTiles, kPool>;
+}
+
+template <int kPool>
+const void *rows_kernel(int r, int tiles, int *smem) {
     switch (r) {
-    case 1: return tiles == 1 ? (const void *)attn4_rows_kernel<1, 1, kWhole> : (const void *)attn4_rows_kernel<1, 2, kWhole>;
-    case 2: return tiles == 1 ? (const void *)attn4_rows_kernel<2, 1, kWhole> : (const void *)attn4_rows_kernel<2, 2, kWhole>;
-    case 3: return (const void *)attn4_rows_kernel<3, 1, kWhole>;
-    default: return (const void *)attn4_rows_kernel<4, 1, kWhole>;
+    case 1: return tiles == 1 ? rows_kernel<1, 1, kPool>(smem) : rows_kernel<1, 2, kPool>(smem);
+    case 2: return tiles == 1 ? rows_kernel<2, 1, kPool>(smem) : rows_kernel<2, 2, kPool>(smem);
+    case 3: return rows_kernel<3, 1, kPool>(smem);
+    default: return rows_kernel<4, 1, kPool>(smem);
     }
 }
 
 // CTAs of a kernel that an SM holds, asked once per kernel and device.
-int resident(const void *f) {
+int resident(const void *f, int smem) {
     static std::mutex mu;
     static std::unordered_map<uint64_t, int> known;
     int dev = 0;
@@ -483,7 +713,8 @@ int resident(const void *f) {
     auto it = known.find(key);
     if (it != known.end()) return it->second;
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, kThreads, 0) != cudaSuccess) return 0;
+    if (!allow_smem(f, (size_t)smem)) return 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, kThreads, (size_t)smem) != cudaSuccess) return 0;
     if (n > 0) known.emplace(key, n);
     return n;
 }
@@ -497,7 +728,27 @@ int row_tiles(const ks_attention_args_t &a) {
     return a.head_dim > 128 || rows <= 8 ? 1 : rows <= 16 ? 2 : kTc;
 }
 
-ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, uintptr_t code_align, uintptr_t scale_align, Attn4Plan *p) {
+// How the pools of a call lie, given the alignment of their addresses.
+int pool_kind(const ks_attention_4bit_args_t &args, uintptr_t code_align, uintptr_t scale_align) {
+    const ks_attention_args_t &a = args.attention;
+    const ks_pages_4bit_t &k = args.k_pages, &v = args.v_pages;
+    const int64_t r = a.head_dim / 64;
+    if (a.head_dim % 64 || a.page_size % 16 || a.pages <= 0) return kAny;
+    const uintptr_t scales = r == 2 ? 7 : r == 4 ? 15 : 3;
+    if ((code_align & 15) || (scale_align & scales)) return kAny;
+    // an axis of one entry has any stride
+    auto same = [](int64_t count, int64_t x, int64_t y, int64_t xs, int64_t ys) { return count == 1 || (x == y && xs == ys && x == 8 * xs); };
+    if (!same(a.pages, k.code_page_stride, v.code_page_stride, k.scale_page_stride, v.scale_page_stride) ||
+        !same(a.page_size, k.code_slot_stride, v.code_slot_stride, k.scale_slot_stride, v.scale_slot_stride))
+        return kAny;
+    if (k.code_slot_stride != 32 * r) return kBlocks;
+    uintptr_t runs = 0;  // a block of scales is copied at once too
+    for (const ks_pages_4bit_t *p : {&k, &v})
+        runs |= (uintptr_t)p->scales | (uintptr_t)(a.pages > 1 ? p->scale_page_stride : 0) | (uintptr_t)(a.kv_heads > 1 ? p->scale_head_stride : 0);
+    return runs & 15 ? kBlocks : kRuns;
+}
+
+ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, int pool, Attn4Plan *p) {
     AttnArgs &s = p->args.s;
     s.a = a.attention;
     s.scale_log2 = (float)((double)a.attention.scale * 1.4426950408889634 * (double)a.k_pages.factor);
@@ -514,12 +765,19 @@ ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, uintptr_t code_a
         p->ctas = attn_ctas(s, sms);
         return KS_SUCCESS;
     }
-    const uintptr_t codes = r % 4 == 0 || r == 2 ? 15 : 7, scales = r == 2 ? 1 : r == 4 ? 3 : 0;
-    const bool whole = dim == 64 * r && (code_align & codes) == 0 && (scale_align & scales) == 0;
-    p->kernel = whole ? rows_kernel<true>(r, tiles) : rows_kernel<false>(r, tiles);
+    p->kernel = pool == kRuns     ? rows_kernel<kRuns>(r, tiles, &p->smem)
+                : pool == kBlocks ? rows_kernel<kBlocks>(r, tiles, &p->smem)
+                                  : rows_kernel<kAny>(r, tiles, &p->smem);
+    // key / page_size for whole blocks of 16: with d = page_size / 16 and k = floor(log2 d), n / d is the high word of
+    // 2 n m, shifted by k, for m = floor(2^(31 + k) / d) + 1 and n below 2^27 (m d is at most d < 2^(k + 1) above 2^(31 + k),
+    // and n times that below 2^(28 + k), too little to reach the next whole number).
+    const uint32_t blocks = (uint32_t)(s.a.page_size / 16);
+    p->args.page_shift = 0;
+    while (blocks >> (p->args.page_shift + 1)) ++p->args.page_shift;
+    p->args.page_magic = blocks ? (uint32_t)((1ull << (31 + p->args.page_shift)) / blocks) + 1 : 0;
     attn_shape(&s, 8 * tiles, kUnit, kTileCost);
     s.rows = kSlotRows;
-    const int per_sm = resident(p->kernel);
+    const int per_sm = resident(p->kernel, p->smem);
     if (per_sm <= 0) return fail(KS_ERR_CUDA, "the attention kernel cannot be resident");
     p->ctas = attn_ctas(s, (int64_t)sms * per_sm);
     return KS_SUCCESS;
@@ -580,11 +838,11 @@ ks_status_t ks_paged_attention_4bit_workspace(const ks_attention_4bit_args_t *ar
     *bytes = 0;
     ks_status_t st = check_sizes4(args->attention);
     if (st != KS_SUCCESS || args->attention.tokens == 0 || args->attention.seqs == 0) return st;
-    // whichever kernel the pools' alignment, or fewer tokens, pick
+    // whichever kernel the pools' layout, or fewer tokens, pick
     for (int tiles = row_tiles(args->attention); tiles > 0; tiles = tiles == kTc ? 2 : tiles - 1)
-        for (uintptr_t align : {(uintptr_t)0, (uintptr_t)8}) {
+        for (int pool : {kAny, kBlocks, kRuns}) {
             Attn4Plan p;
-            if ((st = plan4(*args, tiles, align, align ? 1 : 0, &p)) != KS_SUCCESS) return st;
+            if ((st = plan4(*args, tiles, pool, &p)) != KS_SUCCESS) return st;
             const int64_t need = attn_workspace_bytes(p.args.s, p.ctas);
             *bytes = *bytes > need ? *bytes : need;
         }
@@ -603,7 +861,7 @@ ks_status_t ks_paged_attention_4bit(const ks_attention_4bit_args_t *args, ks_str
     Attn4Plan p;
     int tiles = row_tiles(a);
     if (tiles == kTc && !attn4_tc_fits(a)) tiles = 2;
-    if ((st = plan4(*args, tiles, code_align, scale_align, &p)) != KS_SUCCESS) return st;
+    if ((st = plan4(*args, tiles, pool_kind(*args, code_align, scale_align), &p)) != KS_SUCCESS) return st;
     const int64_t need = attn_workspace_bytes(p.args.s, p.ctas);
     if (a.workspace_bytes < need)
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace has %lld bytes, %lld are needed", (long long)a.workspace_bytes,
@@ -615,7 +873,8 @@ ks_status_t ks_paged_attention_4bit(const ks_attention_4bit_args_t *args, ks_str
         return fail(KS_ERR_OVERLAP, "the workspace overlaps out or what the call reads");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *kp[] = {&p.args};
-    cudaError_t ce = p.kernel ? launch_kernel(p.kernel, dim3((unsigned)p.ctas), dim3(kThreads), 0, kp, s, launch_pdl_enabled())
+    cudaError_t ce = p.kernel ? launch_kernel(p.kernel, dim3((unsigned)p.ctas), dim3(kThreads), (size_t)p.smem, kp, s,
+                                              launch_pdl_enabled())
                               : attn4_tc_launch(p.args, code_align, scale_align, p.ctas, s, launch_pdl_enabled());
     if (ce == cudaSuccess && p.ctas > 1) ce = attn_join_launch(p.args.s, p.ctas, s);
     if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));

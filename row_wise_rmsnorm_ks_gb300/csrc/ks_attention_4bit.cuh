@@ -9,6 +9,8 @@ namespace ks {
 struct Attn4Args {
     AttnArgs s;
     Pool4 k, v;
+    uint32_t page_magic;  // the quotient of a key and page_size, where pages are whole blocks of 16 keys
+    int32_t page_shift;
 };
 
 // The tensor-core kernel (ks_attention_4bit_tc.cu): whether it takes a call, and its launch.
