@@ -422,7 +422,7 @@ attn_join_kernel(const __grid_constant__ AttnArgs s, int ctas) {
                 for (int u = 0; u < 4; ++u) {
                     const int i = i0 + u * shares;
                     if (i >= j.pieces) continue;
-                    float *part = attn_slot(s, c + i, i == 0 ? 1 : 0);
+                    float *part = attn_slot(s, c + i * s.lanes, i == 0 ? 1 : 0);
                     x[u] = *attn_part(s, part, group, col, lane);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -509,6 +509,7 @@ void attn_plan(const ks_attention_args_t &a, bool tc, int sms, AttnPlan *p) {
     p->s.a = a;
     p->s.scale_log2 = a.scale * 1.4426950408889634f;
     p->s.out_scale = 1.0f;
+    p->s.lanes = 1;
     if (tc) attn_shape(&p->s, attn_tc_rows(), attn_tc_unit(), attn_tc_tile_cost());
     else attn_shape(&p->s, kRows, kUnit, kTileCost);
     int per_sm = 1;

@@ -5,7 +5,10 @@
 // group, token after token) are cut into row tiles of at most M rows, and the keys a row tile sees
 // into units of TN keys. A row tile costs its units and a few more for its beginning and end
 // (tile_cost). All cost of a call, in the order sequence, head, row tile, unit, is shared out evenly:
-// CTA c of G takes [U c / G, U (c + 1) / G), G no more than U. A row tile whose units fall to several
+// CTA c of G takes [U c / G, U (c + 1) / G), G no more than U. Or (`lanes` > 1) every head has as many CTAs as the
+// others, c for head c % lanes, and they share out the cost of one head in the same way, so that all heads of a
+// sequence's keys are read at the same time: a pool that holds tokens one behind the other gives each head 64 bytes
+// of one, which DRAM delivers in full only while they lie in L2. A row tile whose units fall to several
 // CTAs is split over its long axis; each of them leaves its running maximum, sum and unnormalised
 // output in the workspace and a second kernel joins them in a fixed order, so results do not depend
 // on timing. The lengths are read on the device: the launch depends on host-known
@@ -28,6 +31,7 @@ struct AttnArgs {
     int32_t tile_cost;   // units that a row tile costs beside its own
     float scale_log2;    // scale * log2(e)
     float out_scale;     // what the values count
+    int32_t lanes;       // heads that each have their own CTAs, 1 if all heads share all
 };
 
 // What a CTA left in its second partial slot: the beginning of a row tile that later CTAs finish.
@@ -162,14 +166,16 @@ __device__ __forceinline__ int64_t attn_owner(const AttnCursor &c, int64_t u) {
 // It is one chain of latencies (2 to 3 us, most of it fetching code that no cache holds yet), which is
 // why it divides by shifts where it can and computes nothing twice.
 template <int kThreads>
-__device__ inline const AttnCursor &attn_begin(const AttnArgs &s, int cta, int ctas) {
+__device__ inline const AttnCursor &attn_begin(const AttnArgs &s, int block, int blocks) {
     constexpr int kWarps = kThreads / 32;
     __shared__ int64_t warp_units[kWarps];
     __shared__ int64_t found_before, found_per_head;
     __shared__ AttnCursor result;
     const int t = threadIdx.x, lane = t & 31, seqs = (int)s.a.seqs;
     const int per = seqs <= kThreads ? 1 : (seqs + kThreads - 1) / kThreads;
-    const int64_t heads = (int64_t)s.a.kv_heads * s.head_splits;
+    const bool own = s.lanes > 1;
+    const int cta = own ? block / s.lanes : block, ctas = own ? blocks / s.lanes : blocks;
+    const int64_t heads = own ? 1 : (int64_t)s.a.kv_heads * s.head_splits;
     const int lo = min(seqs, t * per), hi = min(seqs, lo + per);
     int64_t mine = 0, per_head = 0;
     for (int b = lo; b < hi; ++b) {
@@ -239,7 +245,7 @@ __device__ inline const AttnCursor &attn_begin(const AttnArgs &s, int cta, int c
             size = min(step, size - place * step);
         }
         if (lane == 0) {
-            result.head = head;
+            result.head = own ? block - cta * s.lanes : head;
             result.row_tile = low;
             result.pos = (int32_t)(u - begins);
         }
@@ -253,8 +259,10 @@ __device__ __forceinline__ void attn_next(const AttnArgs &s, AttnCursor &c, Attn
     c.pos = 0;
     if (++c.row_tile < attn_row_tiles(s, q)) return;
     c.row_tile = 0;
-    if (++c.head < s.a.kv_heads * s.head_splits) return;
-    c.head = 0;
+    if (s.lanes == 1) {
+        if (++c.head < s.a.kv_heads * s.head_splits) return;
+        c.head = 0;
+    }
     do {
         ++c.seq;
         if (c.seq >= s.a.seqs) return;  // not reached while units are left
@@ -272,9 +280,10 @@ __device__ __forceinline__ bool attn_row(const AttnArgs &s, int q0, int n, int h
     return i < s.tile_tokens && in_seq < n && g < s.group;
 }
 
-// Pieces of the row tile that the CTA begins: up to the CTA that has its last unit.
+// Pieces of the row tile that the CTA begins: up to the CTA that has its last unit
+// (every lanes-th CTA has one).
 __device__ __forceinline__ int attn_pieces(const AttnArgs &s, const AttnCursor &c, const AttnSpan &p, int cta) {
-    return (int)(attn_owner(c, c.at - c.pos + s.tile_cost + p.units - 1) - cta + 1);
+    return (int)(attn_owner(c, c.at - c.pos + s.tile_cost + p.units - 1) - cta / s.lanes + 1);
 }
 
 // Workspace: per CTA two slots of rows * (dim + 2) floats (outputs, maxima, sums), then an AttnJoin per

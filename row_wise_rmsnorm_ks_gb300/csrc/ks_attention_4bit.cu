@@ -202,7 +202,6 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
     const int k_room = 2 * (dim / 16 - k_first), v_room = dim / 8 - v_first;
     const int v_group = v_first / 2;
     uint8_t *ring = smem + warp * C::kStages * C::kStageBytes;
-    const int64_t code_slot = args.k.code_slot;
     // Where in a stage this lane's codes and scales of the first keys and values are.
     const int k_row = place(g), v_row = t;
     const uint32_t k_lane = k_row * C::kRow + (kR == 4 ? 0 : t * 8 * kR), v_lane = C::kCodes + v_row * C::kRow + (kR == 4 ? 0 : g * 4 * kR);
@@ -231,70 +230,97 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
         uint32_t vc[kWhole ? 4 : 8][kR], vs[kWhole ? 4 : 8];
         const bool whole = first == 0 && last == units;
         const int end = min(sees, last * kUnit);  // steps at and past it are not this CTA's
-        // Where the keys of a step are. kAny: the page and the slot of key `lane`, page -1 where there is no such key or
-        // its page is not in the pool. Otherwise for each block of 16 the page as the table has it and the slot, -1 where
-        // there is no key.
+        // ---- kAny: the page and the slot of key `lane` of a step, page -1 where there is no such key or its page is not
+        // in the pool
         struct Where {
-            int page[kWhole ? 2 : 1], slot[kWhole ? 2 : 1];
+            int page, slot;
         };
         auto look_up = [&](int key_at) {
-            Where w;
-#pragma unroll
-            for (int b = 0; b < (kWhole ? 2 : 1); ++b) {
-                const int key = kWhole ? key_at + 16 * b : key_at + lane;
-                w.page[b] = w.slot[b] = -1;
-                if (kWhole ? key < end : key_at < end && key < sees) {
-                    int index;
-                    if (kWhole) index = (int)(__umulhi((uint32_t)key >> 3, args.page_magic) >> args.page_shift);
-                    else index = key / page_size;
-                    w.slot[b] = key - index * page_size;
-                    w.page[b] = __ldg(table + index);
-                    if (!kWhole && (uint32_t)w.page[b] >= (uint64_t)a.pages) {
-                        atomicOr(&g_fault_flags, kFaultBadIndex);
-                        w.page[b] = -1;
-                    }
+            Where w = {-1, 0};
+            const int key = key_at + lane;
+            if (!kWhole && key_at < end && key < sees) {
+                const int index = key / page_size;
+                w.slot = key - index * page_size;
+                w.page = __ldg(table + index);
+                if ((uint32_t)w.page >= (uint64_t)a.pages) {
+                    atomicOr(&g_fault_flags, kFaultBadIndex);
+                    w.page = -1;
                 }
             }
             return w;
         };
-        // ---- copies of a step. Blocks whose page is not in the pool, and those without a key, come out as zeros.
-        auto copy_step = [&](const Where &w, uint32_t to_stage) {
-            const uint32_t to = smem_addr(ring) + to_stage * C::kStageBytes;
-            int64_t at[2];
-            int n[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const bool good = (uint32_t)w.page[b] < (uint64_t)a.pages;
-                if (!good && w.slot[b] >= 0) atomicOr(&g_fault_flags, kFaultBadIndex);
-                at[b] = good ? w.page[b] * args.k.code_page + w.slot[b] * code_slot : 0;
-                n[b] = good ? 16 : 0;
-#pragma unroll
-                for (int i = 0; i < kR; ++i) {
-                    const int in = i * 32 + lane, key = in / (2 * kR), c = in % (2 * kR);  // 16 bytes of a key's codes
-                    const int64_t off = at[b] + (kPool == kRuns ? in * 16 : key * code_slot + c * 16);
-                    const uint32_t dst = to + C::template piece<kPool>(16 * b + key, c);
-                    copy_async<16>(dst, k_codes + off, n[b]);
-                    copy_async<16>(dst + C::kCodes, v_codes + off, n[b]);
-                }
+        // ---- Otherwise the place of a block of 16 in the pool, in 16 bytes of codes or 2 of scales; kNone where there
+        // is no key, or its page is not in the pool. A warp looks up those of 16 steps at once, two lanes a step, and as
+        // many steps ahead: on its way through the steps a copy's address is then one multiplication.
+        constexpr uint32_t kNone = 0xFFFFFFFFu;
+        auto find = [&](int batch) {
+            const int key = first * kUnit + warp * kStep + (batch * 16 + lane / 2) * kUnit + lane % 2 * 16;
+            if (key >= end) return kNone;
+            const int index = (int)(__umulhi((uint32_t)key >> 3, args.page_magic) >> args.page_shift);
+            const int page = __ldg(table + index), slot = key - index * page_size;
+            if ((uint32_t)page >= (uint64_t)a.pages) {
+                atomicOr(&g_fault_flags, kFaultBadIndex);
+                return kNone;
             }
-            if constexpr (kPool == kRuns) {  // keys' scales of both blocks, then values': 16 bytes a lane
+            return (uint32_t)page * args.page_units + (uint32_t)slot * args.slot_units;
+        };
+        // What a lane copies: 16 bytes of codes kR times a block (kBlocks: of keys 16 / kR apart), of keys and values
+        // each; scales by rows of a key (kBlocks) or 16 bytes (kRuns: keys' of both blocks, then values').
+        constexpr int kScaleBytes = kPool == kRuns ? 16 : kR == 3 ? 4 : C::kScaleRow;
+        constexpr int kPtrs = kPool == kRuns ? 1 : kR;
+        const uint8_t *k_from[kPtrs], *v_from[kPtrs];
+        uint32_t code_at[kR];  // in a block of the stage's codes
 #pragma unroll
-                for (int i = 0; i < (kR + 1) / 2; ++i) {
-                    const int in = i * 32 + lane, part = in / (4 * kR);
-                    const int64_t off = ((part & 1 ? at[1] : at[0]) >> 3) + in % (4 * kR) * 16;
-                    if (kR % 2 == 0 || in < 16 * kR)
-                        copy_async<16>(to + 2 * C::kCodes + in * 16, (part < 2 ? k_scales : v_scales) + off, part & 1 ? n[1] : n[0]);
-                }
-            } else {  // a key's row
-                constexpr int kBytes = kR == 3 ? 4 : C::kScaleRow;
-                const int64_t off = ((lane < 16 ? at[0] : at[1]) + lane % 16 * code_slot) >> 3;
-                const int of = (lane < 16 ? n[0] : n[1]) ? kBytes : 0;
+        for (int i = 0; i < kR; ++i) {
+            const int in = i * 32 + lane, key = in / (2 * kR), c = in % (2 * kR);
+            code_at[i] = C::template piece<kPool>(key, c);
+            if (i < kPtrs) {
+                const int64_t off = kPool == kRuns ? in * 16 : key * args.k.code_slot + c * 16;
+                k_from[i] = k_codes + off;
+                v_from[i] = v_codes + off;
+            }
+        }
+        const uint8_t *ks_from = k_scales + lane % 16 * args.k.scale_slot, *vs_from = v_scales + lane % 16 * args.k.scale_slot;
+        auto copy_step = [&](uint32_t places, int step, uint32_t to_stage) {
+            const uint32_t to = smem_addr(ring) + to_stage * C::kStageBytes;
+            uint32_t at[2] = {__shfl_sync(0xFFFFFFFFu, places, step % 16 * 2), __shfl_sync(0xFFFFFFFFu, places, step % 16 * 2 + 1)};
+            auto copy = [&](const int (&n)[2]) {
 #pragma unroll
-                for (int i = 0; i < C::kScaleRow / kBytes; ++i) {
-                    const uint32_t dst = to + 2 * C::kCodes + lane * C::kScaleRow + i * kBytes;
-                    copy_async<kBytes>(dst, k_scales + off + i * kBytes, of);
-                    copy_async<kBytes>(dst + C::kScales, v_scales + off + i * kBytes, of);
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < kR; ++i) {
+                        const uint32_t dst = to + b * 16 * C::kRow + code_at[i];
+                        const int j = kPool == kRuns ? 0 : i, more = kPool == kRuns ? i * 512 : 0;
+                        copy_async<16>(dst, k_from[j] + at[b] * 16ull + more, n[b]);
+                        copy_async<16>(dst + C::kCodes, v_from[j] + at[b] * 16ull + more, n[b]);
+                    }
+                const uint32_t units = to + 2 * C::kCodes;
+                if constexpr (kPool == kRuns) {
+#pragma unroll
+                    for (int i = 0; i < (kR + 1) / 2; ++i) {
+                        const int in = i * 32 + lane, part = in / (4 * kR);
+                        if (kR % 2 == 0 || in < 16 * kR)
+                            copy_async<16>(units + in * 16, (part < 2 ? k_scales : v_scales) + (part & 1 ? at[1] : at[0]) * 2ull + in % (4 * kR) * 16,
+                                           part & 1 ? n[1] : n[0]);
+                    }
+                } else {
+                    const int of = (lane < 16 ? n[0] : n[1]) ? kScaleBytes : 0;
+                    const uint64_t off = (lane < 16 ? at[0] : at[1]) * 2ull;
+#pragma unroll
+                    for (int i = 0; i < C::kScaleRow / kScaleBytes; ++i) {
+                        const uint32_t dst = units + lane * C::kScaleRow + i * kScaleBytes;
+                        copy_async<kScaleBytes>(dst, ks_from + off + i * kScaleBytes, of);
+                        copy_async<kScaleBytes>(dst + C::kScales, vs_from + off + i * kScaleBytes, of);
+                    }
                 }
+            };
+            if (at[0] != kNone && at[1] != kNone) {
+                copy({16, 16});
+            } else {  // blocks without a place come out as zeros
+                const int n[2] = {at[0] != kNone ? 16 : 0, at[1] != kNone ? 16 : 0};
+                if (!n[0]) at[0] = 0;
+                if (!n[1]) at[1] = 0;
+                copy(n);
             }
         };
         auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
@@ -303,7 +329,7 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
 #pragma unroll
             for (int i = 0; i < (kWhole ? 0 : 4); ++i) {
                 const int at = 8 * i + place(g);
-                const int64_t p = __shfl_sync(0xFFFFFFFFu, w.page[0], at), r = __shfl_sync(0xFFFFFFFFu, w.slot[0], at);
+                const int64_t p = __shfl_sync(0xFFFFFFFFu, w.page, at), r = __shfl_sync(0xFFFFFFFFu, w.slot, at);
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) kc[i][j] = 0;
                 ks[i] = 0;
@@ -317,7 +343,7 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
 #pragma unroll
             for (int i = 0; i < (kWhole ? 0 : 8); ++i) {
                 const int at = 8 * (i / 2) + t + 4 * (i % 2);
-                const int64_t p = __shfl_sync(0xFFFFFFFFu, w.page[0], at), r = __shfl_sync(0xFFFFFFFFu, w.slot[0], at);
+                const int64_t p = __shfl_sync(0xFFFFFFFFu, w.page, at), r = __shfl_sync(0xFFFFFFFFu, w.slot, at);
 #pragma unroll
                 for (int j = 0; j < kR; ++j) vc[i][j] = 0;
                 vs[i] = 0;
@@ -330,17 +356,26 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
         };
 
         int key0 = first * kUnit + warp * kStep;
-        Where next = look_up(key0);
+        Where next = {-1, 0};
+        uint32_t places = kNone, more_places = kNone;
+        int copied = 0;  // steps
+        auto copy_next = [&](uint32_t to_stage) {
+            if (copied && copied % 16 == 0) {
+                places = more_places;
+                more_places = find(copied / 16 + 1);
+            }
+            copy_step(places, copied++, to_stage);
+        };
         if constexpr (kWhole) {
+            places = find(0);
+            more_places = find(1);
 #pragma unroll
             for (int i = 0; i < C::kStages - 1; ++i) {
-                const int at = key0 + i * kUnit;
-                const Where now = next;
-                next = look_up(at + kUnit);  // pages are asked for a step before their keys
-                copy_step(now, stage + i < C::kStages ? stage + i : stage + i - C::kStages);
+                copy_next(stage + i < C::kStages ? stage + i : stage + i - C::kStages);
                 commit();
             }
         } else {
+            next = look_up(key0);
             load_keys(next);
             load_values(next);
         }
@@ -409,10 +444,7 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
         for (; key0 < end; key0 += kUnit) {
             const uint8_t *tile = ring + stage * C::kStageBytes;
             if constexpr (kWhole) {
-                const int ahead = key0 + (C::kStages - 1) * kUnit;
-                const Where now = next;
-                next = look_up(ahead + kUnit);
-                if (ahead < end) copy_step(now, stage ? stage - 1 : C::kStages - 1);
+                if (key0 + (C::kStages - 1) * kUnit < end) copy_next(stage ? stage - 1 : C::kStages - 1);
                 commit();
                 asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
                 __syncwarp();
@@ -741,6 +773,8 @@ int pool_kind(const ks_attention_4bit_args_t &args, uintptr_t code_align, uintpt
     if (!same(a.pages, k.code_page_stride, v.code_page_stride, k.scale_page_stride, v.scale_page_stride) ||
         !same(a.page_size, k.code_slot_stride, v.code_slot_stride, k.scale_slot_stride, v.scale_slot_stride))
         return kAny;
+    // a place in the pool is 32 bits of 16-byte units
+    if ((((__int128)(a.pages - 1) * k.code_page_stride + (a.page_size - 1) * k.code_slot_stride) >> 4) >= 0xFFFFFFFFll) return kAny;
     if (k.code_slot_stride != 32 * r) return kBlocks;
     uintptr_t runs = 0;  // a block of scales is copied at once too
     for (const ks_pages_4bit_t *p : {&k, &v})
@@ -753,6 +787,7 @@ ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, int pool, Attn4P
     s.a = a.attention;
     s.scale_log2 = (float)((double)a.attention.scale * 1.4426950408889634 * (double)a.k_pages.factor);
     s.out_scale = a.v_pages.factor;
+    s.lanes = 1;
     p->args.k = pool4(a.k_pages);
     p->args.v = pool4(a.v_pages);
     const int dim = (int)s.a.head_dim, r = (dim + 63) / 64;
@@ -774,12 +809,20 @@ ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, int pool, Attn4P
     const uint32_t blocks = (uint32_t)(s.a.page_size / 16);
     p->args.page_shift = 0;
     while (blocks >> (p->args.page_shift + 1)) ++p->args.page_shift;
+    p->args.page_units = (uint32_t)(a.k_pages.code_page_stride / 16);
+    p->args.slot_units = (uint32_t)(a.k_pages.code_slot_stride / 16);
     p->args.page_magic = blocks ? (uint32_t)((1ull << (31 + p->args.page_shift)) / blocks) + 1 : 0;
     attn_shape(&s, 8 * tiles, kUnit, kTileCost);
     s.rows = kSlotRows;
     const int per_sm = resident(p->kernel, p->smem);
     if (per_sm <= 0) return fail(KS_ERR_CUDA, "the attention kernel cannot be resident");
     p->ctas = attn_ctas(s, (int64_t)sms * per_sm);
+    // Heads with CTAs of their own, unless that leaves more than a tenth of the CTAs without work.
+    const int64_t heads = s.a.kv_heads * s.head_splits, used = p->ctas / heads * heads;
+    if (heads > 1 && used * 10 >= (int64_t)p->ctas * 9) {
+        p->ctas = (int)used;
+        s.lanes = (int)heads;
+    }
     return KS_SUCCESS;
 }
 

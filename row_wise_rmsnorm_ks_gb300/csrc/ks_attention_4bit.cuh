@@ -11,6 +11,7 @@ struct Attn4Args {
     Pool4 k, v;
     uint32_t page_magic;  // the quotient of a key and page_size, where pages are whole blocks of 16 keys
     int32_t page_shift;
+    uint32_t page_units, slot_units;  // strides of the codes' pages and slots, in 16 bytes
 };
 
 // The tensor-core kernel (ks_attention_4bit_tc.cu): whether it takes a call, and its launch.
