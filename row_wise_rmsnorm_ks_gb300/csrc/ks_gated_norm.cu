@@ -10,7 +10,7 @@
 
 #include <cmath>
 
-#include "ks_kernels.cuh"
+#include "ks_decode.cuh"
 
 namespace ks {
 namespace {
@@ -24,15 +24,7 @@ struct GatedArgs {
 template <typename T>
 __device__ __forceinline__ const T *gate_row(const ks_gated_norm_args_t &a, int64_t row) {
     if (!a.gate) return nullptr;
-    return (const T *)a.gate + (a.rows_per_gate == a.rows ? 0 : row / a.rows_per_gate) * a.gate_row_stride;
-}
-
-// s of some places, in place of x: `scale` is the first norm's (1 without one).
-template <int N>
-__device__ __forceinline__ void gated_sum(float (&x)[N], const float (&r)[N], float scale, const float (&post)[N], const float (&gate)[N],
-                                          float residual_scale, float block_scale) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = fmaf(r[i], residual_scale, x[i] * scale * post[i] * gate[i] * block_scale);
+    return (const T *)a.gate + (a.rows_per_gate == a.rows ? 0 : quotient(row, a.rows_per_gate)) * a.gate_row_stride;
 }
 
 template <int N>
@@ -41,71 +33,111 @@ __device__ __forceinline__ void fill(float (&f)[N], float v) {
     for (int i = 0; i < N; ++i) f[i] = v;
 }
 
-// One CTA per row, V vectors a thread.
-template <typename T, int V>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512) gated_rows_kernel(const __grid_constant__ GatedArgs args) {
+template <bool kPair, int P>
+__device__ __forceinline__ void times(float2 (&s)[P], float v) {
+    const float2 w = make_float2(v, v);
+#pragma unroll
+    for (int i = 0; i < P; ++i) s[i] = pair_mul<kPair>(s[i], w);
+}
+template <bool kPair, int P>
+__device__ __forceinline__ void times(float2 (&s)[P], const float2 (&w)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) s[i] = pair_mul<kPair>(s[i], w[i]);
+}
+
+// A row per team, V vectors a thread: a warp (kTeam 32), several of them a CTA, or the CTA (0). The residual's vectors
+// stay as they came until s takes their place; weights and gate come from L1 when they are wanted.
+template <typename T, int V, int kTeam>
+__global__ void __launch_bounds__(kTeam ? 256 : 512, V <= 2 ? 2048 / (kTeam ? 256 : 512) / 2 : 1)
+gated_rows_kernel(const __grid_constant__ GatedArgs args) {
     using E = Elem<T>;
-    constexpr int N = E::kPerVec;
+    constexpr int P = E::kPerVec / 2;
+    constexpr bool kPair = E::kPairMath;
     __shared__ float red[2][32];
     const ks_gated_norm_args_t &a = args.a;
-    const int g = blockDim.x, t = threadIdx.x;
-    const int64_t hv = args.hv;
+    const int g = kTeam ? kTeam : blockDim.x, t = kTeam ? threadIdx.x % 32 : threadIdx.x;
+    const int teams = kTeam ? blockDim.x / 32 : 1, team = kTeam ? threadIdx.x / 32 : 0;
+    const int hv = (int)args.hv;
     const float hidden = (float)a.hidden;
+    int slot = 0;  // of `red`: every sum takes the other one
     grid_dependency_wait();
     allow_dependents_launch();
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    for (int64_t row = (int64_t)blockIdx.x * teams + team; row < a.rows; row += (int64_t)gridDim.x * teams) {
         uint4 *xr = (uint4 *)a.x + row * hv, *rr = (uint4 *)a.residual + row * hv;
-        uint4 xv[V], rv[V];
-        load_row<V>(xr, t, g, hv, xv);
-        load_row<V>(rr, t, g, hv, rv);
-        const T *gate = gate_row<T>(a, row);
-        float scale = 1.0f;
+        uint4 rv[V];
+        float2 s[V][P];
+        {
+            uint4 xv[V];
+            load_row<V>(xr, t, g, hv, xv);
+            load_row<V>(rr, t, g, hv, rv);
+#pragma unroll
+            for (int k = 0; k < V; ++k) E::unpack2(xv[k], s[k]);
+        }
+        float factor = a.block_scale;
         if (a.post_weight) {
-            SumSq acc;
+            PairSumSq<kPair> acc;
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc.add(s[k]);
+            const float scale = row_scale(team_sum<kTeam>(acc.total(), red[slot ^= 1]), hidden, a.eps);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                float f[N];
-                E::unpack(xv[k], f);
-                acc.add(f);
+                const int c = t + k * g;
+                if (c >= hv) continue;
+                float2 w[P];
+                E::unpack2(__ldg((const uint4 *)a.post_weight + c), w);
+                times<kPair>(s[k], scale);
+                times<kPair>(s[k], w);
             }
-            scale = row_scale(team_sum<0>(acc.total(), red[0]), hidden, a.eps);
         }
-        float s[V][N];
-        SumSq acc;
+        if (a.gate) {
+            const T *gate = gate_row<T>(a, row);
+            if (a.gate_column_stride) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const int c = t + k * g;
+                    if (c >= hv) continue;
+                    float2 w[P];
+                    E::unpack2(__ldg((const uint4 *)gate + c), w);
+                    times<kPair>(s[k], w);
+                }
+            } else {
+                factor *= E::load1(gate, 0);
+            }
+        }
+        PairSumSq<kPair> acc;
+        const float2 f2 = make_float2(factor, factor), r2 = make_float2(a.residual_scale, a.residual_scale);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const int64_t c = t + (int64_t)k * g;
-            float r[N], post[N], gt[N];
-            E::unpack(xv[k], s[k]);
-            E::unpack(rv[k], r);
-            fill(post, 1.0f);
-            fill(gt, 1.0f);
+            const int c = t + k * g;
+            float2 r[P];
+            E::unpack2(rv[k], r);
+#pragma unroll
+            for (int i = 0; i < P; ++i) s[k][i] = pair_fma<kPair>(r[i], r2, pair_mul<kPair>(s[k][i], f2));
             if (c < hv) {
-                if (a.post_weight) E::unpack(__ldg((const uint4 *)a.post_weight + c), post);
-                if (gate) {
-                    if (a.gate_column_stride) E::unpack(__ldg((const uint4 *)gate + c), gt);
-                    else fill(gt, E::load1(gate, 0));
-                }
-            }
-            gated_sum(s[k], r, scale, post, gt, a.residual_scale, a.block_scale);
-            if (c < hv) {
-                __stcs(rr + c, E::pack(s[k]));
+                __stcs(rr + c, E::pack2(s[k]));
                 acc.add(s[k]);
             }
         }
-        const float out_scale = row_scale(team_sum<0>(acc.total(), red[1]), hidden, a.eps);
+        const float out_scale = row_scale(team_sum<kTeam>(acc.total(), red[slot ^= 1]), hidden, a.eps);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const int64_t c = t + (int64_t)k * g;
-            if (c < hv) {
-                float w[N];
-                E::unpack(__ldg((const uint4 *)a.weight + c), w);
-#pragma unroll
-                for (int i = 0; i < N; ++i) s[k][i] = s[k][i] * out_scale * w[i];
-                __stcs(xr + c, E::pack(s[k]));
-            }
+            const int c = t + k * g;
+            if (c >= hv) continue;
+            float2 w[P];
+            E::unpack2(__ldg((const uint4 *)a.weight + c), w);
+            times<kPair>(s[k], out_scale);
+            times<kPair>(s[k], w);
+            __stcs(xr + c, E::pack2(s[k]));
         }
     }
+}
+
+// s of some places, in place of x: `scale` is the first norm's (1 without one).
+template <int N>
+__device__ __forceinline__ void gated_sum(float (&x)[N], const float (&r)[N], float scale, const float (&post)[N], const float (&gate)[N],
+                                          float residual_scale, float block_scale) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = fmaf(r[i], residual_scale, x[i] * scale * post[i] * gate[i] * block_scale);
 }
 
 // Any width and alignment: the row read up to three times, vector by vector or value by value.
@@ -117,6 +149,7 @@ __global__ void __launch_bounds__(512) gated_wide_kernel(const __grid_constant__
     const ks_gated_norm_args_t &a = args.a;
     const int64_t n = kVec ? args.hv : a.hidden;
     const float hidden = (float)a.hidden;
+    int slot = 0;  // of `red`: every sum takes the other one
     grid_dependency_wait();
     allow_dependents_launch();
     auto load = [](const T *p, int64_t c, float (&f)[N]) {
@@ -138,7 +171,7 @@ __global__ void __launch_bounds__(512) gated_wide_kernel(const __grid_constant__
                 load(x, c, f);
                 acc.add(f);
             }
-            scale = row_scale(team_sum<0>(acc.total(), red[0]), hidden, a.eps);
+            scale = row_scale(team_sum<0>(acc.total(), red[slot ^= 1]), hidden, a.eps);
         }
         auto sum = [&](int64_t c, float (&s)[N]) {
             float rv[N], post[N], gt[N];
@@ -159,7 +192,7 @@ __global__ void __launch_bounds__(512) gated_wide_kernel(const __grid_constant__
             sum(c, s);
             acc.add(s);
         }
-        const float out_scale = row_scale(team_sum<0>(acc.total(), red[1]), hidden, a.eps);
+        const float out_scale = row_scale(team_sum<0>(acc.total(), red[slot ^= 1]), hidden, a.eps);
         for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
             float s[N], w[N];
             sum(c, s);
@@ -172,14 +205,27 @@ __global__ void __launch_bounds__(512) gated_wide_kernel(const __grid_constant__
     }
 }
 
+// The kernel for rows of hv vectors (0: no vector fits): threads of a CTA, and rows that one does at once.
 template <typename T>
-const void *pick(int v, bool vec) {
-    switch (v) {
-    case 1: return (const void *)gated_rows_kernel<T, 1>;
-    case 2: return (const void *)gated_rows_kernel<T, 2>;
-    case 4: return (const void *)gated_rows_kernel<T, 4>;
-    default: return vec ? (const void *)gated_wide_kernel<T, true> : (const void *)gated_wide_kernel<T, false>;
+const void *pick(int64_t hv, bool few, int *block, int *rows) {
+    *rows = 1;
+    if (hv == 0 || hv > 4096) {
+        *block = 512;
+        return hv ? (const void *)gated_wide_kernel<T, true> : (const void *)gated_wide_kernel<T, false>;
     }
+    if (hv <= 128 && !few) {  // a warp a row
+        *block = 256;
+        *rows = 8;
+        return hv <= 32   ? (const void *)gated_rows_kernel<T, 1, 32>
+               : hv <= 64 ? (const void *)gated_rows_kernel<T, 2, 32>
+                          : (const void *)gated_rows_kernel<T, 4, 32>;
+    }
+    const int v = hv <= (few ? 512 : 256) ? 1 : hv <= 1024 ? 2 : hv <= 2048 ? 4 : 8;
+    *block = (int)((hv + v - 1) / v + 31) / 32 * 32;
+    return v == 1   ? (const void *)gated_rows_kernel<T, 1, 0>
+           : v == 2 ? (const void *)gated_rows_kernel<T, 2, 0>
+           : v == 4 ? (const void *)gated_rows_kernel<T, 4, 0>
+                    : (const void *)gated_rows_kernel<T, 8, 0>;
 }
 
 }  // namespace
@@ -228,17 +274,13 @@ extern "C" ks_status_t ks_gated_add_rms_norm(const ks_gated_norm_args_t *args, k
     k_args.a = a;
     const bool vec = (align & 15u) == 0 && w % 16 == 0;
     k_args.hv = vec ? w / 16 : 0;
-    int v = 0, block = 512;
-    if (vec && k_args.hv <= 4096) {
-        v = k_args.hv <= 256 ? 1 : k_args.hv <= 1024 ? 2 : 4;
-        if (a.rows <= sms && k_args.hv <= 512) v = 1;
-        block = (int)((k_args.hv + v - 1) / v + 31) / 32 * 32;
-    }
-    const void *f = a.dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(v, vec)
-                    : a.dtype == KS_DTYPE_F16 ? pick<__half>(v, vec)
-                                              : pick<float>(v, vec);
-    const int64_t most = (int64_t)sms * (2048 / block > 32 ? 32 : 2048 / block);
-    const int64_t grid = a.rows < most ? a.rows : most;
+    int block = 0, at_once = 1;
+    const bool few = a.rows <= sms;
+    const void *f = a.dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(k_args.hv, few, &block, &at_once)
+                    : a.dtype == KS_DTYPE_F16 ? pick<__half>(k_args.hv, few, &block, &at_once)
+                                              : pick<float>(k_args.hv, few, &block, &at_once);
+    const int64_t most = (int64_t)sms * (2048 / block > 32 ? 32 : 2048 / block), want = (a.rows + at_once - 1) / at_once;
+    const int64_t grid = want < most ? want : most;
     void *kp[] = {&k_args};
     const cudaError_t ce = launch_kernel(f, dim3((unsigned)grid), dim3((unsigned)block), 0, kp, static_cast<cudaStream_t>(stream),
                                          launch_pdl_enabled());

@@ -1,11 +1,11 @@
 // Rotary positions with the keys and values landing in a cache held in 4 bits (ks_rotary_to_pages_4bit), and the rows
 // of such a cache read back (ks_pages_4bit_to_rows).
 //
-// Writing. CTAs (token, part): the first parts turn the token's queries as ks_rotary does, the last takes its keys and
-// values, a thread per group of 16: it loads its group and, for a key, the group of its pairs' partners, turns in
+// Writing. CTAs (token, part): the first parts turn the token's queries as ks_rotary does, the others take its keys and
+// values (with many tokens, one CTA does both one after the other), a thread per group of 16: it loads its group and, for a key, the group of its pairs' partners, turns in
 // FP32, and finds the group's scale and codes. These are those of the real numbers: the angles have 64 bits, the
 // turn's FP32 error is bounded by 2^-21 (|x| + |y|) |scale| for a pair (x, y), and where the scale or a code could
-// differ within the bound (about one group in ten thousand; every tie of an unturned value) it is decided
+// differ within the bound (about one group in five thousand; every tie of an unturned value) it is decided
 // exactly, in double for turned values, by the sign of a fused multiply-add for the others.
 //
 // Bound by memory: the queries are read and written once, keys and values read once, 9/16 byte written for each.
@@ -29,191 +29,240 @@ struct Group4 {
     uint32_t scale, lo, hi;  // the scale's code, the codes of values 0 .. 7 and 8 .. 15
 };
 
-// The group of turned values in double, for those that FP32 does not decide.
+// Value d of a row, turned, in double: for what FP32 does not decide. (FP64 is slow here, a value takes about two
+// microseconds; about one of 10^5 values asks for it.)
 template <typename T, bool kHalf>
-__device__ __noinline__ Group4 group4_exact(const ks_rotary_args_t &a, const T *row, int group, uint64_t position, float g) {
+__device__ __noinline__ double turned_exact(const ks_rotary_args_t &a, const T *row, int d, uint64_t position) {
     const int rot = (int)a.rotary_dim, half = rot / 2;
-    double y[16], top = 0.0;
-    for (int i = 0; i < 16; ++i) {
-        const int d = group * 16 + i;
-        double x = Elem<T>::load1(row, d);
-        if (d < rot) {
-            const int j = kHalf ? (d < half ? d : d - half) : d / 2;
-            const bool second = kHalf ? d >= half : d & 1;
-            const double z = Elem<T>::load1(row, kHalf ? (second ? d - half : d + half) : d ^ 1);
-            double s, c;
-            sincospi((double)(int64_t)(position * (uint64_t)a.steps[j]) * 1.0842021724855044e-19, &s, &c);  // 2^-63
-            x = (second ? x * c + z * s : x * c - z * s) * (double)a.scale;
-        }
-        y[i] = x;
-        top = fmax(top, fabs(x));
-    }
-    Group4 out = {0, 0, 0};
-    const float v = (float)(top / (6.0 * (double)g));
-    out.scale = fp4_scale(v * (1.0f - kRoundError), v * (1.0f + kRoundError), top, g);
-    const float u = __fmul_rn(e4m3_to_float(out.scale), g);
-    if (u > 0.0f)
-        for (int i = 0; i < 16; ++i) {
-            const double size = fabs(y[i]);
-            const float t = fminf((float)(size / (double)u), 8.0f);
-            const uint32_t c = fp4_codes(t * (1.0f - kRoundError), t * (1.0f + kRoundError));
-            const uint32_t code = fp4_decide(c & 7, c >> 4 & 7, size, u) | (y[i] < 0.0 ? 8u : 0u);
-            if (i < 8) out.lo |= code << (4 * i);
-            else out.hi |= code << (4 * (i - 8));
-        }
-    return out;
+    const double x = Elem<T>::load1(row, d);
+    if (d >= rot) return x;
+    const int j = kHalf ? (d < half ? d : d - half) : d / 2;
+    const bool second = kHalf ? d >= half : d & 1;
+    const double z = Elem<T>::load1(row, kHalf ? (second ? d - half : d + half) : d ^ 1);
+    double s, c;
+    sincospi((double)(int64_t)(position * (uint64_t)a.steps[j]) * 1.0842021724855044e-19, &s, &c);  // 2^-63
+    return (second ? x * c + z * s : x * c - z * s) * (double)a.scale;
 }
 
-// A group's values in FP32, off by at most error[i] (all 0: exact).
+// NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float c;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+    return c;
+}
+
+// Codes of 8 signed quotients, value i in bits 4 i on.
+__device__ __forceinline__ uint32_t fp4_word(const float2 *t) {
+    return fp4_codes(t[0].x, t[0].y) | fp4_codes(t[1].x, t[1].y) << 8 | fp4_codes(t[2].x, t[2].y) << 16 |
+           fp4_codes(t[3].x, t[3].y) << 24;
+}
+
+// A group's values in FP32, each off by at most `off` (kExact: not at all). A quotient's code is taken at both ends
+// of what it may be; the quotient's own rounding is below 2^-19 of the unit, as quotients are below 8.
 template <typename T, bool kHalf, bool kExact>
 __device__ __forceinline__ Group4 group4(const ks_rotary_args_t &a, const T *row, int group, uint64_t position, float g,
-                                         const float (&y)[16], const float (&error)[16]) {
-    float top = 0.0f, off = 0.0f;
-    bool nan = false;
+                                         float2 (&y)[8], float off) {
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        top = fmaxf(top, fabsf(y[i]));
-        nan |= y[i] != y[i];
-        if (!kExact) off = fmaxf(off, error[i]);
-    }
-    if (nan) return {0x7Fu, 0, 0};
+    for (int i = 0; i < 8; ++i) top = max_nan(top, max_nan(fabsf(y[i].x), fabsf(y[i].y)));
+    if (top != top) return {0x7Fu, 0, 0};
     const float per = __frcp_rn(6.0f * g);
     const float low = (top - off) * per * (1.0f - 2 * kRoundError), high = (top + off) * per * (1.0f + 2 * kRoundError);
-    if (!kExact) {
+    Group4 out = {0, 0, 0};
+    if constexpr (kExact) {
+        out.scale = fp4_scale(low, high, top, g);
+    } else {
         const uint32_t c = e4m3_codes(fminf(fmaxf(low, 0.0f), 512.0f), fminf(high, 512.0f));
-        if ((c & 0xFF) != c >> 8) return group4_exact<T, kHalf>(a, row, group, position, g);
+        out.scale = c & 0xFF;
+        if (out.scale != c >> 8) {
+            double most = 0.0;
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) most = fmax(most, fabs(turned_exact<T, kHalf>(a, row, group * 16 + i, position)));
+            const float v = (float)(most / (6.0 * (double)g));
+            out.scale = fp4_scale(v * (1.0f - kRoundError), v * (1.0f + kRoundError), most, g);
+        }
     }
-    Group4 out = {fp4_scale(low, high, top, g), 0, 0};
     const float u = __fmul_rn(e4m3_to_float(out.scale), g);
     if (!(u > 0.0f)) return out;
     const float inv = __frcp_rn(u);
-    uint32_t lo[2] = {0, 0}, hi[2] = {0, 0}, sign[2] = {0, 0};
+    const float2 inv2 = make_float2(inv, inv);
+    float2 t[8];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        float t[2], w[2];
+    for (int i = 0; i < 8; ++i) t[i] = __fmul2_rn(y[i], inv2);
+    if (out.scale == 126) {  // the largest: quotients may be of any size
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            t[k] = fminf(fabsf(y[i + k]) * inv, 8.0f);
-            w[k] = t[k] * kRoundError;
-            if (!kExact) w[k] = fmaf(error[i + k], inv, w[k]);
-            if (y[i + k] < 0.0f) sign[i / 8] |= 8u << (4 * (i % 8 + k));
+        for (int i = 0; i < 8; ++i) {
+            t[i].x = fminf(fmaxf(t[i].x, -8.0f), 8.0f);
+            t[i].y = fminf(fmaxf(t[i].y, -8.0f), 8.0f);
         }
-        lo[i / 8] |= fp4_codes(fmaxf(t[0] - w[0], 0.0f), fmaxf(t[1] - w[1], 0.0f)) << (4 * (i % 8));
-        hi[i / 8] |= fp4_codes(t[0] + w[0], t[1] + w[1]) << (4 * (i % 8));
     }
-    if (lo[0] != hi[0] || lo[1] != hi[1]) {
-        if constexpr (!kExact) {
-            return group4_exact<T, kHalf>(a, row, group, position, g);
-        } else {
+    const float w = (kExact ? 0.0f : off * inv) + 1.9073486328125e-06f;  // 2^-19
+    const float2 more = make_float2(w, w), less = make_float2(-w, -w);
+    uint32_t lo[2], hi[2];
+    {
+        float2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fadd2_rn(t[i], more);
+        hi[0] = fp4_word(v), hi[1] = fp4_word(v + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fadd2_rn(t[i], less);
+        lo[0] = fp4_word(v), lo[1] = fp4_word(v + 4);
+    }
+    // Codes that differ in their sign alone are zeros, unless the window is wider than that: then all are in doubt.
+    const bool wide = !kExact && !(w < 0.125f);
+    if ((((lo[0] ^ hi[0]) | (lo[1] ^ hi[1])) & 0x77777777u) || wide) {
+        if constexpr (kExact) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int at = 4 * (i % 8);
-                const uint32_t l = lo[i / 8] >> at & 7, h = hi[i / 8] >> at & 7;
-                if (l != h) lo[i / 8] ^= (l ^ fp4_decide(l, h, fabsf(y[i]), u)) << at;
+                const uint32_t d = (lo[i / 8] ^ hi[i / 8]) >> at & 7;
+                if (d) {
+                    const float x = i % 2 ? y[i / 2].y : y[i / 2].x;
+                    const uint32_t one = lo[i / 8] >> at & 7, other = one ^ d, small = min(one, other);
+                    const uint32_t code = fp4_decide(small, small + 1, fabsf(x), u) | (x < 0.0f ? 8u : 0u);
+                    lo[i / 8] = (lo[i / 8] & ~(15u << at)) | code << at;
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+                const int at = 4 * (i % 8);
+                if (!wide && ((i < 8 ? lo[0] ^ hi[0] : lo[1] ^ hi[1]) >> at & 7) == 0) continue;
+                const double x = turned_exact<T, kHalf>(a, row, group * 16 + i, position), size = fabs(x);
+                // the window may be wider than two codes: of a group that its pairs all but cancel
+                const float q = fminf((float)(size / (double)u), 8.0f);
+                const uint32_t c = fp4_codes(q * (1.0f - kRoundError), q * (1.0f + kRoundError));
+                const uint32_t code = fp4_decide(c & 7, c >> 4 & 7, size, u) | (x < 0.0 ? 8u : 0u);
+                if (i < 8) lo[0] = (lo[0] & ~(15u << at)) | code << at;
+                else lo[1] = (lo[1] & ~(15u << at)) | code << at;
             }
         }
     }
-    out.lo = lo[0] | sign[0];
-    out.hi = lo[1] | sign[1];
+    out.lo = lo[0];
+    out.hi = lo[1];
     return out;
 }
 
 template <typename T, bool kVec>
-__device__ __forceinline__ void load16(const T *p, float (&x)[16]) {
+__device__ __forceinline__ void load16(const T *p, float2 (&x)[8]) {
     if constexpr (kVec) {
-        constexpr int V = Elem<T>::kPerVec;
-        uint4 v[16 / V];
+        constexpr int P = Elem<T>::kPerVec / 2;
+        uint4 v[8 / P];
 #pragma unroll
-        for (int i = 0; i < 16 / V; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
+        for (int i = 0; i < 8 / P; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
 #pragma unroll
-        for (int i = 0; i < 16 / V; ++i) {
-            float f[V];
-            Elem<T>::unpack(v[i], f);
+        for (int i = 0; i < 8 / P; ++i) {
+            float2 f[P];
+            Elem<T>::unpack2(v[i], f);
 #pragma unroll
-            for (int k = 0; k < V; ++k) x[i * V + k] = f[k];
+            for (int k = 0; k < P; ++k) x[i * P + k] = f[k];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = Elem<T>::load1(p, i);
+        for (int i = 0; i < 8; ++i) x[i] = make_float2(Elem<T>::load1(p, 2 * i), Elem<T>::load1(p, 2 * i + 1));
     }
 }
 
+// Cosines and sines for the groups, apart, 4 places free behind every 16: eight lanes with a group each read 16 bytes
+// of theirs without a conflict.
+constexpr int kTable = kRotMaxDim / 2 / 16 * 20;
+__device__ __forceinline__ int table_at(int j) { return j + (j >> 4) * 4; }
+__device__ __forceinline__ float2 pair_at(const float *table, int i) { return *reinterpret_cast<const float2 *>(table + i); }
+
+// One group of a token's keys or values, into its place.
 template <typename T, bool kHalf, bool kVec>
-__device__ __forceinline__ void pages4_groups(const Rotary4Args &args, int64_t token, int first, int step, float2 *cs) {
+__device__ __forceinline__ void pages4_item(const Rotary4Args &args, int64_t token, uint64_t position, int64_t page, int64_t place,
+                                            int item, const float *cosines, const float *sines) {
     const ks_rotary_args_t &a = args.r.a;
     const int groups = (int)a.head_dim / 16, rot = (int)a.rotary_dim, half = rot / 2;
+    const int row_index = item / groups, group = item - row_index * groups;
+    const bool value = row_index >= a.kv_heads;
+    const int64_t head = value ? row_index - a.kv_heads : row_index;
+    const T *row = value ? (const T *)a.v + token * a.v_token_stride + head * a.v_head_stride
+                         : (const T *)a.k + token * a.k_token_stride + head * a.k_head_stride;
+    const Pool4 &pool = value ? args.v : args.k;
+    float2 x[8];
+    load16<T, kVec>(row + group * 16, x);
+    Group4 out;
+    if (value || group * 16 >= rot) {
+        out = group4<T, kHalf, true>(a, row, group, position, pool.factor, x, 0.0f);
+    } else {
+        float2 y[8];
+        float size = 0.0f;  // the largest |x| + |y| of the group's pairs
+        if constexpr (kHalf && kVec) {
+            const bool second = group * 16 >= half;
+            float2 z[8];
+            load16<T, true>(row + (second ? group * 16 - half : group * 16 + half), z);
+            const int j = table_at(second ? group * 16 - half : group * 16);
+            const float2 sign = make_float2(second ? 1.0f : -1.0f, second ? 1.0f : -1.0f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                size = fmaxf(size, fmaxf(fabsf(x[i].x) + fabsf(z[i].x), fabsf(x[i].y) + fabsf(z[i].y)));
+                y[i] = __ffma2_rn(x[i], pair_at(cosines, j + 2 * i), __fmul2_rn(__fmul2_rn(z[i], pair_at(sines, j + 2 * i)), sign));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int d = group * 16 + i;
+                float &to = i % 2 ? y[i / 2].y : y[i / 2].x;
+                const float m = i % 2 ? x[i / 2].y : x[i / 2].x;
+                to = m;
+                if (d < rot) {
+                    const bool second = kHalf ? d >= half : i & 1;
+                    const int j = table_at(kHalf ? (second ? d - half : d) : d / 2);
+                    const float z = kHalf ? Elem<T>::load1(row, second ? d - half : d + half) : i % 2 ? x[i / 2].x : x[i / 2].y;
+                    to = fmaf(m, cosines[j], second ? z * sines[j] : -z * sines[j]);
+                    size = fmaxf(size, fabsf(m) + fabsf(z));
+                }
+            }
+        }
+        out = group4<T, kHalf, false>(a, row, group, position, pool.factor, y, size * (fabsf(a.scale) * kTurnError));
+    }
+    uint8_t *codes = pool.codes + page * pool.code_page + place * pool.code_slot + head * pool.code_head + group * 8;
+    *reinterpret_cast<uint2 *>(codes) = make_uint2(out.lo, out.hi);
+    pool.scales[page * pool.scale_page + place * pool.scale_slot + head * pool.scale_head + group] = (uint8_t)out.scale;
+}
+
+// A part of a token's groups; its cosines and sines are computed here, or (kMade) taken from `cs`.
+template <typename T, bool kHalf, bool kVec, bool kMade>
+__device__ __forceinline__ void pages4_groups(const Rotary4Args &args, int64_t token, int part, int parts, const float2 *cs,
+                                              float *cosines, float *sines) {
+    const ks_rotary_args_t &a = args.r.a;
     const RotToken t = rot_token<true>(a, token);
-    rot_table(a, t, cs);
+    if (t.slot < 0) return;  // the whole block
+    for (int j = threadIdx.x; j < (int)(a.rotary_dim / 2); j += blockDim.x) {
+        float2 c;
+        if constexpr (kMade) c = cs[j];
+        else c = turn_cos_sin(t.position * (uint64_t)a.steps[j], a.scale);
+        cosines[table_at(j)] = c.x;
+        sines[table_at(j)] = c.y;
+    }
     __syncthreads();
-    if (t.slot < 0) return;
     const int64_t page = quotient(t.slot, a.page_size), place = t.slot - page * a.page_size;
     if (page >= a.pages) {
         if (threadIdx.x == 0) atomicOr(&g_fault_flags, kFaultBadIndex);
         return;
     }
-    const int total = (int)(2 * a.kv_heads * groups);
-    for (int item = first + threadIdx.x; item < total; item += step) {
-        const int row_index = item / groups, group = item - row_index * groups;
-        const bool value = row_index >= a.kv_heads;
-        const int64_t head = value ? row_index - a.kv_heads : row_index;
-        const T *row = value ? (const T *)a.v + token * a.v_token_stride + head * a.v_head_stride
-                             : (const T *)a.k + token * a.k_token_stride + head * a.k_head_stride;
-        const Pool4 &pool = value ? args.v : args.k;
-        float x[16];
-        load16<T, kVec>(row + group * 16, x);
-        Group4 out;
-        const bool turned = !value && group * 16 < rot;
-        if (!turned) {
-            const float none[16] = {};
-            out = group4<T, kHalf, true>(a, row, group, t.position, pool.factor, x, none);
-        } else {
-            float z[16], y[16], error[16];
-            if (!kHalf) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = x[i ^ 1];
-            } else if (kVec) {
-                load16<T, true>(row + (group * 16 < half ? group * 16 + half : group * 16 - half), z);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int d = group * 16 + i;
-                    z[i] = d < rot ? Elem<T>::load1(row, d < half ? d + half : d - half) : 0.0f;
-                }
-            }
-            const float size = fabsf(a.scale) * kTurnError;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int d = group * 16 + i;
-                const bool second = kHalf ? d >= half : i & 1;
-                y[i] = x[i];
-                error[i] = 0.0f;
-                if ((kHalf && kVec) || d < rot) {
-                    const float2 turn = cs[kHalf ? (second ? d - half : d) : d / 2];
-                    y[i] = fmaf(x[i], turn.x, second ? z[i] * turn.y : -z[i] * turn.y);
-                    error[i] = (fabsf(x[i]) + fabsf(z[i])) * size;
-                }
-            }
-            out = group4<T, kHalf, false>(a, row, group, t.position, pool.factor, y, error);
-        }
-        uint8_t *codes = pool.codes + page * pool.code_page + place * pool.code_slot + head * pool.code_head + group * 8;
-        *reinterpret_cast<uint2 *>(codes) = make_uint2(out.lo, out.hi);
-        pool.scales[page * pool.scale_page + place * pool.scale_slot + head * pool.scale_head + group] = (uint8_t)out.scale;
-    }
+    const int total = (int)(2 * a.kv_heads * (a.head_dim / 16));
+    for (int item = part * blockDim.x + threadIdx.x; item < total; item += parts * blockDim.x)
+        pages4_item<T, kHalf, kVec>(args, token, t.position, page, place, item, cosines, sines);
 }
 
 template <typename T, bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kRotThreads) rotary_4bit_kernel(const __grid_constant__ Rotary4Args args) {
     __shared__ float2 cs[kRotMaxDim / 2];
+    __shared__ __align__(16) float cosines[kTable], sines[kTable];
     grid_dependency_wait();
     allow_dependents_launch();
     const int part = blockIdx.y;
+    const int64_t token = blockIdx.x;
     if (part < args.q_parts) {
         const int first = part * args.r.heads_per_y, last = min((int)args.r.a.q_heads, first + args.r.heads_per_y);
-        if constexpr (kVec) rot_heads_vec<T, kHalf, false>(args.r, blockIdx.x, first, last, cs);
-        else rot_heads_scalar<T, kHalf, false>(args.r, blockIdx.x, first, last, cs);
+        if constexpr (kVec) rot_heads_vec<T, kHalf, false>(args.r, token, first, last, cs);
+        else rot_heads_scalar<T, kHalf, false>(args.r, token, first, last, cs);
+        if (gridDim.y == args.q_parts) pages4_groups<T, kHalf, kVec, true>(args, token, 0, 1, cs, cosines, sines);
     } else {
-        const int y = part - args.q_parts, parts = gridDim.y - args.q_parts;
-        pages4_groups<T, kHalf, kVec>(args, blockIdx.x, y * blockDim.x, parts * blockDim.x, cs);
+        pages4_groups<T, kHalf, kVec, false>(args, token, part - args.q_parts, gridDim.y - args.q_parts, cs, cosines, sines);
     }
 }
 
@@ -233,55 +282,65 @@ struct Rows4Args {
 };
 
 constexpr int kRowsThreads = 256;
-constexpr int kRowsEach = 4;  // tokens a thread has in flight
+constexpr int kRowsEach = 4;  // tokens that a thread has in flight
 
-// A thread per group and four tokens: 9 bytes in, 16 values out. Bound by the rows that are written.
+// A thread per group and four tokens: 9 bytes in, 16 values out. Bound by the rows that are written: so where a token's
+// rows lie in the pools is found once per token, in shared memory, and a group's FP32 unit multiplies its values two at
+// a time.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kRowsThreads) pages4_rows_kernel(const __grid_constant__ Rows4Args args) {
+    constexpr int kMost = kRowsThreads * kRowsEach;
+    __shared__ int64_t at[4][kMost];  // k's codes and scales, v's; -1: nowhere
     grid_dependency_wait();
     allow_dependents_launch();
     const ks_pages_4bit_rows_args_t &a = args.a;
+    const int per_cta = args.tokens * kRowsEach;
+    const int64_t first = (int64_t)blockIdx.x * per_cta;
+    for (int i = threadIdx.x; i < per_cta; i += kRowsThreads) {
+        const int64_t slot = first + i < a.tokens ? a.slots[first + i] : -1;
+        at[0][i] = -1;
+        if (slot < 0) continue;
+        const int64_t page = quotient(slot, a.page_size), place = slot - page * a.page_size;
+        if (page >= a.pages) {
+            atomicOr(&g_fault_flags, kFaultBadIndex);
+            continue;
+        }
+        at[0][i] = page * args.k.code_page + place * args.k.code_slot;
+        at[1][i] = page * args.k.scale_page + place * args.k.scale_slot;
+        at[2][i] = page * args.v.code_page + place * args.v.code_slot;
+        at[3][i] = page * args.v.scale_page + place * args.v.scale_slot;
+    }
+    __syncthreads();
     const int groups = (int)a.head_dim / 16, total = (int)(2 * a.kv_heads * groups);
     const int lane = threadIdx.x % args.lanes, in_cta = threadIdx.x / args.lanes;
     if (in_cta >= args.tokens) return;
-    const int64_t first = (int64_t)blockIdx.x * args.tokens * kRowsEach + in_cta;
-    int64_t page[kRowsEach], place[kRowsEach];
-#pragma unroll
-    for (int u = 0; u < kRowsEach; ++u) {
-        const int64_t token = first + u * args.tokens;
-        const int64_t slot = token < a.tokens ? a.slots[token] : -1;
-        page[u] = -1;
-        place[u] = 0;
-        if (slot < 0) continue;
-        page[u] = quotient(slot, a.page_size);
-        place[u] = slot - page[u] * a.page_size;
-        if (page[u] >= a.pages) {
-            atomicOr(&g_fault_flags, kFaultBadIndex);
-            page[u] = -1;
-        }
-    }
     for (int item = lane; item < total; item += args.lanes) {
         const int row_index = item / groups, group = item - row_index * groups;
         const bool value = row_index >= a.kv_heads;
         const int64_t head = value ? row_index - a.kv_heads : row_index;
         const Pool4 &pool = value ? args.v : args.k;
+        const uint8_t *from_codes = pool.codes + head * pool.code_head + group * 8;
+        const uint8_t *from_scales = pool.scales + head * pool.scale_head + group;
+        const int64_t stride = value ? a.v_token_stride : a.k_token_stride;
+        T *dst = (value ? (T *)a.v_out + head * a.v_head_stride : (T *)a.k_out + head * a.k_head_stride) + group * 16 +
+                 (first + in_cta) * stride;
         uint2 codes[kRowsEach];
         uint32_t scale[kRowsEach];
 #pragma unroll
         for (int u = 0; u < kRowsEach; ++u) {
+            const int i = in_cta + u * args.tokens;
             codes[u] = make_uint2(0, 0);
             scale[u] = 0;
-            if (page[u] < 0) continue;
-            codes[u] = *reinterpret_cast<const uint2 *>(pool.codes + page[u] * pool.code_page + place[u] * pool.code_slot +
-                                                        head * pool.code_head + group * 8);
-            scale[u] = pool.scales[page[u] * pool.scale_page + place[u] * pool.scale_slot + head * pool.scale_head + group];
+            if (at[0][i] < 0) continue;
+            codes[u] = __ldg(reinterpret_cast<const uint2 *>(from_codes + at[value ? 2 : 0][i]));
+            scale[u] = __ldg(from_scales + at[value ? 3 : 1][i]);
         }
 #pragma unroll
         for (int u = 0; u < kRowsEach; ++u) {
-            const int64_t token = first + u * args.tokens;
-            if (token >= a.tokens) break;
+            if (first + in_cta + u * args.tokens >= a.tokens) break;
             const float unit = __fmul_rn(e4m3_to_float(scale[u]), pool.factor);
-            float f[16];
+            const float2 units = make_float2(unit, unit);
+            float2 f[8];
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 uint32_t h[4];
@@ -290,26 +349,22 @@ __global__ void __launch_bounds__(kRowsThreads) pages4_rows_kernel(const __grid_
                 for (int i = 0; i < 4; ++i) {
                     __half2 x;
                     memcpy(&x, &h[i], 4);
-                    const float2 p = __half22float2(x);
-                    f[8 * w + 2 * i] = p.x * unit;
-                    f[8 * w + 2 * i + 1] = p.y * unit;
+                    f[4 * w + i] = __fmul2_rn(__half22float2(x), units);
                 }
             }
-            T *dst = value ? (T *)a.v_out + token * a.v_token_stride + head * a.v_head_stride
-                           : (T *)a.k_out + token * a.k_token_stride + head * a.k_head_stride;
-            dst += group * 16;
+            T *to = dst + u * args.tokens * stride;
             if constexpr (kVec) {
-                constexpr int V = Elem<T>::kPerVec;
+                constexpr int P = Elem<T>::kPerVec / 2;
 #pragma unroll
-                for (int i = 0; i < 16 / V; ++i) {
-                    float x[V];
+                for (int i = 0; i < 8 / P; ++i) {
+                    float2 x[P];
 #pragma unroll
-                    for (int k = 0; k < V; ++k) x[k] = f[i * V + k];
-                    reinterpret_cast<uint4 *>(dst)[i] = Elem<T>::pack(x);
+                    for (int k = 0; k < P; ++k) x[k] = f[i * P + k];
+                    __stcs(reinterpret_cast<uint4 *>(to) + i, Elem<T>::pack2(x));
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) Elem<T>::store1(dst, i, f[i]);
+                for (int i = 0; i < 16; ++i) Elem<T>::store1(to, i, i % 2 ? f[i / 2].y : f[i / 2].x);
             }
         }
     }
@@ -381,10 +436,9 @@ cudaError_t rotary_4bit_launch(const RotaryArgs &args, const ks_rotary_4bit_args
     k_args.k = pool4(four.k_pages);
     k_args.v = pool4(four.v_pages);
     k_args.q_parts = parts;
-    const int64_t items = 2 * args.a.kv_heads * (args.a.head_dim / 16);
-    // Few tokens: enough threads for all of a token's groups.
-    int kv_parts = 1;
-    if (args.a.tokens < 1024) kv_parts = (int)((items + threads - 1) / threads < 64 ? (items + threads - 1) / threads : 64);
+    // Many tokens: one CTA does all of a token. Few: CTAs of their own for keys and values, a thread for each group.
+    const int64_t items = 2 * args.a.kv_heads * (args.a.head_dim / 16), most = (items + threads - 1) / threads;
+    const int kv_parts = parts == 1 && args.a.tokens >= 1024 ? 0 : (int)(most < 64 ? most : 64);
     const void *f = args.a.dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(vec, half)
                     : args.a.dtype == KS_DTYPE_F16 ? pick<__half>(vec, half)
                                                    : pick<float>(vec, half);
