@@ -256,7 +256,7 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
         auto find = [&](int batch) {
             const int key = first * kUnit + warp * kStep + (batch * 16 + lane / 2) * kUnit + lane % 2 * 16;
             if (key >= end) return kNone;
-            const int index = (int)(__umulhi((uint32_t)key >> 3, args.page_magic) >> args.page_shift);
+            const int index = (int)args.page_blocks.quotient((uint32_t)key >> 4);
             const int page = __ldg(table + index), slot = key - index * page_size;
             if ((uint32_t)page >= (uint64_t)a.pages) {
                 atomicOr(&g_fault_flags, kFaultBadIndex);
@@ -803,15 +803,9 @@ ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, int pool, Attn4P
     p->kernel = pool == kRuns     ? rows_kernel<kRuns>(r, tiles, &p->smem)
                 : pool == kBlocks ? rows_kernel<kBlocks>(r, tiles, &p->smem)
                                   : rows_kernel<kAny>(r, tiles, &p->smem);
-    // key / page_size for whole blocks of 16: with d = page_size / 16 and k = floor(log2 d), n / d is the high word of
-    // 2 n m, shifted by k, for m = floor(2^(31 + k) / d) + 1 and n below 2^27 (m d is at most d < 2^(k + 1) above 2^(31 + k),
-    // and n times that below 2^(28 + k), too little to reach the next whole number).
-    const uint32_t blocks = (uint32_t)(s.a.page_size / 16);
-    p->args.page_shift = 0;
-    while (blocks >> (p->args.page_shift + 1)) ++p->args.page_shift;
     p->args.page_units = (uint32_t)(a.k_pages.code_page_stride / 16);
     p->args.slot_units = (uint32_t)(a.k_pages.code_slot_stride / 16);
-    p->args.page_magic = blocks ? (uint32_t)((1ull << (31 + p->args.page_shift)) / blocks) + 1 : 0;
+    p->args.page_blocks = Divisor::of((uint32_t)(s.a.page_size / 16));
     attn_shape(&s, 8 * tiles, kUnit, kTileCost);
     s.rows = kSlotRows;
     const int per_sm = resident(p->kernel, p->smem);

@@ -9,8 +9,7 @@ namespace ks {
 struct Attn4Args {
     AttnArgs s;
     Pool4 k, v;
-    uint32_t page_magic;  // the quotient of a key and page_size, where pages are whole blocks of 16 keys
-    int32_t page_shift;
+    Divisor page_blocks;  // page_size / 16, where pages are whole blocks of 16 keys
     uint32_t page_units, slot_units;  // strides of the codes' pages and slots, in 16 bytes
 };
 

@@ -15,4 +15,18 @@ __device__ inline int64_t quotient(int64_t a, int64_t b) {
     return a / b;
 }
 
+// n / d for n below 2^27 by a multiplication: with k = floor(log2 d) and m = floor(2^(31 + k) / d) + 1, m d is at most
+// d < 2^(k + 1) above 2^(31 + k), and n times that is below 2^(28 + k), too little to reach the next whole number.
+struct Divisor {
+    uint32_t magic;
+    int32_t shift;
+    __host__ static Divisor of(uint32_t d) {
+        Divisor v = {0, 0};
+        while (d >> (v.shift + 1)) ++v.shift;
+        if (d) v.magic = (uint32_t)((1ull << (31 + v.shift)) / d) + 1;
+        return v;
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return __umulhi(2 * n, magic) >> shift; }
+};
+
 }  // namespace ks

@@ -245,6 +245,16 @@ ks_status_t rotary(const ks_rotary_args_t *args, bool pages, const ks_rotary_4bi
 
 }  // namespace
 
+cudaError_t rotary_queries_launch(const RotaryArgs &args, bool vec, bool half, int threads, cudaStream_t stream) {
+    RotaryArgs k_args = args;
+    k_args.a.kv_heads = 0;
+    const void *f = args.a.dtype == KS_DTYPE_BF16  ? rotary_pick<__nv_bfloat16, false>(vec, half)
+                    : args.a.dtype == KS_DTYPE_F16 ? rotary_pick<__half, false>(vec, half)
+                                                   : rotary_pick<float, false>(vec, half);
+    void *kp[] = {&k_args};
+    return launch_kernel(f, dim3((unsigned)args.a.tokens), dim3((unsigned)threads), 0, kp, stream, launch_pdl_enabled());
+}
+
 int fault_flags_rotary(bool clear) { return fault_flags_t(clear); }
 
 }  // namespace ks

@@ -226,4 +226,7 @@ __device__ __forceinline__ void rot_heads_scalar(const RotaryArgs &args, int64_t
 cudaError_t rotary_4bit_launch(const RotaryArgs &args, const ks_rotary_4bit_args_t &four, bool vec, bool half, int parts,
                                int threads, cudaStream_t stream);
 
+// The queries alone, a CTA a token: ks_rotary's kernel (`args` without keys).
+cudaError_t rotary_queries_launch(const RotaryArgs &args, bool vec, bool half, int threads, cudaStream_t stream);
+
 }  // namespace ks

@@ -1,8 +1,7 @@
 // Rotary positions with the keys and values landing in a cache held in 4 bits (ks_rotary_to_pages_4bit), and the rows
 // of such a cache read back (ks_pages_4bit_to_rows).
 //
-// Writing. CTAs (token, part): the first parts turn the token's queries as ks_rotary does, the others take its keys and
-// values (with many tokens, one CTA does both one after the other), a thread per group of 16: it loads its group and, for a key, the group of its pairs' partners, turns in
+// Writing. Some CTAs turn a token's queries as ks_rotary does, others take keys and values, a thread per group of 16: it loads its group and, for a key, the group of its pairs' partners, turns in
 // FP32, and finds the group's scale and codes. These are those of the real numbers: the angles have 64 bits, the
 // turn's FP32 error is bounded by 2^-21 (|x| + |y|) |scale| for a pair (x, y), and where the scale or a code could
 // differ within the bound (about one group in five thousand; every tie of an unturned value) it is decided
@@ -22,7 +21,9 @@ constexpr float kRoundError = 2.384185791015625e-07f;  // 2^-22: a quotient by t
 struct Rotary4Args {
     RotaryArgs r;
     Pool4 k, v;
-    int32_t q_parts;
+    int32_t q_parts;                  // CTAs of a token's queries
+    int32_t kv_tokens;                // tokens that a CTA of pages4_kernel takes
+    Divisor per_head, per_token;      // groups of a head, and of a token's keys and values
 };
 
 struct Group4 {
@@ -53,12 +54,25 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // Codes of 8 signed quotients, value i in bits 4 i on.
 __device__ __forceinline__ uint32_t fp4_word(const float2 *t) {
-    return fp4_codes(t[0].x, t[0].y) | fp4_codes(t[1].x, t[1].y) << 8 | fp4_codes(t[2].x, t[2].y) << 16 |
-           fp4_codes(t[3].x, t[3].y) << 24;
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(t[0].x), "f"(t[0].y), "f"(t[1].x), "f"(t[1].y), "f"(t[2].x), "f"(t[2].y), "f"(t[3].x), "f"(t[3].y));
+    return w;
+}
+
+// 1 / x within 2^-23 of it: the windows of quotients have room for that.
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // A group's values in FP32, each off by at most `off` (kExact: not at all). A quotient's code is taken at both ends
-// of what it may be; the quotient's own rounding is below 2^-19 of the unit, as quotients are below 8.
+// of what it may be; a quotient's own error is below 8 (2^-23 + 2^-24), quotients being below 8, and so below 2^-19.
 template <typename T, bool kHalf, bool kExact>
 __device__ __forceinline__ Group4 group4(const ks_rotary_args_t &a, const T *row, int group, uint64_t position, float g,
                                          float2 (&y)[8], float off) {
@@ -66,7 +80,7 @@ __device__ __forceinline__ Group4 group4(const ks_rotary_args_t &a, const T *row
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max_nan(top, max_nan(fabsf(y[i].x), fabsf(y[i].y)));
     if (top != top) return {0x7Fu, 0, 0};
-    const float per = __frcp_rn(6.0f * g);
+    const float per = reciprocal(6.0f * g);
     const float low = (top - off) * per * (1.0f - 2 * kRoundError), high = (top + off) * per * (1.0f + 2 * kRoundError);
     Group4 out = {0, 0, 0};
     if constexpr (kExact) {
@@ -75,16 +89,21 @@ __device__ __forceinline__ Group4 group4(const ks_rotary_args_t &a, const T *row
         const uint32_t c = e4m3_codes(fminf(fmaxf(low, 0.0f), 512.0f), fminf(high, 512.0f));
         out.scale = c & 0xFF;
         if (out.scale != c >> 8) {
+            // those that may be the largest, as a rule one
+            uint32_t may = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (!(fabsf(i % 2 ? y[i / 2].y : y[i / 2].x) + off < top - off)) may |= 1u << i;
             double most = 0.0;
-#pragma unroll 1
-            for (int i = 0; i < 16; ++i) most = fmax(most, fabs(turned_exact<T, kHalf>(a, row, group * 16 + i, position)));
+            for (; may; may &= may - 1)
+                most = fmax(most, fabs(turned_exact<T, kHalf>(a, row, group * 16 + __ffs(may) - 1, position)));
             const float v = (float)(most / (6.0 * (double)g));
             out.scale = fp4_scale(v * (1.0f - kRoundError), v * (1.0f + kRoundError), most, g);
         }
     }
     const float u = __fmul_rn(e4m3_to_float(out.scale), g);
     if (!(u > 0.0f)) return out;
-    const float inv = __frcp_rn(u);
+    const float inv = reciprocal(u);
     const float2 inv2 = make_float2(inv, inv);
     float2 t[8];
 #pragma unroll
@@ -169,101 +188,164 @@ constexpr int kTable = kRotMaxDim / 2 / 16 * 20;
 __device__ __forceinline__ int table_at(int j) { return j + (j >> 4) * 4; }
 __device__ __forceinline__ float2 pair_at(const float *table, int i) { return *reinterpret_cast<const float2 *>(table + i); }
 
-// One group of a token's keys or values, into its place.
+constexpr int kMostTokens = 4;  // whose groups a CTA takes
+
+// Where a token's rows go, and what it is turned by.
+struct Place4 {
+    int64_t k_codes, k_scales, v_codes, v_scales;  // k_codes -1: nowhere
+    uint64_t position;
+};
+
+// A CTA's part of the groups of `tokens` tokens from `first` on, a thread a group. Rows are asked for before all else.
 template <typename T, bool kHalf, bool kVec>
-__device__ __forceinline__ void pages4_item(const Rotary4Args &args, int64_t token, uint64_t position, int64_t page, int64_t place,
-                                            int item, const float *cosines, const float *sines) {
+__device__ __forceinline__ void pages4_groups(const Rotary4Args &args, int64_t first, int tokens, int part, int parts, float *cosines,
+                                              float *sines, Place4 *places) {
     const ks_rotary_args_t &a = args.r.a;
-    const int groups = (int)a.head_dim / 16, rot = (int)a.rotary_dim, half = rot / 2;
-    const int row_index = item / groups, group = item - row_index * groups;
-    const bool value = row_index >= a.kv_heads;
-    const int64_t head = value ? row_index - a.kv_heads : row_index;
-    const T *row = value ? (const T *)a.v + token * a.v_token_stride + head * a.v_head_stride
-                         : (const T *)a.k + token * a.k_token_stride + head * a.k_head_stride;
-    const Pool4 &pool = value ? args.v : args.k;
-    float2 x[8];
-    load16<T, kVec>(row + group * 16, x);
-    Group4 out;
-    if (value || group * 16 >= rot) {
-        out = group4<T, kHalf, true>(a, row, group, position, pool.factor, x, 0.0f);
-    } else {
-        float2 y[8];
-        float size = 0.0f;  // the largest |x| + |y| of the group's pairs
-        if constexpr (kHalf && kVec) {
-            const bool second = group * 16 >= half;
-            float2 z[8];
-            load16<T, true>(row + (second ? group * 16 - half : group * 16 + half), z);
-            const int j = table_at(second ? group * 16 - half : group * 16);
-            const float2 sign = make_float2(second ? 1.0f : -1.0f, second ? 1.0f : -1.0f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                size = fmaxf(size, fmaxf(fabsf(x[i].x) + fabsf(z[i].x), fabsf(x[i].y) + fabsf(z[i].y)));
-                y[i] = __ffma2_rn(x[i], pair_at(cosines, j + 2 * i), __fmul2_rn(__fmul2_rn(z[i], pair_at(sines, j + 2 * i)), sign));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int d = group * 16 + i;
-                float &to = i % 2 ? y[i / 2].y : y[i / 2].x;
-                const float m = i % 2 ? x[i / 2].y : x[i / 2].x;
-                to = m;
-                if (d < rot) {
-                    const bool second = kHalf ? d >= half : i & 1;
-                    const int j = table_at(kHalf ? (second ? d - half : d) : d / 2);
-                    const float z = kHalf ? Elem<T>::load1(row, second ? d - half : d + half) : i % 2 ? x[i / 2].x : x[i / 2].y;
-                    to = fmaf(m, cosines[j], second ? z * sines[j] : -z * sines[j]);
-                    size = fmaxf(size, fabsf(m) + fabsf(z));
-                }
+    const int rot = (int)a.rotary_dim, half = rot / 2, groups = (int)a.head_dim / 16;
+    const int per_token = (int)(2 * a.kv_heads) * groups, total = tokens * per_token;
+    struct Item {
+        float2 x[8], z[8];  // the group, and (kHalf && kVec) its pairs' partners
+    };
+    struct Which {
+        int of, group, head;
+        bool value, turned;
+        const T *row;
+    };
+    auto which = [&](int item) {
+        Which w;
+        w.of = (int)args.per_token.quotient((uint32_t)item);
+        const int in = item - w.of * per_token, r = (int)args.per_head.quotient((uint32_t)in);
+        w.group = in - r * groups;
+        w.value = r >= a.kv_heads;
+        w.head = w.value ? r - (int)a.kv_heads : r;
+        w.turned = !w.value && w.group * 16 < rot;
+        w.row = w.value ? (const T *)a.v + (first + w.of) * a.v_token_stride + w.head * a.v_head_stride
+                        : (const T *)a.k + (first + w.of) * a.k_token_stride + w.head * a.k_head_stride;
+        return w;
+    };
+    auto load = [&](const Which &w, Item &it) {
+        load16<T, kVec>(w.row + w.group * 16, it.x);
+        if (kHalf && kVec && w.turned) load16<T, true>(w.row + (w.group * 16 >= half ? w.group * 16 - half : w.group * 16 + half), it.z);
+    };
+    int item = part * blockDim.x + threadIdx.x;
+    Which w = which(item < total ? item : 0);
+    Item it;
+    if (item < total) load(w, it);
+    for (int i = threadIdx.x; i < tokens; i += blockDim.x) {
+        const int64_t slot = a.slots[first + i];
+        Place4 p = {-1, 0, 0, 0, rot > 0 ? (uint64_t)a.positions[first + i] : 0};
+        if (slot >= 0) {
+            const int64_t page = quotient(slot, a.page_size), place = slot - page * a.page_size;
+            if (page < a.pages) {
+                p.k_codes = page * args.k.code_page + place * args.k.code_slot;
+                p.k_scales = page * args.k.scale_page + place * args.k.scale_slot;
+                p.v_codes = page * args.v.code_page + place * args.v.code_slot;
+                p.v_scales = page * args.v.scale_page + place * args.v.scale_slot;
+            } else {
+                atomicOr(&g_fault_flags, kFaultBadIndex);
             }
         }
-        out = group4<T, kHalf, false>(a, row, group, position, pool.factor, y, size * (fabsf(a.scale) * kTurnError));
+        places[i] = p;
     }
-    uint8_t *codes = pool.codes + page * pool.code_page + place * pool.code_slot + head * pool.code_head + group * 8;
-    *reinterpret_cast<uint2 *>(codes) = make_uint2(out.lo, out.hi);
-    pool.scales[page * pool.scale_page + place * pool.scale_slot + head * pool.scale_head + group] = (uint8_t)out.scale;
-}
-
-// A part of a token's groups; its cosines and sines are computed here, or (kMade) taken from `cs`.
-template <typename T, bool kHalf, bool kVec, bool kMade>
-__device__ __forceinline__ void pages4_groups(const Rotary4Args &args, int64_t token, int part, int parts, const float2 *cs,
-                                              float *cosines, float *sines) {
-    const ks_rotary_args_t &a = args.r.a;
-    const RotToken t = rot_token<true>(a, token);
-    if (t.slot < 0) return;  // the whole block
-    for (int j = threadIdx.x; j < (int)(a.rotary_dim / 2); j += blockDim.x) {
-        float2 c;
-        if constexpr (kMade) c = cs[j];
-        else c = turn_cos_sin(t.position * (uint64_t)a.steps[j], a.scale);
-        cosines[table_at(j)] = c.x;
-        sines[table_at(j)] = c.y;
+    for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
+        const int of = i / half, j = i - of * half;
+        const float2 c = turn_cos_sin((uint64_t)a.positions[first + of] * (uint64_t)a.steps[j], a.scale);
+        cosines[table_at(i)] = c.x;
+        sines[table_at(i)] = c.y;
     }
     __syncthreads();
-    const int64_t page = quotient(t.slot, a.page_size), place = t.slot - page * a.page_size;
-    if (page >= a.pages) {
-        if (threadIdx.x == 0) atomicOr(&g_fault_flags, kFaultBadIndex);
-        return;
+    while (item < total) {
+        const int next = item + parts * blockDim.x;
+        const Which now = w;
+        Item cur = it;
+        if (next < total) {
+            w = which(next);
+            load(w, it);
+        }
+        item = next;
+        const Place4 &p = places[now.of];
+        if (p.k_codes < 0) continue;
+        const Pool4 &pool = now.value ? args.v : args.k;
+        Group4 out;
+        if (!now.turned) {
+            out = group4<T, kHalf, true>(a, now.row, now.group, p.position, pool.factor, cur.x, 0.0f);
+        } else {
+            float2 y[8];
+            float size = 0.0f;  // the largest |x| + |y| of the group's pairs
+            if constexpr (kHalf && kVec) {
+                const bool second = now.group * 16 >= half;
+                const int j = table_at(now.of * half + (second ? now.group * 16 - half : now.group * 16));
+                const float2 sign = make_float2(second ? 1.0f : -1.0f, second ? 1.0f : -1.0f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 x = cur.x[i], z = cur.z[i];
+                    size = fmaxf(size, fmaxf(fabsf(x.x) + fabsf(z.x), fabsf(x.y) + fabsf(z.y)));
+                    y[i] = __ffma2_rn(x, pair_at(cosines, j + 2 * i), __fmul2_rn(__fmul2_rn(z, pair_at(sines, j + 2 * i)), sign));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int d = now.group * 16 + i;
+                    float &to = i % 2 ? y[i / 2].y : y[i / 2].x;
+                    const float m = i % 2 ? cur.x[i / 2].y : cur.x[i / 2].x;
+                    to = m;
+                    if (d < rot) {
+                        const bool second = kHalf ? d >= half : i & 1;
+                        const int j = table_at(now.of * half + (kHalf ? (second ? d - half : d) : d / 2));
+                        const float z = kHalf ? Elem<T>::load1(now.row, second ? d - half : d + half)
+                                              : i % 2 ? cur.x[i / 2].x : cur.x[i / 2].y;
+                        to = fmaf(m, cosines[j], second ? z * sines[j] : -z * sines[j]);
+                        size = fmaxf(size, fabsf(m) + fabsf(z));
+                    }
+                }
+            }
+            out = group4<T, kHalf, false>(a, now.row, now.group, p.position, pool.factor, y, size * (fabsf(a.scale) * kTurnError));
+        }
+        *reinterpret_cast<uint2 *>(pool.codes + (now.value ? p.v_codes : p.k_codes) + now.head * pool.code_head + now.group * 8) =
+            make_uint2(out.lo, out.hi);
+        pool.scales[(now.value ? p.v_scales : p.k_scales) + now.head * pool.scale_head + now.group] = (uint8_t)out.scale;
     }
-    const int total = (int)(2 * a.kv_heads * (a.head_dim / 16));
-    for (int item = part * blockDim.x + threadIdx.x; item < total; item += parts * blockDim.x)
-        pages4_item<T, kHalf, kVec>(args, token, t.position, page, place, item, cosines, sines);
 }
 
+// Few tokens: CTAs (token, part), the first parts for the queries, the others for the groups.
 template <typename T, bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kRotThreads) rotary_4bit_kernel(const __grid_constant__ Rotary4Args args) {
-    __shared__ float2 cs[kRotMaxDim / 2];
-    __shared__ __align__(16) float cosines[kTable], sines[kTable];
+    __shared__ __align__(16) float tables[2 * kTable];
+    __shared__ Place4 places[kMostTokens];
+    static_assert(sizeof(tables) >= kRotMaxDim / 2 * sizeof(float2), "the queries' table fits");
+    float2 *cs = reinterpret_cast<float2 *>(tables);
     grid_dependency_wait();
     allow_dependents_launch();
     const int part = blockIdx.y;
-    const int64_t token = blockIdx.x;
     if (part < args.q_parts) {
         const int first = part * args.r.heads_per_y, last = min((int)args.r.a.q_heads, first + args.r.heads_per_y);
-        if constexpr (kVec) rot_heads_vec<T, kHalf, false>(args.r, token, first, last, cs);
-        else rot_heads_scalar<T, kHalf, false>(args.r, token, first, last, cs);
-        if (gridDim.y == args.q_parts) pages4_groups<T, kHalf, kVec, true>(args, token, 0, 1, cs, cosines, sines);
+        if constexpr (kVec) rot_heads_vec<T, kHalf, false>(args.r, blockIdx.x, first, last, cs);
+        else rot_heads_scalar<T, kHalf, false>(args.r, blockIdx.x, first, last, cs);
     } else {
-        pages4_groups<T, kHalf, kVec, false>(args, token, part - args.q_parts, gridDim.y - args.q_parts, cs, cosines, sines);
+        pages4_groups<T, kHalf, kVec>(args, blockIdx.x, 1, part - args.q_parts, gridDim.y - args.q_parts, tables, tables + kTable, places);
     }
+}
+
+// Many tokens: the queries are ks_rotary's kernel, the groups this one, for kv_tokens tokens a CTA. (Both in one kernel
+// have its registers in common: measured at 8192 tokens of 56 + 8 + 8 heads, 88 us and more for 43 and KSX.) It is
+// launched to start while the queries' last CTAs run: those began after all earlier work was done, and of their own
+// they write nothing that is read here. It ends after them.
+template <typename T, bool kHalf, bool kVec>
+__global__ void __launch_bounds__(kRotThreads, 3) pages4_kernel(const __grid_constant__ Rotary4Args args, int alone) {
+    __shared__ __align__(16) float tables[2 * kTable];
+    __shared__ Place4 places[kMostTokens];
+    if (alone) grid_dependency_wait();
+    const int64_t first = (int64_t)blockIdx.x * args.kv_tokens;
+    pages4_groups<T, kHalf, kVec>(args, first, (int)min((int64_t)args.kv_tokens, args.r.a.tokens - first), 0, 1, tables,
+                                  tables + kTable, places);
+    if (!alone) grid_dependency_wait();
+    else allow_dependents_launch();
+}
+
+template <typename T>
+const void *pick_groups(bool vec, bool half) {
+    if (vec) return half ? (const void *)pages4_kernel<T, true, true> : (const void *)pages4_kernel<T, false, true>;
+    return half ? (const void *)pages4_kernel<T, true, false> : (const void *)pages4_kernel<T, false, false>;
 }
 
 template <typename T>
@@ -436,15 +518,34 @@ cudaError_t rotary_4bit_launch(const RotaryArgs &args, const ks_rotary_4bit_args
     k_args.k = pool4(four.k_pages);
     k_args.v = pool4(four.v_pages);
     k_args.q_parts = parts;
-    // Many tokens: one CTA does all of a token. Few: CTAs of their own for keys and values, a thread for each group.
-    const int64_t items = 2 * args.a.kv_heads * (args.a.head_dim / 16), most = (items + threads - 1) / threads;
-    const int kv_parts = parts == 1 && args.a.tokens >= 1024 ? 0 : (int)(most < 64 ? most : 64);
-    const void *f = args.a.dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(vec, half)
-                    : args.a.dtype == KS_DTYPE_F16 ? pick<__half>(vec, half)
-                                                   : pick<float>(vec, half);
+    const int64_t groups = args.a.head_dim / 16, items = 2 * args.a.kv_heads * groups, half_dim = args.a.rotary_dim / 2;
+    k_args.per_head = Divisor::of((uint32_t)groups);
+    k_args.per_token = Divisor::of((uint32_t)items);
+    k_args.kv_tokens = 1;
+    const int dtype = args.a.dtype;
+    if (parts <= 1 && args.a.tokens >= 1024) {
+        // as many tokens a CTA as have their sines fit its tables
+        k_args.kv_tokens = kMostTokens;
+        while (k_args.kv_tokens > 1 && k_args.kv_tokens * half_dim > kRotMaxDim / 2) --k_args.kv_tokens;
+        int alone = parts == 0;
+        if (!alone) {
+            const cudaError_t ce = rotary_queries_launch(args, vec, half, threads, stream);
+            if (ce != cudaSuccess) return ce;
+        }
+        const void *f = dtype == KS_DTYPE_BF16  ? pick_groups<__nv_bfloat16>(vec, half)
+                        : dtype == KS_DTYPE_F16 ? pick_groups<__half>(vec, half)
+                                                : pick_groups<float>(vec, half);
+        void *kp[] = {&k_args, &alone};
+        return launch_kernel(f, dim3((unsigned)((args.a.tokens + k_args.kv_tokens - 1) / k_args.kv_tokens)), dim3(kRotThreads), 0, kp,
+                             stream, alone ? launch_pdl_enabled() : true);
+    }
+    const int64_t most = (items + threads - 1) / threads;
+    const void *f = dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(vec, half)
+                    : dtype == KS_DTYPE_F16 ? pick<__half>(vec, half)
+                                            : pick<float>(vec, half);
     void *kp[] = {&k_args};
-    return launch_kernel(f, dim3((unsigned)args.a.tokens, (unsigned)(parts + kv_parts)), dim3((unsigned)threads), 0, kp, stream,
-                         launch_pdl_enabled());
+    return launch_kernel(f, dim3((unsigned)args.a.tokens, (unsigned)(parts + (most < 64 ? most : 64))), dim3((unsigned)threads), 0, kp,
+                         stream, launch_pdl_enabled());
 }
 
 int fault_flags_rotary_4bit(bool clear) { return fault_flags_t(clear); }
