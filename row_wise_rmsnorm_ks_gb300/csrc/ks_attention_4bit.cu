@@ -760,23 +760,30 @@ int row_tiles(const ks_attention_args_t &a) {
     return a.head_dim > 128 || rows <= 8 ? 1 : rows <= 16 ? 2 : kTc;
 }
 
+// Whether both pools have the same strides, those of the scales an eighth of the codes', and a place in them is 32 bits of
+// 16-byte units.
+bool pools_alike(const ks_attention_4bit_args_t &args) {
+    const ks_attention_args_t &a = args.attention;
+    const ks_pages_4bit_t &k = args.k_pages, &v = args.v_pages;
+    // an axis of one entry has any stride
+    auto same = [](int64_t count, int64_t x, int64_t y, int64_t xs, int64_t ys) {
+        return count == 1 || (x == y && xs == ys && x == 8 * xs && x % 16 == 0);
+    };
+    return a.pages > 0 && same(a.pages, k.code_page_stride, v.code_page_stride, k.scale_page_stride, v.scale_page_stride) &&
+           same(a.page_size, k.code_slot_stride, v.code_slot_stride, k.scale_slot_stride, v.scale_slot_stride) &&
+           (((__int128)(a.pages - 1) * k.code_page_stride + (a.page_size - 1) * k.code_slot_stride) >> 4) < 0xFFFFFFFFll;
+}
+
 // How the pools of a call lie, given the alignment of their addresses.
 int pool_kind(const ks_attention_4bit_args_t &args, uintptr_t code_align, uintptr_t scale_align) {
     const ks_attention_args_t &a = args.attention;
     const ks_pages_4bit_t &k = args.k_pages, &v = args.v_pages;
     const int64_t r = a.head_dim / 64;
-    if (a.head_dim % 64 || a.page_size % 16 || a.pages <= 0) return kAny;
+    if (a.head_dim % 64 || a.page_size % 16 || !pools_alike(args)) return kAny;
     const uintptr_t scales = r == 2 ? 7 : r == 4 ? 15 : 3;
     if ((code_align & 15) || (scale_align & scales)) return kAny;
-    // an axis of one entry has any stride
-    auto same = [](int64_t count, int64_t x, int64_t y, int64_t xs, int64_t ys) { return count == 1 || (x == y && xs == ys && x == 8 * xs); };
-    if (!same(a.pages, k.code_page_stride, v.code_page_stride, k.scale_page_stride, v.scale_page_stride) ||
-        !same(a.page_size, k.code_slot_stride, v.code_slot_stride, k.scale_slot_stride, v.scale_slot_stride))
-        return kAny;
-    // a place in the pool is 32 bits of 16-byte units
-    if ((((__int128)(a.pages - 1) * k.code_page_stride + (a.page_size - 1) * k.code_slot_stride) >> 4) >= 0xFFFFFFFFll) return kAny;
     if (k.code_slot_stride != 32 * r) return kBlocks;
-    uintptr_t runs = 0;  // a block of scales is copied at once too
+    uintptr_t runs = 0;  // a block of scales is copied by 16 bytes too
     for (const ks_pages_4bit_t *p : {&k, &v})
         runs |= (uintptr_t)p->scales | (uintptr_t)(a.pages > 1 ? p->scale_page_stride : 0) | (uintptr_t)(a.kv_heads > 1 ? p->scale_head_stride : 0);
     return runs & 15 ? kBlocks : kRuns;
@@ -794,6 +801,9 @@ ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, int pool, Attn4P
     int sms = 0;
     const ks_status_t st = device_sms(&sms);
     if (st != KS_SUCCESS) return st;
+    p->args.alike = pools_alike(a);
+    p->args.page_units = (uint32_t)(a.k_pages.code_page_stride / 16);
+    p->args.slot_units = (uint32_t)(a.k_pages.code_slot_stride / 16);
     if (tiles == kTc) {
         p->kernel = nullptr;
         attn_shape(&s, attn_tc_rows(), attn_tc_unit(), attn_tc_tile_cost());
@@ -803,8 +813,6 @@ ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, int pool, Attn4P
     p->kernel = pool == kRuns     ? rows_kernel<kRuns>(r, tiles, &p->smem)
                 : pool == kBlocks ? rows_kernel<kBlocks>(r, tiles, &p->smem)
                                   : rows_kernel<kAny>(r, tiles, &p->smem);
-    p->args.page_units = (uint32_t)(a.k_pages.code_page_stride / 16);
-    p->args.slot_units = (uint32_t)(a.k_pages.code_slot_stride / 16);
     p->args.page_blocks = Divisor::of((uint32_t)(s.a.page_size / 16));
     attn_shape(&s, 8 * tiles, kUnit, kTileCost);
     s.rows = kSlotRows;

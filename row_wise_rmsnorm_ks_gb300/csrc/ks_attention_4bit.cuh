@@ -10,6 +10,7 @@ struct Attn4Args {
     AttnArgs s;
     Pool4 k, v;
     Divisor page_blocks;  // page_size / 16, where pages are whole blocks of 16 keys
+    bool alike;  // both pools have the same strides, those of the scales an eighth of the codes', and places 32 bits:
     uint32_t page_units, slot_units;  // strides of the codes' pages and slots, in 16 bytes
 };
 

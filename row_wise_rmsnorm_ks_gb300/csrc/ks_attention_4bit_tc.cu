@@ -23,7 +23,9 @@ cudaError_t attn4_tc_launch(const Attn4Args &args, uintptr_t code_align, uintptr
     pages.k = args.k;
     pages.v = args.v;
     const int dim = (int)s.a.head_dim;
-    pages.whole = (dim == 64 || dim == 128) && (code_align & 15) == 0 && (scale_align & 3) == 0;
+    pages.whole = (dim == 64 || dim == 128) && (code_align & 15) == 0 && (scale_align & (dim / 16 - 1)) == 0 && args.alike;
+    pages.page_units = args.page_units;
+    pages.slot_units = args.slot_units;
     const bool bf16 = s.a.dtype == KS_DTYPE_BF16;
     const void *f = dim <= 64 ? (bf16 ? (const void *)attn_tc_kernel<__nv_bfloat16, 64, Pages4>
                                       : (const void *)attn_tc_kernel<__half, 64, Pages4>)

@@ -42,7 +42,10 @@ struct Pages16 {
 struct Pages4 {
     static constexpr bool k4 = true;
     Pool4 k, v;
-    int32_t whole;  // rows are 4 kDim / 8 bytes of codes at 16-byte boundaries, and scales at kDim / 16
+    // Rows are kDim / 2 bytes of codes at 16-byte boundaries and kDim / 16 of scales at as many, both pools lie alike, and a
+    // place has 32 bits of 16-byte units: the strides of pages and slots in those.
+    int32_t whole;
+    uint32_t page_units, slot_units;
 };
 constexpr int kHalfBytes = kKeys * 128;  // 128 rows of 64 values
 constexpr int kTileCost = 3;       // steps that beginning and ending a row tile costs
@@ -56,9 +59,14 @@ template <int kDim, bool k4 = false>
 struct Tc {
     static constexpr int kHalves = kDim / 64;
     static constexpr int kTileBytes = kHalves * kHalfBytes;  // a tile of Q, K or V
-    static constexpr int kStages = kDim == 128 ? 5 : 10;
+    static constexpr int kStages = kDim == 128 ? (k4 ? 4 : 5) : (k4 ? 8 : 10);
     static constexpr int kBars = (k4 ? 2 : 3) * kStages + 14;
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kBars * 8 + 16;
+    // 4-bit pages: each converting warp's ring of rows as the pools hold them, codes and scales; rows 16 bytes apart from a
+    // multiple of 32, so that eight lanes read 16 bytes of theirs without a conflict.
+    static constexpr int kRawStages = 3, kRawRow = kDim / 2 + 16;
+    static constexpr int kRawAt = (2 + kStages) * kTileBytes + (kBars * 8 + 16 + 15) / 16 * 16;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + (kBars * 8 + 16) +
+                                 (k4 ? 16 + kConvertWarps * kRawStages * 32 * kRawRow : 0);
     static constexpr uint32_t kO = 256;  // tensor-memory columns: S0 0, S1 128, then the O tiles
 };
 
@@ -327,84 +335,115 @@ __device__ __forceinline__ void make_queries(uint8_t *q_tile, int first, float (
     unit[1] = __shfl_sync(0xFFFFFFFFu, mine, lane / 4 + 8);
 }
 
-// The converting warps: a thread per key of a step. Codes and scales of the next step's keys are asked for as soon as this
-// step's are used up, and so for the values; a row becomes fp16 in the layout that the matrix instructions read. Rows
-// behind the last key that the row tile sees are zeros.
+// The converting warps: a thread per key of a step, a warp for 32 of them. A warp copies its keys' codes and scales to a
+// ring of its own, two tiles ahead, neighbouring lanes neighbouring bytes (with loads to registers, a key a thread, the
+// long prompt takes 1.3 times as long); a thread then makes its row fp16 in the layout that the matrix instructions read.
+// Rows behind the last key that the row tile sees are zeros.
 template <int kDim>
-__device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &pages, Place &place, bool more, uint8_t *ring,
+__device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &pages, Place &place, bool more, uint8_t *ring, uint8_t *raw,
                                               uint64_t *full, uint64_t *empty, volatile uint32_t *gave_up) {
     using C = Tc<kDim, true>;
     constexpr int kGroups = kDim / 16;
+    constexpr uint32_t kNone = 0xFFFFFFFFu;
     const ks_attention_args_t &a = s.a;
-    const int row = threadIdx.x - kConvert * 32, lane = threadIdx.x % 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kConvert, row = warp * 32 + lane;
     const int groups = (int)a.head_dim / 16, page_size = (int)a.page_size;
-    uint32_t codes[2][2 * kGroups], scales[2][kGroups / 4];
+    uint8_t *mine = raw + warp * C::kRawStages * 32 * C::kRawRow;
     uint32_t at = 0;  // tiles made so far: K and V of each step in turn
+    uint32_t raw_at = 0;
     while (more) {
         const AttnSpan span = attn_span(s, place.cur, place.q);
         const int head = place.cur.head / s.head_splits, sees = attn_tile_keys(s, place.q, place.cur.row_tile);
         const int32_t *table = a.page_table + (int64_t)place.cur.seq * a.table_stride;
-        auto look_up = [&](int j, int &slot) {
+        // The place of this thread's key of a step: whole pools, in 16 bytes of codes (2 of scales); others, its page, and its
+        // slot. kNone: no key, or its page is not in the pool.
+        auto look_up = [&](int j, uint32_t &slot) {
             const int key = j * kKeys + row;
             slot = 0;
-            if (j >= span.last || key >= sees) return -1;
+            if (j >= span.last || key >= sees) return kNone;
             const int index = key / page_size;
-            slot = key - index * page_size;
-            const int page = __ldg(table + index);
-            if ((uint32_t)page < (uint64_t)a.pages) return page;
-            atomicOr(&g_fault_flags, kFaultBadIndex);  // past the pool: zeros
-            return -1;
-        };
-        auto load = [&](const Pool4 &pool, int page, int slot, uint32_t (&c)[2 * kGroups], uint32_t (&e)[kGroups / 4]) {
-#pragma unroll
-            for (int i = 0; i < 2 * kGroups; ++i) c[i] = 0;
-#pragma unroll
-            for (int i = 0; i < kGroups / 4; ++i) e[i] = 0;
-            if (page < 0) return;
-            const uint8_t *cp = pool.codes + head * pool.code_head + page * pool.code_page + slot * pool.code_slot;
-            const uint8_t *ep = pool.scales + head * pool.scale_head + page * pool.scale_page + slot * pool.scale_slot;
-            if (pages.whole) {
-#pragma unroll
-                for (int i = 0; i < kGroups / 2; ++i) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(cp) + i);
-                    c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
-                }
-#pragma unroll
-                for (int i = 0; i < kGroups / 4; ++i) e[i] = __ldg(reinterpret_cast<const uint32_t *>(ep) + i);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kGroups; ++i)
-                    if (i < groups) {
-                        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(cp) + i);
-                        c[2 * i] = x.x, c[2 * i + 1] = x.y;
-                        e[i / 4] |= (uint32_t)__ldg(ep + i) << (8 * (i % 4));
-                    }
+            const uint32_t page = (uint32_t)__ldg(table + index);
+            slot = (uint32_t)(key - index * page_size);
+            if (page >= (uint64_t)a.pages) {
+                atomicOr(&g_fault_flags, kFaultBadIndex);
+                return kNone;
             }
+            return pages.whole ? page * pages.page_units + slot * pages.slot_units : page;
         };
-        int slot;
-        int page = look_up(span.first, slot);
-        load(pages.k, page, slot, codes[0], scales[0]);
-        load(pages.v, page, slot, codes[1], scales[1]);
+        // A tile's codes (and scales, of whole pools) to the raw ring; zeros where there is no key.
+        auto copy = [&](const Pool4 &pool, uint32_t where, uint32_t slots, uint32_t to) {
+            const uint32_t dst = smem_addr(mine) + to * 32 * C::kRawRow;
+            const uint8_t *codes = pool.codes + head * pool.code_head;
+            if (pages.whole) {
+                constexpr int kPieces = kDim / 32;  // of 16 bytes in a row
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int key = i * (32 / kPieces) + lane / kPieces, c = lane % kPieces;
+                    const uint32_t w = __shfl_sync(0xFFFFFFFFu, where, key);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + key * C::kRawRow + c * 16),
+                                 "l"(codes + c * 16 + (w == kNone ? 0 : w) * 16ull), "r"(w == kNone ? 0 : 16) : "memory");
+                }
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst + lane * C::kRawRow + kDim / 2),
+                             "l"(pool.scales + head * pool.scale_head + (where == kNone ? 0 : where) * 2ull), "n"(kGroups),
+                             "r"(where == kNone ? 0 : kGroups) : "memory");
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kGroups; ++i) {
+                    const int key = i * 32 / kGroups + lane / kGroups, g = lane % kGroups;
+                    const uint32_t w = __shfl_sync(0xFFFFFFFFu, where, key), r = __shfl_sync(0xFFFFFFFFu, slots, key);
+                    const bool in = w != kNone && g < groups;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + key * C::kRawRow + g * 8),
+                                 "l"(in ? codes + w * pool.code_page + r * pool.code_slot + g * 8 : pool.codes), "r"(in ? 8 : 0) : "memory");
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        uint32_t slot[2];  // of this step and the next
+        uint32_t where[2];
+        where[0] = look_up(span.first, slot[0]);
+        copy(pages.k, where[0], slot[0], raw_at);
+        copy(pages.v, where[0], slot[0], raw_at + 1 < C::kRawStages ? raw_at + 1 : raw_at + 1 - C::kRawStages);
+        where[1] = look_up(span.first + 1, slot[1]);
         bool ok = true;
         for (int j = span.first; j < span.last && ok; ++j) {
-            page = look_up(j + 1, slot);
+            const uint32_t now = where[0], now_slot = slot[0];
+            where[0] = where[1];
+            slot[0] = slot[1];
+            where[1] = look_up(j + 2, slot[1]);
 #pragma unroll
             for (int v = 0; v < 2; ++v, ++at) {
+                const Pool4 &pool = v ? pages.v : pages.k;
+                copy(pool, where[0], slot[0], raw_at ? raw_at - 1 : C::kRawStages - 1);  // the next step's tile, two on
                 const uint32_t stage = at % C::kStages;
                 ok = ok && bar_wait_warp(empty + stage, (at / C::kStages & 1) ^ 1, gave_up);
                 if (!ok) break;
+                uint32_t scales[kGroups / 4] = {};
+                if (!pages.whole && now != kNone) {
+                    const uint8_t *e = pool.scales + head * pool.scale_head + now * pool.scale_page + now_slot * pool.scale_slot;
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+                        if (g < groups) scales[g / 4] |= (uint32_t)__ldg(e + g) << (8 * (g % 4));
+                }
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                __syncwarp();
+                const uint8_t *from = mine + (raw_at * 32 + lane) * C::kRawRow;
+                if (pages.whole) {
+#pragma unroll
+                    for (int i = 0; i < kGroups / 4; ++i) scales[i] = reinterpret_cast<const uint32_t *>(from + kDim / 2)[i];
+                }
                 uint8_t *tile = ring + stage * C::kTileBytes + row * 128;
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    const uint32_t byte = scales[v][g / 4] >> (8 * (g % 4)) & 0xFF;
-                    const uint32_t scale = e4m3_to_half(byte | byte << 8);
+                for (int i = 0; i < kGroups / 2; ++i) {  // two groups
+                    const uint4 x = *reinterpret_cast<const uint4 *>(from + i * 16);
+                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = 4 * i + k, g = c / 2;
+                        const uint32_t scale = e4m3_to_half(__byte_perm(scales[g / 4], 0, (g % 4) | (g % 4) << 4));
                         uint32_t h[4];
-                        fp4_to_half(codes[v][2 * g + k], h);
+                        fp4_to_half(words[k], h);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) h[i] = half2_mul(h[i], scale);
-                        const int c = 2 * g + k;
+                        for (int n = 0; n < 4; ++n) h[n] = half2_mul(h[n], scale);
                         *reinterpret_cast<uint4 *>(tile + c / 8 * kHalfBytes + ((c % 8 ^ (row & 7)) << 4)) =
                             make_uint4(h[0], h[1], h[2], h[3]);
                     }
@@ -412,9 +451,11 @@ __device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &p
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) bar_arrive(full + stage);
-                load(v ? pages.v : pages.k, page, slot, codes[v], scales[v]);
+                if (++raw_at == C::kRawStages) raw_at = 0;
             }
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");  // those of no step among them
+        __syncwarp();
         more = ok && next_tile(s, place, span.cost);
     }
 }
@@ -498,7 +539,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     if (k4 && warp >= kConvert) {
         if constexpr (k4) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<k4>::kConvertRegs));
-            convert_pages<kDim>(s, pages, place, more, smem + 2 * C::kTileBytes, full, empty, gave_up);
+            convert_pages<kDim>(s, pages, place, more, smem + 2 * C::kTileBytes, smem + C::kRawAt, full, empty, gave_up);
         }
     } else if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<k4>::kOtherRegs));
