@@ -6,6 +6,12 @@
 // 4096 16-byte vectors lie in a CTA's registers, x and r each read and written once, which bounds the operator by
 // memory (4 values a place); wider rows, and rows that no vector fits, are read three times, the second and third
 // time mostly from L2.
+//
+// What counts is how many bytes are on their way while rows are summed, so a thread holds x as it was read, packed,
+// until the second sum's values take its place, and asks for the weights where they are used: 64 registers at four
+// vectors a thread, 1024 threads an SM. (Measured, bf16 [16383, 8192], both norms, a gate per sequence: 176 us, 158 us
+// at the copy rate; 207 with x unpacked and the weights asked for ahead, 216 through a ring of bulk copies, which is
+// slower yet for narrower rows. bf16 [4, 1536], gate per channel: 3.1 us by graph replay, the two sums' latency.)
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -45,90 +51,100 @@ __device__ __forceinline__ void times(float2 (&s)[P], const float2 (&w)[P]) {
     for (int i = 0; i < P; ++i) s[i] = pair_mul<kPair>(s[i], w[i]);
 }
 
-// A row per team, V vectors a thread: a warp (kTeam 32), several of them a CTA, or the CTA (0). The residual's vectors
-// stay as they came until s takes their place; weights and gate come from L1 when they are wanted.
-template <typename T, int V, int kTeam>
-__global__ void __launch_bounds__(kTeam ? 256 : 512, V <= 2 ? 2048 / (kTeam ? 256 : 512) / 2 : 1)
-gated_rows_kernel(const __grid_constant__ GatedArgs args) {
+// What a thread does with its vectors of a row. kAhead asks for weights and gate before the sums that they wait for, at
+// the cost of their registers; without it, x stays packed until the second sum, so that more rows are on their way.
+template <typename T, int V, int kTeam, bool kAhead>
+__device__ __forceinline__ void gated_row(const ks_gated_norm_args_t &a, int64_t row, int hv, int t, int g, uint4 (&xv)[V], const uint4 (&rv)[V],
+                                          float (&red)[2][32], int &slot) {
     using E = Elem<T>;
     constexpr int P = E::kPerVec / 2;
     constexpr bool kPair = E::kPairMath;
+    constexpr int A = kAhead ? V : 1;
+    const float hidden = (float)a.hidden;
+    uint4 *xr = (uint4 *)a.x + row * hv, *rr = (uint4 *)a.residual + row * hv;
+    auto get = [&](const void *p, int k) {
+        const int c = t + k * g;
+        return c < hv ? __ldg((const uint4 *)p + c) : make_uint4(0, 0, 0, 0);
+    };
+    auto ask = [&](const void *p, uint4 (&v)[A]) {
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = get(p, k);
+        }
+    };
+    auto apply = [&](const void *p, const uint4 (&v)[A], int k, float2 (&s)[P]) {
+        float2 w[P];
+        E::unpack2(kAhead ? v[kAhead ? k : 0] : get(p, k), w);
+        times<kPair>(s, w);
+    };
+    float factor = a.block_scale;
+    uint4 post[A], gate[A], weight[A];
+    const T *const of = gate_row<T>(a, row);
+    const bool gates = of && a.gate_column_stride;
+    if (a.post_weight) ask(a.post_weight, post);
+    if (gates) ask(of, gate);
+    else if (of) factor *= E::load1(of, 0);
+    float scale = 1.0f;
+    if (a.post_weight) {
+        PairSumSq<kPair> acc;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            float2 x[P];
+            E::unpack2(xv[k], x);
+            acc.add(x);
+        }
+        scale = row_scale(team_sum<kTeam>(acc.total(), red[slot ^= 1]), hidden, a.eps);
+    }
+    ask(a.weight, weight);
+    float2 s[V][P];
+    PairSumSq<kPair> acc;
+    const float2 f2 = make_float2(factor, factor), r2 = make_float2(a.residual_scale, a.residual_scale);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int c = t + k * g;
+        if (!kAhead) opaque(xv[k]);  // unpacked again
+        E::unpack2(xv[k], s[k]);
+        if (a.post_weight) {
+            times<kPair>(s[k], scale);
+            apply(a.post_weight, post, k, s[k]);
+        }
+        if (gates) apply(of, gate, k, s[k]);
+        float2 r[P];
+        E::unpack2(rv[k], r);
+#pragma unroll
+        for (int i = 0; i < P; ++i) s[k][i] = pair_fma<kPair>(r[i], r2, pair_mul<kPair>(s[k][i], f2));
+        if (c < hv) {
+            __stcs(rr + c, E::pack2(s[k]));
+            acc.add(s[k]);
+        }
+    }
+    const float out_scale = row_scale(team_sum<kTeam>(acc.total(), red[slot ^= 1]), hidden, a.eps);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int c = t + k * g;
+        times<kPair>(s[k], out_scale);
+        apply(a.weight, weight, k, s[k]);
+        if (c < hv) __stcs(xr + c, E::pack2(s[k]));
+    }
+}
+
+// A row per team, V vectors a thread: a warp (kTeam 32), several of them a CTA, or the CTA (0).
+template <typename T, int V, int kTeam, bool kAhead>
+__global__ void __launch_bounds__(kTeam ? 256 : 512, (V <= 4 && !kAhead ? 2 : 1) * (kTeam ? 2 : 1))
+gated_rows_kernel(const __grid_constant__ GatedArgs args) {
     __shared__ float red[2][32];
     const ks_gated_norm_args_t &a = args.a;
     const int g = kTeam ? kTeam : blockDim.x, t = kTeam ? threadIdx.x % 32 : threadIdx.x;
     const int teams = kTeam ? blockDim.x / 32 : 1, team = kTeam ? threadIdx.x / 32 : 0;
     const int hv = (int)args.hv;
-    const float hidden = (float)a.hidden;
     int slot = 0;  // of `red`: every sum takes the other one
     grid_dependency_wait();
     allow_dependents_launch();
     for (int64_t row = (int64_t)blockIdx.x * teams + team; row < a.rows; row += (int64_t)gridDim.x * teams) {
-        uint4 *xr = (uint4 *)a.x + row * hv, *rr = (uint4 *)a.residual + row * hv;
-        uint4 rv[V];
-        float2 s[V][P];
-        {
-            uint4 xv[V];
-            load_row<V>(xr, t, g, hv, xv);
-            load_row<V>(rr, t, g, hv, rv);
-#pragma unroll
-            for (int k = 0; k < V; ++k) E::unpack2(xv[k], s[k]);
-        }
-        float factor = a.block_scale;
-        if (a.post_weight) {
-            PairSumSq<kPair> acc;
-#pragma unroll
-            for (int k = 0; k < V; ++k) acc.add(s[k]);
-            const float scale = row_scale(team_sum<kTeam>(acc.total(), red[slot ^= 1]), hidden, a.eps);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const int c = t + k * g;
-                if (c >= hv) continue;
-                float2 w[P];
-                E::unpack2(__ldg((const uint4 *)a.post_weight + c), w);
-                times<kPair>(s[k], scale);
-                times<kPair>(s[k], w);
-            }
-        }
-        if (a.gate) {
-            const T *gate = gate_row<T>(a, row);
-            if (a.gate_column_stride) {
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int c = t + k * g;
-                    if (c >= hv) continue;
-                    float2 w[P];
-                    E::unpack2(__ldg((const uint4 *)gate + c), w);
-                    times<kPair>(s[k], w);
-                }
-            } else {
-                factor *= E::load1(gate, 0);
-            }
-        }
-        PairSumSq<kPair> acc;
-        const float2 f2 = make_float2(factor, factor), r2 = make_float2(a.residual_scale, a.residual_scale);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = t + k * g;
-            float2 r[P];
-            E::unpack2(rv[k], r);
-#pragma unroll
-            for (int i = 0; i < P; ++i) s[k][i] = pair_fma<kPair>(r[i], r2, pair_mul<kPair>(s[k][i], f2));
-            if (c < hv) {
-                __stcs(rr + c, E::pack2(s[k]));
-                acc.add(s[k]);
-            }
-        }
-        const float out_scale = row_scale(team_sum<kTeam>(acc.total(), red[slot ^= 1]), hidden, a.eps);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = t + k * g;
-            if (c >= hv) continue;
-            float2 w[P];
-            E::unpack2(__ldg((const uint4 *)a.weight + c), w);
-            times<kPair>(s[k], out_scale);
-            times<kPair>(s[k], w);
-            __stcs(xr + c, E::pack2(s[k]));
-        }
+        uint4 xv[V], rv[V];
+        load_row<V>((const uint4 *)a.x + row * hv, t, g, hv, xv);
+        load_row<V>((const uint4 *)a.residual + row * hv, t, g, hv, rv);
+        gated_row<T, V, kTeam, kAhead>(a, row, hv, t, g, xv, rv, red, slot);
     }
 }
 
@@ -213,22 +229,33 @@ const void *pick(int64_t hv, bool few, int *block, int *rows) {
         *block = 512;
         return hv ? (const void *)gated_wide_kernel<T, true> : (const void *)gated_wide_kernel<T, false>;
     }
-    if (hv <= 128 && !few) {  // a warp a row
+    // Rows that fill no GPU: latency counts, so a vector a thread where that fits, and everything asked for at once.
+    if (few) {
+        const int v = hv <= 512 ? 1 : hv <= 1024 ? 2 : hv <= 2048 ? 4 : 8;
+        *block = (int)((hv + v - 1) / v + 31) / 32 * 32;
+        return v == 1   ? (const void *)gated_rows_kernel<T, 1, 0, true>
+               : v == 2 ? (const void *)gated_rows_kernel<T, 2, 0, true>
+               : v == 4 ? (const void *)gated_rows_kernel<T, 4, 0, true>
+                        : (const void *)gated_rows_kernel<T, 8, 0, false>;
+    }
+    // Many rows: a warp's sums wait for no other warp, and from four vectors a thread on enough bytes are on their way.
+    // (Measured, bf16 with both norms and a gate, 192 MB a tensor, GB/s by vectors a thread, w: a warp a row:
+    //  32 vectors a row w1 5352, w2 4615, 1 4762; 64 w2 6512, 2 6208, w4 5457; 128 2 6049, 4 5821, w4 5986;
+    //  192 2 5892, 4 6070; 448 2 5487, 4 6343; 1024 2 5200, 4 6238, 8 6186; 2048 4 6248, 8 6020.)
+    if (hv <= 64) {
         *block = 256;
         *rows = 8;
-        return hv <= 32   ? (const void *)gated_rows_kernel<T, 1, 32>
-               : hv <= 64 ? (const void *)gated_rows_kernel<T, 2, 32>
-                          : (const void *)gated_rows_kernel<T, 4, 32>;
+        return hv <= 32 ? (const void *)gated_rows_kernel<T, 1, 32, false> : (const void *)gated_rows_kernel<T, 2, 32, false>;
     }
-    const int v = hv <= (few ? 512 : 256) ? 1 : hv <= 1024 ? 2 : hv <= 2048 ? 4 : 8;
+    const int v = hv <= 160 ? 2 : hv <= 2048 ? 4 : 8;
     *block = (int)((hv + v - 1) / v + 31) / 32 * 32;
-    return v == 1   ? (const void *)gated_rows_kernel<T, 1, 0>
-           : v == 2 ? (const void *)gated_rows_kernel<T, 2, 0>
-           : v == 4 ? (const void *)gated_rows_kernel<T, 4, 0>
-                    : (const void *)gated_rows_kernel<T, 8, 0>;
+    return v == 2   ? (const void *)gated_rows_kernel<T, 2, 0, false>
+           : v == 4 ? (const void *)gated_rows_kernel<T, 4, 0, false>
+                    : (const void *)gated_rows_kernel<T, 8, 0, false>;
 }
 
 }  // namespace
+
 }  // namespace ks
 
 using namespace ks;
@@ -279,8 +306,8 @@ extern "C" ks_status_t ks_gated_add_rms_norm(const ks_gated_norm_args_t *args, k
     const void *f = a.dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(k_args.hv, few, &block, &at_once)
                     : a.dtype == KS_DTYPE_F16 ? pick<__half>(k_args.hv, few, &block, &at_once)
                                               : pick<float>(k_args.hv, few, &block, &at_once);
-    const int64_t most = (int64_t)sms * (2048 / block > 32 ? 32 : 2048 / block), want = (a.rows + at_once - 1) / at_once;
-    const int64_t grid = want < most ? want : most;
+    const int64_t most = (int64_t)sms * (2048 / block > 32 ? 32 : 2048 / block);
+    const int64_t want = (a.rows + at_once - 1) / at_once, grid = want < most ? want : most;
     void *kp[] = {&k_args};
     const cudaError_t ce = launch_kernel(f, dim3((unsigned)grid), dim3((unsigned)block), 0, kp, static_cast<cudaStream_t>(stream),
                                          launch_pdl_enabled());

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_4bit_kernel(const __grid_c
 }
 
 // Many tokens: the queries are ks_rotary's kernel, the groups this one, for kv_tokens tokens a CTA. (Both in one kernel
-// have its registers in common: measured at 8192 tokens of 56 + 8 + 8 heads, 88 us and more for 43 and KSX.) It is
+// have its registers in common: measured at 8192 tokens of 56 + 8 + 8 heads, 88 us and more for 42 and 29.) It is
 // launched to start while the queries' last CTAs run: those began after all earlier work was done, and of their own
 // they write nothing that is read here. It ends after them.
 template <typename T, bool kHalf, bool kVec>
