@@ -19,9 +19,8 @@ from __future__ import annotations
 import torch
 
 from . import _abi
-from .decode import (_BIG, _I32, _I64, _check_attention_rows, _first, _grad, _index, _inference, _launch, _rows,
-                     _turned, _turns)
-from .ops import _DTYPES
+from .decode import (_I32, _I64, _check_attention_rows, _first, _index, _inference, _rows, _turned, _turns)
+from .ops import _BIG, _DTYPES, _grad, _launch
 
 _U8, _F8 = torch.uint8, torch.float8_e4m3fn
 _LEAST, _MOST = 2.0 ** -64, 2.0 ** 64
@@ -159,11 +158,7 @@ def rotary_to_pages_4bit(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tenso
     return out
 
 
-def pages_4bit_to_rows(k_pages, v_pages, slots: torch.Tensor, *, k_scale: float = 1.0, v_scale: float = 1.0,
-                       dtype: torch.dtype = torch.bfloat16, out: tuple | None = None) -> tuple:
-    """What 4-bit pools hold in some slots: (k, v), each [tokens, kv_heads, head_dim] of `dtype`, rounded once (with
-    a factor that is a power of two 16-bit types hold the values exactly, within their range). A negative slot gives
-    zeros; slots may repeat. `out`: (k, v), tensors to write to that share nothing with each other, the pools or slots."""
+def _check_to_rows(k_pages, v_pages, slots, k_scale, v_scale, dtype):
     if not isinstance(k_pages, (tuple, list)) or len(k_pages) != 2 or not isinstance(k_pages[0], torch.Tensor):
         raise TypeError("k_pages must be a pair (codes, scales); empty_pages_4bit makes one")
     codes = k_pages[0]
@@ -179,6 +174,28 @@ def pages_4bit_to_rows(k_pages, v_pages, slots: torch.Tensor, *, k_scale: float 
         raise TypeError("slots must be a 1-D int64 tensor")
     tokens = slots.shape[0]
     _index(slots, "slots", _I64, dev, (tokens,))
+    return codes, dev, hk, dim, tokens
+
+
+def pages_4bit_to_rows(k_pages, v_pages, slots: torch.Tensor, *, k_scale: float = 1.0, v_scale: float = 1.0,
+                       dtype: torch.dtype = torch.bfloat16, out: tuple | None = None) -> tuple:
+    """What 4-bit pools hold in some slots: (k, v), each [tokens, kv_heads, head_dim] of `dtype`, rounded once (with
+    a factor that is a power of two 16-bit types hold the values exactly, within their range). A negative slot gives
+    zeros; slots may repeat. `out`: (k, v), tensors to write to that share nothing with each other, the pools or slots."""
+    try:
+        codes = k_pages[0]
+        pages, page_size, hk, half = codes.shape
+        dim, dev = 2 * half, codes.device
+        tokens, = slots.shape
+        fine = (codes.is_cuda and hk > 0 and page_size > 0 and half > 0 and half % 8 == 0 and len(k_pages) == 2
+                and len(v_pages) == 2 and _fine(k_pages, (pages, page_size), hk, dim, dev)
+                and _fine(v_pages, (pages, page_size), hk, dim, dev) and dtype in _DTYPES and slots.dtype is _I64
+                and slots.device == dev and slots.is_contiguous()
+                and _LEAST <= k_scale <= _MOST and _LEAST <= v_scale <= _MOST)
+    except (AttributeError, KeyError, ValueError, TypeError, IndexError):
+        fine = False
+    if not fine:
+        codes, dev, hk, dim, tokens = _check_to_rows(k_pages, v_pages, slots, k_scale, v_scale, dtype)
     if out is None:
         k = torch.empty((tokens, hk, dim), dtype=dtype, device=dev)
         v = torch.empty((tokens, hk, dim), dtype=dtype, device=dev)

@@ -24,7 +24,7 @@ import math
 import torch
 
 from . import _abi
-from .ops import _DTYPES
+from .ops import _BIG, _DTYPES, _grad, _launch
 
 
 def rotary_steps(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None,
@@ -75,22 +75,7 @@ def rotary_steps(rotary_dim: int, base: float = 10000.0, *, scaling: str | None 
 # each first asks everything in one expression, and goes through the checks one by one, which name what
 # is wrong, only if that fails; the stream comes as its handle; the device is only changed where it is
 # not the current one.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # torch without CUDA has none, nor CUDA tensors
-_current_device = torch.cuda.current_device
-_grad = torch.is_grad_enabled
 _I32, _I64 = torch.int32, torch.int64
-_BIG = 2.0 ** 127  # what a scale may be: finite in 32 bits, times log2(e) too
-
-
-def _launch(call, args: bytes, device: torch.device) -> None:
-    index = device.index
-    if _current_device() == index:
-        status = call(args, _raw_stream(index))
-    else:
-        with torch.cuda.device(device):
-            status = call(args, _raw_stream(index))
-    if status:
-        _abi.check(status)
 
 
 def _rows(t, name, dtype, device):

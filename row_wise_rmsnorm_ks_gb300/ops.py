@@ -28,6 +28,21 @@ from . import _abi
 
 _DTYPES = {torch.float32: _abi.KS_DTYPE_F32, torch.float16: _abi.KS_DTYPE_F16,
            torch.bfloat16: _abi.KS_DTYPE_BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # torch without CUDA has none, nor CUDA tensors
+_current_device = torch.cuda.current_device
+_grad = torch.is_grad_enabled
+_BIG = 2.0 ** 127  # what a scale may be: finite in 32 bits, times log2(e) too
+
+
+def _launch(call, args: bytes, device: torch.device) -> None:
+    index = device.index
+    if _current_device() == index:
+        status = call(args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = call(args, _raw_stream(index))
+    if status:
+        _abi.check(status)
 
 
 def _check(x: torch.Tensor, weight: torch.Tensor, eps: float, names=("x", "weight")):
@@ -95,6 +110,9 @@ def fused_add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Te
 
 def _gate_rows(gate: torch.Tensor, x: torch.Tensor):
     """(rows that share a row of the gate, its row stride, its column stride)."""
+    if gate.__class__ is torch.Tensor and gate.shape == x.shape[-1:] and gate.dtype is x.dtype \
+            and gate.device == x.device and gate.is_contiguous() and not gate.requires_grad:
+        return x.numel() // x.shape[-1], 0, 1  # one for all rows
     if not isinstance(gate, torch.Tensor) or gate.dtype != x.dtype:
         raise TypeError(f"gate must be a tensor of {x.dtype}")
     if gate.device != x.device or not gate.is_contiguous():
@@ -125,6 +143,38 @@ def gated_add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Te
     dimensions up to some point and ones behind it for one per sequence or token ((B, 1, hidden) for an x of
     (B, S, hidden)); a last dimension of 1 is one value for a row. weight and post_weight are (hidden,); all
     tensors have x's dtype. Returns None."""
+    try:  # what a call mostly is, in one go; anything else is looked at point by point
+        dt, dev, shape, code = x.dtype, x.device, x.shape, _DTYPES[x.dtype]
+        row = shape[-1:]
+        fine = (x.is_cuda and row[0] > 0 and residual.shape == shape and weight.shape == row and residual.dtype is dt
+                and weight.dtype is dt and residual.device == dev and weight.device == dev and x.is_contiguous()
+                and residual.is_contiguous() and weight.is_contiguous() and 0.0 < eps < math.inf
+                and (post_weight is None or (post_weight.shape == row and post_weight.dtype is dt
+                                             and post_weight.device == dev and post_weight.is_contiguous()
+                                             and not post_weight.requires_grad))
+                and eps.__class__ is residual_scale.__class__ is block_scale.__class__ is float
+                and -_BIG < residual_scale < _BIG and -_BIG < block_scale < _BIG
+                and not (x.requires_grad or residual.requires_grad or weight.requires_grad))
+    except (AttributeError, KeyError, ValueError, TypeError, IndexError):
+        fine = False
+    if not fine:
+        _check_gated(x, residual, weight, post_weight, residual_scale, block_scale, eps)
+        dt, dev, shape, code = x.dtype, x.device, x.shape, _DTYPES[x.dtype]
+    gate_p, per_gate, row_stride, column_stride = 0, 1, 0, 0
+    if gate is not None:
+        per_gate, row_stride, column_stride = _gate_rows(gate, x)
+        gate_p = gate.data_ptr()
+    hidden = shape[-1]
+    rows = x.numel() // hidden
+    if rows == 0:
+        return None
+    _launch(_abi.ks_gated_add_rms_norm, _abi.GATED_NORM_ARGS.pack(
+        x.data_ptr(), residual.data_ptr(), weight.data_ptr(), post_weight.data_ptr() if post_weight is not None else 0,
+        gate_p, rows, hidden, per_gate, row_stride, column_stride, eps, residual_scale, block_scale, code), dev)
+    return None
+
+
+def _check_gated(x, residual, weight, post_weight, residual_scale, block_scale, eps):
     _check(x, weight, eps)
     if not isinstance(residual, torch.Tensor) or residual.shape != x.shape:
         raise ValueError("residual must have the same shape as x")
@@ -135,23 +185,8 @@ def gated_add_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Te
     if torch.is_grad_enabled() and residual.requires_grad:
         raise RuntimeError("these kernels are inference-only: inputs must not require grad")
     for v, n in ((residual_scale, "residual_scale"), (block_scale, "block_scale")):
-        if not (isinstance(v, (int, float)) and abs(v) < 2.0 ** 127):
+        if not (isinstance(v, (int, float)) and abs(v) < _BIG):
             raise ValueError(f"{n} must be finite (below 2^127)")
-    gate_p, per_gate, row_stride, column_stride = 0, 1, 0, 0
-    if gate is not None:
-        per_gate, row_stride, column_stride = _gate_rows(gate, x)
-        gate_p = gate.data_ptr()
-    hidden = x.shape[-1]
-    rows = x.numel() // hidden
-    if rows == 0:
-        return None
-    args = _abi.GATED_NORM_ARGS.pack(
-        x.data_ptr(), residual.data_ptr(), weight.data_ptr(), post_weight.data_ptr() if post_weight is not None else 0,
-        gate_p, rows, hidden, per_gate, row_stride, column_stride, float(eps), residual_scale, block_scale,
-        _DTYPES[x.dtype])
-    with torch.cuda.device(x.device):
-        _abi.check(_abi.ks_gated_add_rms_norm(args, _stream(x.device)))
-    return None
 
 
 def _check_host(x: torch.Tensor, weight: torch.Tensor, workspace: torch.Tensor, eps: float):
