@@ -26,6 +26,16 @@ cudaError_t attn4_tc_launch(const Attn4Args &args, uintptr_t code_align, uintptr
     pages.whole = (dim == 64 || dim == 128) && (code_align & 15) == 0 && (scale_align & (dim / 16 - 1)) == 0 && args.alike;
     pages.page_units = args.page_units;
     pages.slot_units = args.slot_units;
+    pages.by_map = 0;
+    if (pages.whole && s.a.page_size % 8 == 0 && (kKeys % s.a.page_size == 0 || s.a.page_size % kKeys == 0)) {
+        // the maps' strides are below 2^40 bytes and not zero
+        const int64_t strides[3] = {args.k.code_page, args.k.code_slot, args.k.code_head}, counts[3] = {s.a.pages, s.a.page_size, s.a.kv_heads};
+        pages.by_map = 1;
+        for (int i = 0; i < 3; ++i)
+            if (counts[i] > 1 && (strides[i] <= 0 || strides[i] >= (1ll << 39))) pages.by_map = 0;
+    }
+    if (pages.by_map && (!attn_codes_map(&pages.k_map, s, args.k) || !attn_codes_map(&pages.v_map, s, args.v)))
+        return cudaErrorInvalidValue;
     const bool bf16 = s.a.dtype == KS_DTYPE_BF16;
     const void *f = dim <= 64 ? (bf16 ? (const void *)attn_tc_kernel<__nv_bfloat16, 64, Pages4>
                                       : (const void *)attn_tc_kernel<__half, 64, Pages4>)

@@ -14,6 +14,8 @@ namespace ks {
 
 // The queries as columns, heads, tokens; boxes of 64 columns, a row tile's heads and its tokens.
 bool attn_query_map(CUtensorMap *map, const AttnArgs &s);
+// A pool's codes as bytes of a row, slots, heads, pages; boxes of a head's rows that lie together.
+bool attn_codes_map(CUtensorMap *map, const AttnArgs &s, const Pool4 &pool);
 
 namespace {
 
@@ -46,6 +48,9 @@ struct Pages4 {
     // place has 32 bits of 16-byte units: the strides of pages and slots in those.
     int32_t whole;
     uint32_t page_units, slot_units;
+    // A step's keys are whole pages or part of one: the copying warp brings their codes, by these maps.
+    int32_t by_map;
+    CUtensorMap k_map, v_map;
 };
 constexpr int kHalfBytes = kKeys * 128;  // 128 rows of 64 values
 constexpr int kTileCost = 3;       // steps that beginning and ending a row tile costs
@@ -60,13 +65,16 @@ struct Tc {
     static constexpr int kHalves = kDim / 64;
     static constexpr int kTileBytes = kHalves * kHalfBytes;  // a tile of Q, K or V
     static constexpr int kStages = kDim == 128 ? (k4 ? 4 : 5) : (k4 ? 8 : 10);
-    static constexpr int kBars = (k4 ? 2 : 3) * kStages + 14;
+    static constexpr int kBars = (k4 ? 2 : 3) * kStages + 14 + (k4 ? 2 * 3 : 0);
     // 4-bit pages: each converting warp's ring of rows as the pools hold them, codes and scales; rows 16 bytes apart from a
     // multiple of 32, so that eight lanes read 16 bytes of theirs without a conflict.
     static constexpr int kRawStages = 3, kRawRow = kDim / 2 + 16;
-    static constexpr int kRawAt = (2 + kStages) * kTileBytes + (kBars * 8 + 16 + 15) / 16 * 16;
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + (kBars * 8 + 16) +
-                                 (k4 ? 16 + kConvertWarps * kRawStages * 32 * kRawRow : 0);
+    // In one ring for all of them, what the copies by map bring: rows end to end, 16-byte pieces swizzled.
+    static constexpr int kRawAt = (2 + kStages) * kTileBytes + (kBars * 8 + 16 + 511) / 512 * 512;
+    static constexpr int kRawTile = kKeys * kDim / 2;
+    static_assert(kRawTile <= kConvertWarps * 32 * kRawRow, "both rings lie in the same place");
+    static constexpr int kSmem = 1024 + (k4 ? kRawAt + kConvertWarps * kRawStages * 32 * kRawRow
+                                            : (2 + kStages) * kTileBytes + (kBars * 8 + 16));
     static constexpr uint32_t kO = 256;  // tensor-memory columns: S0 0, S1 128, then the O tiles
 };
 
@@ -335,7 +343,99 @@ __device__ __forceinline__ void make_queries(uint8_t *q_tile, int first, float (
     unit[1] = __shfl_sync(0xFFFFFFFFu, mine, lane / 4 + 8);
 }
 
-// The converting warps: a thread per key of a step, a warp for 32 of them. A warp copies its keys' codes and scales to a
+// A row of 4-bit values made fp16 in the layout that the matrix instructions read: `piece` gives 16 bytes of codes.
+template <int kDim, typename Piece>
+__device__ __forceinline__ void convert_row(uint8_t *tile, int row, const uint32_t (&scales)[kDim / 64], Piece piece) {
+#pragma unroll
+    for (int i = 0; i < kDim / 32; ++i) {  // two groups
+        const uint4 x = piece(i);
+        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = 4 * i + k, g = c / 2;
+            const uint32_t scale = e4m3_to_half(__byte_perm(scales[g / 4], 0, (g % 4) | (g % 4) << 4));
+            uint32_t h[4];
+            fp4_to_half(words[k], h);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) h[n] = half2_mul(h[n], scale);
+            *reinterpret_cast<uint4 *>(tile + row * 128 + c / 8 * kHalfBytes + ((c % 8 ^ (row & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+}
+
+// The converting warps where the copying warp brings the codes: a thread per key of a step, which reads the row's scales a
+// step ahead. Rows behind the last key that the row tile sees get scales of 0, whatever lies in their place.
+template <int kDim>
+__device__ __forceinline__ void convert_copied(const AttnArgs &s, const Pages4 &pages, Place &place, bool more, uint8_t *ring,
+                                               const uint8_t *raw, uint64_t *full, uint64_t *empty, uint64_t *raw_full,
+                                               uint64_t *raw_empty, volatile uint32_t *gave_up) {
+    using C = Tc<kDim, true>;
+    constexpr int kWords = kDim / 64;
+    const ks_attention_args_t &a = s.a;
+    const int lane = threadIdx.x % 32, row = (threadIdx.x / 32 - kConvert) * 32 + lane;
+    const int page_size = (int)a.page_size;
+    uint32_t at = 0;  // tiles made so far: K and V of each step in turn
+    RingAt<C::kRawStages> from;
+    while (more) {
+        const AttnSpan span = attn_span(s, place.cur, place.q);
+        const int head = place.cur.head / s.head_splits, sees = attn_tile_keys(s, place.q, place.cur.row_tile);
+        const int32_t *table = a.page_table + (int64_t)place.cur.seq * a.table_stride;
+        const uint8_t *k_scales = pages.k.scales + head * pages.k.scale_head, *v_scales = pages.v.scales + head * pages.v.scale_head;
+        uint32_t next[2][kWords];
+        auto read_scales = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) next[0][i] = next[1][i] = 0;
+            const int key = j * kKeys + row;
+            if (j >= span.last || key >= sees) return;
+            const int index = key / page_size;
+            const uint32_t page = (uint32_t)__ldg(table + index);
+            if (page >= (uint64_t)a.pages) return;  // the copying warp reports it
+            const uint64_t e = (uint64_t)(page * pages.page_units + (uint32_t)(key - index * page_size) * pages.slot_units) * 2;
+            if constexpr (kWords == 2) {
+                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(k_scales + e)), y = __ldg(reinterpret_cast<const uint2 *>(v_scales + e));
+                next[0][0] = x.x;
+                next[0][1] = x.y;
+                next[1][0] = y.x;
+                next[1][1] = y.y;
+            } else {
+                next[0][0] = __ldg(reinterpret_cast<const uint32_t *>(k_scales + e));
+                next[1][0] = __ldg(reinterpret_cast<const uint32_t *>(v_scales + e));
+            }
+        };
+        read_scales(span.first);
+        bool ok = true;
+        for (int j = span.first; j < span.last && ok; ++j) {
+            uint32_t scales[2][kWords];
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) scales[v][i] = next[v][i];
+            read_scales(j + 1);
+#pragma unroll
+            for (int v = 0; v < 2; ++v, ++at) {
+                const uint32_t stage = at % C::kStages;
+                ok = ok && bar_wait_warp(empty + stage, (at / C::kStages & 1) ^ 1, gave_up) &&
+                     bar_wait_warp(raw_full + from.stage, from.phase, gave_up);
+                if (!ok) break;
+                const uint8_t *codes = raw + from.stage * C::kRawTile + row * (kDim / 2);
+                const int turn = kDim == 128 ? row >> 1 & 3 : row >> 2 & 1;
+                convert_row<kDim>(ring + stage * C::kTileBytes, row, scales[v],
+                                  [&](int i) { return *reinterpret_cast<const uint4 *>(codes + ((i ^ turn) << 4)); });
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(full + stage);
+                    bar_arrive(raw_empty + from.stage);
+                }
+                from.next();
+            }
+        }
+        more = ok && next_tile(s, place, span.cost);
+    }
+}
+
+// The converting warps where they copy for themselves: a thread per key of a step, a warp for 32 of them. A warp copies its keys' codes and scales to a
 // ring of its own, two tiles ahead, neighbouring lanes neighbouring bytes (with loads to registers, a key a thread, the
 // long prompt takes 1.3 times as long); a thread then makes its row fp16 in the layout that the matrix instructions read.
 // Rows behind the last key that the row tile sees are zeros.
@@ -431,23 +531,8 @@ __device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &p
 #pragma unroll
                     for (int i = 0; i < kGroups / 4; ++i) scales[i] = reinterpret_cast<const uint32_t *>(from + kDim / 2)[i];
                 }
-                uint8_t *tile = ring + stage * C::kTileBytes + row * 128;
-#pragma unroll
-                for (int i = 0; i < kGroups / 2; ++i) {  // two groups
-                    const uint4 x = *reinterpret_cast<const uint4 *>(from + i * 16);
-                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = 4 * i + k, g = c / 2;
-                        const uint32_t scale = e4m3_to_half(__byte_perm(scales[g / 4], 0, (g % 4) | (g % 4) << 4));
-                        uint32_t h[4];
-                        fp4_to_half(words[k], h);
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) h[n] = half2_mul(h[n], scale);
-                        *reinterpret_cast<uint4 *>(tile + c / 8 * kHalfBytes + ((c % 8 ^ (row & 7)) << 4)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
-                    }
-                }
+                convert_row<kDim>(ring + stage * C::kTileBytes, row, scales,
+                                  [&](int i) { return *reinterpret_cast<const uint4 *>(from + i * 16); });
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) bar_arrive(full + stage);
@@ -479,6 +564,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     uint64_t *q_full = empty + C::kStages, *q_free = q_full + 1, *s_full = q_full + 2, *p_full = s_full + 2;
     uint64_t *o_full = p_full + 2;
     uint64_t *turn = o_full + 2, *done = turn + 2, *q_made = done + 2, *tail = q_made + 2;
+    uint64_t *raw_full = tail, *raw_empty = tail + C::kRawStages;  // in place of the tails'
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile uint32_t *gave_up = tmem_at + 1;
     const int warp = warp_uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
@@ -489,6 +575,9 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         if constexpr (!k4) {
             prefetch_map(&pages.k);
             prefetch_map(&pages.v);
+        } else if (pages.by_map) {
+            prefetch_map(&pages.k_map);
+            prefetch_map(&pages.v_map);
         }
     }
     if (threadIdx.x == 0) {
@@ -496,6 +585,12 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
             mbar_init(full + i, k4 ? kConvertWarps : 1);
             mbar_init(empty + i, k4 ? 2 : 3);  // the issuing warps and the one that clears tails
             if (!k4) mbar_init(tail + i, 1);
+        }
+        if (k4) {
+            for (int i = 0; i < C::kRawStages; ++i) {
+                mbar_init(raw_full + i, 1);
+                mbar_init(raw_empty + i, kConvertWarps);
+            }
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(s_full + w, 1);
@@ -539,14 +634,21 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
     if (k4 && warp >= kConvert) {
         if constexpr (k4) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<k4>::kConvertRegs));
-            convert_pages<kDim>(s, pages, place, more, smem + 2 * C::kTileBytes, smem + C::kRawAt, full, empty, gave_up);
+            uint8_t *tiles = smem + 2 * C::kTileBytes, *rows = smem + C::kRawAt;
+            if (pages.by_map) convert_copied<kDim>(s, pages, place, more, tiles, rows, full, empty, raw_full, raw_empty, gave_up);
+            else convert_pages<kDim>(s, pages, place, more, tiles, rows, full, empty, gave_up);
         }
     } else if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<k4>::kOtherRegs));
         if (warp == kCopy) {
             // ---- copies
-            const int page_size = (int)a.page_size, in_tile = min(page_size, kKeys);  // keys of a copy
-            const int part = lane / C::kHalves, half = lane % C::kHalves;
+            // A copy's keys; with 4-bit pages, tiles go to the ring of codes, and a lane's copy has whole rows.
+            constexpr int kParts = k4 ? 1 : C::kHalves, kTo = k4 ? C::kRawStages : C::kStages;
+            constexpr int kToTile = k4 ? C::kRawTile : C::kTileBytes, kRowBytes = k4 ? kDim / 2 : 128;
+            uint64_t *to_full = k4 ? raw_full : full, *to_empty = k4 ? raw_empty : empty;
+            const uint32_t to = k4 ? base + C::kRawAt : ring;
+            const int page_size = (int)a.page_size, in_tile = min(page_size, kKeys);
+            const int part = lane / kParts, half = lane % kParts;
             uint32_t at = 0;  // tiles copied so far: K and V of each step in turn
             uint32_t queries = 0;
             // A row tile's queries, as soon as the tile before has had its last product with its own: a
@@ -573,12 +675,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 // and values, which need not wait.
                 const uint32_t tile = queries;
                 if (tile == 0 && span.first < span.last) ok = copy_queries(head);
-                if constexpr (k4) {  // the pages are the converting warps' work
-                    if (tile > 0 && span.first < span.last) ok = copy_queries(head);
-                    more = ok && next_tile(s, place, span.cost);
-                    continue;
-                } else {
-                for (int j = span.first; j < span.last && ok; ++j) {
+                int last = span.last;
+                if constexpr (k4) {
+                    if (!pages.by_map) {  // the pages are the converting warps' work
+                        if (tile > 0 && span.first < span.last) ok = copy_queries(head);
+                        last = span.first;
+                    }
+                }
+                for (int j = span.first; j < last && ok; ++j) {
                     const int key = j * kKeys + part * in_tile;
                     const bool wanted = part * in_tile < kKeys && key < keys;
                     int page = 0, slot = 0;
@@ -590,26 +694,28 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                             page = (int)a.pages;
                         }
                     }
-                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, wanted)) * in_tile * 128;
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, wanted)) * in_tile * kRowBytes;
                     for (int v = 0; v < 2 && ok; ++v, ++at) {
-                        const uint32_t stage = at % C::kStages;
-                        ok = bar_wait_warp(empty + stage, (at / C::kStages & 1) ^ 1, gave_up);
+                        const uint32_t stage = at % kTo;
+                        ok = bar_wait_warp(to_empty + stage, (at / kTo & 1) ^ 1, gave_up);
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(full + stage, bytes);
+                        if (lane == 0) mbar_arrive_expect_tx(to_full + stage, bytes);
                         __syncwarp();
+                        const CUtensorMap *map;
+                        if constexpr (k4) map = v ? &pages.v_map : &pages.k_map;
+                        else map = v ? &pages.v : &pages.k;
                         if (wanted)
-                            tma_load(ring + stage * C::kTileBytes + half * kHalfBytes + part * in_tile * 128,
-                                     v ? &pages.v : &pages.k, half * 64, slot, head, page, smem_addr(full + stage));
+                            tma_load(to + stage * kToTile + half * kHalfBytes + part * in_tile * kRowBytes, map, half * 64, slot,
+                                     head, page, smem_addr(to_full + stage));
                     }
                     if (tile > 0 && j == span.first) ok = ok && copy_queries(head);
                 }
                 more = ok && next_tile(s, place, span.cost);
-                }
             }
             if (queries) (void)mbar_wait_bounded(q_full, (queries - 1) & 1);
             // nothing of this CTA's is in flight when it ends, also after a wait that gave up
-            const uint32_t from = at > (uint32_t)C::kStages ? at - C::kStages : 0;
-            for (uint32_t i = from; i < at; ++i) (void)mbar_wait_bounded(full + i % C::kStages, i / C::kStages & 1);
+            const uint32_t from = at > (uint32_t)kTo ? at - kTo : 0;
+            for (uint32_t i = from; i < at; ++i) (void)mbar_wait_bounded(to_full + i % kTo, i / kTo & 1);
         } else if (warp == kMma || warp == kMma + 2) {
             // ---- matrix instructions of tile w, issued by one thread: for each step P V, then Q K of the
             // next step. The two warps take turns, a whole batch each: the other tile's softmax runs beside
