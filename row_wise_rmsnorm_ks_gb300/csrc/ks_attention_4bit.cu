@@ -806,7 +806,7 @@ ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, int pool, Attn4P
     p->args.slot_units = (uint32_t)(a.k_pages.code_slot_stride / 16);
     if (tiles == kTc) {
         p->kernel = nullptr;
-        attn_shape(&s, attn_tc_rows(), attn_tc_unit(), attn_tc_tile_cost());
+        attn_shape(&s, attn_tc_rows(), attn_tc_unit(), attn4_tc_tile_cost());
         p->ctas = attn_ctas(s, sms);
         return KS_SUCCESS;
     }

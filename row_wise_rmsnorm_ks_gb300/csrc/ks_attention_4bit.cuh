@@ -14,8 +14,10 @@ struct Attn4Args {
     uint32_t page_units, slot_units;  // strides of the codes' pages and slots, in 16 bytes
 };
 
-// The tensor-core kernel (ks_attention_4bit_tc.cu): whether it takes a call, and its launch.
+// The tensor-core kernel (ks_attention_4bit_tc.cu): whether it takes a call, the steps that a row tile costs beyond its
+// own, and its launch.
 bool attn4_tc_fits(const ks_attention_args_t &a);
+int attn4_tc_tile_cost();
 cudaError_t attn4_tc_launch(const Attn4Args &args, uintptr_t code_align, uintptr_t scale_align, int ctas, cudaStream_t stream,
                             bool pdl);
 

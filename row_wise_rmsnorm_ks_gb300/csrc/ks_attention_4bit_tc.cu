@@ -14,6 +14,10 @@ bool attn4_tc_fits(const ks_attention_args_t &a) {
     return true;
 }
 
+// (Measured, 16 sequences of 1..517 tokens over 392..4439 keys: 212 us with 2, 188 with 3, 177 with 5, 184 with 8; the long
+// prompt's time does not change.)
+int attn4_tc_tile_cost() { return 5; }
+
 cudaError_t attn4_tc_launch(const Attn4Args &args, uintptr_t code_align, uintptr_t scale_align, int ctas, cudaStream_t stream,
                             bool pdl) {
     AttnArgs s = args.s;
