@@ -561,8 +561,9 @@ ks_status_t ks_pages_4bit_to_rows(const ks_pages_4bit_rows_args_t *args, ks_stre
  * ks_paged_attention over 4-bit pools. args->attention is read as there, except for k_pages and v_pages and their
  * strides. Keys and values enter the products exactly as they are held. bfloat16 queries enter as fp16 after a
  * row's largest magnitude is brought to 1 .. 2 by a power of two (values 2^-14 times as large and smaller lose
- * at most 2^-25 of it), and probabilities as fp16 for either type. head_dim: a multiple of 16, at most 256. The
- * workspace is that of ks_paged_attention_4bit_workspace.
+ * at most 2^-25 of it), and probabilities as fp16 for either type (those below 2^-22 of a row's largest to multiples
+ * of 2^-32 of it). head_dim: a multiple of 16, at most 256. The workspace is that of
+ * ks_paged_attention_4bit_workspace.
  */
 typedef struct ks_attention_4bit_args {
     ks_attention_args_t attention;

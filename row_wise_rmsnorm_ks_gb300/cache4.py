@@ -125,7 +125,8 @@ def rotary_to_pages_4bit(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tenso
                 and q.device == dev and v.device == dev and len(k_pages) == 2 and len(v_pages) == 2
                 and _fine(k_pages, shape, hk, dim, dev) and _fine(v_pages, shape, hk, dim, dev)
                 and slots.dtype is _I64 and slots.device == dev and slots.shape == (tokens,) and slots.is_contiguous()
-                and -_BIG < scale < _BIG and _LEAST <= k_scale <= _MOST and _LEAST <= v_scale <= _MOST
+                and -_BIG < scale < _BIG and k_scale.__class__ is v_scale.__class__ is float
+                and _LEAST <= k_scale <= _MOST and _LEAST <= v_scale <= _MOST
                 and _turned(positions, steps, tokens, dim, dev)
                 and not (_grad() and (q.requires_grad or k.requires_grad or v.requires_grad)))
         if fine:
@@ -191,7 +192,8 @@ def pages_4bit_to_rows(k_pages, v_pages, slots: torch.Tensor, *, k_scale: float 
                 and len(v_pages) == 2 and _fine(k_pages, (pages, page_size), hk, dim, dev)
                 and _fine(v_pages, (pages, page_size), hk, dim, dev) and dtype in _DTYPES and slots.dtype is _I64
                 and slots.device == dev and slots.is_contiguous()
-                and _LEAST <= k_scale <= _MOST and _LEAST <= v_scale <= _MOST)
+                and k_scale.__class__ is v_scale.__class__ is float and _LEAST <= k_scale <= _MOST
+                and _LEAST <= v_scale <= _MOST)
     except (AttributeError, KeyError, ValueError, TypeError, IndexError):
         fine = False
     if not fine:
@@ -286,7 +288,8 @@ def paged_attention_4bit(q: torch.Tensor, k_pages, v_pages, page_table: torch.Te
                 and kv_lens.dtype is _I32 and q_starts.dtype is _I32 and page_table.device == dev
                 and kv_lens.device == dev and q_starts.device == dev and kv_lens.shape == (seqs,)
                 and q_starts.shape == (seqs + 1,) and kv_lens.is_contiguous() and q_starts.is_contiguous()
-                and (scale is None or -_BIG < scale < _BIG) and _LEAST <= k_scale <= _MOST and _LEAST <= v_scale <= _MOST
+                and (scale is None or -_BIG < scale < _BIG) and k_scale.__class__ is v_scale.__class__ is float
+                and _LEAST <= k_scale <= _MOST and _LEAST <= v_scale <= _MOST
                 and (max_q_len is None or 0 <= max_q_len < 2 ** 31) and not (_grad() and q.requires_grad))
     except (AttributeError, KeyError, ValueError, TypeError, IndexError):
         fine = False

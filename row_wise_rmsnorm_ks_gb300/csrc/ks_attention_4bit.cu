@@ -254,10 +254,11 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
         // many steps ahead: on its way through the steps a copy's address is then one multiplication.
         constexpr uint32_t kNone = 0xFFFFFFFFu;
         auto find = [&](int batch) {
-            const int key = first * kUnit + warp * kStep + (batch * 16 + lane / 2) * kUnit + lane % 2 * 16;
-            if (key >= end) return kNone;
-            const int index = (int)args.page_blocks.quotient((uint32_t)key >> 4);
-            const int page = __ldg(table + index), slot = key - index * page_size;
+            // (no sign: it looks some thousands of keys past the last, which may be the largest int but 1024)
+            const uint32_t key = (uint32_t)first * kUnit + warp * kStep + (batch * 16 + lane / 2) * kUnit + lane % 2 * 16;
+            if (key >= (uint32_t)end) return kNone;
+            const uint32_t index = args.page_blocks.quotient(key >> 4);
+            const int page = __ldg(table + index), slot = (int)(key - index * page_size);
             if ((uint32_t)page >= (uint64_t)a.pages) {
                 atomicOr(&g_fault_flags, kFaultBadIndex);
                 return kNone;

@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_4bit_kernel(const __grid_c
 // Many tokens: the queries are ks_rotary's kernel, the groups this one, for kv_tokens tokens a CTA. (Both in one kernel
 // have its registers in common: measured at 8192 tokens of 56 + 8 + 8 heads, 88 us and more for 42 and 29.) It is
 // launched to start while the queries' last CTAs run: those began after all earlier work was done, and of their own
-// they write nothing that is read here. It ends after them.
+// they write nothing that is read here. It ends after them. (`alone`: without queries, or where the queries' kernel may
+// itself start before earlier work's end, it waits at its beginning.)
 template <typename T, bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kRotThreads, 3) pages4_kernel(const __grid_constant__ Rotary4Args args, int alone) {
     __shared__ __align__(16) float tables[2 * kTable];
@@ -525,8 +526,9 @@ cudaError_t rotary_4bit_launch(const RotaryArgs &args, const ks_rotary_4bit_args
         // as many tokens a CTA as have their sines fit its tables
         k_args.kv_tokens = kMostTokens;
         while (k_args.kv_tokens > 1 && k_args.kv_tokens * half_dim > kRotMaxDim / 2) --k_args.kv_tokens;
-        int alone = parts == 0;
-        if (!alone) {
+        const bool queries = parts > 0;
+        int alone = !queries || launch_pdl_enabled();
+        if (queries) {
             const cudaError_t ce = rotary_queries_launch(args, vec, half, threads, stream);
             if (ce != cudaSuccess) return ce;
         }
@@ -535,7 +537,7 @@ cudaError_t rotary_4bit_launch(const RotaryArgs &args, const ks_rotary_4bit_args
                                                 : pick_groups<float>(vec, half);
         void *kp[] = {&k_args, &alone};
         return launch_kernel(f, dim3((unsigned)((args.a.tokens + k_args.kv_tokens - 1) / k_args.kv_tokens)), dim3(kRotThreads), 0, kp,
-                             stream, alone ? launch_pdl_enabled() : true);
+                             stream, queries || launch_pdl_enabled());
     }
     const int64_t most = (items + threads - 1) / threads;
     const void *f = dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(vec, half)
