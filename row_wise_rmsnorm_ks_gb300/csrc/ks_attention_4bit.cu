@@ -21,6 +21,13 @@
 // in the loop; one ring for eight warps, which then wait for each other, takes 1.4 times as long; bulk copies, which
 // lanes issue one after the other, take as many instructions as these). Pools that copies cannot take are loaded to
 // registers a step ahead (kAny).
+//
+// Bound by instructions and latency together, at 60 % of the DRAM's cycles: a 32-key step is 588 instructions for 4608
+// bytes of cache, an SM's 16 warps issue 2.4 a cycle, and finding the work, the first keys and the join take 20 us that no
+// split shortens. Measured, 8 key/value heads of 128: 64 contexts of 700..8100 keys 83 us (53 at the copy rate; 203 with
+// 16-bit pages), 4 of 131000 keys 128 us (87; 320), 1 token over 1001 keys 9.8 us (11.5). Heads with CTAs of their own
+// read a page's heads together (where they lie token by token, 196 us become 128), and rings of asynchronous copies take 94
+// where registers a step ahead take 98 and, with the bases kept and places looked up 16 at a time, 83.
 #include <cuda_runtime.h>
 
 #include <cmath>

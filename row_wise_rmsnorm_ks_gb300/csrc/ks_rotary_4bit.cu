@@ -1,13 +1,17 @@
 // Rotary positions with the keys and values landing in a cache held in 4 bits (ks_rotary_to_pages_4bit), and the rows
 // of such a cache read back (ks_pages_4bit_to_rows).
 //
-// Writing. Some CTAs turn a token's queries as ks_rotary does, others take keys and values, a thread per group of 16: it loads its group and, for a key, the group of its pairs' partners, turns in
-// FP32, and finds the group's scale and codes. These are those of the real numbers: the angles have 64 bits, the
-// turn's FP32 error is bounded by 2^-21 (|x| + |y|) |scale| for a pair (x, y), and where the scale or a code could
-// differ within the bound (about one group in five thousand; every tie of an unturned value) it is decided
-// exactly, in double for turned values, by the sign of a fused multiply-add for the others.
+// Writing. Some CTAs turn a token's queries as ks_rotary does, others take keys and values, a thread per group of 16: it
+// loads its group and, for a key, the group of its pairs' partners, turns in FP32, and finds the group's scale and codes.
+// These are those of the real numbers: the angles have 64 bits, the turn's FP32 error is bounded by
+// 2^-21 (|x| + |y|) |scale| for a pair (x, y), and where the scale or a code could differ within the bound (about one
+// group in five thousand; every tie of an unturned value) it is decided exactly, in double for turned values, by the sign
+// of a fused multiply-add for the others.
 //
-// Bound by memory: the queries are read and written once, keys and values read once, 9/16 byte written for each.
+// Bound by memory where there are many tokens: the queries are read and written once, keys and values read once, 9/16 byte
+// written for each. Measured, 8192 tokens of 56 + 8 + 8 heads of 128, fp16, with the read-back: 86 us, 46 at the copy rate:
+// 42 the queries (4.5 TB/s while the cache ends in L2), 30 the groups (issue: a quotient, two windows and their codes for each
+// value), 13 the read-back. 64 tokens with the read-back 9.3 us, two launches and a chain of loads each.
 #include <cuda_runtime.h>
 
 #include "ks_rotary.cuh"
