@@ -320,7 +320,11 @@ extern "C" ks_status_t ks_gated_add_rms_norm(const ks_gated_norm_args_t *args, k
     const void *f = a.dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(k_args.hv, few, &block, &at_once)
                     : a.dtype == KS_DTYPE_F16 ? pick<__half>(k_args.hv, few, &block, &at_once)
                                               : pick<float>(k_args.hv, few, &block, &at_once);
-    const int64_t most = (int64_t)sms * (2048 / block > 32 ? 32 : 2048 / block);
+    int64_t most = (int64_t)sms * (2048 / block > 32 ? 32 : 2048 / block);
+    // Rows read more than once: no more at a time than leave half of L2 to others' reads, while every SM has one. (Measured,
+    // fp32, GB/s with and without: 20480 places a row 5390, 4688; 32768 4724, 4085. 131072, of which no SM's fit: 2806, 3092.)
+    const int64_t room = ((int64_t)64 << 20) / (2 * w);
+    if (k_args.hv > 4096 && room >= sms && room < most) most = room;
     const int64_t want = (a.rows + at_once - 1) / at_once, grid = want < most ? want : most;
     void *kp[] = {&k_args};
     const cudaError_t ce = launch_kernel(f, dim3((unsigned)grid), dim3((unsigned)block), 0, kp, static_cast<cudaStream_t>(stream),
