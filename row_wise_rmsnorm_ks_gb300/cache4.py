@@ -65,19 +65,19 @@ def _pools(k_pages, v_pages, k_scale, v_scale, device, kv_heads, dim):
 
 
 def _fine(pool, shape, heads, dim, device):
-    """Whether a pool is as it must be, in one go; its strides if so."""
+    """A pool as the library's struct, but for the factor, if it is as it must be; all asked in one go."""
     codes, scales = pool
-    cs, ss = codes.stride(), scales.stride()
+    c0, c1, c2, c3 = codes.stride()
+    s0, s1, s2, s3 = scales.stride()
     return (codes.dtype is _U8 and scales.dtype is _F8 and codes.device == device and scales.device == device
             and codes.shape == (*shape, heads, dim // 2) and scales.shape == (*shape, heads, dim // 16)
-            and cs[3] == ss[3] == 1)
+            and c3 == s3 == 1 and (codes.data_ptr(), scales.data_ptr(), c0, c1, c2, s0, s1, s2))
 
 
-def _packed(pool, factor):
-    """A pool as the library's struct."""
+def _packed(pool):
+    """A pool as the library's struct, but for the factor."""
     codes, scales = pool
-    c, s = codes.stride(), scales.stride()
-    return codes.data_ptr(), scales.data_ptr(), c[0], c[1], c[2], s[0], s[1], s[2], factor, 0
+    return codes.data_ptr(), scales.data_ptr(), *codes.stride()[:3], *scales.stride()[:3]
 
 
 def _check_to_pages(q, k, v, positions, steps, k_pages, v_pages, slots, k_scale, v_scale, scale, out):
@@ -123,7 +123,7 @@ def rotary_to_pages_4bit(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tenso
         fine = (q is not None and out is None and k.is_cuda and hk > 0 and dim >= 16 and dim % 16 == 0
                 and shape[1] > 0 and v.shape == k.shape and ks_[2] == vs[2] == 1 and q.dtype is dt and v.dtype is dt
                 and q.device == dev and v.device == dev and len(k_pages) == 2 and len(v_pages) == 2
-                and _fine(k_pages, shape, hk, dim, dev) and _fine(v_pages, shape, hk, dim, dev)
+                and (kp := _fine(k_pages, shape, hk, dim, dev)) and (vp := _fine(v_pages, shape, hk, dim, dev))
                 and slots.dtype is _I64 and slots.device == dev and slots.shape == (tokens,) and slots.is_contiguous()
                 and -_BIG < scale < _BIG and k_scale.__class__ is v_scale.__class__ is float
                 and _LEAST <= k_scale <= _MOST and _LEAST <= v_scale <= _MOST
@@ -137,7 +137,7 @@ def rotary_to_pages_4bit(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tenso
         fine = False
     if not fine:
         _check_to_pages(q, k, v, positions, steps, k_pages, v_pages, slots, k_scale, v_scale, scale, out)
-        shape = k_pages[0].shape[:2]
+        shape, kp, vp = k_pages[0].shape[:2], _packed(k_pages), _packed(v_pages)
         hq, qs = (q.shape[1], q.stride()) if q is not None else (0, (0, 0))
     if q is not None and out is None:
         out = torch.empty((tokens, hq, dim), dtype=dt, device=dev)
@@ -155,7 +155,7 @@ def rotary_to_pages_4bit(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tenso
         o_p, q_p, 0, k.data_ptr(), v.data_ptr(), pos_p, steps_p, 0, 0, slots.data_ptr(), tokens, hq, hk, dim, rot,
         shape[0], shape[1], qos[0], qos[1], qs[0], qs[1], 0, 0, ks_[0], ks_[1], vs[0], vs[1],
         0, 0, 0, 0, 0, 0, scale, _abi.KS_ROTARY_INTERLEAVED if interleaved else 0, code, 0,
-        *_packed(k_pages, k_scale), *_packed(v_pages, v_scale)), dev)
+        *kp, k_scale, 0, *vp, v_scale, 0), dev)
     return out
 
 
@@ -189,8 +189,8 @@ def pages_4bit_to_rows(k_pages, v_pages, slots: torch.Tensor, *, k_scale: float 
         dim, dev = 2 * half, codes.device
         tokens, = slots.shape
         fine = (codes.is_cuda and hk > 0 and page_size > 0 and half > 0 and half % 8 == 0 and len(k_pages) == 2
-                and len(v_pages) == 2 and _fine(k_pages, (pages, page_size), hk, dim, dev)
-                and _fine(v_pages, (pages, page_size), hk, dim, dev) and dtype in _DTYPES and slots.dtype is _I64
+                and len(v_pages) == 2 and (kp := _fine(k_pages, (pages, page_size), hk, dim, dev))
+                and (vp := _fine(v_pages, (pages, page_size), hk, dim, dev)) and dtype in _DTYPES and slots.dtype is _I64
                 and slots.device == dev and slots.is_contiguous()
                 and k_scale.__class__ is v_scale.__class__ is float and _LEAST <= k_scale <= _MOST
                 and _LEAST <= v_scale <= _MOST)
@@ -198,9 +198,11 @@ def pages_4bit_to_rows(k_pages, v_pages, slots: torch.Tensor, *, k_scale: float 
         fine = False
     if not fine:
         codes, dev, hk, dim, tokens = _check_to_rows(k_pages, v_pages, slots, k_scale, v_scale, dtype)
+        pages, page_size, kp, vp = *codes.shape[:2], _packed(k_pages), _packed(v_pages)
     if out is None:
         k = torch.empty((tokens, hk, dim), dtype=dtype, device=dev)
         v = torch.empty((tokens, hk, dim), dtype=dtype, device=dev)
+        ks_ = vs = (hk * dim, dim)
     else:
         if not isinstance(out, (tuple, list)) or len(out) != 2:
             raise ValueError("out must be (k, v)")
@@ -210,12 +212,12 @@ def pages_4bit_to_rows(k_pages, v_pages, slots: torch.Tensor, *, k_scale: float 
             if t.shape != (tokens, hk, dim):
                 raise ValueError(f"out's {n} must be [{tokens}, {hk}, {dim}], got {tuple(t.shape)}")
         _inference(k, v)
+        ks_, vs = k.stride(), v.stride()
     if tokens == 0:
         return k, v
-    ks_, vs = k.stride(), v.stride()
     _launch(_abi.ks_pages_4bit_to_rows, _abi.ROWS_4BIT_ARGS.pack(
-        k.data_ptr(), v.data_ptr(), slots.data_ptr(), *_packed(k_pages, k_scale), *_packed(v_pages, v_scale),
-        tokens, hk, dim, codes.shape[0], codes.shape[1], ks_[0], ks_[1], vs[0], vs[1], _DTYPES[dtype], 0), dev)
+        k.data_ptr(), v.data_ptr(), slots.data_ptr(), *kp, k_scale, 0, *vp, v_scale, 0,
+        tokens, hk, dim, pages, page_size, ks_[0], ks_[1], vs[0], vs[1], _DTYPES[dtype], 0), dev)
     return k, v
 
 
@@ -283,8 +285,9 @@ def paged_attention_4bit(q: torch.Tensor, k_pages, v_pages, page_table: torch.Te
         table_stride, in_row = page_table.stride()
         fine = (out is None and workspace is None and code and q.is_cuda and hk > 0 and hq > 0 and hq % hk == 0
                 and dim >= 16 and dim % 16 == 0 and page_size > 0 and qs[2] == in_row == 1
-                and len(k_pages) == 2 and len(v_pages) == 2 and _fine(k_pages, (pages, page_size), hk, dim, dev)
-                and _fine(v_pages, (pages, page_size), hk, dim, dev) and page_table.dtype is _I32
+                and len(k_pages) == 2 and len(v_pages) == 2
+                and (kp := _fine(k_pages, (pages, page_size), hk, dim, dev))
+                and (vp := _fine(v_pages, (pages, page_size), hk, dim, dev)) and page_table.dtype is _I32
                 and kv_lens.dtype is _I32 and q_starts.dtype is _I32 and page_table.device == dev
                 and kv_lens.device == dev and q_starts.device == dev and kv_lens.shape == (seqs,)
                 and q_starts.shape == (seqs + 1,) and kv_lens.is_contiguous() and q_starts.is_contiguous()
@@ -296,10 +299,14 @@ def paged_attention_4bit(q: torch.Tensor, k_pages, v_pages, page_table: torch.Te
     if not fine or type(max_q_len) not in (int, type(None)):
         _check_attention(q, k_pages, v_pages, page_table, kv_lens, q_starts, k_scale, v_scale, scale, max_q_len, out,
                          workspace)
+        kp, vp = _packed(k_pages), _packed(v_pages)
     if scale is None:
         scale = dim ** -0.5
     if out is None:
         out = torch.empty((tokens, hq, dim), dtype=dt, device=dev)
+        os_ = (hq * dim, dim)
+    else:
+        os_ = out.stride()
     if tokens == 0 or seqs == 0:
         return out
     if workspace is None:
@@ -307,11 +314,10 @@ def paged_attention_4bit(q: torch.Tensor, k_pages, v_pages, page_table: torch.Te
         workspace = torch.empty(ws_bytes, dtype=_U8, device=dev)
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
-    os_ = out.stride()
     _launch(_abi.ks_paged_attention_4bit, _abi.ATTENTION_4BIT_ARGS.pack(
         out.data_ptr(), q.data_ptr(), 0, 0, page_table.data_ptr(), kv_lens.data_ptr(), q_starts.data_ptr(),
         workspace.data_ptr(), ws_bytes, tokens, seqs, hq, hk, dim, pages, page_size, width, table_stride,
         max_q_len or 0, os_[0], os_[1], qs[0], qs[1], 0, 0, 0, 0, 0, 0, scale,
         _abi.KS_ATTENTION_CAUSAL if causal else 0, code, 0,
-        *_packed(k_pages, k_scale), *_packed(v_pages, v_scale)), dev)
+        *kp, k_scale, 0, *vp, v_scale, 0), dev)
     return out

@@ -395,6 +395,17 @@ def test_attention_strides_and_rows_left_alone(cuda_device, order, q_layout, dim
     assert bool((out[-5:] == 7.0).all()), "rows behind the last sequence are left as they were"
 
 
+@pytest.mark.parametrize("order", ["heads_outer", "slots_outer", "one_buffer"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page_size", [8, 16, 24, 64, 128, 200, 256])
+def test_attention_pages_within_and_beyond_a_step(cuda_device, order, dim, page_size):
+    """Many rows over pages that a step of 128 keys is made of, or that it is part of, and that it is neither."""
+    st = build([90, 0, 40, 3], [700, 64, 41, 300], 8, 2, dim, BF16, page_size, cuda_device, seed=dim + page_size, order=order,
+               k_scale=2.0, v_scale=0.7)
+    for causal in (True, False):
+        check_all(attend(st, causal=causal), st, causal=causal, name=f"causal {causal}")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("hint", [1, 200])
 def test_attention_large_and_small_queries(cuda_device, dtype, hint):
