@@ -4,8 +4,8 @@
 //     r = cast(s),  x = cast(s * rsqrt(mean(s^2) + eps) * weight)
 // Two sums over the row, the second of what the first gives: the row has to stay at hand between them. Rows of up to
 // 4096 16-byte vectors lie in a CTA's registers, x and r each read and written once, which bounds the operator by
-// memory (4 values a place); wider rows, and rows that no vector fits, are read three times, the second and third
-// time mostly from L2.
+// memory (4 values a place), or in a CTA's registers by smaller words where no vector fits (bound by instructions, a load or
+// store for one to four values); wider rows are read three times, the second and third time mostly from L2.
 //
 // What counts is how many bytes are on their way while rows are summed, so a thread holds x as it was read, packed,
 // until the second sum's values take its place, and asks for the weights where they are used: 64 registers at four
@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "ks_decode.cuh"
 
@@ -160,6 +161,111 @@ gated_rows_kernel(const __grid_constant__ GatedArgs args) {
     }
 }
 
+// N values that lie together, N a power of two of up to 8 bytes.
+template <typename T, int N>
+struct Few {
+    static constexpr int kBytes = N * (int)sizeof(T);
+    using Word = typename std::conditional<kBytes == 8, uint2, typename std::conditional<kBytes == 4, uint32_t, uint16_t>::type>::type;
+    static_assert(sizeof(Word) == kBytes, "2, 4 or 8 bytes");
+    __device__ __forceinline__ static void unpack(Word w, float (&f)[N]) {
+        T v[N];
+        memcpy(v, &w, kBytes);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = Elem<T>::load1(v, i);
+    }
+    __device__ __forceinline__ static Word pack(const float (&f)[N]) {
+        T v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) Elem<T>::store1(v, i, f[i]);
+        Word w;
+        memcpy(&w, v, kBytes);
+        return w;
+    }
+};
+
+// Rows that no 16-byte vector fits, kValues for each thread: N values an access, the row in registers between its sums as
+// above.
+template <typename T, int N, int kValues>
+__global__ void __launch_bounds__(1024, 1) gated_odd_kernel(const __grid_constant__ GatedArgs args) {
+    using F = Few<T, N>;
+    using Word = typename F::Word;
+    constexpr int K = kValues / N;
+    __shared__ float red[2][32];
+    const ks_gated_norm_args_t &a = args.a;
+    const int n = (int)a.hidden / N, g = blockDim.x, t = threadIdx.x;
+    const float hidden = (float)a.hidden;
+    int slot = 0;  // of `red`: every sum takes the other one
+    grid_dependency_wait();
+    allow_dependents_launch();
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        Word *x = (Word *)((T *)a.x + row * a.hidden), *r = (Word *)((T *)a.residual + row * a.hidden);
+        Word xv[K], rv[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = t + k * g;
+            xv[k] = rv[k] = Word{};
+            if (c < n) {
+                xv[k] = __ldcs(x + c);
+                rv[k] = __ldcs(r + c);
+            }
+        }
+        float factor = a.block_scale, scale = 1.0f;
+        const T *const gate = gate_row<T>(a, row);
+        const bool gates = gate && a.gate_column_stride;
+        if (gate && !gates) factor *= Elem<T>::load1(gate, 0);
+        auto times_at = [&](const void *p, int c, float (&s)[N]) {
+            float w[N];
+            F::unpack(__ldg((const Word *)p + c), w);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] *= w[i];
+        };
+        if (a.post_weight) {
+            SumSq acc;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                    float f[N];
+                F::unpack(xv[k], f);
+                acc.add(f);
+            }
+            scale = row_scale(team_sum<0>(acc.total(), red[slot ^= 1]), hidden, a.eps);
+        }
+        float s[K][N];
+        SumSq acc;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = t + k * g;
+            float f[N];
+            F::unpack(xv[k], s[k]);
+            F::unpack(rv[k], f);
+            if (c < n) {
+                if (a.post_weight) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) s[k][i] *= scale;
+                    times_at(a.post_weight, c, s[k]);
+                }
+                if (gates) times_at(gate, c, s[k]);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[k][i] = fmaf(f[i], a.residual_scale, s[k][i] * factor);
+            if (c < n) {
+                __stcs(r + c, F::pack(s[k]));
+                acc.add(s[k]);
+            }
+        }
+        const float out_scale = row_scale(team_sum<0>(acc.total(), red[slot ^= 1]), hidden, a.eps);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = t + k * g;
+            if (c < n) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) s[k][i] *= out_scale;
+                times_at(a.weight, c, s[k]);
+                __stcs(x + c, F::pack(s[k]));
+            }
+        }
+    }
+}
+
 // s of some places, in place of x: `scale` is the first norm's (1 without one).
 template <int N>
 __device__ __forceinline__ void gated_sum(float (&x)[N], const float (&r)[N], float scale, const float (&post)[N], const float (&gate)[N],
@@ -233,10 +339,28 @@ __global__ void __launch_bounds__(512) gated_wide_kernel(const __grid_constant__
     }
 }
 
-// The kernel for rows of hv vectors (0: no vector fits): threads of a CTA, and rows that one does at once.
+template <typename T, int N>
+const void *odd_kernel(bool small) {
+    return small ? (const void *)gated_odd_kernel<T, N, 4> : (const void *)gated_odd_kernel<T, N, 16>;
+}
+
+// The kernel for rows of hv vectors (0: no vector fits, rows and pointers are aligned to `align` bytes): threads of a CTA, and
+// rows that one does at once.
 template <typename T>
-const void *pick(int64_t hv, bool few, int *block, int *rows) {
+const void *pick(int64_t hv, int64_t hidden, int align, bool few, int *block, int *rows) {
     *rows = 1;
+    if (hv == 0 && hidden <= 1024 * 16) {
+        // Sixteen values a thread, so that an SM holds more rows; for few rows, a few values of an access a thread each.
+        // (Measured, bf16, many rows GB/s and 100 rows us: 1001 places 16 values 2239, 6.8, 4 values 2153, 4.3; 404 3567, 3.7,
+        // and 2121, 3.2; 4098 2799, 6.2. In three passes 656, 5.2 for 1001.)
+        const int n = align / (int)sizeof(T), most = 8 / (int)sizeof(T), each = n < most ? n : most;
+        const bool small = few && hidden <= 1024 * 4;
+        const int64_t threads = few ? hidden / each : (hidden + 15) / 16;
+        *block = (int)(threads < 1024 ? (threads + 31) / 32 * 32 : 1024);
+        return each == 4   ? odd_kernel<T, sizeof(T) == 2 ? 4 : 2>(small)
+               : each == 2 ? odd_kernel<T, 2>(small)
+                           : odd_kernel<T, 1>(small);
+    }
     if (hv == 0 || hv > 4096) {
         *block = 512;
         return hv ? (const void *)gated_wide_kernel<T, true> : (const void *)gated_wide_kernel<T, false>;
@@ -315,11 +439,13 @@ extern "C" ks_status_t ks_gated_add_rms_norm(const ks_gated_norm_args_t *args, k
     k_args.a = a;
     const bool vec = (align & 15u) == 0 && w % 16 == 0;
     k_args.hv = vec ? w / 16 : 0;
+    const uintptr_t bits = align | (uintptr_t)w | 16u;
+    const int lowest = (int)(bits & (~bits + 1));
     int block = 0, at_once = 1;
     const bool few = a.rows <= sms;
-    const void *f = a.dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(k_args.hv, few, &block, &at_once)
-                    : a.dtype == KS_DTYPE_F16 ? pick<__half>(k_args.hv, few, &block, &at_once)
-                                              : pick<float>(k_args.hv, few, &block, &at_once);
+    const void *f = a.dtype == KS_DTYPE_BF16  ? pick<__nv_bfloat16>(k_args.hv, a.hidden, lowest, few, &block, &at_once)
+                    : a.dtype == KS_DTYPE_F16 ? pick<__half>(k_args.hv, a.hidden, lowest, few, &block, &at_once)
+                                              : pick<float>(k_args.hv, a.hidden, lowest, few, &block, &at_once);
     int64_t most = (int64_t)sms * (2048 / block > 32 ? 32 : 2048 / block);
     // Rows read more than once: no more at a time than leave half of L2 to others' reads, while every SM has one. (Measured,
     // fp32, GB/s with and without: 20480 places a row 5390, 4688; 32768 4724, 4085. 131072, of which no SM's fit: 2806, 3092.)

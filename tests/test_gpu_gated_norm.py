@@ -60,6 +60,28 @@ def test_matches_64_bits(cuda_device, dtype, post, gate, shape):
     check(x, r, x0, r0, w, p, g, 0.75, 1.5, 1e-5, str(shape))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("rows, hidden", [(400, 129), (400, 130), (400, 132), (50, 4095), (50, 4100), (200, 2001), (200, 2002), (50, 1),
+                                          (160, 8196), (160, 16382), (20, 16383), (1, 16385), (160, 16390), (400, 1024)])
+@pytest.mark.parametrize("offset", [0, 1, 2, 4])
+def test_rows_that_no_vector_fits(cuda_device, dtype, rows, hidden, offset):
+    """Widths and addresses of every alignment, few rows and many; what lies beside the rows stays."""
+    def rows_at(seed, factor):
+        whole = torch.full((offset + rows * hidden + 8,), 7.0, dtype=dtype, device=cuda_device)
+        part = whole[offset:offset + rows * hidden].view(rows, hidden)
+        part.copy_(normal((rows, hidden), dtype, seed, cuda_device, factor))
+        return whole, part
+    (all_x, x), (all_r, r) = rows_at(1, 3.0), rows_at(2, 2.0)
+    w = (1 + 0.1 * normal((hidden,), F32, 3, cuda_device)).to(dtype)
+    p = (0.5 + 0.1 * normal((hidden,), F32, 4, cuda_device)).to(dtype)
+    gate = normal((rows, hidden), dtype, 5, cuda_device)
+    x0, r0 = x.clone(), r.clone()
+    ks.gated_add_rms_norm(x, r, w, post_weight=p, gate=gate, residual_scale=0.75, block_scale=0.5)
+    check(x, r, x0, r0, w, p, gate, 0.75, 0.5, 1e-6, f"{rows} of {hidden}")
+    for whole in (all_x, all_r):
+        assert bool((whole[:offset] == 7.0).all()) and bool((whole[offset + rows * hidden:] == 7.0).all())
+
+
 @pytest.mark.parametrize("hidden", [4096, 4100, 1001])
 def test_without_anything_is_the_fused_add(cuda_device, hidden):
     x, r = normal((37, hidden), BF16, 1, cuda_device), normal((37, hidden), BF16, 2, cuda_device)
