@@ -759,13 +759,18 @@ int resident(const void *f, int smem) {
     return n;
 }
 
-// Query rows of a tile, in eights: 16 where head_dim leaves the registers and a sequence may have more than 8; 32,
-// those of the tensor-core kernel, where it may have more than 16.
+// Query rows of a tile, in eights: 16 where head_dim leaves the registers and a sequence may have more than 8; 32, the
+// tensor-core kernel's, where it may have more than 32, or 48 of up to 64 dims: its row tiles begin and end in the time of 5
+// of their steps, and it makes fp16 tiles of all keys for however few rows, where each 16 rows of the other kernel read and
+// convert them again. (Measured, us, 16-row tiles and tensor cores, 32 / 8 heads. 128 dims, 8 sequences of 4000 keys: 32 rows 33, 42;
+// 48 43, 43; 64 53, 42; 64 sequences of 4000: 32 173, 208; 48 251, 212; 64 of 60: 35, 40; 48, 40. 64 dims, 64 sequences of
+// 4000: 48 152, 177; 64 196, 178.) More than 16 already where 16-row tiles have to load to registers and the tensor cores'
+// codes come by maps (96 dims, 64 sequences of 4000: 32 rows 384, 208; 80 dims, neither: 370, 480).
 constexpr int kTc = 32;
-int row_tiles(const ks_attention_args_t &a) {
+int row_tiles(const ks_attention_args_t &a, int most) {
     const int64_t q_len = a.max_q_len > 0 && a.max_q_len < a.tokens ? a.max_q_len : a.tokens;
     const int64_t rows = q_len * (a.q_heads / a.kv_heads);
-    return a.head_dim > 128 || rows <= 8 ? 1 : rows <= 16 ? 2 : kTc;
+    return a.head_dim > 128 || rows <= 8 ? 1 : rows <= most ? 2 : kTc;
 }
 
 // Whether both pools have the same strides, those of the scales an eighth of the codes', and a place in them is 32 bits of
@@ -892,7 +897,7 @@ ks_status_t ks_paged_attention_4bit_workspace(const ks_attention_4bit_args_t *ar
     ks_status_t st = check_sizes4(args->attention);
     if (st != KS_SUCCESS || args->attention.tokens == 0 || args->attention.seqs == 0) return st;
     // whichever kernel the pools' layout, or fewer tokens, pick
-    for (int tiles = row_tiles(args->attention); tiles > 0; tiles = tiles == kTc ? 2 : tiles - 1)
+    for (int tiles = row_tiles(args->attention, 16); tiles > 0; tiles = tiles == kTc ? 2 : tiles - 1)
         for (int pool : {kAny, kBlocks, kRuns}) {
             Attn4Plan p;
             if ((st = plan4(*args, tiles, pool, &p)) != KS_SUCCESS) return st;
@@ -912,9 +917,10 @@ ks_status_t ks_paged_attention_4bit(const ks_attention_4bit_args_t *args, ks_str
     if (!a.workspace || ((uintptr_t)a.workspace & 15u))
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace must be device memory aligned to 16 bytes");
     Attn4Plan p;
-    int tiles = row_tiles(a);
+    const int pool = pool_kind(*args, code_align, scale_align);
+    int tiles = row_tiles(a, pool == kAny && a.head_dim % 32 == 0 ? 16 : a.head_dim > 64 ? 32 : 48);
     if (tiles == kTc && !attn4_tc_fits(a)) tiles = 2;
-    if ((st = plan4(*args, tiles, pool_kind(*args, code_align, scale_align), &p)) != KS_SUCCESS) return st;
+    if ((st = plan4(*args, tiles, pool, &p)) != KS_SUCCESS) return st;
     const int64_t need = attn_workspace_bytes(p.args.s, p.ctas);
     if (a.workspace_bytes < need)
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace has %lld bytes, %lld are needed", (long long)a.workspace_bytes,

@@ -5,9 +5,9 @@
 // factors go into the scores' scale and the output's. A thread of the four warps has one key of a step: 64 bytes of codes
 // become 256 bytes in the swizzled layout, 64 conversions of a pair and as many products a tile. bf16 queries become fp16 in
 // shared memory, each row times a power of two, by the warps that read their scores; fp16 probabilities follow.
-//   - Where a step is whole pages or part of one, and rows of codes lie 16 bytes aligned, the copying warp brings the codes
+//   - Where a step is whole pages or part of one, and rows of codes lie 16 bytes aligned (heads of any 32), the copying warp brings the codes
 //     by tensor maps to a ring of three tiles, in 16-byte pieces swizzled for the threads' reads; the scales, 8 bytes a key,
-//     are read a step ahead. Other pools (any page size, heads of any 16, unaligned rows) are copied by the four warps
+//     are read a step ahead. Other pools (any page size, odd heads of 16, unaligned rows) are copied by the four warps
 //     themselves, two tiles ahead (1.07 times the time where rows are aligned).
 //   - 768 threads launch with 80 registers each; the softmax takes 96 (104 with 16-bit pages: some spills), the four warps 56,
 //     the other four 40. Four tiles of 128 keys in the ring instead of five make room for the codes.
@@ -46,7 +46,7 @@ cudaError_t attn4_tc_launch(const Attn4Args &args, uintptr_t code_align, uintptr
     pages.page_units = args.page_units;
     pages.slot_units = args.slot_units;
     pages.by_map = 0;
-    if (pages.whole && s.a.page_size % 8 == 0 && (kKeys % s.a.page_size == 0 || s.a.page_size % kKeys == 0)) {
+    if (dim % 32 == 0 && (code_align & 15) == 0 && (scale_align & 1) == 0 && args.alike && s.a.page_size % 8 == 0 && (kKeys % s.a.page_size == 0 || s.a.page_size % kKeys == 0)) {
         // the maps' strides are below 2^40 bytes and not zero
         const int64_t strides[3] = {args.k.code_page, args.k.code_slot, args.k.code_head}, counts[3] = {s.a.pages, s.a.page_size, s.a.kv_heads};
         pages.by_map = 1;

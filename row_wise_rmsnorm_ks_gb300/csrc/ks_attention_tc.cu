@@ -94,14 +94,14 @@ bool attn_codes_map(CUtensorMap *map, const AttnArgs &s, const Pool4 &pool) {
     const ks_attention_args_t &a = s.a;
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
-    const cuuint64_t row = (cuuint64_t)a.head_dim / 2;
-    const cuuint64_t dims[4] = {row, (cuuint64_t)a.page_size, (cuuint64_t)a.kv_heads, (cuuint64_t)a.pages};
+    const cuuint64_t row = (cuuint64_t)(a.head_dim <= 64 ? 32 : 64);  // places past head_dim read as zeros
+    const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim / 2, (cuuint64_t)a.page_size, (cuuint64_t)a.kv_heads, (cuuint64_t)a.pages};
     const cuuint64_t strides[3] = {a.page_size > 1 ? (cuuint64_t)pool.code_slot : row, a.kv_heads > 1 ? (cuuint64_t)pool.code_head : row,
                                    a.pages > 1 ? (cuuint64_t)pool.code_page : row};
     const cuuint32_t box[4] = {(cuuint32_t)row, (cuuint32_t)(a.page_size < kKeys ? a.page_size : kKeys), 1, 1};
     const cuuint32_t steps[4] = {1, 1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(pool.codes), dims, strides, box, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, a.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -48,7 +48,8 @@ struct Pages4 {
     // place has 32 bits of 16-byte units: the strides of pages and slots in those.
     int32_t whole;
     uint32_t page_units, slot_units;
-    // A step's keys are whole pages or part of one: the copying warp brings their codes, by these maps.
+    // A step's keys are whole pages or part of one, rows of codes are at 16-byte boundaries, of scales at 2: the copying warp
+    // brings the codes, by these maps.
     int32_t by_map;
     CUtensorMap k_map, v_map;
 };
@@ -366,7 +367,7 @@ __device__ __forceinline__ void convert_row(uint8_t *tile, int row, const uint32
 
 // The converting warps where the copying warp brings the codes: a thread per key of a step, which reads the row's scales a
 // step ahead. Rows behind the last key that the row tile sees get scales of 0, whatever lies in their place.
-template <int kDim>
+template <int kDim, bool kWhole>
 __device__ __forceinline__ void convert_copied(const AttnArgs &s, const Pages4 &pages, Place &place, bool more, uint8_t *ring,
                                                const uint8_t *raw, uint64_t *full, uint64_t *empty, uint64_t *raw_full,
                                                uint64_t *raw_empty, volatile uint32_t *gave_up) {
@@ -374,7 +375,7 @@ __device__ __forceinline__ void convert_copied(const AttnArgs &s, const Pages4 &
     constexpr int kWords = kDim / 64;
     const ks_attention_args_t &a = s.a;
     const int lane = threadIdx.x % 32, row = (threadIdx.x / 32 - kConvert) * 32 + lane;
-    const int page_size = (int)a.page_size;
+    const int page_size = (int)a.page_size, pairs = (int)a.head_dim / 32;
     uint32_t at = 0;  // tiles made so far: K and V of each step in turn
     RingAt<C::kRawStages> from;
     while (more) {
@@ -382,17 +383,26 @@ __device__ __forceinline__ void convert_copied(const AttnArgs &s, const Pages4 &
         const int head = place.cur.head / s.head_splits, sees = attn_tile_keys(s, place.q, place.cur.row_tile);
         const int32_t *table = a.page_table + (int64_t)place.cur.seq * a.table_stride;
         const uint8_t *k_scales = pages.k.scales + head * pages.k.scale_head, *v_scales = pages.v.scales + head * pages.v.scale_head;
-        uint32_t next[2][kWords];
+        // The next step's, words of whole rows; of others (96 dims, or unaligned) pairs, joined when their turn comes.
+        constexpr int kNext = kWhole ? kWords : 2 * kWords;
+        uint32_t next[2][kNext];
         auto read_scales = [&](int j) {
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) next[0][i] = next[1][i] = 0;
+            for (int i = 0; i < kNext; ++i) next[0][i] = next[1][i] = 0;
             const int key = j * kKeys + row;
             if (j >= span.last || key >= sees) return;
             const int index = key / page_size;
             const uint32_t page = (uint32_t)__ldg(table + index);
             if (page >= (uint64_t)a.pages) return;  // the copying warp reports it
             const uint64_t e = (uint64_t)(page * pages.page_units + (uint32_t)(key - index * page_size) * pages.slot_units) * 2;
-            if constexpr (kWords == 2) {
+            if constexpr (!kWhole) {
+#pragma unroll
+                for (int i = 0; i < kNext; ++i)
+                    if (i < pairs) {
+                        next[0][i] = __ldg(reinterpret_cast<const uint16_t *>(k_scales + e) + i);
+                        next[1][i] = __ldg(reinterpret_cast<const uint16_t *>(v_scales + e) + i);
+                    }
+            } else if constexpr (kWords == 2) {
                 const uint2 x = __ldg(reinterpret_cast<const uint2 *>(k_scales + e)), y = __ldg(reinterpret_cast<const uint2 *>(v_scales + e));
                 next[0][0] = x.x;
                 next[0][1] = x.y;
@@ -410,7 +420,10 @@ __device__ __forceinline__ void convert_copied(const AttnArgs &s, const Pages4 &
 #pragma unroll
             for (int v = 0; v < 2; ++v)
 #pragma unroll
-                for (int i = 0; i < kWords; ++i) scales[v][i] = next[v][i];
+                for (int i = 0; i < kWords; ++i) {
+                    if constexpr (kWhole) scales[v][i] = next[v][i];
+                    else scales[v][i] = next[v][2 * i] | next[v][2 * i + 1] << 16;
+                }
             read_scales(j + 1);
 #pragma unroll
             for (int v = 0; v < 2; ++v, ++at) {
@@ -635,7 +648,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
         if constexpr (k4) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<k4>::kConvertRegs));
             uint8_t *tiles = smem + 2 * C::kTileBytes, *rows = smem + C::kRawAt;
-            if (pages.by_map) convert_copied<kDim>(s, pages, place, more, tiles, rows, full, empty, raw_full, raw_empty, gave_up);
+            if (pages.by_map && pages.whole)
+                convert_copied<kDim, true>(s, pages, place, more, tiles, rows, full, empty, raw_full, raw_empty, gave_up);
+            else if (pages.by_map)
+                convert_copied<kDim, false>(s, pages, place, more, tiles, rows, full, empty, raw_full, raw_empty, gave_up);
             else convert_pages<kDim>(s, pages, place, more, tiles, rows, full, empty, gave_up);
         }
     } else if (warp >= kSoftmaxWarps) {

@@ -396,7 +396,7 @@ def test_attention_strides_and_rows_left_alone(cuda_device, order, q_layout, dim
 
 
 @pytest.mark.parametrize("order", ["heads_outer", "slots_outer", "one_buffer"])
-@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dim", [32, 64, 96, 112, 128])
 @pytest.mark.parametrize("page_size", [8, 16, 24, 64, 128, 200, 256])
 def test_attention_pages_within_and_beyond_a_step(cuda_device, order, dim, page_size):
     """Many rows over pages that a step of 128 keys is made of, or that it is part of, and that it is neither."""
@@ -404,6 +404,15 @@ def test_attention_pages_within_and_beyond_a_step(cuda_device, order, dim, page_
                k_scale=2.0, v_scale=0.7)
     for causal in (True, False):
         check_all(attend(st, causal=causal), st, causal=causal, name=f"causal {causal}")
+
+
+@pytest.mark.parametrize("dim", [64, 80, 96, 128])
+@pytest.mark.parametrize("group", [1, 4, 5])
+def test_attention_of_drafts(cuda_device, dim, group):
+    """A few tokens a sequence, on either side of the numbers of rows at which another kernel is taken."""
+    for n in (2, 3, 4, 5, 8, 9, 12, 13, 17, 33, 49):
+        st = build([n, 1, n - 1, n], [n, 130, 1000, 257], 2 * group, 2, dim, BF16, 16, cuda_device, seed=n)
+        check_all(attend(st, max_q_len=n), st, name=f"{n} tokens")
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
