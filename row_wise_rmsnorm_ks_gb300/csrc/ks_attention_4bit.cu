@@ -765,7 +765,7 @@ int resident(const void *f, int smem) {
 // convert them again. (Measured, us, 16-row tiles and tensor cores, 32 / 8 heads. 128 dims, 8 sequences of 4000 keys: 32 rows 33, 42;
 // 48 43, 43; 64 53, 42; 64 sequences of 4000: 32 173, 208; 48 251, 212; 64 of 60: 35, 40; 48, 40. 64 dims, 64 sequences of
 // 4000: 48 152, 177; 64 196, 178.) More than 16 already where 16-row tiles have to load to registers and the tensor cores'
-// codes come by maps (96 dims, 64 sequences of 4000: 32 rows 384, 208; 80 dims, neither: 370, 480).
+// codes come by maps (96 dims, 64 sequences of 4000: 32 rows 384, 208; 80 dims, neither: 370, 424).
 constexpr int kTc = 32;
 int row_tiles(const ks_attention_args_t &a, int most) {
     const int64_t q_len = a.max_q_len > 0 && a.max_q_len < a.tokens ? a.max_q_len : a.tokens;

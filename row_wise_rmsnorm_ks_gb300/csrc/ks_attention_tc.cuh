@@ -452,7 +452,7 @@ __device__ __forceinline__ void convert_copied(const AttnArgs &s, const Pages4 &
 // ring of its own, two tiles ahead, neighbouring lanes neighbouring bytes (with loads to registers, a key a thread, the
 // long prompt takes 1.3 times as long); a thread then makes its row fp16 in the layout that the matrix instructions read.
 // Rows behind the last key that the row tile sees are zeros.
-template <int kDim>
+template <int kDim, bool kWhole>
 __device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &pages, Place &place, bool more, uint8_t *ring, uint8_t *raw,
                                               uint64_t *full, uint64_t *empty, volatile uint32_t *gave_up) {
     using C = Tc<kDim, true>;
@@ -481,13 +481,13 @@ __device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &p
                 atomicOr(&g_fault_flags, kFaultBadIndex);
                 return kNone;
             }
-            return pages.whole ? page * pages.page_units + slot * pages.slot_units : page;
+            return kWhole ? page * pages.page_units + slot * pages.slot_units : page;
         };
         // A tile's codes (and scales, of whole pools) to the raw ring; zeros where there is no key.
         auto copy = [&](const Pool4 &pool, uint32_t where, uint32_t slots, uint32_t to) {
             const uint32_t dst = smem_addr(mine) + to * 32 * C::kRawRow;
             const uint8_t *codes = pool.codes + head * pool.code_head;
-            if (pages.whole) {
+            if constexpr (kWhole) {
                 constexpr int kPieces = kDim / 32;  // of 16 bytes in a row
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
@@ -511,12 +511,20 @@ __device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &p
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        // Scales of rows that no copy takes, a byte a register so that nothing waits for them before they are used.
+        uint32_t next_scales[kWhole ? 1 : kGroups];
+        auto read_scales = [&](const Pool4 &pool, uint32_t w, uint32_t r) {
+            const uint8_t *e = pool.scales + head * pool.scale_head + (int64_t)w * pool.scale_page + r * pool.scale_slot;
+#pragma unroll
+            for (int g = 0; g < (kWhole ? 0 : kGroups); ++g) next_scales[g] = w != kNone && g < groups ? __ldg(e + g) : 0;
+        };
         uint32_t slot[2];  // of this step and the next
         uint32_t where[2];
         where[0] = look_up(span.first, slot[0]);
         copy(pages.k, where[0], slot[0], raw_at);
         copy(pages.v, where[0], slot[0], raw_at + 1 < C::kRawStages ? raw_at + 1 : raw_at + 1 - C::kRawStages);
         where[1] = look_up(span.first + 1, slot[1]);
+        if constexpr (!kWhole) read_scales(pages.k, where[0], slot[0]);
         bool ok = true;
         for (int j = span.first; j < span.last && ok; ++j) {
             const uint32_t now = where[0], now_slot = slot[0];
@@ -531,16 +539,16 @@ __device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &p
                 ok = ok && bar_wait_warp(empty + stage, (at / C::kStages & 1) ^ 1, gave_up);
                 if (!ok) break;
                 uint32_t scales[kGroups / 4] = {};
-                if (!pages.whole && now != kNone) {
-                    const uint8_t *e = pool.scales + head * pool.scale_head + now * pool.scale_page + now_slot * pool.scale_slot;
+                if constexpr (!kWhole) {  // this tile's, read while the one before was made; the next one's
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
-                        if (g < groups) scales[g / 4] |= (uint32_t)__ldg(e + g) << (8 * (g % 4));
+                    for (int g = 0; g < kGroups; ++g) scales[g / 4] |= next_scales[g] << (8 * (g % 4));
+                    if (v) read_scales(pages.k, where[0], slot[0]);
+                    else read_scales(pages.v, now, now_slot);
                 }
                 asm volatile("cp.async.wait_group 2;" ::: "memory");
                 __syncwarp();
                 const uint8_t *from = mine + (raw_at * 32 + lane) * C::kRawRow;
-                if (pages.whole) {
+                if constexpr (kWhole) {
 #pragma unroll
                     for (int i = 0; i < kGroups / 4; ++i) scales[i] = reinterpret_cast<const uint32_t *>(from + kDim / 2)[i];
                 }
@@ -652,7 +660,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs s, const __grid_constant__ CUten
                 convert_copied<kDim, true>(s, pages, place, more, tiles, rows, full, empty, raw_full, raw_empty, gave_up);
             else if (pages.by_map)
                 convert_copied<kDim, false>(s, pages, place, more, tiles, rows, full, empty, raw_full, raw_empty, gave_up);
-            else convert_pages<kDim>(s, pages, place, more, tiles, rows, full, empty, gave_up);
+            else if (pages.whole) convert_pages<kDim, true>(s, pages, place, more, tiles, rows, full, empty, gave_up);
+            else convert_pages<kDim, false>(s, pages, place, more, tiles, rows, full, empty, gave_up);
         }
     } else if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<k4>::kOtherRegs));
