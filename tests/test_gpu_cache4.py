@@ -733,6 +733,47 @@ def test_graph_replays_with_other_lengths(cuda_device):
         check_all(o, f)
 
 
+@pytest.mark.parametrize("tokens", [3, 1500])
+def test_captured_writes_and_norms_replay_with_other_contents(cuda_device, tokens):
+    """A norm, a write and a read-back in one graph, replayed with other rows, positions and slots: what eager calls give."""
+    hq, hk, dim, page = 6, 2, 128, 32
+    steps, w = ks.rotary_steps(dim, device=cuda_device), normal(((hq + 2 * hk) * dim,), BF16, 1, cuda_device)
+
+    def inputs(seed):
+        g = torch.Generator().manual_seed(seed)
+        return [normal((tokens, (hq + 2 * hk) * dim), BF16, seed, cuda_device), normal((tokens, (hq + 2 * hk) * dim), BF16, seed + 1, cuda_device),
+                torch.randint(0, 1 << 40, (tokens,), generator=g).to(cuda_device), (torch.randperm(64 * page, generator=g)[:tokens] - 1).to(cuda_device)]
+
+    def run(x, r, pos, slots, kp, vp):
+        ks.gated_add_rms_norm(x, r, w, block_scale=0.5)
+        q, k, v = (t.view(tokens, -1, dim) for t in x.split([hq * dim, hk * dim, hk * dim], 1))
+        return [ks.rotary_to_pages_4bit(q, k, v, pos, steps, kp, vp, slots, k_scale=0.5), *ks.pages_4bit_to_rows(kp, vp, slots, k_scale=0.5)]
+
+    def fresh():
+        return [ks.empty_pages_4bit(64, page, hk, dim, device=cuda_device) for _ in range(2)]
+    held_in, pools_in = inputs(20), fresh()
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        run(*inputs(30), *fresh())
+    torch.cuda.current_stream().wait_stream(warm)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = run(*held_in, *pools_in)
+    for seed in (40, 50):
+        new, pools_new = inputs(seed), fresh()
+        for a, b in zip(held_in, new):
+            a.copy_(b)
+        for pool in pools_in:
+            for t in pool:
+                t.view(torch.uint8).zero_()
+        g.replay()
+        want = run(*new, *pools_new)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip([*outs, *held_in[:2]], [*want, *new[:2]]))
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for p, n in zip(pools_in, pools_new) for a, b in zip(p, n))
+
+
 def test_calls_on_another_stream(cuda_device):
     st = build(*CHUNK, 8, 2, 128, BF16, 16, cuda_device, seed=6)
     want = attend(st)
