@@ -514,7 +514,7 @@ ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stre
  * the values call for another) and the group's largest magnitude A:
  *     s = A / (6 g), at most 448;   u = s g, in FP32;   code = x / u, at most 6 (0 where s is 0)
  * s and the codes to the nearest, ties to the even code, as of real numbers: an FP32 result near a border is
- * decided exactly. What is held is u * code. Infinities are held as the largest value; a group with a NaN gets
+ * decided exactly. Bit 3 is set where x < 0, also if the magnitude becomes 0 (unless s is 0). What is held is u * code. Infinities are held as the largest value; a group with a NaN gets
  * the scale NaN.
  */
 typedef struct ks_pages_4bit {

@@ -5,7 +5,7 @@
 // magnitude:
 //     s = A / (6 g) to the nearest, ties to the even code, at most 448
 //     u = s g, rounded to FP32
-//     code = x / u to the nearest, ties to the even code, at most 6 (0 where s is 0)
+//     code = x / u to the nearest, ties to the even code, at most 6 (0 where s is 0); its sign that of x, none for -0
 // A group with a NaN has the scale NaN, and reads back as NaN.
 //
 // A code times a scale has at most 6 significant bits and lies in 2^-10 .. 2688: fp16 holds it exactly. The

@@ -44,6 +44,7 @@ __device__ __noinline__ double turned_exact(const ks_rotary_args_t &a, const T *
     const int j = kHalf ? (d < half ? d : d - half) : d / 2;
     const bool second = kHalf ? d >= half : d & 1;
     const double z = Elem<T>::load1(row, kHalf ? (second ? d - half : d + half) : d ^ 1);
+    if (x == 0.0 && z == 0.0) return 0.0;  // rows may have many
     double s, c;
     sincospi((double)(int64_t)(position * (uint64_t)a.steps[j]) * 1.0842021724855044e-19, &s, &c);  // 2^-63
     return (second ? x * c + z * s : x * c - z * s) * (double)a.scale;
@@ -76,7 +77,9 @@ __device__ __forceinline__ float reciprocal(float x) {
 }
 
 // A group's values in FP32, each off by at most `off` (kExact: not at all). A quotient's code is taken at both ends
-// of what it may be; a quotient's own error is below 8 (2^-23 + 2^-24), quotients being below 8, and so below 2^-19.
+// of what it may be. A quotient's own error is at most 2^-23 + 2^-24 of it: for kExact both ends are multiples of it, of its
+// sign (-0, which is not below 0, having been made +0). Otherwise the ends are a distance apart, the error being below
+// 2^-19 of quotients below 10, and a zero's sign may be what is in doubt.
 template <typename T, bool kHalf, bool kExact>
 __device__ __forceinline__ Group4 group4(const ks_rotary_args_t &a, const T *row, int group, uint64_t position, float g,
                                          float2 (&y)[8], float off) {
@@ -84,6 +87,10 @@ __device__ __forceinline__ Group4 group4(const ks_rotary_args_t &a, const T *row
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max_nan(top, max_nan(fabsf(y[i].x), fabsf(y[i].y)));
     if (top != top) return {0x7Fu, 0, 0};
+    if constexpr (kExact) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __fadd2_rn(y[i], make_float2(0.0f, 0.0f));
+    }
     const float per = reciprocal(6.0f * g);
     const float low = (top - off) * per * (1.0f - 2 * kRoundError), high = (top + off) * per * (1.0f + 2 * kRoundError);
     Group4 out = {0, 0, 0};
@@ -119,21 +126,22 @@ __device__ __forceinline__ Group4 group4(const ks_rotary_args_t &a, const T *row
             t[i].y = fminf(fmaxf(t[i].y, -8.0f), 8.0f);
         }
     }
-    const float w = (kExact ? 0.0f : off * inv) + 1.9073486328125e-06f;  // 2^-19
-    const float2 more = make_float2(w, w), less = make_float2(-w, -w);
+    const float w = kExact ? 4.76837158203125e-07f : off * inv + 1.9073486328125e-06f;  // 2^-21, 2^-19
+    const float2 more = kExact ? make_float2(1.0f + w, 1.0f + w) : make_float2(w, w);
+    const float2 less = kExact ? make_float2(1.0f - w, 1.0f - w) : make_float2(-w, -w);
     uint32_t lo[2], hi[2];
     {
         float2 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fadd2_rn(t[i], more);
+        for (int i = 0; i < 8; ++i) v[i] = kExact ? __fmul2_rn(t[i], more) : __fadd2_rn(t[i], more);
         hi[0] = fp4_word(v), hi[1] = fp4_word(v + 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fadd2_rn(t[i], less);
+        for (int i = 0; i < 8; ++i) v[i] = kExact ? __fmul2_rn(t[i], less) : __fadd2_rn(t[i], less);
         lo[0] = fp4_word(v), lo[1] = fp4_word(v + 4);
     }
-    // Codes that differ in their sign alone are zeros, unless the window is wider than that: then all are in doubt.
+    // (A window of infinite ends has no codes to compare.)
     const bool wide = !kExact && !(w < 0.125f);
-    if ((((lo[0] ^ hi[0]) | (lo[1] ^ hi[1])) & 0x77777777u) || wide) {
+    if (lo[0] != hi[0] || lo[1] != hi[1] || wide) {
         if constexpr (kExact) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -150,7 +158,7 @@ __device__ __forceinline__ Group4 group4(const ks_rotary_args_t &a, const T *row
 #pragma unroll 1
             for (int i = 0; i < 16; ++i) {
                 const int at = 4 * (i % 8);
-                if (!wide && ((i < 8 ? lo[0] ^ hi[0] : lo[1] ^ hi[1]) >> at & 7) == 0) continue;
+                if (!wide && ((i < 8 ? lo[0] ^ hi[0] : lo[1] ^ hi[1]) >> at & 15) == 0) continue;
                 const double x = turned_exact<T, kHalf>(a, row, group * 16 + i, position), size = fabs(x);
                 // the window may be wider than two codes: of a group that its pairs all but cancel
                 const float q = fminf((float)(size / (double)u), 8.0f);

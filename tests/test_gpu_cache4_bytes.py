@@ -1,0 +1,75 @@
+"""The 4-bit cache's bytes: what is written, compared byte for byte (a zero's sign too), and what is read back, compared
+with the one rounding of u * code to its type.
+"""
+import math
+
+import pytest
+import torch
+
+import row_wise_rmsnorm_ks_gb300 as ks
+from test_gpu_cache4 import bits, pools, stored, unpacked
+from test_gpu_decode_ops import freqs, no_faults, normal, rotated  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+def same_bytes(pool, slots, x, factor, name):
+    """The pool's slots hold x (64 bits): codes with bit 3 set where x < 0, none where the scale is 0."""
+    codes, scales = stored(x, factor)
+    codes = torch.where((scales == 0).repeat_interleave(16, -1), 0, codes)
+    page_size = pool[0].shape[1]
+    at = tuple(i.cpu() for i in (slots // page_size, slots % page_size))
+    got = bits(pool[1])[at]
+    assert torch.equal(got, scales), f"{name}: {int((got != scales).sum())} of {scales.numel()} scales differ"
+    got = unpacked(pool[0][tuple(i.to(pool[0].device) for i in at)])
+    assert torch.equal(got, codes), f"{name}: {int((got != codes).sum())} of {codes.numel()} codes differ"
+
+
+def view(tokens, heads, dim, dtype, seed, device, aligned):
+    x = normal((tokens * heads * dim + 1,), dtype, seed, device)
+    return (x[:-1] if aligned else x[1:]).view(tokens, heads, dim)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("turn", [None, "halves", "neighbours"])
+@pytest.mark.parametrize("tokens, aligned", [(40, True), (40, False), (1100, True), (1100, False)])
+def test_signs_of_stored_zeros(cuda_device, dtype, turn, tokens, aligned):
+    """Zeros of either sign, and values that become zero: a code has the sign of its value, and only a value below 0 has one.
+    Half of the tokens are turned by nothing, which leaves the values next to 0 where they are."""
+    hk, dim = 2, 64
+    k, v = (view(tokens, hk, dim, dtype, s, cuda_device, aligned) for s in (1, 2))
+    least = 2.0 ** -24 if dtype == F16 else 2.0 ** -40
+    for x in (k, v):
+        x[..., 0::16], x[..., 1::16], x[..., 2::16], x[..., 3::16] = 0.0, -0.0, least, -least
+        x[..., 4::16], x[..., 5::16] = 0.0, 0.0
+        x[..., 6::16], x[..., 7::16] = x[..., 6::16] * 2.0 ** -9, x[..., 7::16] * 2.0 ** -9
+        x[3, 0, 16:32] = x[3, 0, 16:32] * 0.0                # a group of zeros of both signs
+        x[5, 1, :16] = -(x[5, 1, :16].abs() * 2.0 ** -13)    # a group whose scale is 0
+    kp, vp = (pools(-(-tokens // 16), 16, hk, dim, cuda_device, seed=s) for s in (4, 5))
+    slots = torch.arange(tokens, device=cuda_device)
+    pos = torch.randint(0, 1 << 18, (tokens,), generator=torch.Generator().manual_seed(6))
+    pos[::2] = 0
+    steps = ks.rotary_steps(dim, device=cuda_device) if turn else None
+    ks.rotary_to_pages_4bit(None, k, v, pos.to(cuda_device) if turn else None, steps, kp, vp, slots, interleaved=turn == "neighbours")
+    same_bytes(kp, slots, rotated(k, pos, freqs(dim), turn == "neighbours")[0] if turn else k, 1.0, "k")
+    same_bytes(vp, slots, v, 1.0, "v")
+
+
+@pytest.mark.parametrize("dtype, size, scale", [(F32, 1e30, 2.0 ** 60), (BF16, 1e30, -2.0 ** 60), (F16, 1000.0, 2.0 ** 126),
+                                                (F32, 3e38, 2.0), (F32, 1.0, 2.0 ** 126)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens", [9, 1030])
+def test_turned_values_beyond_32_bits(cuda_device, dtype, size, scale, interleaved, tokens):
+    """Products of a turn past FP32's largest number, whose difference has a sign all the same. NaN stays NaN."""
+    hk, dim, factor = 2, 32, 2.0 ** 60
+    k = normal((tokens, hk, dim), F32, 1, cuda_device).clamp(-1, 1).mul(size).to(dtype)
+    k[2, 0, 3] = math.nan
+    v = normal((tokens, hk, dim), dtype, 2, cuda_device)
+    kp, vp = (pools(-(-tokens // 16), 16, hk, dim, cuda_device, seed=s) for s in (4, 5))
+    slots = torch.arange(tokens, device=cuda_device)
+    pos = torch.randint(1, 1 << 18, (tokens,), generator=torch.Generator().manual_seed(6))
+    ks.rotary_to_pages_4bit(None, k, v, pos.to(cuda_device), ks.rotary_steps(dim, device=cuda_device), kp, vp, slots,
+                            interleaved=interleaved, scale=scale, k_scale=factor)
+    same_bytes(kp, slots, rotated(k, pos, freqs(dim), interleaved, scale=scale)[0], factor, "k")
