@@ -205,7 +205,7 @@ constexpr int kMostTokens = 4;  // whose groups a CTA takes
 // Where a token's rows go, and what it is turned by.
 struct Place4 {
     int64_t k_codes, k_scales, v_codes, v_scales;  // k_codes -1: nowhere
-    uint64_t position;
+    uint64_t position;  // negated where the turn is the inverse one
 };
 
 // A CTA's part of the groups of `tokens` tokens from `first` on, a thread a group. Rows are asked for before all else.
@@ -222,6 +222,12 @@ __device__ __forceinline__ void pages4_groups(const Rotary4Args &args, int64_t f
         int of, group, head;
         bool value, turned;
         const T *row;
+    };
+    // Angles are a multiple of the position, so the inverse turn is that by the position negated, exactly.
+    const bool inverse = (a.flags & KS_ROTARY_INVERSE) != 0;
+    auto position = [&](int of) {
+        const uint64_t at = (uint64_t)a.positions[first + of];
+        return inverse ? 0 - at : at;
     };
     auto which = [&](int item) {
         Which w;
@@ -245,7 +251,7 @@ __device__ __forceinline__ void pages4_groups(const Rotary4Args &args, int64_t f
     if (item < total) load(w, it);
     for (int i = threadIdx.x; i < tokens; i += blockDim.x) {
         const int64_t slot = a.slots[first + i];
-        Place4 p = {-1, 0, 0, 0, rot > 0 ? (uint64_t)a.positions[first + i] : 0};
+        Place4 p = {-1, 0, 0, 0, rot > 0 ? position(i) : 0};
         if (slot >= 0) {
             const int64_t page = quotient(slot, a.page_size), place = slot - page * a.page_size;
             if (page < a.pages) {
@@ -261,7 +267,7 @@ __device__ __forceinline__ void pages4_groups(const Rotary4Args &args, int64_t f
     }
     for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
         const int of = i / half, j = i - of * half;
-        const float2 c = turn_cos_sin((uint64_t)a.positions[first + of] * (uint64_t)a.steps[j], a.scale);
+        const float2 c = turn_cos_sin(position(of) * (uint64_t)a.steps[j], a.scale);
         cosines[table_at(i)] = c.x;
         sines[table_at(i)] = c.y;
     }

@@ -2,13 +2,15 @@
 with the one rounding of u * code to its type.
 """
 import math
+import struct
 
 import pytest
 import torch
 
 import row_wise_rmsnorm_ks_gb300 as ks
+from row_wise_rmsnorm_ks_gb300 import _abi
 from test_gpu_cache4 import bits, pools, stored, unpacked
-from test_gpu_decode_ops import freqs, no_faults, normal, rotated  # noqa: F401
+from test_gpu_decode_ops import close, freqs, no_faults, normal, rotated  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -30,6 +32,32 @@ def same_bytes(pool, slots, x, factor, name):
 def view(tokens, heads, dim, dtype, seed, device, aligned):
     x = normal((tokens * heads * dim + 1,), dtype, seed, device)
     return (x[:-1] if aligned else x[1:]).view(tokens, heads, dim)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens, aligned", [(1, True), (37, True), (37, False), (1101, True), (1101, False)])
+def test_inverse_turns_queries_and_keys_alike(cuda_device, monkeypatch, dtype, interleaved, tokens, aligned):
+    """KS_ROTARY_INVERSE, a flag of the C call: both sides turn the other way."""
+    hq, hk, dim, rot, factor = 3, 2, 64, 32, 0.375
+    call = _abi.ks_rotary_to_pages_4bit
+    at = struct.calcsize("=10Q23qf")
+
+    def inverse(args, stream):
+        flags, = struct.unpack_from("=i", args, at)
+        return call(args[:at] + struct.pack("=i", flags | _abi.KS_ROTARY_INVERSE) + args[at + 4:], stream)
+
+    monkeypatch.setattr(_abi, "ks_rotary_to_pages_4bit", inverse)
+    q, k, v = (view(tokens, h, dim, dtype, s, cuda_device, aligned) for h, s in ((hq, 1), (hk, 2), (hk, 3)))
+    kp, vp = (pools(-(-tokens // 16), 16, hk, dim, cuda_device, seed=s) for s in (4, 5))
+    slots = torch.arange(tokens, device=cuda_device)
+    pos = torch.randint(-(1 << 20), 1 << 40, (tokens,), generator=torch.Generator().manual_seed(6))
+    out = ks.rotary_to_pages_4bit(q, k, v, pos.to(cuda_device), ks.rotary_steps(rot, device=cuda_device), kp, vp, slots,
+                                  interleaved=interleaved, k_scale=factor, scale=1.25)
+    f = freqs(rot)
+    close(out, *rotated(q, pos, f, interleaved, scale=1.25, inverse=True), "q")
+    same_bytes(kp, slots, rotated(k, pos, f, interleaved, scale=1.25, inverse=True)[0], factor, "k")
+    same_bytes(vp, slots, v, 1.0, "v")
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
