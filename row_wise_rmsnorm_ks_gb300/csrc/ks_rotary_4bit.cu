@@ -382,6 +382,21 @@ struct Rows4Args {
     int32_t tokens;  // tokens at once in a CTA
 };
 
+// Whether a product of u and a code, rounded to FP32, may look like a tie of a 16-bit type without being one. Codes are 1 or
+// 1.5 times a power of two, and a tie's last 12 bits are 0 (fp16's; 15 for bf16, more for subnormal numbers).
+__device__ __forceinline__ bool twice_rounded(float u) {
+    const float p = __fmul_rn(u, 1.5f);
+    return (__float_as_uint(p) & 0xFFFu) == 0 && __fmaf_rn(u, 1.5f, -p) != 0.0f;
+}
+
+// u times a code for a 16-bit type: where FP32 does not hold it, FP32's neighbour towards 0 with its last bit set, which no
+// later rounding takes for a tie or for a number of that type. (A product has at most 26 bits: 24 of u, which is s times a
+// factor of any bits, and 2 of the code.)
+__device__ __forceinline__ float times_odd(float code, float u) {
+    const float p = __fmul_rz(code, u);
+    return __uint_as_float(__float_as_uint(p) | (__fmaf_rn(code, u, -p) != 0.0f ? 1u : 0u));
+}
+
 constexpr int kRowsThreads = 256;
 constexpr int kRowsEach = 8;  // tokens that a thread has in flight
 
@@ -390,7 +405,10 @@ constexpr int kRowsEach = 8;  // tokens that a thread has in flight
 // thread makes one 16-byte store of a row where the rows allow it, so that a warp's store is 512 bytes on end. (Measured,
 // 131001 tokens of 8 + 8 heads of 128 to bf16: 113 us, 102 us at the copy rate; 138 with a group,
 // two stores, a thread; 131 with four tokens a thread or with six CTAs an SM, 120 with four.)
-template <typename T, bool kVec>
+// kOdd: a factor has more than 18 bits, u then more than 22, and FP32 may round a product that its type rounds again: looked at
+// once a group, and one group in some thousands has its products rounded to odd first (factor 0.3: 116 us without, 120 with,
+// 140 with every product rounded to odd; a factor of 1 would take 118 to 120 here).
+template <typename T, bool kVec, bool kOdd>
 __global__ void __launch_bounds__(kRowsThreads, 5) pages4_rows_kernel(const __grid_constant__ Rows4Args args) {
     constexpr int kVals = kVec ? 16 / (int)sizeof(T) : 16, kParts = 16 / kVals;
     extern __shared__ __align__(16) int64_t at_token[][4];  // k's codes and scales, v's; -1: nowhere
@@ -447,17 +465,21 @@ __global__ void __launch_bounds__(kRowsThreads, 5) pages4_rows_kernel(const __gr
             const float unit = __fmul_rn(e4m3_to_float(scale[u]), pool.factor);
             const float2 units = make_float2(unit, unit);
             float2 f[kVals / 2];
+            auto values = [&](auto times) {
 #pragma unroll
-            for (int w = 0; w < (kVals + 7) / 8; ++w) {
-                uint32_t h[4];
-                fp4_to_half(w ? codes[u].y : codes[u].x, h);
+                for (int w = 0; w < (kVals + 7) / 8; ++w) {
+                    uint32_t h[4];
+                    fp4_to_half(w ? codes[u].y : codes[u].x, h);
 #pragma unroll
-                for (int i = 0; i < 4 && 4 * w + i < kVals / 2; ++i) {
-                    __half2 x;
-                    memcpy(&x, &h[i], 4);
-                    f[4 * w + i] = __fmul2_rn(__half22float2(x), units);
+                    for (int i = 0; i < 4 && 4 * w + i < kVals / 2; ++i) {
+                        __half2 x;
+                        memcpy(&x, &h[i], 4);
+                        f[4 * w + i] = times(__half22float2(x));
+                    }
                 }
-            }
+            };
+            if (kOdd && twice_rounded(unit)) values([&](float2 x) { return make_float2(times_odd(x.x, unit), times_odd(x.y, unit)); });
+            else values([&](float2 x) { return __fmul2_rn(x, units); });
             T *to = dst + u * args.tokens * stride;
             if constexpr (kVec) {
                 __stcs(reinterpret_cast<uint4 *>(to), Elem<T>::pack2(f));
@@ -467,6 +489,12 @@ __global__ void __launch_bounds__(kRowsThreads, 5) pages4_rows_kernel(const __gr
             }
         }
     }
+}
+
+template <typename T>
+const void *pick_rows(bool vec, bool odd) {
+    if (vec) return odd ? (const void *)pages4_rows_kernel<T, true, true> : (const void *)pages4_rows_kernel<T, true, false>;
+    return odd ? (const void *)pages4_rows_kernel<T, false, true> : (const void *)pages4_rows_kernel<T, false, false>;
 }
 
 // Strides whose product with their count, and a factor, that the kernels' arithmetic holds.
@@ -614,12 +642,16 @@ extern "C" ks_status_t ks_pages_4bit_to_rows(const ks_pages_4bit_rows_args_t *ar
     k_args.lanes = items < kRowsThreads ? (int32_t)items : kRowsThreads;
     k_args.tokens = kRowsThreads / k_args.lanes;
     const int64_t per_cta = (int64_t)k_args.tokens * kRowsEach;
-    const void *f;
-    switch (a.dtype) {
-    case KS_DTYPE_BF16: f = vec ? (const void *)pages4_rows_kernel<__nv_bfloat16, true> : (const void *)pages4_rows_kernel<__nv_bfloat16, false>; break;
-    case KS_DTYPE_F16: f = vec ? (const void *)pages4_rows_kernel<__half, true> : (const void *)pages4_rows_kernel<__half, false>; break;
-    default: f = vec ? (const void *)pages4_rows_kernel<float, true> : (const void *)pages4_rows_kernel<float, false>; break;
-    }
+    auto bits = [](float factor) {  // up to 18 of a number's 24 bits: the last 6 are 0
+        uint32_t w;
+        memcpy(&w, &factor, 4);
+        return w;
+    };
+    const bool odd = ((bits(a.k_pages.factor) | bits(a.v_pages.factor)) & 63u) != 0;
+    const void *f = a.dtype == KS_DTYPE_BF16  ? pick_rows<__nv_bfloat16>(vec, odd)
+                    : a.dtype == KS_DTYPE_F16 ? pick_rows<__half>(vec, odd)
+                    : vec                     ? (const void *)pages4_rows_kernel<float, true, false>
+                                              : (const void *)pages4_rows_kernel<float, false, false>;
     void *kp[] = {&k_args};
     const cudaError_t ce = launch_kernel(f, dim3((unsigned)((a.tokens + per_cta - 1) / per_cta)), dim3(kRowsThreads), (size_t)per_cta * 32, kp,
                                          static_cast<cudaStream_t>(stream), launch_pdl_enabled());

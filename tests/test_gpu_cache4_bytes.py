@@ -9,7 +9,7 @@ import torch
 
 import row_wise_rmsnorm_ks_gb300 as ks
 from row_wise_rmsnorm_ks_gb300 import _abi
-from test_gpu_cache4 import bits, pools, stored, unpacked
+from test_gpu_cache4 import F8, MAGNITUDES, bits, pools, stored, unpacked
 from test_gpu_decode_ops import close, freqs, no_faults, normal, rotated  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +101,39 @@ def test_turned_values_beyond_32_bits(cuda_device, dtype, size, scale, interleav
     ks.rotary_to_pages_4bit(None, k, v, pos.to(cuda_device), ks.rotary_steps(dim, device=cuda_device), kp, vp, slots,
                             interleaved=interleaved, scale=scale, k_scale=factor)
     same_bytes(kp, slots, rotated(k, pos, freqs(dim), interleaved, scale=scale)[0], factor, "k")
+
+
+def once(x, dtype):
+    """x (64 bits) rounded once to dtype, to the nearest, ties to even, in 64 bits."""
+    digits, least, most = {F16: (11, -14, 65504.0), BF16: (8, -126, torch.finfo(BF16).max), F32: (24, -126, torch.finfo(F32).max)}[dtype]
+    exponent = torch.frexp(x).exponent.sub(1).clamp(min=least).double()
+    step = torch.exp2(exponent - (digits - 1))
+    y = torch.round(x / step) * step
+    return torch.where(y.abs() > most, torch.copysign(torch.tensor(math.inf, dtype=torch.float64), x), y)
+
+
+def test_once_rounds_to_even():
+    x = torch.tensor([1 + 2.0 ** -11, 1 + 3 * 2.0 ** -11, 65519.0, 65520.0, 2.0 ** -25, 3 * 2.0 ** -25, 0.0], dtype=torch.float64)
+    assert once(x, F16).tolist() == [1.0, 1 + 2.0 ** -9, 65504.0, math.inf, 0.0, 2.0 ** -23, 0.0]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_rows_are_rounded_once(cuda_device, dtype, aligned):
+    """Every scale with every code, under factors of few and of 24 bits. u is the FP32 product of scale and factor."""
+    scale = torch.arange(127, dtype=torch.uint8)
+    codes = torch.arange(16, dtype=torch.uint8)
+    row = (codes[0::2] | codes[1::2] << 4).to(cuda_device)
+    pool = ks.empty_pages_4bit(1, 127, 1, 16, device=cuda_device)
+    pool[0].copy_(row.expand(1, 127, 1, 8))
+    pool[1].view(torch.uint8).copy_(scale.view(1, 127, 1, 1))
+    value = MAGNITUDES[codes.long() & 7] * torch.where(codes > 7, -1.0, 1.0)
+    slots = torch.arange(127, device=cuda_device)
+    g = torch.Generator().manual_seed(1)
+    factors = torch.exp2(torch.rand(300, generator=g) * 20 - 14).tolist()
+    for factor in [0.64040798, 1.0, 0.375, 0.3, 251 / 4096, 2.0 ** -64, 2.0 ** 64, 1 + 2.0 ** -23, 1 + 2.0 ** -22, *factors]:
+        unit = (scale.view(F8).float() * torch.tensor(factor, dtype=F32)).double()
+        want = once(unit[:, None] * value, dtype)
+        out = tuple(torch.zeros(127 * 16 + 1, dtype=dtype, device=cuda_device)[0 if aligned else 1:][:127 * 16].view(127, 1, 16) for _ in range(2))
+        for rows in ks.pages_4bit_to_rows(pool, pool, slots, k_scale=factor, v_scale=factor, dtype=dtype, out=out):
+            assert torch.equal(rows[:, 0].double().cpu(), want), f"factor {factor}"
