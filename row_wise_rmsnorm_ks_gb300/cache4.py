@@ -62,6 +62,7 @@ def _pools(k_pages, v_pages, k_scale, v_scale, device, kv_heads, dim):
     for v, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if not (isinstance(v, (int, float)) and _LEAST <= v <= _MOST):
             raise ValueError(f"{n} must be a number in 2^-64 .. 2^64")
+    _inference(k_pages[1], v_pages[1])
 
 
 def _fine(pool, shape, heads, dim, device):
@@ -71,7 +72,8 @@ def _fine(pool, shape, heads, dim, device):
     s0, s1, s2, s3 = scales.stride()
     return (codes.dtype is _U8 and scales.dtype is _F8 and codes.device == device and scales.device == device
             and codes.shape == (*shape, heads, dim // 2) and scales.shape == (*shape, heads, dim // 16)
-            and c3 == s3 == 1 and (codes.data_ptr(), scales.data_ptr(), c0, c1, c2, s0, s1, s2))
+            and c3 == s3 == 1 and not (scales.requires_grad and _grad())
+            and (codes.data_ptr(), scales.data_ptr(), c0, c1, c2, s0, s1, s2))
 
 
 def _packed(pool):

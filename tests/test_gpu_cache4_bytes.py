@@ -137,3 +137,24 @@ def test_rows_are_rounded_once(cuda_device, dtype, aligned):
         out = tuple(torch.zeros(127 * 16 + 1, dtype=dtype, device=cuda_device)[0 if aligned else 1:][:127 * 16].view(127, 1, 16) for _ in range(2))
         for rows in ks.pages_4bit_to_rows(pool, pool, slots, k_scale=factor, v_scale=factor, dtype=dtype, out=out):
             assert torch.equal(rows[:, 0].double().cpu(), want), f"factor {factor}"
+
+
+def test_pools_that_require_grad_are_refused(cuda_device):
+    """As those of 16 bits: a pool's scales are a floating-point tensor, which may be a leaf."""
+    k = normal((3, 2, 64), BF16, 1, cuda_device)
+    kp, vp = (ks.empty_pages_4bit(4, 8, 2, 64, device=cuda_device) for _ in range(2))
+    leaf = kp[0], kp[1].detach().requires_grad_()
+    slots = torch.arange(3, device=cuda_device)
+    i32 = dict(dtype=torch.int32, device=cuda_device)
+    table, lens, starts = torch.zeros(1, 1, **i32), torch.full((1,), 3, **i32), torch.tensor([0, 3], **i32)
+    calls = [lambda a, b: ks.rotary_to_pages_4bit(k, k, k, slots, ks.rotary_steps(64, device=cuda_device), a, b, slots),
+             lambda a, b: ks.rotary_to_pages_4bit(None, k, k, None, None, a, b, slots),
+             lambda a, b: ks.pages_4bit_to_rows(a, b, slots),
+             lambda a, b: ks.paged_attention_4bit(k, a, b, table, lens, starts),
+             lambda a, b: ks.paged_attention_4bit(k, a, b, table, lens, starts, out=torch.empty_like(k))]
+    for call in calls:
+        for pair in ((leaf, vp), (vp, leaf)):
+            with pytest.raises(RuntimeError, match="inference"):
+                call(*pair)
+            with torch.no_grad():
+                call(*pair)
