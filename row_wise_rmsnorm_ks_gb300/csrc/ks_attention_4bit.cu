@@ -760,12 +760,8 @@ int resident(const void *f, int smem) {
 }
 
 // Query rows of a tile, in eights: 16 where head_dim leaves the registers and a sequence may have more than 8; 32, the
-// tensor-core kernel's, where it may have more than 32, or 48 of up to 64 dims: its row tiles begin and end in the time of 5
-// of their steps, and it makes fp16 tiles of all keys for however few rows, where each 16 rows of the other kernel read and
-// convert them again. (Measured, us, 16-row tiles and tensor cores, 32 / 8 heads. 128 dims, 8 sequences of 4000 keys: 32 rows 33, 42;
-// 48 43, 43; 64 53, 42; 64 sequences of 4000: 32 173, 208; 48 251, 212; 64 of 60: 35, 40; 48, 40. 64 dims, 64 sequences of
-// 4000: 48 152, 177; 64 196, 178.) More than 16 already where 16-row tiles have to load to registers and the tensor cores'
-// codes come by maps (96 dims, 64 sequences of 4000: 32 rows 384, 208; 80 dims, neither: 370, 424).
+// tensor-core kernel's, where it may have more than `most`: its row tiles begin and end in the time of 5 of their steps, and it
+// makes fp16 tiles of all keys for however few rows, where each 16 rows of the other kernel read and convert them again.
 constexpr int kTc = 32;
 int row_tiles(const ks_attention_args_t &a, int most) {
     const int64_t q_len = a.max_q_len > 0 && a.max_q_len < a.tokens ? a.max_q_len : a.tokens;
@@ -800,6 +796,17 @@ int pool_kind(const ks_attention_4bit_args_t &args, uintptr_t code_align, uintpt
     for (const ks_pages_4bit_t *p : {&k, &v})
         runs |= (uintptr_t)p->scales | (uintptr_t)(a.pages > 1 ? p->scale_page_stride : 0) | (uintptr_t)(a.kv_heads > 1 ? p->scale_head_stride : 0);
     return runs & 15 ? kBlocks : kRuns;
+}
+
+// Rows up to which 16-row tiles pay. (Measured, us, 16-row tiles and tensor cores, 64 contexts of 4000 keys, 32 / 8 heads,
+// pages of 16 keys, or of 24 where it says so. Rings: 128 dims, 32 rows 171, 210; 48 245, 212; 64 dims, 48 151, 174; 64 192, 175.
+// Where 16-row tiles load to registers and the tensor cores' codes come by maps: 96 dims, 24 rows 384, 207; 32 dims 192, 172; by 16
+// bytes: 128 dims in 24s, 24 rows 396, 205; 64 dims in 24s 204, 161; by 8: 96 dims in 24s, 32 rows 380, 457; 48 557, 460; 128 dims,
+// unaligned, 32 415, 467; 48 611, 469; 80 dims, 32 381, 454; 48 556, 455; 48 dims, 32 200, 241; 48 287, 242.)
+int most_rows(const ks_attention_4bit_args_t &args, int pool, uintptr_t code_align, uintptr_t scale_align) {
+    const ks_attention_args_t &a = args.attention;
+    if (pool != kAny) return a.head_dim > 64 ? 32 : 48;
+    return attn4_tc_copies(a, pool4(args.k_pages), pool4(args.v_pages), pools_alike(args), code_align, scale_align) == kCopyBy8 ? 32 : 16;
 }
 
 ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, int pool, Attn4Plan *p) {
@@ -918,7 +925,7 @@ ks_status_t ks_paged_attention_4bit(const ks_attention_4bit_args_t *args, ks_str
         return fail(KS_ERR_INVALID_ARGUMENT, "the workspace must be device memory aligned to 16 bytes");
     Attn4Plan p;
     const int pool = pool_kind(*args, code_align, scale_align);
-    int tiles = row_tiles(a, pool == kAny && a.head_dim % 32 == 0 ? 16 : a.head_dim > 64 ? 32 : 48);
+    int tiles = row_tiles(a, most_rows(*args, pool, code_align, scale_align));
     if (tiles == kTc && !attn4_tc_fits(a)) tiles = 2;
     if ((st = plan4(*args, tiles, pool, &p)) != KS_SUCCESS) return st;
     const int64_t need = attn_workspace_bytes(p.args.s, p.ctas);

@@ -29,6 +29,20 @@ bool attn4_tc_fits(const ks_attention_args_t &a) {
     return true;
 }
 
+int attn4_tc_copies(const ks_attention_args_t &a, const Pool4 &k, const Pool4 &v, bool alike, uintptr_t code_align, uintptr_t scale_align) {
+    const int64_t dim = a.head_dim;
+    if ((code_align & 15) != 0 || !alike) return kCopyBy8;
+    bool map = dim % 32 == 0 && (scale_align & 1) == 0 && a.page_size % 8 == 0 && (kKeys % a.page_size == 0 || a.page_size % kKeys == 0);
+    // the maps' strides are below 2^40 bytes and not zero
+    const int64_t counts[3] = {a.pages, a.page_size, a.kv_heads};
+    for (const Pool4 *p : {&k, &v}) {
+        const int64_t strides[3] = {p->code_page, p->code_slot, p->code_head};
+        for (int i = 0; i < 3; ++i)
+            if (counts[i] > 1 && (strides[i] <= 0 || strides[i] >= (1ll << 39))) map = false;
+    }
+    return map ? kCopyByMap : (dim == 64 || dim == 128) && (scale_align & (dim / 16 - 1)) == 0 ? kCopyBy16 : kCopyBy8;
+}
+
 // Steps that beginning and ending a row tile costs: more than with 16-bit pages, whose next tile's first keys are there
 // sooner. (Measured, 16 sequences of 1..517 tokens over 392..4439 keys: 212 us with 2, 188 with 3, 177 with 5, 184 with 8; the long
 // prompt's time does not change.)
@@ -46,14 +60,7 @@ cudaError_t attn4_tc_launch(const Attn4Args &args, uintptr_t code_align, uintptr
     pages.whole = (dim == 64 || dim == 128) && (code_align & 15) == 0 && (scale_align & (dim / 16 - 1)) == 0 && args.alike;
     pages.page_units = args.page_units;
     pages.slot_units = args.slot_units;
-    pages.by_map = 0;
-    if (dim % 32 == 0 && (code_align & 15) == 0 && (scale_align & 1) == 0 && args.alike && s.a.page_size % 8 == 0 && (kKeys % s.a.page_size == 0 || s.a.page_size % kKeys == 0)) {
-        // the maps' strides are below 2^40 bytes and not zero
-        const int64_t strides[3] = {args.k.code_page, args.k.code_slot, args.k.code_head}, counts[3] = {s.a.pages, s.a.page_size, s.a.kv_heads};
-        pages.by_map = 1;
-        for (int i = 0; i < 3; ++i)
-            if (counts[i] > 1 && (strides[i] <= 0 || strides[i] >= (1ll << 39))) pages.by_map = 0;
-    }
+    pages.by_map = attn4_tc_copies(s.a, args.k, args.v, args.alike, code_align, scale_align) == kCopyByMap;
     if (pages.by_map && (!attn_codes_map(&pages.k_map, s, args.k) || !attn_codes_map(&pages.v_map, s, args.v)))
         return cudaErrorInvalidValue;
     const bool bf16 = s.a.dtype == KS_DTYPE_BF16;

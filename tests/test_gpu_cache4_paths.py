@@ -34,16 +34,21 @@ def needed(st, rows):
     return int(re.search(r"(\d+) are needed", str(e.value)).group(1))
 
 
-@pytest.mark.parametrize("dim, page_size, order, maps", [(96, 16, "heads_outer", True), (96, 24, "heads_outer", False),
-                                                         (96, 16, "unaligned", False), (32, 128, "heads_outer", True),
-                                                         (32, 5, "heads_outer", False), (160, 16, "heads_outer", False)])
-def test_drafts_on_tensor_cores_where_copies_by_map_pay(cuda_device, dim, page_size, order, maps):
-    """17 .. 32 rows of heads that 16-row tiles load to registers: the tensor cores' kernel only where its codes come by
-    tensor maps."""
+@pytest.mark.parametrize("dim, page_size, order, rows, cores", [
+    (128, 16, "heads_outer", 24, False), (128, 16, "heads_outer", 40, True), (64, 16, "heads_outer", 40, False),  # rings
+    (96, 16, "heads_outer", 24, True), (112, 16, "heads_outer", 24, False), (128, 24, "heads_outer", 24, True),
+    (96, 24, "heads_outer", 24, False), (96, 16, "unaligned", 24, False), (128, 16, "unaligned", 24, False),
+    (96, 24, "heads_outer", 40, True), (128, 16, "unaligned", 40, True), (64, 24, "heads_outer", 24, True),
+    (64, 16, "unaligned", 24, False), (32, 128, "heads_outer", 24, True), (48, 5, "slots_outer", 24, False),
+    (48, 5, "slots_outer", 40, True),
+    (160, 16, "heads_outer", 40, False),
+])
+def test_drafts_on_tensor_cores_where_that_pays(cuda_device, dim, page_size, order, rows, cores):
+    """17 .. 48 rows: 16-row tiles or the tensor cores' kernel, by how either's codes come."""
     st = build([24, 20], [500, 300], 2, 2, dim, BF16, page_size, cuda_device, order=order)
     tiles = needed(st, 16)
-    assert (needed(st, 24) > tiles) == maps
-    check_all(attend(st, max_q_len=24), st)
+    assert (needed(st, rows) > tiles) == cores
+    check_all(attend(st, max_q_len=rows), st)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
