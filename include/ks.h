@@ -514,8 +514,8 @@ ks_status_t ks_paged_attention(const ks_attention_args_t *args, ks_stream_t stre
  * the values call for another) and the group's largest magnitude A:
  *     s = A / (6 g), at most 448;   u = s g, in FP32;   code = x / u, at most 6 (0 where s is 0)
  * s and the codes to the nearest, ties to the even code, as of real numbers: an FP32 result near a border is
- * decided exactly. Bit 3 is set where x < 0, also if the magnitude becomes 0 (unless s is 0). What is held is u * code. Infinities are held as the largest value; a group with a NaN gets
- * the scale NaN.
+ * decided exactly. Bit 3 is set where x < 0, also if the magnitude becomes 0 (unless s is 0). What is held is
+ * u * code. Infinities are held as the largest value; a group with a NaN gets the scale NaN and codes 0.
  */
 typedef struct ks_pages_4bit {
     void *codes;                 /* [pages, page_size, kv_heads, head_dim / 2] bytes; address and strides
@@ -559,11 +559,12 @@ ks_status_t ks_pages_4bit_to_rows(const ks_pages_4bit_rows_args_t *args, ks_stre
 
 /*
  * ks_paged_attention over 4-bit pools. args->attention is read as there, except for k_pages and v_pages and their
- * strides. Keys and values enter the products exactly as they are held. bfloat16 queries enter as fp16 after a
- * row's largest magnitude is brought to 1 .. 2 by a power of two (values 2^-14 times as large and smaller lose
- * at most 2^-25 of it), and probabilities as fp16 for either type (those below 2^-22 of a row's largest to multiples
- * of 2^-32 of it). head_dim: a multiple of 16, at most 256. The workspace is that of
- * ks_paged_attention_4bit_workspace.
+ * strides. Keys and values enter the products as s * code, which fp16 holds exactly; the pools' factors enter in
+ * FP32 with the scores' scale and the output's (u's own rounding, 2^-24 where a factor is no power of two, is left
+ * out). bfloat16 queries enter as fp16 after a row's largest magnitude is brought to 1 .. 2 by a power of two (values
+ * 2^-14 times as large and smaller lose at most 2^-25 of it), and probabilities as fp16 for either type (those below
+ * 2^-22 of a row's largest to multiples of 2^-32 of it). head_dim: a multiple of 16, at most 256. The workspace is that
+ * of ks_paged_attention_4bit_workspace.
  */
 typedef struct ks_attention_4bit_args {
     ks_attention_args_t attention;

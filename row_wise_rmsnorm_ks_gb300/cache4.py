@@ -275,9 +275,10 @@ def paged_attention_4bit(q: torch.Tensor, k_pages, v_pages, page_table: torch.Te
     """paged_attention() over 4-bit pools: q, page_table, kv_lens, q_starts, scale, causal, max_q_len, out and
     workspace are as there (the workspace of at least paged_attention_4bit_workspace(...) bytes).
 
-    Keys and values enter the products exactly as they are held. bfloat16 queries enter as float16 after a power of
-    two has brought a row's largest magnitude to 1 .. 2 (values below 2^-14 of it lose at most 2^-25 of it), and
-    probabilities as float16 for either type; scores, sums and outputs are FP32, one rounding at the end."""
+    Keys and values enter the products as codes times scales, without a rounding, and the factors in FP32 with the
+    scores' scale and the output's. bfloat16 queries enter as float16 after a power of two has brought a row's largest
+    magnitude to 1 .. 2 (values below 2^-14 of it lose at most 2^-25 of it), and probabilities as float16 for either
+    type; scores, sums and outputs are FP32, one rounding at the end."""
     try:
         dt, dev, code = q.dtype, q.device, _DTYPES[q.dtype]
         tokens, hq, dim = q.shape

@@ -4,7 +4,8 @@
 // Keys and values are fp16 numbers exactly (ks_fp4.cuh), so both products run as fp16 with FP32 sums. A bf16 query row
 // is brought to a largest magnitude of 1 .. 2 by a power of two, which its scores are given back: values down to
 // 2^-14 of the largest stay exact, smaller ones lose at most 2^-25 of it, less than an FP32 sum of the row's
-// products does. Probabilities are fp16 too, 2^15 times as large as they are (as in ks_attention.cu).
+// products does. Probabilities are fp16 too, 2^11 times as large as they are when a row's base is taken, and up to 2^15
+// times as later scores outgrow it (kLift, kGrowth). The pools' factors go into the scores' scale and the output's, in FP32.
 //
 // Few rows make this a stream of the cache, 144 bytes per key of 128 values, and of the instructions that make fp16 of
 // it: each pair of codes is a conversion and a product with its group's scale. So the matrix instructions
@@ -308,7 +309,8 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
                     for (int i = 0; i < (kR + 1) / 2; ++i) {
                         const int in = i * 32 + lane, part = in / (4 * kR);
                         if (kR % 2 == 0 || in < 16 * kR)
-                            copy_async<16>(units + in * 16, (part < 2 ? k_scales : v_scales) + (part & 1 ? at[1] : at[0]) * 2ull + in % (4 * kR) * 16,
+                            copy_async<16>(units + in * 16,
+                                           (part < 2 ? k_scales : v_scales) + (part & 1 ? at[1] : at[0]) * 2ull + in % (4 * kR) * 16,
                                            part & 1 ? n[1] : n[0]);
                     }
                 } else {
@@ -614,7 +616,7 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
 #pragma unroll
                 for (int w = 0; w < kR; ++w) {
                     // the word's group among the lane's scales; with kR odd it depends on whether v_first is
-                    const int i0 = kR % 2 ? w / 2 : w / 2, i1 = kR % 2 ? (w + 1) / 2 : w / 2;
+                    const int i0 = w / 2, i1 = kR % 2 ? (w + 1) / 2 : w / 2;
                     uint32_t h[2][2][4];  // [pair of keys][even, odd dims][byte]
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -659,7 +661,8 @@ attn4_rows_kernel(const __grid_constant__ Attn4Args args) {
                 const int r = n * 8 + 2 * t + i;
 #pragma unroll
                 for (int j = 0; j < 4 * kR; ++j)
-                    *reinterpret_cast<float2 *>(ow + (warp * kRows + r) * kPitch + 8 * kR * g + 2 * j) = make_float2(o[n][j][i], o[n][j][2 + i]);
+                    *reinterpret_cast<float2 *>(ow + (warp * kRows + r) * kPitch + 8 * kR * g + 2 * j) =
+                        make_float2(o[n][j][i], o[n][j][2 + i]);
                 if (g == 0) {
                     mw[warp][r] = m[n][i];
                     lw[warp][r] = l[n][i];
@@ -762,6 +765,10 @@ int resident(const void *f, int smem) {
 // Query rows of a tile, in eights: 16 where head_dim leaves the registers and a sequence may have more than 8; 32, the
 // tensor-core kernel's, where it may have more than `most`: its row tiles begin and end in the time of 5 of their steps, and it
 // makes fp16 tiles of all keys for however few rows, where each 16 rows of the other kernel read and convert them again.
+// Above 128 dims, which no tensor-core kernel takes, 8 rows whatever their number: at 256 dims two tiles take all 255 registers
+// and spill 88 to 692 bytes. (Measured, us, 8 rows and 16. 256 dims, 32 / 2 heads: one context of 100000 keys 46, 52; 64 of
+// 4000 keys 76, 63; 16 / 4 heads, 2048 tokens over 8192 keys 1441, 997; 192 dims 1160, 757. So 16 rows would pay but for one
+// context, and tensor cores more for prompts; both are left.)
 constexpr int kTc = 32;
 int row_tiles(const ks_attention_args_t &a, int most) {
     const int64_t q_len = a.max_q_len > 0 && a.max_q_len < a.tokens ? a.max_q_len : a.tokens;
@@ -794,7 +801,8 @@ int pool_kind(const ks_attention_4bit_args_t &args, uintptr_t code_align, uintpt
     if (k.code_slot_stride != 32 * r) return kBlocks;
     uintptr_t runs = 0;  // a block of scales is copied by 16 bytes too
     for (const ks_pages_4bit_t *p : {&k, &v})
-        runs |= (uintptr_t)p->scales | (uintptr_t)(a.pages > 1 ? p->scale_page_stride : 0) | (uintptr_t)(a.kv_heads > 1 ? p->scale_head_stride : 0);
+        runs |= (uintptr_t)p->scales | (uintptr_t)(a.pages > 1 ? p->scale_page_stride : 0) |
+                (uintptr_t)(a.kv_heads > 1 ? p->scale_head_stride : 0);
     return runs & 15 ? kBlocks : kRuns;
 }
 
@@ -851,7 +859,8 @@ ks_status_t plan4(const ks_attention_4bit_args_t &a, int tiles, int pool, Attn4P
 ks_status_t check_sizes4(const ks_attention_args_t &a) {
     const ks_status_t st = attn_check_sizes(a);
     if (st != KS_SUCCESS) return st;
-    if (a.head_dim % 16) return fail(KS_ERR_INVALID_ARGUMENT, "4-bit pages take head_dims of whole groups of 16 (got %lld)", (long long)a.head_dim);
+    if (a.head_dim % 16)
+        return fail(KS_ERR_INVALID_ARGUMENT, "4-bit pages take head_dims of whole groups of 16 (got %lld)", (long long)a.head_dim);
     return KS_SUCCESS;
 }
 

@@ -1,7 +1,7 @@
 // Paged attention over 4-bit pages on the fifth-generation tensor cores: the kernel of ks_attention_tc.cu, its operands
 // fp16, with four more warps that make the tiles of keys and values.
 //
-// Code times scale is an fp16 number exactly, so what the matrix instructions read is what the cache holds; the pools'
+// Code times scale is an fp16 number exactly, and so enters the matrix instructions without a rounding; the pools'
 // factors go into the scores' scale and the output's. A thread of the four warps has one key of a step: 64 bytes of codes
 // become 256 bytes in the swizzled layout, 64 conversions of a pair and as many products a tile. bf16 queries become fp16 in
 // shared memory, each row times a power of two, by the warps that read their scores; fp16 probabilities follow.
@@ -10,8 +10,8 @@
 //     8 bytes a key, are read a step ahead. Other pools (any page size, odd heads of 16, unaligned rows) are copied by the four
 //     warps themselves, two tiles ahead (1.07 times the time where rows are aligned; with 80 dims, whose rows are copied by 8
 //     bytes, twice: 64 contexts of 4000 keys, 64 rows, 424 us for 210).
-//   - 768 threads launch with 80 registers each; the softmax takes 96 (104 with 16-bit pages: some spills), the four warps 56,
-//     the other four 40. Four tiles of 128 keys in the ring instead of five make room for the codes.
+//   - 768 threads launch with 80 registers each; the softmax takes 96 (104 with 16-bit pages; 64 to 232 bytes a thread spill), the
+//     four warps 56, the other four 40. Four tiles of 128 keys in the ring instead of five make room for the codes.
 // Bound by issue and the chain of a step: 8192 tokens over 16384 keys, 32 query and 8 key/value heads of 128, bf16, 1.08 ms,
 // 1.52 PFLOP/s; the same without making tiles 0.98, with 16-bit pages 0.92 (bf16) and 0.97 (fp16, whose probabilities need the
 // lift). About 3000 cycles a step, 2048 of them products. With loads of the codes to registers 1.42, by the warps' own copies 1.16.
@@ -44,8 +44,9 @@ int attn4_tc_copies(const ks_attention_args_t &a, const Pool4 &k, const Pool4 &v
 }
 
 // Steps that beginning and ending a row tile costs: more than with 16-bit pages, whose next tile's first keys are there
-// sooner. (Measured, 16 sequences of 1..517 tokens over 392..4439 keys: 212 us with 2, 188 with 3, 177 with 5, 184 with 8; the long
-// prompt's time does not change.)
+// sooner. (Measured, us with 2, 3, 5 and 8: 16 sequences of 1..517 tokens over 392..4439 keys 212, 188, 177, 184; of sequences of
+// one length, 16 of 128 tokens over 2000 keys 99, 99, 97, 97; 64 of 20 over 1000 110, 108, 106, 106; 40 of 65 over 300, 64 dims, 67,
+// 67, 69, 67; 3 of 700 over 5000, 64 dims, 79, 79, 81, 85. The long prompt's does not change.)
 int attn4_tc_tile_cost() { return 5; }
 
 cudaError_t attn4_tc_launch(const Attn4Args &args, uintptr_t code_align, uintptr_t scale_align, int ctas, cudaStream_t stream,

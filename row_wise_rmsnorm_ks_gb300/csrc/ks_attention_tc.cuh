@@ -403,7 +403,8 @@ __device__ __forceinline__ void convert_copied(const AttnArgs &s, const Pages4 &
                         next[1][i] = __ldg(reinterpret_cast<const uint16_t *>(v_scales + e) + i);
                     }
             } else if constexpr (kWords == 2) {
-                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(k_scales + e)), y = __ldg(reinterpret_cast<const uint2 *>(v_scales + e));
+                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(k_scales + e));
+                const uint2 y = __ldg(reinterpret_cast<const uint2 *>(v_scales + e));
                 next[0][0] = x.x;
                 next[0][1] = x.y;
                 next[1][0] = y.x;
@@ -448,9 +449,10 @@ __device__ __forceinline__ void convert_copied(const AttnArgs &s, const Pages4 &
     }
 }
 
-// The converting warps where they copy for themselves: a thread per key of a step, a warp for 32 of them. A warp copies its keys' codes and scales to a
-// ring of its own, two tiles ahead, neighbouring lanes neighbouring bytes (with loads to registers, a key a thread, the
-// long prompt takes 1.3 times as long); a thread then makes its row fp16 in the layout that the matrix instructions read.
+// The converting warps where they copy for themselves: a thread per key of a step, a warp for 32 of them. A warp copies its
+// keys' codes and scales to a ring of its own, two tiles ahead, neighbouring lanes neighbouring bytes (with loads to registers,
+// a key a thread, the long prompt takes 1.3 times as long); a thread then makes its row fp16 in the layout that the matrix
+// instructions read.
 // Rows behind the last key that the row tile sees are zeros.
 template <int kDim, bool kWhole>
 __device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &pages, Place &place, bool more, uint8_t *ring, uint8_t *raw,
@@ -506,7 +508,8 @@ __device__ __forceinline__ void convert_pages(const AttnArgs &s, const Pages4 &p
                     const uint32_t w = __shfl_sync(0xFFFFFFFFu, where, key), r = __shfl_sync(0xFFFFFFFFu, slots, key);
                     const bool in = w != kNone && g < groups;
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst + key * C::kRawRow + g * 8),
-                                 "l"(in ? codes + w * pool.code_page + r * pool.code_slot + g * 8 : pool.codes), "r"(in ? 8 : 0) : "memory");
+                                 "l"(in ? codes + w * pool.code_page + r * pool.code_slot + g * 8 : pool.codes), "r"(in ? 8 : 0)
+                                 : "memory");
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");

@@ -9,7 +9,9 @@
 // A group with a NaN has the scale NaN, and reads back as NaN.
 //
 // A code times a scale has at most 6 significant bits and lies in 2^-10 .. 2688: fp16 holds it exactly. The
-// attention's products therefore take keys and values as fp16 without a rounding, whatever the queries' type.
+// attention's products therefore take codes times scales as fp16 without a rounding, whatever the queries' type, and
+// the factors in FP32 with the scores' scale and the output's: u's own rounding, 2^-24 with a factor that is no power of
+// two, is not in them.
 #pragma once
 
 #include "ks_decode.cuh"
@@ -100,8 +102,8 @@ __device__ __forceinline__ float fp4_magnitude(uint32_t code) {  // of a code wi
 __device__ __forceinline__ float product_less(float a, float b, float x) { return __fmaf_rn(a, b, -x); }
 __device__ __forceinline__ double product_less(float a, float b, double x) { return (double)a * (double)b - x; }
 
-// The group's scale, given that the quotient A / (6 g) lies in [low, high], FP32 numbers; with `sure` false the two may
-// have different codes, neighbours, and A itself decides.
+// The group's scale, given that the quotient A / (6 g) lies in [low, high], FP32 numbers whose codes are one or
+// neighbours: then A itself decides.
 template <typename F>
 __device__ __forceinline__ uint32_t fp4_scale(float low, float high, F A, float g) {
     const uint32_t c = e4m3_codes(fminf(fmaxf(low, 0.0f), 512.0f), fminf(high, 512.0f));

@@ -60,8 +60,8 @@ __device__ __forceinline__ void prefetch_l2(const void *p, int n) {
 // What a thread does with its vectors of a row. kAhead asks for weights and gate before the sums that they wait for, at
 // the cost of their registers; without it, x stays packed until the second sum, so that more rows are on their way.
 template <typename T, int V, int kTeam, bool kAhead>
-__device__ __forceinline__ void gated_row(const ks_gated_norm_args_t &a, int64_t row, int hv, int t, int g, uint4 (&xv)[V], const uint4 (&rv)[V],
-                                          float (&red)[2][32], int &slot) {
+__device__ __forceinline__ void gated_row(const ks_gated_norm_args_t &a, int64_t row, int hv, int t, int g, uint4 (&xv)[V],
+                                          const uint4 (&rv)[V], float (&red)[2][32], int &slot) {
     using E = Elem<T>;
     constexpr int P = E::kPerVec / 2;
     constexpr bool kPair = E::kPairMath;
@@ -184,7 +184,7 @@ struct Few {
 };
 
 // Rows that no 16-byte vector fits, kValues for each thread: N values an access, the row in registers between its sums as
-// above.
+// above (64 at most; of one value an access and 16 a thread, 24 to 32 bytes of them spill).
 template <typename T, int N, int kValues>
 __global__ void __launch_bounds__(1024, 1) gated_odd_kernel(const __grid_constant__ GatedArgs args) {
     using F = Few<T, N>;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(1024, 1) gated_odd_kernel(const __grid_constan
             SumSq acc;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                    float f[N];
+                float f[N];
                 F::unpack(xv[k], f);
                 acc.add(f);
             }

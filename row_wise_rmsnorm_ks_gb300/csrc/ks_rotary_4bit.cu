@@ -9,9 +9,10 @@
 // of a fused multiply-add for the others.
 //
 // Bound by memory where there are many tokens: the queries are read and written once, keys and values read once, 9/16 byte
-// written for each. Measured, 8192 tokens of 56 + 8 + 8 heads of 128, fp16, with the read-back: 86 us, 46 at the copy rate:
+// written for each. Measured, 8192 tokens of 56 + 8 + 8 heads of 128, fp16, with the read-back: 84 us, 46 at the copy rate:
 // 42 the queries (4.5 TB/s while the cache ends in L2), 30 the groups (issue: a quotient, two windows and their codes for each
-// value), 13 the read-back. 64 tokens with the read-back 9.3 us, two launches and a chain of loads each.
+// value; at 80 registers, three CTAs an SM, 24 to 156 bytes of them spill), 13 the read-back. 64 tokens with the read-back 8.4 us,
+// two launches and a chain of loads each.
 #include <cuda_runtime.h>
 
 #include "ks_rotary.cuh"
@@ -348,7 +349,10 @@ __global__ void __launch_bounds__(kRotThreads) rotary_4bit_kernel(const __grid_c
 // have its registers in common: measured at 8192 tokens of 56 + 8 + 8 heads, 88 us and more for 42 and 29.) It is
 // launched to start while the queries' last CTAs run: those began after all earlier work was done, and of their own
 // they write nothing that is read here. It ends after them. (`alone`: without queries, or where the queries' kernel may
-// itself start before earlier work's end, it waits at its beginning.)
+// itself start before earlier work's end, it waits at its beginning.) Taken from 1024 tokens on. (Measured with cold caches, us, one
+// kernel and two, at 512, 1024 and 2048 tokens, bf16: 32 + 8 + 8 heads of 128 18.6, 27.8, 44.3 and 18.8, 21.6, 30.9; 0 + 8 + 8 15.5,
+// 22.2, 32.4 and 15.0, 16.0, 22.6; 8 + 1 + 1 12.4, 14.5, 19.6 and 13.4, 15.5, 18.5; 16 + 16 + 16 of 64 13.5, 15.5, 21.7 and 15.5, 17.5,
+// 23.7, equal at 1536.)
 template <typename T, bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kRotThreads, 3) pages4_kernel(const __grid_constant__ Rotary4Args args, int alone) {
     __shared__ __align__(16) float tables[2 * kTable];
@@ -404,7 +408,8 @@ constexpr int kRowsEach = 8;  // tokens that a thread has in flight
 // the pools is found once per token, in shared memory, and a group's FP32 unit multiplies its values two at a time; and a
 // thread makes one 16-byte store of a row where the rows allow it, so that a warp's store is 512 bytes on end. (Measured,
 // 131001 tokens of 8 + 8 heads of 128 to bf16: 113 us, 102 us at the copy rate; 138 with a group,
-// two stores, a thread; 131 with four tokens a thread or with six CTAs an SM, 120 with four.)
+// two stores, a thread; 131 with four tokens a thread or with six CTAs an SM, 120 with four. Five leave 48 registers, of which
+// 24 to 44 bytes a thread spill.)
 // kOdd: a factor has more than 18 bits, u then more than 22, and FP32 may round a product that its type rounds again: looked at
 // once a group, and one group in some thousands has its products rounded to odd first (factor 0.3: 116 us without, 120 with,
 // 140 with every product rounded to odd; a factor of 1 would take 118 to 120 here).
@@ -653,8 +658,8 @@ extern "C" ks_status_t ks_pages_4bit_to_rows(const ks_pages_4bit_rows_args_t *ar
                     : vec                     ? (const void *)pages4_rows_kernel<float, true, false>
                                               : (const void *)pages4_rows_kernel<float, false, false>;
     void *kp[] = {&k_args};
-    const cudaError_t ce = launch_kernel(f, dim3((unsigned)((a.tokens + per_cta - 1) / per_cta)), dim3(kRowsThreads), (size_t)per_cta * 32, kp,
-                                         static_cast<cudaStream_t>(stream), launch_pdl_enabled());
+    const cudaError_t ce = launch_kernel(f, dim3((unsigned)((a.tokens + per_cta - 1) / per_cta)), dim3(kRowsThreads),
+                                         (size_t)per_cta * 32, kp, static_cast<cudaStream_t>(stream), launch_pdl_enabled());
     if (ce != cudaSuccess) return fail(KS_ERR_CUDA, "launch: %s", cudaGetErrorString(ce));
     return KS_SUCCESS;
 }

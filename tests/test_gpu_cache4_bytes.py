@@ -134,7 +134,8 @@ def test_rows_are_rounded_once(cuda_device, dtype, aligned):
     for factor in [0.64040798, 1.0, 0.375, 0.3, 251 / 4096, 2.0 ** -64, 2.0 ** 64, 1 + 2.0 ** -23, 1 + 2.0 ** -22, *factors]:
         unit = (scale.view(F8).float() * torch.tensor(factor, dtype=F32)).double()
         want = once(unit[:, None] * value, dtype)
-        out = tuple(torch.zeros(127 * 16 + 1, dtype=dtype, device=cuda_device)[0 if aligned else 1:][:127 * 16].view(127, 1, 16) for _ in range(2))
+        whole = [torch.zeros(127 * 16 + 1, dtype=dtype, device=cuda_device) for _ in range(2)]
+        out = tuple((t[:-1] if aligned else t[1:]).view(127, 1, 16) for t in whole)
         for rows in ks.pages_4bit_to_rows(pool, pool, slots, k_scale=factor, v_scale=factor, dtype=dtype, out=out):
             assert torch.equal(rows[:, 0].double().cpu(), want), f"factor {factor}"
 
