@@ -11,6 +11,7 @@ A pool is a pair (codes, scales): uint8 [pages, page_size, kv_heads, head_dim / 
 3, 4, 6 times s times the pool's factor (k_scale, v_scale: one number per pool, the same in every call that
 uses it). With the largest magnitude A of a group, s is A / (6 factor) rounded to e4m3 (2^-9 .. 448): a factor
 of 1 serves values whose groups reach some hundredths to some thousands, another brings them there.
+Factors, and the scale of rotated values, are FP32 numbers: what is held is defined by their FP32 values.
 
 Tokens, checks, streams and errors are those of the 16-bit cache's operators.
 """
